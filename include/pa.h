@@ -86,6 +86,8 @@ typedef enum {
                                         block table gives position seq_lens[i] - 1          */
 #define PA_DEVERR_PREFIX_MISMATCH 0x20u /* pa_decode_shared_prefix: a table row does not start
                                            with row 0's prefix blocks (results invalid)   */
+#define PA_DEVERR_PAIR_ORDER   0x40u /* pa_move_blocks: src ids not strictly ascending while a
+                                        block table is rewritten (the table is unspecified)  */
 
 /*
  * pa_reshape_and_cache: write the K/V rows of num_tokens new tokens into their slots.
@@ -397,6 +399,83 @@ typedef struct {
 PA_API pa_status pa_step(const pa_step_desc* step, void* stream);
 
 /*
+ * Scored attention: decode and chunked prefill over the paged pool with scores that are capped,
+ * biased by distance or masked beyond the causal bound. For a query row at position p of a
+ * sequence with L keys, q head h, kv head g = h / (num_q_heads / num_kv_heads):
+ *   z_j = scale * q . k_j
+ *   z_j = softcap * tanh(z_j / softcap)              when softcap > 0
+ *   z_j = z_j - alibi_slopes[h] * |p - j|            when alibi_slopes is given
+ *   key j is visible when  j < L,  j >= key_start,  and
+ *       ( j < prefix_len  or  ( j <= p  and  (window == 0 or j > p - window) ) )
+ *   out = sum over visible j of softmax(z)_j v_j;  an all-zero row when no key is visible
+ * softcap bounds the scores; alibi_slopes is a linear distance bias; window a sliding window that
+ * counts the row's own key; prefix_len names the first keys of a sequence that every row of it
+ * sees, rows before them included (prompts whose prefix is attended in both directions, and
+ * first tokens that stay visible under a window); key_start the first key a row may see (a
+ * document mask for packed documents: the position where the row's document starts).
+ *   softcap       0 (none) or a positive finite number
+ *   alibi_slopes  NULL or [num_q_heads] fp32
+ *   window        0 (none) or a positive number of keys
+ *   key_start     NULL or int32 per query row: [num_seqs] for decode, [total_query_tokens] for
+ *                 prefill; a negative entry counts as 0, one past the row's keys leaves it empty
+ *   prefix_len    NULL or [num_seqs] int32; clamped to [0, seq_lens[i]]
+ * All arrays are device arrays, 4-byte aligned. A NULL descriptor, or one of zeros, gives plain
+ * causal attention.
+ *
+ * Pages (block-table entries) none of whose keys is visible to a row of the call may be freed:
+ * their table entries must only be valid ids (the null block, as pa_bm_release_behind leaves
+ * them), and their cells may hold anything. K of an invisible key never reaches a result. V of a
+ * key that no row of the sequence sees never does either; V of a key that some rows of the call
+ * see and others do not must be finite for the others.
+ * Scores, softmax statistics and outputs are accumulated in fp32; on bf16 data the probabilities
+ * are rounded to bf16 for the tensor-core product with V, and outputs are rounded once.
+ */
+typedef struct {
+    float softcap;
+    int32_t window;
+    const float* alibi_slopes;
+    const int32_t* key_start;
+    const int32_t* prefix_len;
+} pa_score;
+
+/*
+ * pa_decode_scored: pa_decode_bs with scored attention; one query row per sequence, at position
+ * seq_lens[i] - 1. Supported: bf16 or fp32, head_dim 64 or 128, any number of q heads per kv
+ * head, block sizes 16, 32, 64 and 128.
+ *   score      host pointer to the descriptor above (its arrays are device arrays), or NULL
+ *   workspace  >= pa_decode_scored_workspace_size(...) bytes, 16-byte aligned, zero-filled before
+ *              its first use; every call that completes without a device error leaves it ready
+ *              for the next one. Calls that use the same workspace must not overlap on the GPU.
+ * The workspace size does not depend on the block size or on the descriptor.
+ * No counterpart exists on the source pages; the calls stand beside pa_decode_bs and
+ * pa_prefill_chunk_bs for models whose attention has such scores.
+ */
+PA_API size_t pa_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t max_seq_len, pa_dtype dtype);
+PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                  int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale,
+                                  const pa_score* score, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * pa_prefill_scored: pa_prefill_chunk_bs with scored attention; chunk row r of sequence i sits at
+ * position seq_lens[i] - C_i + r. A chunk longer than max_chunk_len or than its sequence sets
+ * PA_DEVERR_LEN_RANGE and leaves its rows unwritten. workspace: as for pa_decode_scored, sized by
+ * pa_prefill_scored_workspace_size (may be NULL when that is 0). Supported: as pa_decode_scored.
+ */
+PA_API size_t pa_prefill_scored_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
+                                               int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                                               pa_dtype dtype);
+PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
+                                   int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t num_blocks, int32_t block_size, float scale, const pa_score* score,
+                                   pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * pa_get_device_errors: read the device error word of the current device (PA_DEVERR_*
  * bits OR-ed by the kernels since the last clear) into *errors, and clear it when
  * `clear` is non-zero. Synchronises the current device. The library owns the word.
@@ -517,6 +596,23 @@ PA_API pa_status pa_bm_slot_mapping(const pa_block_manager* bm, int64_t req_id, 
  * PA_ERR_NO_SPACE if some remain. */
 PA_API pa_status pa_bm_take_copies(pa_block_manager* bm, int32_t* src, int32_t* dst, int32_t capacity,
                                    int32_t* n_copies);
+/* Gives back the request's blocks that lie wholly in positions [keep, first_pos) (a sliding window
+ * has passed them; the first `keep` tokens stay): their entries become the null block, the blocks
+ * are released tail first as by pa_bm_free_request (a hashed one can still be hit by another
+ * request). *num_released = blocks given back by this call. first_pos at most the request's token
+ * count, keep >= 0. Positions given back have no slots: pa_bm_slot_mapping refuses them. */
+PA_API pa_status pa_bm_release_behind(pa_block_manager* bm, int64_t req_id, int32_t first_pos, int32_t keep,
+                                      int32_t* num_released);
+/* Changes the pool's size to num_blocks (>= 2). Growing adds free blocks at the back of the queue.
+ * Shrinking moves every held block with id >= num_blocks to a free block below it (taken in queue
+ * order; a cached one is evicted), in all requests' lists and with its hash, and removes the blocks
+ * from num_blocks on. The moves come out as (src[i], dst[i]), i < *n_moves, both strictly
+ * ascending and every dst below every src; the caller hands them to pa_move_blocks before the next
+ * access to the pool. PA_ERR_NO_SPACE when fewer free blocks are left below than moves are needed,
+ * or `capacity` is below *n_moves (set to the moves needed); PA_ERR_INVALID_ARG while
+ * copy-on-write pairs wait for pa_bm_take_copies. A failed call changes nothing. */
+PA_API pa_status pa_bm_resize(pa_block_manager* bm, int32_t num_blocks, int32_t* src, int32_t* dst, int32_t capacity,
+                              int32_t* n_moves);
 /* Inspection: the free queue from front to back, and one block's reference count and hash. */
 PA_API pa_status pa_bm_free_queue(const pa_block_manager* bm, int32_t* order, int32_t capacity, int32_t* n);
 PA_API pa_status pa_bm_block_info(const pa_block_manager* bm, int32_t block_id, int32_t* ref_count,
@@ -548,6 +644,34 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* blo
 PA_API pa_status pa_copy_blocks_bs(void* k_cache, void* v_cache, const int32_t* block_pairs, int32_t n_pairs,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
                                    pa_dtype dtype, void* stream);
+
+/*
+ * pa_move_blocks: copy pages between physical blocks in every layer's pools at once, and rewrite
+ * block tables to follow. For each (src, dst) pair of block_pairs (device int32 [n_pairs][2]) and
+ * every pool: block src, every kv head, is copied into block dst. Forked requests' last pages
+ * (copy-on-write), compaction after pa_bm_resize, and reordering of pages are such copies; a
+ * model has two pools per layer, and one launch serves all of them.
+ *   pools        host array of num_pools device pointers, each [num_blocks][num_kv_heads]
+ *                [block_size][head_dim], 16-byte aligned (K and V pools alike); the array is read
+ *                during the call only
+ *   tokens       NULL (whole blocks) or device int32 [n_pairs]: only the first tokens[i] tokens of
+ *                each head's page are copied (the filled part of a partly filled block); clamped
+ *                to [0, block_size]
+ *   block_table  NULL or device int32 [num_seqs][max_blocks_per_seq]: every entry equal to some
+ *                pair's src becomes that pair's dst, among the first ceil(seq_lens[i] / block_size)
+ *                entries of row i (clamped to the row); other entries keep their value. The
+ *                pairs' src must then be strictly ascending (as pa_bm_resize returns them); pairs
+ *                that are not set PA_DEVERR_PAIR_ORDER, and the table is then unspecified.
+ *   seq_lens     device int32 [num_seqs], needed with block_table
+ * Several pairs may share a src. Every dst must be distinct, and no dst may be another pair's src
+ * or a block that a kernel running at the same time reads. src == dst is skipped; ids outside
+ * [0, num_blocks) are not copied and set PA_DEVERR_BLOCK_RANGE. Asynchronous on `stream`.
+ * No counterpart on the source pages beyond the copy-on-write of pa_copy_blocks.
+ */
+PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, pa_dtype dtype, const int32_t* block_pairs,
+                                int32_t n_pairs, const int32_t* tokens, int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, void* stream);
 
 #ifdef __cplusplus
 }

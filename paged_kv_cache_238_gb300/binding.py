@@ -18,6 +18,7 @@ PA_F32, PA_BF16 = 0, 1
 PA_DEVERR_SLOT_RANGE, PA_DEVERR_BLOCK_RANGE, PA_DEVERR_LEN_RANGE, PA_DEVERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 PA_DEVERR_APPEND_SLOT = 0x10
 PA_DEVERR_PREFIX_MISMATCH = 0x20
+PA_DEVERR_PAIR_ORDER = 0x40
 PA_DECODE_TABLES_READY = 0x1
 PA_DECODE_POOL_READY = 0x2
 PA_DRILL_OFF, PA_DRILL_DECODE_STAGE, PA_DRILL_PREFILL_K_TILE = 0, 1, 2
@@ -32,7 +33,9 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode", "pa
             "pa_copy_blocks", "pa_reshape_and_cache_bs", "pa_decode_bs", "pa_prefill_chunk_bs",
             "pa_copy_blocks_bs", "pa_step", "pa_decode_append", "pa_bm_create_bs",
             "pa_bm_num_blocks_for_memory_bs", "pa_debug_set_wait_drill", "pa_decode_shared_prefix_workspace_size",
-            "pa_decode_shared_prefix", "pa_debug_decode_slices")
+            "pa_decode_shared_prefix", "pa_debug_decode_slices", "pa_decode_scored_workspace_size",
+            "pa_decode_scored", "pa_prefill_scored_workspace_size", "pa_prefill_scored", "pa_move_blocks",
+            "pa_bm_release_behind", "pa_bm_resize")
 #: block sizes the *_bs entry points accept
 BLOCK_SIZES = (16, 32, 64, 128)
 #: size of the library's fixed scratch used by pa_decode_noalloc
@@ -62,6 +65,12 @@ class StepDesc(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("decode_sms", ctypes.c_int32), ("timing_events", ctypes.c_void_p),
     ]
+
+
+class ScoreDesc(ctypes.Structure):
+    """Mirror of pa_score in include/pa.h (same fields, same order, C layout)."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", ctypes.c_void_p),
+                ("key_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
 
 
 class PaError(RuntimeError):
@@ -131,6 +140,17 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
                                                            i32, i32, i32, f32, ctypes.c_int, vp]),
                     ("pa_copy_blocks_bs", ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp]),
                     ("pa_step", ctypes.c_int, [ctypes.POINTER(StepDesc), vp]),
+                    ("pa_decode_scored_workspace_size", sz, [i32, i32, i32, i32, i32, ctypes.c_int]),
+                    ("pa_decode_scored", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                                        f32, ctypes.POINTER(ScoreDesc), ctypes.c_int, vp, sz, vp]),
+                    ("pa_prefill_scored_workspace_size", sz, [i32, i32, i32, i32, i32, i32, ctypes.c_int]),
+                    ("pa_prefill_scored", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                                         i32, i32, f32, ctypes.POINTER(ScoreDesc), ctypes.c_int, vp,
+                                                         sz, vp]),
+                    ("pa_move_blocks", ctypes.c_int, [vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, i32, vp, vp, i32,
+                                                      vp, i32, vp]),
+                    ("pa_bm_release_behind", ctypes.c_int, [vp, i64, i32, i32, pi32]),
+                    ("pa_bm_resize", ctypes.c_int, [vp, i32, pi32, pi32, i32, pi32]),
                     ("pa_bm_create_bs", ctypes.c_int, [i32, i32, i32, ctypes.c_char_p, ctypes.POINTER(vp)]),
                     ("pa_bm_num_blocks_for_memory_bs", i64, [sz, ctypes.c_double, i32, i32, i32, i32, ctypes.c_int]),
                     ("pa_decode_append", ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
@@ -425,6 +445,164 @@ def pa_step(k_cache, v_cache, scale: float, k_new=None, v_new=None, slot_mapping
     _check("pa_step", load().pa_step(ctypes.byref(d), _stream(stream)))
 
 
+# ------------------------------------------------------------------------------------------
+# scored attention and page moves
+# ------------------------------------------------------------------------------------------
+
+def _need(what: str, t, dtype, shape, device: int) -> None:
+    """A contiguous tensor of this dtype and shape on the given CUDA device (-1 in `shape`: any size)."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: libpa takes contiguous CUDA tensors")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype} where {dtype} is needed")
+    if t.get_device() != device:
+        raise ValueError(f"{what}: on device {t.get_device()}, the others on device {device}")
+    if t.dim() != len(shape) or any(n >= 0 and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} where {tuple(shape)} is needed (-1: any size)")
+
+
+def _need_current(device: int) -> None:
+    import torch
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is {torch.cuda.current_device()}")
+
+
+class Score:
+    """How scored attention scores a key (C ABI pa_score): scores capped at +-softcap by a tanh
+    (0: not), a linear distance bias of alibi_slopes [H_q] fp32 per query head, a sliding window
+    of `window` keys (0: none), key_start int32 per query row (the first key the row sees) and
+    prefix_len [S] int32 (keys that every row of the sequence sees). Keeps its tensors alive."""
+
+    __slots__ = ("softcap", "window", "alibi_slopes", "key_start", "prefix_len", "_desc")
+
+    def __init__(self, softcap: float = 0.0, alibi_slopes=None, window: int = 0, key_start=None, prefix_len=None):
+        self.softcap, self.window = float(softcap), int(window)
+        self.alibi_slopes, self.key_start, self.prefix_len = alibi_slopes, key_start, prefix_len
+        self._desc = ScoreDesc(self.softcap, self.window, _ptr(alibi_slopes), _ptr(key_start), _ptr(prefix_len))
+
+    def _check(self, H_q: int, rows: int, S: int, device: int) -> None:
+        import torch
+        if self.alibi_slopes is not None:
+            _need("alibi_slopes", self.alibi_slopes, torch.float32, (H_q,), device)
+        if self.key_start is not None:
+            _need("key_start", self.key_start, torch.int32, (rows,), device)
+        if self.prefix_len is not None:
+            _need("prefix_len", self.prefix_len, torch.int32, (S,), device)
+
+
+def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace):
+    """Shape and type checks shared by the scored calls; returns (rows, H_q, D, NB, H_kv, BS, S, dtype code)."""
+    import torch
+    code = _dtype_code(q)
+    dev = q.get_device()
+    _need("q", q, q.dtype, (-1, -1, -1), dev)
+    T, H_q, D = q.shape
+    _need("out", out, q.dtype, (T, H_q, D), dev)
+    _need("k_cache", k_cache, q.dtype, (-1, -1, -1, D), dev)
+    NB, H_kv, BS, _ = k_cache.shape
+    _need("v_cache", v_cache, q.dtype, (NB, H_kv, BS, D), dev)
+    _need("seq_lens", seq_lens, torch.int32, (-1,), dev)
+    S = seq_lens.shape[0]
+    _need("block_table", block_table, torch.int32, (S, -1), dev)
+    if score is not None:
+        score._check(H_q, T, S, dev)
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != dev):
+        raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
+    _need_current(dev)
+    return T, H_q, D, NB, H_kv, BS, S, code
+
+
+def pa_decode_scored_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                    max_seq_len: int, dtype) -> int:
+    import torch
+    code = dtype if isinstance(dtype, int) else (PA_F32 if dtype == torch.float32 else PA_BF16)
+    return int(load().pa_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, code))
+
+
+def pa_decode_scored(out, q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, scale: float, score=None,
+                     workspace=None, stream=None) -> None:
+    """pa_decode with scored attention (C ABI pa_decode_scored). out, q: [S, H_q, D]; score: a
+    Score or None; workspace: zeroed uint8 CUDA tensor of pa_decode_scored_workspace_size(...)
+    bytes (None when that is 0); the rest as for pa_decode, any block size."""
+    T, H_q, D, NB, H_kv, BS, S, code = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace)
+    if T != S:
+        raise ValueError(f"decode takes one query row per sequence: {T} rows, {S} sequences")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("pa_decode_scored", load().pa_decode_scored(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S,
+        int(max_seq_len), H_q, H_kv, D, NB, BS, float(scale), None if score is None else score._desc, code,
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def pa_prefill_scored_workspace_size(num_seqs: int, max_chunk_len: int, num_q_heads: int, num_kv_heads: int,
+                                     head_dim: int, max_seq_len: int, dtype) -> int:
+    import torch
+    code = dtype if isinstance(dtype, int) else (PA_F32 if dtype == torch.float32 else PA_BF16)
+    return int(load().pa_prefill_scored_workspace_size(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                       max_seq_len, code))
+
+
+def pa_prefill_scored(out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_chunk_len: int,
+                      max_seq_len: int, scale: float, score=None, workspace=None, stream=None) -> None:
+    """pa_prefill_chunk with scored attention (C ABI pa_prefill_scored). out, q: [T_q, H_q, D];
+    query_start_loc: [S + 1] int32; score: a Score (key_start per row of q) or None; workspace: as
+    for pa_decode_scored, of pa_prefill_scored_workspace_size(...) bytes."""
+    import torch
+    T, H_q, D, NB, H_kv, BS, S, code = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace)
+    _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), q.get_device())
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("pa_prefill_scored", load().pa_prefill_scored(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        _ptr(query_start_loc), S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS, float(scale),
+        None if score is None else score._desc, code, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+class PoolList:
+    """The pools that pa_move_blocks copies in: tensors [NB, H_kv, BS, D] of one shape, dtype and
+    device (the K and V pool of every layer), checked once. Keeps them alive."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("PoolList needs at least one pool")
+        first = self.pools[0]
+        self.dtype_code = _dtype_code(first)
+        self.device = first.get_device()
+        for i, p in enumerate(self.pools):
+            _need(f"pools[{i}]", p, first.dtype, (-1, -1, -1, -1), self.device)
+            if p.shape != first.shape:
+                raise ValueError(f"pools[{i}]: shape {tuple(p.shape)} where {tuple(first.shape)} is needed")
+        self.shape = tuple(int(n) for n in first.shape)
+        self._ptrs = (ctypes.c_void_p * len(self.pools))(*[p.data_ptr() for p in self.pools])
+
+
+def pa_move_blocks(pools, block_pairs, tokens=None, block_table=None, seq_lens=None, stream=None) -> None:
+    """Copy block src to block dst of every pool, for each (src, dst) row of block_pairs (int32
+    CUDA [n, 2]); C ABI pa_move_blocks. pools: a PoolList or a list of pools; tokens: None or int32
+    [n], tokens copied per block; block_table [S, max_blocks] int32 with seq_lens [S] int32: its
+    used entries that name a src are rewritten to its dst (the src must then be ascending)."""
+    import torch
+    if not isinstance(pools, PoolList):
+        pools = PoolList(pools)
+    dev = pools.device
+    _need("block_pairs", block_pairs, torch.int32, (-1, 2), dev)
+    n = block_pairs.shape[0]
+    if tokens is not None:
+        _need("tokens", tokens, torch.int32, (n,), dev)
+    S = mb = 0
+    if block_table is not None:
+        if seq_lens is None:
+            raise ValueError("a block table is rewritten up to each row's seq_lens entry: seq_lens is needed")
+        _need("block_table", block_table, torch.int32, (-1, -1), dev)
+        S, mb = block_table.shape
+        _need("seq_lens", seq_lens, torch.int32, (S,), dev)
+    _need_current(dev)
+    NB, H_kv, BS, D = pools.shape
+    _check("pa_move_blocks", load().pa_move_blocks(
+        pools._ptrs, len(pools.pools), H_kv, D, NB, BS, pools.dtype_code, _ptr(block_pairs), n, _ptr(tokens),
+        _ptr(block_table), mb, _ptr(seq_lens) if block_table is not None else None, S, _stream(stream)))
+
+
 def pa_sha256(data: bytes) -> bytes:
     out = (ctypes.c_uint8 * 32)()
     buf = (ctypes.c_uint8 * max(1, len(data))).from_buffer_copy(data or b"\0")
@@ -515,6 +693,23 @@ class BlockManager:
     def take_copies(self, capacity: int = 4096):
         src, dst, n = (ctypes.c_int32 * capacity)(), (ctypes.c_int32 * capacity)(), ctypes.c_int32(0)
         _check("pa_bm_take_copies", self._lib.pa_bm_take_copies(self._h, src, dst, capacity, ctypes.byref(n)))
+        return [(src[i], dst[i]) for i in range(n.value)]
+
+    def release_behind(self, req_id: int, first_pos: int, keep: int = 0) -> int:
+        """Gives back the request's blocks wholly in positions [keep, first_pos); their entries
+        become the null block. Returns how many were given back."""
+        n = ctypes.c_int32(0)
+        _check("pa_bm_release_behind", self._lib.pa_bm_release_behind(self._h, req_id, int(first_pos), int(keep),
+                                                                      ctypes.byref(n)))
+        return int(n.value)
+
+    def resize(self, num_blocks: int):
+        """Changes the pool's size; returns the (src, dst) moves that a shrink needs, ascending
+        (hand them to pa_move_blocks before the next access to the pool)."""
+        n = ctypes.c_int32(0)
+        cap = max(1, int(num_blocks))  # a move needs a block below the new end
+        src, dst = (ctypes.c_int32 * cap)(), (ctypes.c_int32 * cap)()
+        _check("pa_bm_resize", self._lib.pa_bm_resize(self._h, int(num_blocks), src, dst, cap, ctypes.byref(n)))
         return [(src[i], dst[i]) for i in range(n.value)]
 
     def free_queue(self):

@@ -23,6 +23,7 @@
 //    (copy-on-write); the (source, destination) pairs wait for pa_copy_blocks.
 //  * A full block enters the cache when the caller commits that its K/V has been computed; a
 //    key already cached keeps its block and the new block stays unhashed.
+#include <algorithm>
 #include <array>
 #include <cstdint>
 #include <cstring>
@@ -261,6 +262,7 @@ class Manager {
         extend_hashes(r, n_full);
         if (!caching_) return PA_OK;
         for (int32_t k = 0; k < n_full; ++k) {
+            if (r.blocks[k] == null_) continue;  // given back by release_behind
             BlockRec& b = recs_[r.blocks[k]];
             if (b.hashed) continue;
             const Key key = make_key(r.hashes[k], 0);
@@ -288,6 +290,85 @@ class Manager {
         const std::vector<int32_t>& blocks = it->second.blocks;
         for (auto b = blocks.rbegin(); b != blocks.rend(); ++b) release(*b);  // tail first
         reqs_.erase(it);
+        return PA_OK;
+    }
+
+    // Gives back the blocks wholly in positions [keep, first_pos); their entries become null.
+    pa_status release_behind(int64_t id, int32_t first_pos, int32_t keep, int32_t* released) {
+        auto it = reqs_.find(id);
+        if (it == reqs_.end() || keep < 0 || first_pos < 0) return PA_ERR_INVALID_ARG;
+        Request& r = it->second;
+        if (first_pos > static_cast<int32_t>(r.tokens.size())) return PA_ERR_INVALID_ARG;
+        const int32_t from = keep / bs_ + (keep % bs_ != 0 ? 1 : 0), to = first_pos / bs_;
+        int32_t n = 0;
+        for (int32_t k = to - 1; k >= from; --k) {  // tail first
+            if (r.blocks[k] == null_) continue;
+            release(r.blocks[k]);
+            r.blocks[k] = null_;
+            ++n;
+        }
+        *released = n;
+        return PA_OK;
+    }
+
+    // Changes the number of blocks; held blocks past the new end move to free ones below it.
+    pa_status resize(int32_t nb, int32_t* src, int32_t* dst, int32_t cap, int32_t* n_moves) {
+        *n_moves = 0;
+        if (nb < 2 || nb > INT32_MAX - 2 || !copies_.empty()) return PA_ERR_INVALID_ARG;
+        std::vector<int32_t> from, to;
+        for (int32_t i = nb; i < nb_; ++i)
+            if (recs_[i].ref > 0) from.push_back(i);
+        for (int32_t i = recs_[head_].next; i != tail_ && to.size() < from.size(); i = recs_[i].next)
+            if (i < nb) to.push_back(i);
+        *n_moves = static_cast<int32_t>(from.size());
+        if (to.size() < from.size() || cap < *n_moves) return PA_ERR_NO_SPACE;
+        std::sort(to.begin(), to.end());
+        // everything that allocates comes before the first change
+        std::vector<BlockRec> next(static_cast<size_t>(nb) + 2);
+        std::vector<int32_t> moved(static_cast<size_t>(nb_ > nb ? nb_ - nb : 0), -1);  // new id of block nb + i
+        for (size_t k = 0; k < from.size(); ++k) {
+            src[k] = from[k];
+            dst[k] = to[k];
+            moved[from[k] - nb] = to[k];
+            unlink(to[k]);
+            evict(to[k]);
+            BlockRec &a = recs_[from[k]], &b = recs_[to[k]];
+            b.ref = a.ref;
+            b.hashed = a.hashed;
+            b.key = a.key;
+            if (a.hashed) {
+                auto it = cache_.find(a.key);
+                if (it != cache_.end())
+                    for (int32_t& x : it->second)
+                        if (x == from[k]) x = to[k];
+            }
+            a.ref = 0;
+            a.hashed = false;
+        }
+        if (!from.empty())
+            for (auto& kv : reqs_)
+                for (int32_t& x : kv.second.blocks)
+                    if (x >= nb) x = moved[x - nb];
+        for (int32_t i = nb; i < nb_; ++i) {
+            if (recs_[i].queued) unlink(i);
+            evict(i);
+        }
+        // the records of the new size, the queue's two ends behind them
+        const int32_t kept = nb < nb_ ? nb : nb_, old_head = head_, old_tail = tail_;
+        const auto renamed = [&](int32_t x) { return x == old_head ? nb : x == old_tail ? nb + 1 : x; };
+        for (int32_t i = 0; i < kept; ++i) next[i] = recs_[i];
+        next[nb] = recs_[old_head];
+        next[nb + 1] = recs_[old_tail];
+        for (BlockRec& b : next) {
+            b.prev = renamed(b.prev);
+            b.next = renamed(b.next);
+        }
+        const int32_t old = nb_;
+        recs_ = std::move(next);
+        nb_ = nb;
+        head_ = nb;
+        tail_ = nb + 1;
+        for (int32_t i = old; i < nb; ++i) push_back(i);
         return PA_OK;
     }
 
@@ -356,24 +437,27 @@ class Manager {
         unlink(i);
         return i;
     }
+    // takes a block out of the cache map
+    void evict(int32_t i) {
+        BlockRec& b = recs_[i];
+        if (!b.hashed) return;
+        auto it = cache_.find(b.key);
+        if (it != cache_.end()) {
+            auto& lst = it->second;
+            for (size_t k = 0; k < lst.size(); ++k)
+                if (lst[k] == i) {
+                    lst.erase(lst.begin() + static_cast<std::ptrdiff_t>(k));
+                    break;
+                }
+            if (lst.empty()) cache_.erase(it);
+        }
+        b.hashed = false;
+    }
     // a block for new content: from the front; a cached one is evicted now (lazily)
     int32_t take() {
         const int32_t i = pop_front();
-        BlockRec& b = recs_[i];
-        if (b.hashed) {
-            auto it = cache_.find(b.key);
-            if (it != cache_.end()) {
-                auto& lst = it->second;
-                for (size_t k = 0; k < lst.size(); ++k)
-                    if (lst[k] == i) {
-                        lst.erase(lst.begin() + static_cast<std::ptrdiff_t>(k));
-                        break;
-                    }
-                if (lst.empty()) cache_.erase(it);
-            }
-            b.hashed = false;
-        }
-        b.ref = 1;
+        evict(i);
+        recs_[i].ref = 1;
         return i;
     }
     void touch(int32_t i) {
@@ -480,9 +564,26 @@ PA_API pa_status pa_bm_slot_mapping(const pa_block_manager* bm, int64_t req_id, 
     if (static_cast<int64_t>(first_pos) + n > cap) return PA_ERR_INVALID_ARG;
     for (int32_t i = 0; i < n; ++i) {
         const int32_t p = first_pos + i;
+        if (r->blocks[p / bs] == 0) return PA_ERR_INVALID_ARG;  // given back (pa_bm_release_behind)
         slots[i] = static_cast<int64_t>(r->blocks[p / bs]) * bs + p % bs;
     }
     return PA_OK;
+}
+
+PA_API pa_status pa_bm_release_behind(pa_block_manager* bm, int64_t req_id, int32_t first_pos, int32_t keep,
+                                      int32_t* num_released) {
+    if (!bm || !num_released) return PA_ERR_INVALID_ARG;
+    return bm->m.release_behind(req_id, first_pos, keep, num_released);
+}
+
+PA_API pa_status pa_bm_resize(pa_block_manager* bm, int32_t num_blocks, int32_t* src, int32_t* dst, int32_t capacity,
+                              int32_t* n_moves) {
+    if (!bm || !n_moves || capacity < 0 || (capacity > 0 && (!src || !dst))) return PA_ERR_INVALID_ARG;
+    try {
+        return bm->m.resize(num_blocks, src, dst, capacity, n_moves);
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_NO_SPACE;
+    }
 }
 
 PA_API pa_status pa_bm_take_copies(pa_block_manager* bm, int32_t* src, int32_t* dst, int32_t capacity,

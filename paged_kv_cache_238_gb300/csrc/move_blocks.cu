@@ -1,0 +1,84 @@
+// move_blocks: copies of pages between physical blocks in every layer's pools, and the rewrite of
+// block tables to follow them. Pure data movement, bound by HBM: each moved byte is read and
+// written once.
+//
+// Grid: x = pair (the last rows of CTAs after the pairs rewrite the table), y = pool. A block of
+// all kv heads is contiguous, so a whole-block copy is one run of 16-byte chunks; with `tokens` the
+// copy is a run per head. A table entry finds its pair by binary search over the ascending src ids.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Pools {
+    int4* p[kMoveMaxPools];
+};
+
+__global__ void __launch_bounds__(kThreads) move_blocks_kernel(const __grid_constant__ Pools pools,
+                                                               const __grid_constant__ MoveArgs a) {
+    const int2* pairs = reinterpret_cast<const int2*>(a.pairs);
+    if (static_cast<int32_t>(blockIdx.x) >= a.num_pairs) {  // block-table rewrite
+        if (blockIdx.y != 0) return;
+        const int32_t ctas = static_cast<int32_t>(gridDim.x) - a.num_pairs;
+        const int64_t entries = static_cast<int64_t>(a.num_seqs) * a.max_blocks;
+        for (int64_t i = (static_cast<int64_t>(blockIdx.x) - a.num_pairs) * kThreads + threadIdx.x; i < entries;
+             i += static_cast<int64_t>(ctas) * kThreads) {
+            const int32_t s = static_cast<int32_t>(i / a.max_blocks), col = static_cast<int32_t>(i - static_cast<int64_t>(s) * a.max_blocks);
+            if (static_cast<int64_t>(col) * a.block_size >= __ldg(a.seq_lens + s)) continue;
+            const int32_t id = a.block_table[i];
+            int32_t lo = 0, hi = a.num_pairs;
+            while (lo < hi) {
+                const int32_t mid = (lo + hi) >> 1;
+                if (__ldg(&pairs[mid].x) < id) lo = mid + 1; else hi = mid;
+            }
+            if (lo < a.num_pairs && __ldg(&pairs[lo].x) == id) {
+                const int32_t to = __ldg(&pairs[lo].y);
+                if (to >= 0 && to < a.num_blocks) a.block_table[i] = to;
+            }
+        }
+        return;
+    }
+    const int2 pr = __ldg(pairs + blockIdx.x);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (pr.x < 0 || pr.x >= a.num_blocks || pr.y < 0 || pr.y >= a.num_blocks) raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
+        if (a.block_table != nullptr && blockIdx.x > 0 && __ldg(&pairs[blockIdx.x - 1].x) >= pr.x)
+            raise_error(a.err, PA_DEVERR_PAIR_ORDER);
+    }
+    if (pr.x < 0 || pr.x >= a.num_blocks || pr.y < 0 || pr.y >= a.num_blocks || pr.x == pr.y) return;
+    int4* pool = pools.p[blockIdx.y];
+    const int4* src = pool + static_cast<int64_t>(pr.x) * a.block_chunks;
+    int4* dst = pool + static_cast<int64_t>(pr.y) * a.block_chunks;
+    if (a.tokens == nullptr) {
+        for (int32_t c = threadIdx.x; c < a.block_chunks; c += kThreads) dst[c] = src[c];
+        return;
+    }
+    const int32_t n = min(max(__ldg(a.tokens + blockIdx.x), 0), a.block_size) * a.row_chunks;  // chunks per head
+    const int32_t head = a.block_size * a.row_chunks;
+    for (int32_t h = 0; h * head < a.block_chunks; ++h)
+        for (int32_t c = threadIdx.x; c < n; c += kThreads) dst[h * head + c] = src[h * head + c];
+}
+
+}  // namespace
+
+cudaError_t launch_move_blocks(const MoveArgs& a, void* const* pools, int32_t num_pools, cudaStream_t stream) {
+    for (int32_t p0 = 0; p0 < num_pools || p0 == 0; p0 += kMoveMaxPools) {
+        Pools ps{};
+        const int32_t n = num_pools - p0 < kMoveMaxPools ? num_pools - p0 : kMoveMaxPools;
+        for (int32_t i = 0; i < n; ++i) ps.p[i] = static_cast<int4*>(pools[p0 + i]);
+        MoveArgs m = a;
+        if (p0 > 0) m.block_table = nullptr;  // once
+        const int64_t entries = m.block_table ? static_cast<int64_t>(m.num_seqs) * m.max_blocks : 0;
+        const int64_t table_ctas = (entries + kThreads - 1) / kThreads < 512 ? (entries + kThreads - 1) / kThreads : 512;
+        if (m.num_pairs + table_ctas == 0) return cudaSuccess;
+        const dim3 grid(static_cast<unsigned>(m.num_pairs + table_ctas), n > 0 ? n : 1);
+        move_blocks_kernel<<<grid, kThreads, 0, stream>>>(ps, m);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace pa

@@ -523,6 +523,122 @@ PA_API pa_status pa_prefill_chunk(void* out, const void* q, const void* k_cache,
                                PA_BLOCK_SIZE, scale, dtype, stream);
 }
 
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Host checks of a score descriptor (null: plain causal attention).
+pa_status prepare_score(const pa_score* score, ScoreArgs* a) {
+    *a = ScoreArgs{};
+    if (!score) return PA_OK;
+    if (!(score->softcap >= 0.f) || score->softcap > 3.0e38f || score->window < 0) return PA_ERR_INVALID_ARG;
+    if (!aligned4(score->alibi_slopes) || !aligned4(score->key_start) || !aligned4(score->prefix_len))
+        return PA_ERR_INVALID_ARG;
+    *a = ScoreArgs{score->softcap, score->window, score->alibi_slopes, score->key_start, score->prefix_len};
+    return PA_OK;
+}
+
+// Grid limits of the scored kernels: kv heads times head chunks in the grid's y dimension.
+pa_status check_scored_grid(int32_t num_q_heads, int32_t num_kv_heads) {
+    const int64_t y = static_cast<int64_t>(num_kv_heads) * scored_simt_head_chunks(num_q_heads / num_kv_heads);
+    return y > 65535 || num_q_heads > 65535 ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+}  // namespace
+
+PA_API size_t pa_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t max_seq_len, pa_dtype dtype) {
+    if (check_attention_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, 1, max_seq_len / 16 + 1, max_seq_len,
+                              dtype, PA_BLOCK_SIZE) != PA_OK)
+        return 0;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return 0;
+    return plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
+        .workspace_bytes;
+}
+
+PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                  int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale,
+                                  const pa_score* score, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    DecodeArgs a;
+    pa_status st = prepare_decode(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
+                                  max_seq_len, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale,
+                                  dtype, workspace, workspace_bytes, &a);
+    if (st != PA_OK) return st;
+    ScoreArgs sa;
+    st = prepare_score(score, &sa);
+    if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
+    if (st != PA_OK || num_seqs == 0) return st;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    const ScoredSimtPlan plan =
+        plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+        return PA_ERR_INVALID_ARG;
+    a.err = dev->err;
+    return launch_scored_decode_simt(a, sa, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                     : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_prefill_scored_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
+                                               int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                                               pa_dtype dtype) {
+    (void)num_seqs; (void)max_chunk_len; (void)num_q_heads; (void)num_kv_heads; (void)head_dim; (void)max_seq_len;
+    (void)dtype;
+    return 0;
+}
+
+PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
+                                   int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t num_blocks, int32_t block_size, float scale, const pa_score* score,
+                                   pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    (void)workspace; (void)workspace_bytes;
+    PrefillArgs a;
+    pa_status st = prepare_prefill(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens,
+                                   query_start_loc, num_seqs, max_chunk_len, max_seq_len, num_q_heads, num_kv_heads,
+                                   head_dim, num_blocks, block_size, scale, dtype, &a);
+    if (st != PA_OK) return st;
+    ScoreArgs sa;
+    st = prepare_score(score, &sa);
+    if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
+    if (st != PA_OK || !prefill_has_work(a)) return st;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    a.err = dev->err;
+    return launch_scored_prefill_simt(a, sa, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, pa_dtype dtype, const int32_t* block_pairs,
+                                int32_t n_pairs, const int32_t* tokens, int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, void* stream) {
+    if (num_pools < 0 || n_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(block_size)) return block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return PA_ERR_INVALID_ARG;
+    const int64_t row_bytes = static_cast<int64_t>(head_dim) * elem_bytes(dtype);
+    if (row_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
+    const int64_t chunks = row_bytes / 16 * num_kv_heads * block_size;
+    if (chunks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (block_table && (num_seqs < 0 || max_blocks_per_seq <= 0 || !seq_lens || !aligned4(block_table) || !aligned4(seq_lens)))
+        return PA_ERR_INVALID_ARG;
+    if (n_pairs == 0) return PA_OK;
+    if (n_pairs > 0x7fffffff / 2) return PA_ERR_UNSUPPORTED;
+    if (!block_pairs || (reinterpret_cast<uintptr_t>(block_pairs) & 7u) || !aligned4(tokens) || (num_pools > 0 && !pools))
+        return PA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < num_pools; ++i)
+        if (!pools[i] || !aligned16(pools[i])) return PA_ERR_INVALID_ARG;
+    if (num_pools == 0 && !block_table) return PA_OK;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    MoveArgs a{block_pairs, tokens, block_table, seq_lens, n_pairs, num_blocks, block_size, block_table ? num_seqs : 0,
+               max_blocks_per_seq, static_cast<int32_t>(row_bytes / 16), static_cast<int32_t>(chunks), dev->err};
+    return launch_move_blocks(a, pools, num_pools, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                      : PA_ERR_CUDA;
+}
+
 PA_API pa_status pa_step(const pa_step_desc* d, void* stream_ptr) {
     if (!d) return PA_ERR_INVALID_ARG;
     if (d->decode_sms < 0 || d->num_new_tokens < 0 || d->num_prefill_seqs < 0 || d->num_decode_seqs < 0)

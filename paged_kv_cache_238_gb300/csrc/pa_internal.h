@@ -200,6 +200,46 @@ cudaError_t launch_prefill(const PrefillArgs& a, const DeviceInfo& dev, cudaStre
 cudaError_t launch_prefill_simt(const PrefillArgs& a, int32_t total_rows, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
+// scored attention (scores capped, biased by distance or masked beyond the causal bound)
+// ------------------------------------------------------------------------------------------
+// pa_score as the kernels take it.
+struct ScoreArgs {
+    float cap;  // 0: none
+    int32_t window;
+    const float* slopes;
+    const int32_t* key_start;
+    const int32_t* prefix_len;
+};
+
+// CUDA-core path (scored_simt.cu): a decode row's visible pages in num_parts partitions of up to
+// part_pages.
+struct ScoredSimtPlan {
+    int32_t part_pages, num_parts;
+    size_t workspace_bytes;
+};
+int32_t scored_simt_head_chunks(int32_t group);
+ScoredSimtPlan plan_scored_simt(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t max_seq_len, int num_sms);
+cudaError_t launch_scored_decode_simt(const DecodeArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
+                                      cudaStream_t stream);
+cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& score, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
+// move_blocks (page copies in every layer's pools, block tables rewritten)
+// ------------------------------------------------------------------------------------------
+constexpr int kMoveMaxPools = 256;  // pools of one launch (their pointers are kernel parameters)
+struct MoveArgs {
+    const int32_t* pairs;   // device [num_pairs][2] (src, dst)
+    const int32_t* tokens;  // device [num_pairs] or null
+    int32_t* block_table;   // device [num_seqs][max_blocks] or null
+    const int32_t* seq_lens;
+    int32_t num_pairs, num_blocks, block_size, num_seqs, max_blocks;
+    int32_t row_chunks, block_chunks;  // 16-byte chunks of a token's row, of a block
+    uint32_t* err;
+};
+cudaError_t launch_move_blocks(const MoveArgs& a, void* const* pools, int32_t num_pools, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
 // tensor maps (driver entry point resolved at run time; no libcuda link needed)
 // ------------------------------------------------------------------------------------------
 // Encodes a 2-D bf16 tensor map over `rows` rows of `cols` elements (row pitch cols*2 bytes)

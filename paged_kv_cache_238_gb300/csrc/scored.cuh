@@ -1,0 +1,51 @@
+// Scores of the scored attention kernels: the descriptor as the kernels take it, and which keys a
+// query row sees.
+//
+//   z = scale q.k;  z = cap tanh(z / cap);  z -= slope |p - j|
+//   visible(j) = j < L and j >= key_start and (j < prefix or (j <= p and j > p - window))
+//
+// The visible keys are two spans without a common key, [a0, a1) (the prefix part) and [b0, b1)
+// (the window part), so a kernel walks only their pages.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+struct KeySpans {
+    int32_t a0, a1, b0, b1;
+    __device__ __forceinline__ bool sees(int32_t j) const { return (j >= a0 && j < a1) || (j >= b0 && j < b1); }
+};
+
+// Spans of a row at position p of a sequence with len keys (p < len).
+__device__ __forceinline__ KeySpans key_spans(int32_t len, int32_t p, int32_t key_start, int32_t prefix,
+                                              int32_t window) {
+    KeySpans s;
+    const int32_t start = max(key_start, 0);
+    s.a0 = start;
+    s.a1 = max(start, min(prefix, len));
+    s.b0 = max(start, window > 0 ? p + 1 - window : 0);
+    if (s.a1 > s.a0) s.b0 = max(s.b0, s.a1);
+    s.b1 = max(s.b0, p + 1);
+    return s;
+}
+
+// The 16-token pages that hold the spans' keys, in ascending order: n_a pages from first_a, then
+// the rest from first_b (a page that both spans touch is counted once).
+struct PageList {
+    int32_t first_a, n_a, first_b, n;
+    __device__ __forceinline__ int32_t page(int32_t i) const { return i < n_a ? first_a + i : first_b + (i - n_a); }
+};
+
+__device__ __forceinline__ PageList page_list(const KeySpans& s) {
+    PageList l;
+    l.first_a = s.a0 / kPageTokens;
+    l.n_a = s.a1 > s.a0 ? (s.a1 + kPageTokens - 1) / kPageTokens - l.first_a : 0;
+    l.first_b = s.b0 / kPageTokens;
+    if (l.n_a > 0) l.first_b = max(l.first_b, l.first_a + l.n_a);
+    const int32_t end_b = s.b1 > s.b0 ? (s.b1 + kPageTokens - 1) / kPageTokens : 0;
+    l.n = l.n_a + max(0, end_b - l.first_b);
+    return l;
+}
+
+}  // namespace pa
