@@ -608,7 +608,10 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
-    return launch_scored_prefill_simt(a, sa, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = prefill_scored_tc_ok(a, dev->info) ? launch_prefill_scored_tc(a, sa, s)
+                                                             : launch_scored_prefill_simt(a, sa, s);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t num_kv_heads, int32_t head_dim,

@@ -1,0 +1,768 @@
+// Scored chunked prefill on the 5th-generation tensor cores (bf16, head_dim 64 or 128, up to 128 q
+// heads per kv head): attention of a chunk of new rows over the paged pool with scores that are
+// capped by a tanh, biased by distance or masked (window, visible prefix, document start).
+//
+// One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head): row r of a tile is
+// token r / G, q head r % G of the G heads that share the kv head, so every K/V tile is read once
+// for both. Keys come in tiles of 128, and only the tiles that hold a key some row of the CTA sees
+// (TileList: the prefix's tiles, then the window's):
+//   warp 0     - K producer, warp 10 - V producer: block ids 32 pages ahead, TMA copies of 16-token
+//                pages (128-byte swizzle) into rings of key tiles;
+//   warp 1     - tensor-memory owner and MMA issuer: S = Q K^T, O += P V with P from tensor memory,
+//                in the order PV_a(j), QK_a(j+1), PV_b(j), QK_b(j+1), so that the tensor cores
+//                serve one query tile while the other one's softmax runs;
+//   warps 2-9  - scores and softmax, one thread per query row: tile a (2-5) and tile b (6-9).
+//
+// Scores. Four variants of the score arithmetic (Mode), all in the log2 domain:
+//   plain      arg = s c1;                       online maximum, two passes over S
+//   cap        arg = s Q(s^2) - ref;             no maximum: see below, one pass over S
+//   distance   arg = s c1 - slope |p - j|;       online maximum, two passes
+//   general    both, or a cap beyond the fixed reference's range
+// A capped score lies in [-cap, cap], so the weights 2^(arg - ref) against the fixed reference
+// ref = cap log2(e) / 2 lie in [2^-112, 2^37] for caps up to kMaxFixedCap: no running maximum, no
+// second pass over S and no rescaling of O are needed. tanh is the odd polynomial x Q(x^2) of degree
+// 9, fitted to tanh on |x| <= 0.8 by Remez's minimax method (absolute error 2^-21.5, that times cap
+// in the score, below the 2^-9 of the bf16 weights), evaluated on the FMA pipes two elements an
+// instruction; a warp whose 32 scores of a row block hold a larger one takes
+// tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block, exact at every x.
+//
+// V rows of keys that no row of the CTA sees are zeroed in shared memory before P V (their pool
+// cells may hold anything); their scores are masked. Every wait is bounded; a timeout sets
+// PA_DEVERR_WAIT_TIMEOUT and the CTA winds down.
+#include <cuda.h>
+#include <math.h>
+
+#include "pa_internal.h"
+#include "pa_tcgen05.cuh"
+#include "scored.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRows = 128;  // query rows per tile (M)
+constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
+constexpr int kKWarp = 0, kMmaWarp = 1, kSoftWarp0 = 2, kVWarp = 10;
+constexpr int kThreads = 32 * (kVWarp + 1);
+constexpr int kSoftThreads = 256;
+constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 bf16 columns)
+constexpr float kRescaleThreshold = 8.f;  // log2 units: O is rescaled only when the maximum grows by more
+constexpr int kLptMaxSeqs = 64;           // sequences ordered longest first inside the kernel
+constexpr float kMaxFixedCap = 51.f;      // 1.5 cap log2(e) <= 112
+
+enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kGeneral = 3 };
+
+template <int D>
+struct Smem {
+    static constexpr int k_stages = D == 128 ? 3 : 4;
+    static constexpr int v_stages = D == 128 ? 2 : 4;
+    static constexpr uint32_t tile = (D / 64) * kHalf;  // 128 x D bf16
+    static constexpr uint32_t q = 0;                    // query tiles a, b
+    static constexpr uint32_t k = q + 2 * tile;
+    static constexpr uint32_t v = k + k_stages * tile;
+    static constexpr uint32_t bars = v + v_stages * tile;
+    static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 8;
+    static constexpr uint32_t misc = bars + num_bars * 8;  // tmem base, abort flag
+    static constexpr uint32_t total = misc + 16 + 1024;
+};
+
+// Keys that some valid row of one query tile sees: the two spans' unions.
+struct SpanUnion {
+    int32_t a0, a1, b0, b1;
+    __device__ __forceinline__ bool touches(int32_t lo, int32_t hi) const {
+        return (a0 < a1 && a0 < hi && a1 > lo) || (b0 < b1 && b0 < hi && b1 > lo);
+    }
+    __device__ __forceinline__ bool covers(int32_t lo, int32_t hi) const {
+        return (lo >= a0 && hi <= a1) || (lo >= b0 && hi <= b1);
+    }
+};
+
+// Key tiles walked by the CTA: n_a from first_a, the rest from first_b.
+struct TileList {
+    int32_t first_a, n_a, first_b, n;
+    __device__ __forceinline__ int32_t tile(int32_t i) const { return i < n_a ? first_a + i : first_b + (i - n_a); }
+};
+
+__device__ __forceinline__ TileList tile_list(const SpanUnion& u) {
+    TileList l;
+    l.first_a = u.a0 / kKeys;
+    l.n_a = u.a0 < u.a1 ? (u.a1 + kKeys - 1) / kKeys - l.first_a : 0;
+    l.first_b = u.b0 / kKeys;
+    if (l.n_a > 0) l.first_b = max(l.first_b, l.first_a + l.n_a);
+    const int32_t end = u.b0 < u.b1 ? (u.b1 + kKeys - 1) / kKeys : 0;
+    l.n = l.n_a + max(0, end - l.first_b);
+    return l;
+}
+
+__device__ __forceinline__ SpanUnion join(const SpanUnion& x, const SpanUnion& y) {
+    SpanUnion u = x;
+    if (y.a0 < y.a1) {
+        u.a0 = x.a0 < x.a1 ? min(x.a0, y.a0) : y.a0;
+        u.a1 = x.a0 < x.a1 ? max(x.a1, y.a1) : y.a1;
+    }
+    if (y.b0 < y.b1) {
+        u.b0 = x.b0 < x.b1 ? min(x.b0, y.b0) : y.b0;
+        u.b1 = x.b0 < x.b1 ? max(x.b1, y.b1) : y.b1;
+    }
+    return u;
+}
+
+// Score constants, log2 domain.
+struct TcScore {
+    float c1;       // scale log2 e
+    float q[5];     // s Q(s^2) = cap log2(e) tanh(s scale / cap), coefficients of s, s^3, ..
+    float s_max;    // |s| up to which the polynomial holds
+    float two_k;    // 2 log2(e) scale / cap
+    float cap_l2;   // cap log2 e
+    float ref;      // fixed reference
+    bool capped;
+    int32_t window;
+    const float* slopes;
+    const int32_t* key_start;
+    const int32_t* prefix_len;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Packed fp32 pairs: one instruction for two elements.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// cap log2(e) tanh(s scale / cap) at any s.
+__device__ __forceinline__ float capped_exact(float s, const TcScore& sc) {
+    return sc.cap_l2 - 2.f * sc.cap_l2 * rcp_approx(1.f + exp2_approx(s * sc.two_k));
+}
+
+// tcgen05.wait::ld tied to the registers it makes valid, so that no use of them moves above it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+    if (mbar_wait_bounded(bar, parity, abort)) return true;
+    if (!*abort) raise_error(err, PA_DEVERR_WAIT_TIMEOUT);
+    *abort = 1;
+    return false;
+}
+
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src, bool zero) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src),
+                 "r"(zero ? 0 : 16)
+                 : "memory");
+}
+
+// Bits i of a 32-key group whose keys base + i lie in [lo, hi).
+__device__ __forceinline__ uint32_t span_bits(int32_t base, int32_t lo, int32_t hi) {
+    const int32_t l = min(max(lo - base, 0), 32), h = min(max(hi - base, 0), 32);
+    if (h <= l) return 0u;
+    return (h == 32 ? 0xffffffffu : (1u << h) - 1u) & ~(l == 32 ? 0xffffffffu : (1u << l) - 1u);
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ block_table,
+    int32_t max_blocks, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ query_start_loc,
+    int32_t num_kv_heads, int32_t G, int32_t num_blocks, int32_t sub_log2, int32_t cap_tokens, int32_t max_chunk,
+    const __grid_constant__ TcScore sc, uint32_t* err) {
+    using L_ = Smem<D>;
+    constexpr uint32_t kTile = L_::tile;
+    constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
+    constexpr int kHalves = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::bars);
+    uint64_t* k_full = bars;                // [kKStages] K tile landed
+    uint64_t* k_empty = k_full + kKStages;  // [kKStages] the QKs that read the stage are done
+    uint64_t* v_full = k_empty + kKStages;  // [kVStages]
+    uint64_t* v_empty = v_full + kVStages;  // [kVStages] the PVs that read the stage are done
+    uint64_t* s_full = v_empty + kVStages;  // [2] S of tile a / b written
+    uint64_t* p_full = s_full + 2;          // [2] P of tile a / b written (4 warps)
+    uint64_t* o_done = p_full + 2;          // [2] last PV of tile a / b finished
+    uint64_t* q_full = o_done + 2;          // query tiles in shared memory
+    uint64_t* idle = q_full + 1;            // every MMA issued has finished
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L_::misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
+
+    const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
+    __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_seq;
+    __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
+    __shared__ uint32_t seen_own[8];  // documents: the CTA's own positions that some row sees
+    int32_t seq = blockIdx.z;
+    const int32_t n_seqs = gridDim.z;
+    if (n_seqs > 1 && n_seqs <= kLptMaxSeqs) {
+        if (tid < n_seqs) lpt_len[tid] = __ldg(seq_lens + tid);
+        __syncthreads();
+        if (tid < n_seqs) {
+            const int32_t mine = lpt_len[tid];
+            int32_t rank = 0;
+            for (int32_t u = 0; u < n_seqs; ++u) rank += (lpt_len[u] > mine || (lpt_len[u] == mine && u < tid)) ? 1 : 0;
+            if (rank == seq) lpt_seq = tid;
+        }
+        __syncthreads();
+        seq = lpt_seq;
+    }
+    const int32_t h = blockIdx.y, TT = kRows / G, Hq = G * num_kv_heads;
+    const int32_t pair = gridDim.x - 1 - blockIdx.x;  // the longest pairs start first
+    const int32_t q0 = __ldg(query_start_loc + seq), C = __ldg(query_start_loc + seq + 1) - q0;
+    const int32_t L = __ldg(seq_lens + seq);
+    if (C < 0 || C > max_chunk || C > L || L > cap_tokens) {
+        if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
+        return;
+    }
+    const int32_t t0a = 2 * pair * TT, t0b = t0a + TT;
+    if (t0a >= C) return;  // uniform over the CTA
+    const int32_t P0 = L - C;
+    const int32_t prefix = sc.prefix_len ? __ldg(sc.prefix_len + seq) : 0;
+
+    // ---- rows of the softmax threads, and the keys each query tile sees ------------------------
+    const bool softmax_warp = warp >= kSoftWarp0 && warp < kVWarp;
+    const int32_t xq = softmax_warp ? (warp - kSoftWarp0) >> 2 : 0;
+    const int32_t quad = warp & 3;  // TMEM lane quadrant of a softmax warp
+    const int32_t r = quad * 32 + lane;
+    const int32_t tl = r / G, g = r - tl * G;
+    const int32_t t_row = (xq ? t0b : t0a) + tl;
+    const bool row_valid = softmax_warp && tl < TT && t_row < C;
+    const int32_t pos = P0 + t_row;
+    KeySpans row{0, 0, 0, 0};
+    if (row_valid)
+        row = key_spans(L, pos, sc.key_start ? __ldg(sc.key_start + q0 + t_row) : 0, prefix, sc.window);
+    SpanUnion ux[2];
+    if (sc.key_start == nullptr) {  // rows' spans move with their position: the first and the last row tell
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int32_t t0 = x ? t0b : t0a, t1 = min(t0 + TT, C);
+            if (t0 >= t1) {
+                ux[x] = SpanUnion{0, 0, 0, 0};
+                continue;
+            }
+            const KeySpans f = key_spans(L, P0 + t0, 0, prefix, sc.window);
+            const KeySpans l = key_spans(L, P0 + t1 - 1, 0, prefix, sc.window);
+            ux[x] = SpanUnion{f.a0, f.a1, f.b0, l.b1};
+        }
+    } else {
+        if (tid < 8) {
+            red[tid >> 2][tid & 3] = (tid & 1) ? 0 : 0x7fffffff;
+            seen_own[tid] = 0u;
+        }
+        __syncthreads();
+        if (softmax_warp) {
+            const bool in_a = row.a0 < row.a1, in_b = row.b0 < row.b1;
+            const int32_t a0 = __reduce_min_sync(0xffffffffu, in_a ? row.a0 : 0x7fffffff);
+            const int32_t a1 = __reduce_max_sync(0xffffffffu, in_a ? row.a1 : 0);
+            const int32_t b0 = __reduce_min_sync(0xffffffffu, in_b ? row.b0 : 0x7fffffff);
+            const int32_t b1 = __reduce_max_sync(0xffffffffu, in_b ? row.b1 : 0);
+            if (lane == 0) {
+                atomicMin(&red[xq][0], a0);
+                atomicMax(&red[xq][1], a1);
+                atomicMin(&red[xq][2], b0);
+                atomicMax(&red[xq][3], b1);
+            }
+            if (in_b && g == 0) {
+                // the CTA's own positions P0 + t0a + i that this row sees; a key before them that
+                // any row's window span reaches past is seen by the row with the lowest start
+                const int32_t own = P0 + t0a, lo = max(row.b0 - own, 0), hi = row.b1 - own;
+                for (int32_t w = lo >> 5; w * 32 < hi; ++w) atomicOr(&seen_own[w], span_bits(w * 32, lo, hi));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ux[x] = SpanUnion{red[x][0], red[x][1], red[x][2], red[x][3]};
+    }
+    const SpanUnion uni = join(ux[0], ux[1]);
+    const TileList tiles = tile_list(uni);
+    const int32_t n_kv = tiles.n;
+    auto used = [&](int32_t x, int32_t i) -> bool {
+        if (i >= n_kv) return false;
+        const int32_t lo = tiles.tile(i) * kKeys;
+        return ux[x].touches(lo, lo + kKeys);
+    };
+    const int32_t npages = (L + kPageTokens - 1) / kPageTokens;
+
+    // ---- query tiles: 16-byte copies into the swizzled K-major layout; rows without a query zero
+    if (softmax_warp) {
+        const int32_t ti = tid - 32 * kSoftWarp0 - xq * 128;
+        uint8_t* sq = smem + xq * kTile;
+        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+        const int32_t t0 = xq ? t0b : t0a;
+#pragma unroll
+        for (int k = 0; k < kRows * kChunks / 128; ++k) {
+            const int32_t i = ti + k * 128;
+            const int32_t rr = i / kChunks, c16 = i % kChunks;
+            const int32_t tt = rr / G, t = t0 + tt;
+            const bool in = tt < TT && t < C;
+            const __nv_bfloat16* src =
+                in ? q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D + c16 * 8 : q;
+            cp_async16(sq + (c16 >> 3) * kHalf + sw128_offset(rr, c16 & 7), src, !in);
+        }
+    }
+    // Pool row of list page 8 i + s (page s of the i-th key tile); lane l of a producer warp holds
+    // page 32 w + l of window w, fetched one window ahead.
+    auto page_row = [&](int32_t lp) -> int32_t {
+        int32_t phys = 0, pg = 0;
+        if ((lp >> 3) < n_kv) {
+            pg = tiles.tile(lp >> 3) * (kKeys / kPageTokens) + (lp & 7);
+            if (pg < npages) {  // keys past the sequence end read the null block; masked
+                phys = __ldg(block_table + static_cast<int64_t>(seq) * max_blocks + (pg >> sub_log2));
+                if (phys < 0 || phys >= num_blocks) {
+                    raise_error(err, PA_DEVERR_BLOCK_RANGE);
+                    phys = 0;
+                }
+            }
+        }
+        return (((phys * num_kv_heads + h) << sub_log2) + (pg & ((1 << sub_log2) - 1))) * kPageTokens;
+    };
+    int32_t row_cur = 0, row_nxt = 0;
+    if (warp == kKWarp || warp == kVWarp) {
+        row_cur = page_row(lane);
+        row_nxt = page_row(32 + lane);
+    }
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < L_::num_bars; ++i) mbar_init(&bars[i], 1);
+        mbar_init(&p_full[0], 4);
+        mbar_init(&p_full[1], 4);
+        mbar_init(q_full, kSoftThreads);
+        fence_mbarrier_init();
+    }
+    if (warp == kMmaWarp) {
+        umma::tmem_alloc(tmem_holder, 512);
+        umma::tmem_relinquish();
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    // tensor memory columns: S of tile x at 128 x (its P, bf16 pairs, overwrites the first 64
+    // columns once read), O of tile x at 256 + 128 x
+    const uint32_t tmem = *tmem_holder;
+    if (softmax_warp) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_shared();
+        mbar_arrive(q_full);
+    }
+
+    int32_t last_j = -1;  // producers: last key tile issued
+    if (warp == kKWarp || warp == kVWarp) {
+        // ======================================= producers ======================================
+        const bool is_v = warp == kVWarp;
+        const int32_t nst = is_v ? kVStages : kKStages;
+        const void* tm = is_v ? static_cast<const void*>(&tm_v) : static_cast<const void*>(&tm_k);
+        uint64_t* full = is_v ? v_full : k_full;
+        uint64_t* empty = is_v ? v_empty : k_empty;
+        uint8_t* ring = smem + (is_v ? L_::v : L_::k);
+        if (lane == 0) prefetch_tensormap(tm);
+        for (int32_t j = 0; j < n_kv; ++j) {
+            const int32_t st = j % nst;
+            const uint32_t use = static_cast<uint32_t>(j / nst);
+            if (j > 0 && (j & 3) == 0) {
+                row_cur = row_nxt;
+                row_nxt = page_row(32 * ((j >> 2) + 1) + lane);
+            }
+            bool ok = true;
+            if (use > 0 && lane == 0) ok = wait_or_abort(&empty[st], (use - 1) & 1u, abort_flag, err);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            uint8_t* dst = ring + st * kTile;
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], kTile);
+            last_j = j;
+            const int32_t rk = __shfl_sync(0xffffffffu, row_cur, (j & 3) * 8 + (lane & 7));
+            __syncwarp();
+            if (lane < 8 * kHalves)  // lane = (column half, page)
+                tma_load_2d(dst + (lane >> 3) * kHalf + (lane & 7) * 2048u, tm, (lane >> 3) * 64, rk, &full[st]);
+        }
+    } else if (warp == kMmaWarp) {
+        // ======================================= MMA issuer =====================================
+        const bool leader = umma::elect_one();
+        const uint32_t idesc_qk = umma::idesc_bf16_f32(128, 128, 0, 0);  // Q, K both K-major
+        const uint32_t idesc_pv = umma::idesc_bf16_f32(128, D, 0, 1);    // P (TMEM), V MN-major
+        const uint64_t dq0 = umma::smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dk0 = umma::smem_desc_sw128(smem_u32(smem + L_::k), 16, 1024);
+        const uint64_t dv0 = umma::smem_desc_sw128(smem_u32(smem + L_::v), kHalf, 1024);
+        auto qk = [&](int32_t x, int32_t j) {
+            const uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4);
+            const uint64_t dk = dk0 + static_cast<uint64_t>(j % kKStages) * (kTile >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                if (leader) umma::mma_bf16(tmem + x * 128, dq + off, dk + off, idesc_qk, ks > 0);
+            }
+            if (leader) umma::commit(&s_full[x]);
+            __syncwarp();
+        };
+        auto pv = [&](int32_t x, int32_t j, bool acc) {
+            const uint64_t dv = dv0 + static_cast<uint64_t>(j % kVStages) * (kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 keys per instruction: 8 P columns
+                if (leader)
+                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + kk * 8,
+                                          dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || kk > 0));
+            __syncwarp();
+        };
+        auto wait_k = [&](int32_t j) {
+            const bool ok = wait_or_abort(&k_full[j % kKStages], static_cast<uint32_t>(j / kKStages) & 1u, abort_flag, err);
+            umma::fence_after_sync();
+            return ok;
+        };
+        int32_t last[2], done[2] = {0, 0};  // last list position and PVs issued, per query tile
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            last[x] = n_kv - 1;
+            while (last[x] >= 0 && !used(x, last[x])) --last[x];
+        }
+        bool ok = wait_or_abort(q_full, 0, abort_flag, err);
+        if (ok && n_kv > 0) {
+            ok = wait_k(0);
+            if (ok) {
+                if (used(0, 0)) qk(0, 0);
+                if (used(1, 0)) qk(1, 0);
+                if (leader) umma::commit(&k_empty[0]);
+            }
+        }
+        auto step_pv = [&](int32_t x, int32_t j) {  // P_x written, S_x read: O_x += P_x V(j)
+            ok = wait_or_abort(&p_full[x], done[x] & 1, abort_flag, err);
+            umma::fence_after_sync();
+            if (!ok) return;
+            pv(x, j, done[x] > 0);
+            ++done[x];
+            if (j == last[x] && leader) umma::commit(&o_done[x]);
+        };
+        for (int32_t j = 0; j < n_kv && ok; ++j) {
+            const bool more = j + 1 < n_kv;
+            ok = wait_or_abort(&v_full[j % kVStages], static_cast<uint32_t>(j / kVStages) & 1u, abort_flag, err);
+            if (ok && used(0, j)) step_pv(0, j);
+            if (ok && more) ok = wait_k(j + 1);
+            if (ok && used(0, j + 1)) qk(0, j + 1);
+            if (ok && used(1, j)) step_pv(1, j);
+            if (ok && leader) umma::commit(&v_empty[j % kVStages]);
+            if (ok && used(1, j + 1)) qk(1, j + 1);
+            if (ok && more && leader) umma::commit(&k_empty[(j + 1) % kKStages]);
+            __syncwarp();
+        }
+        if (leader) umma::commit(idle);  // arrives once every MMA issued above has finished
+        __syncwarp();
+    } else if (softmax_warp) {
+        // ==================================== scores and softmax ================================
+        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t tmem_s = tmem + xq * 128 + lane_off, tmem_o = tmem + 256 + xq * 128 + lane_off;
+        const float slope = (MODE == kDistance || MODE == kGeneral) && sc.slopes && row_valid
+                                ? __ldg(sc.slopes + h * G + g) * kLog2e
+                                : 0.f;
+        const uint64_t c1 = pack2(sc.c1, sc.c1);
+        float m_ref = -INFINITY, l_sum = 0.f;
+        bool ok = true;
+        int32_t cnt = 0;  // key tiles this query tile has used
+        for (int32_t i = 0; i < n_kv; ++i) {
+            if (!used(xq, i)) continue;
+            ok = wait_or_abort(&s_full[xq], cnt & 1, abort_flag, err);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            umma::fence_after_sync();
+            const int32_t kbase = tiles.tile(i) * kKeys;
+            const bool first = cnt == 0;
+            ++cnt;
+            // rows that see the whole tile need no mask (nor do rows without a query, whose Q is
+            // zero and whose results go nowhere)
+            const bool whole = !row_valid || (kbase >= row.a0 && kbase + kKeys <= row.a1) || (kbase >= row.b0 && kbase + kKeys <= row.b1);
+            const bool mask = !__all_sync(0xffffffffu, whole);
+            const bool behind = __any_sync(0xffffffffu, row_valid && kbase + kKeys - 1 > pos);
+            const float d0 = static_cast<float>(kbase - pos);
+            // weight arguments (log2 domain) of columns 2 e, 2 e + 1 of 32-column group c
+            auto args = [&](uint64_t s, int c, int e, uint64_t add) -> uint64_t {
+                const int col = c * 32 + 2 * e;
+                if constexpr (MODE == kPlain) {
+                    return fma2(s, c1, add);
+                } else if constexpr (MODE == kDistance) {
+                    const float x0 = d0 + col, x1 = d0 + (col + 1);
+                    const uint64_t away = behind ? pack2(-slope * fabsf(x0), -slope * fabsf(x1)) : pack2(slope * x0, slope * x1);
+                    return add2(fma2(s, c1, away), add);
+                } else {
+                    float s0, s1;
+                    unpack2(s, s0, s1);
+                    s0 = sc.capped ? capped_exact(s0, sc) : s0 * sc.c1;
+                    s1 = sc.capped ? capped_exact(s1, sc) : s1 * sc.c1;
+                    return add2(pack2(s0 - slope * fabsf(d0 + col), s1 - slope * fabsf(d0 + (col + 1))), add);
+                }
+            };
+            float alpha = 1.f;
+            bool grow = false;
+            uint64_t shift = pack2(-sc.ref, -sc.ref);
+            if constexpr (MODE != kCap) {
+                // pass 1: the tile's maximum over visible keys
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t raw[32];
+                    umma::ld_32x32b_x32(tmem_s + c * 32, raw);
+                    wait_ld(raw);
+                    uint32_t vis = 0xffffffffu;
+                    if (mask) vis = span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        unpack2(args(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), c, e, 0ull), x0, x1);
+                        if (mask) {
+                            if (!(vis >> (2 * e) & 1u)) x0 = -INFINITY;
+                            if (!(vis >> (2 * e + 1) & 1u)) x1 = -INFINITY;
+                        }
+                        mx[e & 3] = max3(mx[e & 3], x0, x1);
+                    }
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
+                const float m_new = grow ? top : m_ref;
+                alpha = grow ? exp2_approx(m_ref - m_new) : 1.f;
+                m_ref = m_new;
+                const float neg = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
+                shift = pack2(neg, neg);
+            }
+            // pass 2: P = 2^arg in bf16 pairs over the first 64 columns of S, 32 keys at a time
+            // (each group of S is read before the P columns that overwrite part of it)
+            uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t raw[2][32];
+            umma::ld_32x32b_x32(tmem_s, raw[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t(&cur)[32] = raw[c & 1];
+                wait_ld(cur);
+                if (c < 3) umma::ld_32x32b_x32(tmem_s + (c + 1) * 32, raw[(c + 1) & 1]);
+                uint32_t vis = 0xffffffffu;
+                if (mask) vis = span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+                uint32_t pk[16];
+                bool exact = false;
+                if constexpr (MODE == kCap) {
+                    float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        big[e & 3] = max3(big[e & 3], fabsf(__uint_as_float(cur[2 * e])), fabsf(__uint_as_float(cur[2 * e + 1])));
+                    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+                    exact = __any_sync(0xffffffffu, b > sc.s_max);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t s = pack2(__uint_as_float(cur[2 * e]), __uint_as_float(cur[2 * e + 1]));
+                    float x0, x1;
+                    if constexpr (MODE == kCap) {
+                        if (!exact) {
+                            const uint64_t w = mul2(s, s);
+                            uint64_t p = fma2(w, pack2(sc.q[4], sc.q[4]), pack2(sc.q[3], sc.q[3]));
+                            p = fma2(w, p, pack2(sc.q[2], sc.q[2]));
+                            p = fma2(w, p, pack2(sc.q[1], sc.q[1]));
+                            p = fma2(w, p, pack2(sc.q[0], sc.q[0]));
+                            unpack2(fma2(s, p, shift), x0, x1);
+                        } else {
+                            x0 = capped_exact(__uint_as_float(cur[2 * e]), sc) - sc.ref;
+                            x1 = capped_exact(__uint_as_float(cur[2 * e + 1]), sc) - sc.ref;
+                        }
+                    } else {
+                        unpack2(args(s, c, e, shift), x0, x1);
+                    }
+                    if (mask) {
+                        if (!(vis >> (2 * e) & 1u)) x0 = -INFINITY;
+                        if (!(vis >> (2 * e + 1) & 1u)) x1 = -INFINITY;
+                    }
+                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                    psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
+                    pk[e] = pack_bf16x2(p0, p1);
+                }
+                umma::st_32x32b_x16(tmem_s + c * 16, pk);
+            }
+            umma::wait_st();
+            float s0, s1;
+            unpack2(add2(add2(psum[0], psum[1]), add2(psum[2], psum[3])), s0, s1);
+            l_sum = l_sum * alpha + (s0 + s1);
+            if constexpr (MODE != kCap) {
+                if (!first && __any_sync(0xffffffffu, grow)) {
+                    // O holds the tiles before under the old reference; their last PV finished before
+                    // this S was committed, so O can be rescaled now
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        umma::ld_32x32b_x32(tmem_o + c * 32, o);
+                        wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        umma::st_32x32b_x32(tmem_o + c * 32, o);
+                    }
+                    umma::wait_st();
+                }
+            }
+            // keys of this tile that no row of the CTA sees: zero their V rows (thread r: key row r),
+            // by the first query tile that uses the key tile
+            const int32_t own = P0 + t0a;
+            const bool gaps = !uni.covers(kbase, kbase + kKeys) || (sc.key_start != nullptr && kbase + kKeys > own);
+            if (gaps && (xq == 0 || !used(0, i))) {
+                const int32_t key = kbase + r;
+                bool seen = (key >= uni.a0 && key < uni.a1) || (key >= uni.b0 && key < uni.b1);
+                if (seen && sc.key_start != nullptr && key >= own && !(key >= uni.a0 && key < uni.a1))
+                    seen = (seen_own[(key - own) >> 5] >> ((key - own) & 31)) & 1u;
+                const int32_t st = i % kVStages;
+                const bool okv = wait_or_abort(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
+                if (okv && !seen) {
+                    uint8_t* sv = smem + L_::v + st * kTile;
+#pragma unroll
+                    for (int hf = 0; hf < kHalves; ++hf)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<int4*>(sv + hf * kHalf + r * 128u + c * 16u) = make_int4(0, 0, 0, 0);
+                }
+                fence_proxy_async_shared();
+            }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[xq]);
+        }
+        if (ok && cnt > 0) ok = wait_or_abort(&o_done[xq], 0, abort_flag, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            umma::fence_after_sync();
+            const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+            __nv_bfloat16* orow = out + (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (cnt > 0) {
+                    umma::ld_32x32b_x32(tmem_o + c * 32, o);
+                    wait_ld(o);
+                }
+                if (row_valid) {
+#pragma unroll
+                    for (int v4 = 0; v4 < 4; ++v4) {
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = l_sum == 0.f ? 0.f : __uint_as_float(o[v4 * 8 + k]) * inv;
+                        *reinterpret_cast<uint4*>(orow + c * 32 + v4 * 8) =
+                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                       pack_bf16x2(f[6], f[7]));
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- wind down: copies landed and MMAs retired before shared and tensor memory go ------
+    if ((warp == kKWarp || warp == kVWarp) && lane == 0) {
+        const int32_t nst = warp == kVWarp ? kVStages : kKStages;
+        uint64_t* full = warp == kVWarp ? v_full : k_full;
+        for (int32_t j = max(0, last_j - nst + 1); j <= last_j; ++j)
+            mbar_wait_timeout(&full[j % nst], static_cast<uint32_t>(j / nst) & 1u);
+    }
+    if (warp == kMmaWarp && lane == 0) mbar_wait_timeout(idle, 0);
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Minimax (Remez) coefficients of tanh x = x (t0 + t1 x^2 + .. + t4 x^8) on |x| <= 0.8; absolute
+// error 3.5e-7.
+constexpr double kTanh[5] = {0.999995135, -0.333174266, 0.131862196, -0.0482613134, 0.0114646536};
+constexpr float kTanhRange = 0.8f;
+
+template <int D, int MODE>
+cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t stream) {
+    alignas(64) CUtensorMap tm_k, tm_v;
+    const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.num_kv_heads * a.block_size;
+    cudaError_t e = encode_bf16_2d_sw128(&tm_k, a.k_cache, D, rows, 64, kPageTokens);
+    if (e != cudaSuccess) return e;
+    e = encode_bf16_2d_sw128(&tm_v, a.v_cache, D, rows, 64, kPageTokens);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(prefill_scored_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(Smem<D>::total));
+    if (e != cudaSuccess) return e;
+    const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
+    const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
+    const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
+    const dim3 grid((a.max_chunk_len + 2 * TT - 1) / (2 * TT), a.num_kv_heads, a.num_seqs);
+    prefill_scored_kernel<D, MODE><<<grid, kThreads, Smem<D>::total, stream>>>(
+        tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(a.q), a.block_table,
+        a.max_blocks_per_seq, a.seq_lens, a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens,
+        a.max_chunk_len, sc, a.err);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, cudaStream_t stream) {
+    switch (mode) {
+        case kPlain: return launch_impl<D, kPlain>(a, sc, stream);
+        case kCap: return launch_impl<D, kCap>(a, sc, stream);
+        case kDistance: return launch_impl<D, kDistance>(a, sc, stream);
+        default: return launch_impl<D, kGeneral>(a, sc, stream);
+    }
+}
+
+}  // namespace
+
+bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
+    return a.dtype == PA_BF16 && a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
+           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128>::total) <= dev.max_smem_optin;
+}
+
+cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, cudaStream_t stream) {
+    TcScore sc{};
+    sc.c1 = a.scale * kLog2e;
+    sc.capped = s.cap > 0.f;
+    if (sc.capped) {
+        const double k = static_cast<double>(a.scale) / s.cap;
+        double c = static_cast<double>(s.cap) * 1.4426950408889634 * k;
+        for (int i = 0; i < 5; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
+        sc.s_max = static_cast<float>(kTanhRange / fabs(k));
+        sc.two_k = static_cast<float>(2 * 1.4426950408889634 * k);
+        sc.cap_l2 = s.cap * kLog2e;
+        sc.ref = 0.5f * sc.cap_l2;
+    }
+    sc.window = s.window;
+    sc.slopes = s.slopes;
+    sc.key_start = s.key_start;
+    sc.prefix_len = s.prefix_len;
+    const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
+                                 : (!s.slopes && s.cap <= kMaxFixedCap ? kCap : kGeneral);
+    return a.head_dim == 128 ? pick<128>(a, sc, mode, stream) : pick<64>(a, sc, mode, stream);
+}
+
+}  // namespace pa
