@@ -111,7 +111,7 @@ __device__ __forceinline__ SpanUnion join(const SpanUnion& x, const SpanUnion& y
 struct TcScore {
     float c1;       // scale log2 e
     float q[5];     // s Q(s^2) = cap log2(e) tanh(s scale / cap), coefficients of s, s^3, ..
-    float s_max;    // |s| up to which the polynomial holds
+    float s2_max;   // s^2 up to which the polynomial holds
     float two_k;    // 2 log2(e) scale / cap
     float cap_l2;   // cap log2 e
     float ref;      // fixed reference
@@ -142,6 +142,16 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
     return d;
+}
+// The pair (x, x), opaque to the compiler so that it stays in registers.
+__device__ __forceinline__ uint64_t hold2(float x) {
+    uint64_t d;
+    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+    return d;
+}
+// Columns 2 e, 2 e + 1 of a group of 32 scores.
+__device__ __forceinline__ uint64_t raw_pair(const uint32_t (&r)[32], int e) {
+    return pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
@@ -490,6 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
         const uint64_t c1 = pack2(sc.c1, sc.c1);
+        uint64_t tq[5];  // the polynomial's coefficients, kept in registers
+#pragma unroll
+        for (int k = 0; k < 5; ++k) tq[k] = hold2(sc.q[k]);
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         int32_t cnt = 0;  // key tiles this query tile has used
@@ -510,54 +523,91 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             const bool mask = !__all_sync(0xffffffffu, whole);
             const bool behind = __any_sync(0xffffffffu, row_valid && kbase + kKeys - 1 > pos);
             const float d0 = static_cast<float>(kbase - pos);
-            // weight arguments (log2 domain) of columns 2 e, 2 e + 1 of 32-column group c
-            auto args = [&](uint64_t s, int c, int e, uint64_t add) -> uint64_t {
-                const int col = c * 32 + 2 * e;
+            // Bits of the 32 keys of group c that the row sees.
+            auto visible = [&](int c) -> uint32_t {
+                return span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+            };
+            // Weight arguments (log2 domain) of group c: x = score + shift, in pairs. Straight-line
+            // code over the group; what differs by warp is branched on once per group.
+            auto args = [&](const uint32_t(&raw)[32], int c, float shift, float(&x)[32]) {
                 if constexpr (MODE == kPlain) {
-                    return fma2(s, c1, add);
+                    const uint64_t add = pack2(shift, shift);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) unpack2(fma2(raw_pair(raw, e), c1, add), x[2 * e], x[2 * e + 1]);
+                } else if constexpr (MODE == kCap) {
+                    const uint64_t add = pack2(shift, shift);
+                    float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint64_t s = raw_pair(raw, e), w = mul2(s, s);
+                        uint64_t p = fma2(w, tq[4], tq[3]);
+                        p = fma2(w, p, tq[2]);
+                        p = fma2(w, p, tq[1]);
+                        p = fma2(w, p, tq[0]);
+                        unpack2(fma2(s, p, add), x[2 * e], x[2 * e + 1]);
+                        float w0, w1;
+                        unpack2(w, w0, w1);
+                        big[e & 3] = max3(big[e & 3], w0, w1);
+                    }
+                    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+                    if (__any_sync(0xffffffffu, b > sc.s2_max)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = capped_exact(__uint_as_float(raw[k]), sc) + shift;
+                    }
                 } else if constexpr (MODE == kDistance) {
-                    const float x0 = d0 + col, x1 = d0 + (col + 1);
-                    const uint64_t away = behind ? pack2(-slope * fabsf(x0), -slope * fabsf(x1)) : pack2(slope * x0, slope * x1);
-                    return add2(fma2(s, c1, away), add);
+                    if (!behind) {  // -slope |p - j| = slope (j - p), stepped along the columns
+                        uint64_t away[4];
+                        const uint64_t step = pack2(8.f * slope, 8.f * slope);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            away[k] = pack2(fmaf(slope, d0 + (c * 32 + 2 * k), shift), fmaf(slope, d0 + (c * 32 + 2 * k + 1), shift));
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            unpack2(fma2(raw_pair(raw, e), c1, away[e & 3]), x[2 * e], x[2 * e + 1]);
+                            away[e & 3] = add2(away[e & 3], step);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            x[k] = fmaf(__uint_as_float(raw[k]), sc.c1, fmaf(-slope, fabsf(d0 + (c * 32 + k)), shift));
+                    }
                 } else {
-                    float s0, s1;
-                    unpack2(s, s0, s1);
-                    s0 = sc.capped ? capped_exact(s0, sc) : s0 * sc.c1;
-                    s1 = sc.capped ? capped_exact(s1, sc) : s1 * sc.c1;
-                    return add2(pack2(s0 - slope * fabsf(d0 + col), s1 - slope * fabsf(d0 + (col + 1))), add);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float s = __uint_as_float(raw[k]);
+                        const float z = sc.capped ? capped_exact(s, sc) : s * sc.c1;
+                        x[k] = fmaf(-slope, fabsf(d0 + (c * 32 + k)), z) + shift;
+                    }
+                }
+                if (mask) {
+                    const uint32_t vis = visible(c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(vis >> k & 1u)) x[k] = -INFINITY;
                 }
             };
-            float alpha = 1.f;
+            float alpha = 1.f, shift = -sc.ref;
             bool grow = false;
-            uint64_t shift = pack2(-sc.ref, -sc.ref);
             if constexpr (MODE != kCap) {
                 // pass 1: the tile's maximum over visible keys
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t raw[2][32];
+                umma::ld_32x32b_x32(tmem_s, raw[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t raw[32];
-                    umma::ld_32x32b_x32(tmem_s + c * 32, raw);
-                    wait_ld(raw);
-                    uint32_t vis = 0xffffffffu;
-                    if (mask) vis = span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+                    wait_ld(raw[c & 1]);
+                    if (c < 3) umma::ld_32x32b_x32(tmem_s + (c + 1) * 32, raw[(c + 1) & 1]);
+                    float x[32];
+                    args(raw[c & 1], c, 0.f, x);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        unpack2(args(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), c, e, 0ull), x0, x1);
-                        if (mask) {
-                            if (!(vis >> (2 * e) & 1u)) x0 = -INFINITY;
-                            if (!(vis >> (2 * e + 1) & 1u)) x1 = -INFINITY;
-                        }
-                        mx[e & 3] = max3(mx[e & 3], x0, x1);
-                    }
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
                 const float m_new = grow ? top : m_ref;
                 alpha = grow ? exp2_approx(m_ref - m_new) : 1.f;
                 m_ref = m_new;
-                const float neg = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
-                shift = pack2(neg, neg);
+                shift = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
             }
             // pass 2: P = 2^arg in bf16 pairs over the first 64 columns of S, 32 keys at a time
             // (each group of S is read before the P columns that overwrite part of it)
@@ -566,45 +616,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             umma::ld_32x32b_x32(tmem_s, raw[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t(&cur)[32] = raw[c & 1];
-                wait_ld(cur);
+                wait_ld(raw[c & 1]);
                 if (c < 3) umma::ld_32x32b_x32(tmem_s + (c + 1) * 32, raw[(c + 1) & 1]);
-                uint32_t vis = 0xffffffffu;
-                if (mask) vis = span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+                float x[32];
+                args(raw[c & 1], c, shift, x);
                 uint32_t pk[16];
-                bool exact = false;
-                if constexpr (MODE == kCap) {
-                    float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        big[e & 3] = max3(big[e & 3], fabsf(__uint_as_float(cur[2 * e])), fabsf(__uint_as_float(cur[2 * e + 1])));
-                    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-                    exact = __any_sync(0xffffffffu, b > sc.s_max);
-                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const uint64_t s = pack2(__uint_as_float(cur[2 * e]), __uint_as_float(cur[2 * e + 1]));
-                    float x0, x1;
-                    if constexpr (MODE == kCap) {
-                        if (!exact) {
-                            const uint64_t w = mul2(s, s);
-                            uint64_t p = fma2(w, pack2(sc.q[4], sc.q[4]), pack2(sc.q[3], sc.q[3]));
-                            p = fma2(w, p, pack2(sc.q[2], sc.q[2]));
-                            p = fma2(w, p, pack2(sc.q[1], sc.q[1]));
-                            p = fma2(w, p, pack2(sc.q[0], sc.q[0]));
-                            unpack2(fma2(s, p, shift), x0, x1);
-                        } else {
-                            x0 = capped_exact(__uint_as_float(cur[2 * e]), sc) - sc.ref;
-                            x1 = capped_exact(__uint_as_float(cur[2 * e + 1]), sc) - sc.ref;
-                        }
-                    } else {
-                        unpack2(args(s, c, e, shift), x0, x1);
-                    }
-                    if (mask) {
-                        if (!(vis >> (2 * e) & 1u)) x0 = -INFINITY;
-                        if (!(vis >> (2 * e + 1) & 1u)) x1 = -INFINITY;
-                    }
-                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                    const float p0 = exp2_approx(x[2 * e]), p1 = exp2_approx(x[2 * e + 1]);
                     psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
                     pk[e] = pack_bf16x2(p0, p1);
                 }
@@ -751,7 +770,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
         const double k = static_cast<double>(a.scale) / s.cap;
         double c = static_cast<double>(s.cap) * 1.4426950408889634 * k;
         for (int i = 0; i < 5; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
-        sc.s_max = static_cast<float>(kTanhRange / fabs(k));
+        sc.s2_max = static_cast<float>(kTanhRange * kTanhRange / (k * k));
         sc.two_k = static_cast<float>(2 * 1.4426950408889634 * k);
         sc.cap_l2 = s.cap * kLog2e;
         sc.ref = 0.5f * sc.cap_l2;
