@@ -6,12 +6,13 @@
 // token r / G, q head r % G of the G heads that share the kv head, so every K/V tile is read once
 // for both. Keys come in tiles of 128, and only the tiles that hold a key some row of the CTA sees
 // (TileList: the prefix's tiles, then the window's):
-//   warp 0     - K producer, warp 10 - V producer: block ids 32 pages ahead, TMA copies of 16-token
+//   warp 16    - K producer, warp 18 - V producer: block ids 32 pages ahead, TMA copies of 16-token
 //                pages (128-byte swizzle) into rings of key tiles;
-//   warp 1     - tensor-memory owner and MMA issuer: S = Q K^T, O += P V with P from tensor memory,
+//   warp 17    - tensor-memory owner and MMA issuer: S = Q K^T, O += P V with P from tensor memory,
 //                in the order PV_a(j), QK_a(j+1), PV_b(j), QK_b(j+1), so that the tensor cores
 //                serve one query tile while the other one's softmax runs;
-//   warps 2-9  - scores and softmax, one thread per query row: tile a (2-5) and tile b (6-9).
+//   warps 0-15 - scores and softmax, two threads per query row, each on 64 of the tile's 128 keys
+//                (four warps a scheduler to cover the arithmetic's and tensor memory's latencies).
 //
 // Scores. Four variants of the score arithmetic (Mode), all in the log2 domain:
 //   plain      arg = s c1;                       online maximum, two passes over S
@@ -42,9 +43,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
-constexpr int kKWarp = 0, kMmaWarp = 1, kSoftWarp0 = 2, kVWarp = 10;
+constexpr int kSoftWarps = 16;  // warps 0-15: scores and softmax
+constexpr int kKWarp = 16, kMmaWarp = 17, kVWarp = 18;
 constexpr int kThreads = 32 * (kVWarp + 1);
-constexpr int kSoftThreads = 256;
+constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 bf16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units: O is rescaled only when the maximum grows by more
 constexpr int kLptMaxSeqs = 64;           // sequences ordered longest first inside the kernel
@@ -61,7 +63,7 @@ struct Smem {
     static constexpr uint32_t k = q + 2 * tile;
     static constexpr uint32_t v = k + k_stages * tile;
     static constexpr uint32_t bars = v + v_stages * tile;
-    static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 8;
+    static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 16;
     static constexpr uint32_t misc = bars + num_bars * 8;  // tmem base, abort flag
     static constexpr uint32_t total = misc + 16 + 1024;
 };
@@ -202,6 +204,10 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src, bool
                  : "memory");
 }
 
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Bits i of a 32-key group whose keys base + i lie in [lo, hi).
 __device__ __forceinline__ uint32_t span_bits(int32_t base, int32_t lo, int32_t hi) {
     const int32_t l = min(max(lo - base, 0), 32), h = min(max(hi - base, 0), 32);
@@ -228,10 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     uint64_t* v_full = k_empty + kKStages;  // [kVStages]
     uint64_t* v_empty = v_full + kVStages;  // [kVStages] the PVs that read the stage are done
     uint64_t* s_full = v_empty + kVStages;  // [2] S of tile a / b written
-    uint64_t* p_full = s_full + 2;          // [2] P of tile a / b written (4 warps)
+    uint64_t* p_full = s_full + 2;          // [2] P of tile a / b written (8 warps)
     uint64_t* o_done = p_full + 2;          // [2] last PV of tile a / b finished
     uint64_t* q_full = o_done + 2;          // query tiles in shared memory
     uint64_t* idle = q_full + 1;            // every MMA issued has finished
+    uint64_t* mx_full = idle + 1;           // [2][4] both halves' maxima of a tile's 32 rows stored
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L_::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
 
@@ -240,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_seq;
     __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
     __shared__ uint32_t seen_own[8];  // documents: the CTA's own positions that some row sees
+    __shared__ __nv_bfloat16 row_max[2][2][kRows];  // per query tile and half of the keys: the rows' maxima
     int32_t seq = blockIdx.z;
     const int32_t n_seqs = gridDim.z;
     if (n_seqs > 1 && n_seqs <= kLptMaxSeqs) {
@@ -268,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const int32_t prefix = sc.prefix_len ? __ldg(sc.prefix_len + seq) : 0;
 
     // ---- rows of the softmax threads, and the keys each query tile sees ------------------------
-    const bool softmax_warp = warp >= kSoftWarp0 && warp < kVWarp;
-    const int32_t xq = softmax_warp ? (warp - kSoftWarp0) >> 2 : 0;
-    const int32_t quad = warp & 3;  // TMEM lane quadrant of a softmax warp
+    const bool softmax_warp = warp < kSoftWarps;
+    const int32_t xq = (warp >> 2) & 1, half = (warp >> 3) & 1;  // query tile and key half of a softmax warp
+    const int32_t quad = warp & 3;                                // its TMEM lane quadrant
     const int32_t r = quad * 32 + lane;
     const int32_t tl = r / G, g = r - tl * G;
     const int32_t t_row = (xq ? t0b : t0a) + tl;
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             seen_own[tid] = 0u;
         }
         __syncthreads();
-        if (softmax_warp) {
+        if (softmax_warp && half == 0) {
             const bool in_a = row.a0 < row.a1, in_b = row.b0 < row.b1;
             const int32_t a0 = __reduce_min_sync(0xffffffffu, in_a ? row.a0 : 0x7fffffff);
             const int32_t a1 = __reduce_max_sync(0xffffffffu, in_a ? row.a1 : 0);
@@ -333,13 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 
     // ---- query tiles: 16-byte copies into the swizzled K-major layout; rows without a query zero
     if (softmax_warp) {
-        const int32_t ti = tid - 32 * kSoftWarp0 - xq * 128;
+        const int32_t ti = half * 128 + (tid & 127);
         uint8_t* sq = smem + xq * kTile;
         constexpr int kChunks = D / 8;  // 16-byte chunks of a row
         const int32_t t0 = xq ? t0b : t0a;
 #pragma unroll
-        for (int k = 0; k < kRows * kChunks / 128; ++k) {
-            const int32_t i = ti + k * 128;
+        for (int k = 0; k < kRows * kChunks / 256; ++k) {
+            const int32_t i = ti + k * 256;
             const int32_t rr = i / kChunks, c16 = i % kChunks;
             const int32_t tt = rr / G, t = t0 + tt;
             const bool in = tt < TT && t < C;
@@ -372,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     if (tid == 0) {
         *abort_flag = 0;
         for (int i = 0; i < L_::num_bars; ++i) mbar_init(&bars[i], 1);
-        mbar_init(&p_full[0], 4);
-        mbar_init(&p_full[1], 4);
+        mbar_init(&p_full[0], 8);
+        mbar_init(&p_full[1], 8);
+        for (int i = 0; i < 8; ++i) mbar_init(&mx_full[i], 2);
         mbar_init(q_full, kSoftThreads);
         fence_mbarrier_init();
     }
@@ -384,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    // tensor memory columns: S of tile x at 128 x (its P, bf16 pairs, overwrites the first 64
-    // columns once read), O of tile x at 256 + 128 x
+    // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, bf16 pairs,
+    // overwrites the first 32 of the half's 64 columns once read), O of tile x at 256 + 128 x
     const uint32_t tmem = *tmem_holder;
     if (softmax_warp) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 keys per instruction: 8 P columns
                 if (leader)
-                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + kk * 8,
+                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                                           dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || kk > 0));
             __syncwarp();
         };
@@ -495,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     } else if (softmax_warp) {
         // ==================================== scores and softmax ================================
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tmem_s = tmem + xq * 128 + lane_off, tmem_o = tmem + 256 + xq * 128 + lane_off;
+        const uint32_t tmem_s = tmem + xq * 128 + half * 64 + lane_off;
+        const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (D / 2) + lane_off;
         const float slope = (MODE == kDistance || MODE == kGeneral) && sc.slopes && row_valid
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
@@ -514,14 +524,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 break;
             }
             umma::fence_after_sync();
-            const int32_t kbase = tiles.tile(i) * kKeys;
+            const int32_t ktile = tiles.tile(i) * kKeys, kbase = ktile + half * (kKeys / 2);
             const bool first = cnt == 0;
             ++cnt;
             // rows that see the whole tile need no mask (nor do rows without a query, whose Q is
             // zero and whose results go nowhere)
-            const bool whole = !row_valid || (kbase >= row.a0 && kbase + kKeys <= row.a1) || (kbase >= row.b0 && kbase + kKeys <= row.b1);
+            const bool whole = !row_valid || (kbase >= row.a0 && kbase + kKeys / 2 <= row.a1) ||
+                               (kbase >= row.b0 && kbase + kKeys / 2 <= row.b1);
             const bool mask = !__all_sync(0xffffffffu, whole);
-            const bool behind = __any_sync(0xffffffffu, row_valid && kbase + kKeys - 1 > pos);
+            const bool behind = __any_sync(0xffffffffu, row_valid && kbase + kKeys / 2 - 1 > pos);
             const float d0 = static_cast<float>(kbase - pos);
             // Bits of the 32 keys of group c that the row sees.
             auto visible = [&](int c) -> uint32_t {
@@ -591,35 +602,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             if constexpr (MODE != kCap) {
                 // pass 1: the tile's maximum over visible keys
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                uint32_t raw[2][32];
-                umma::ld_32x32b_x32(tmem_s, raw[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    wait_ld(raw[c & 1]);
-                    if (c < 3) umma::ld_32x32b_x32(tmem_s + (c + 1) * 32, raw[(c + 1) & 1]);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t raw[32];
+                    umma::ld_32x32b_x32(tmem_s + c * 32, raw);
+                    wait_ld(raw);
                     float x[32];
-                    args(raw[c & 1], c, 0.f, x);
+                    args(raw, c, 0.f, x);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // the row's other half of the keys is another thread's: exchange the maxima, rounded
+                // up to bf16 (any reference at or above the maximum serves, if both take the same)
+                const __nv_bfloat16 mine = __float2bfloat16_ru(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                row_max[xq][half][r] = mine;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
+                ok = wait_or_abort(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const float top = fmaxf(__bfloat162float(mine), __bfloat162float(row_max[xq][half ^ 1][r]));
                 grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
                 const float m_new = grow ? top : m_ref;
                 alpha = grow ? exp2_approx(m_ref - m_new) : 1.f;
                 m_ref = m_new;
                 shift = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
             }
-            // pass 2: P = 2^arg in bf16 pairs over the first 64 columns of S, 32 keys at a time
-            // (each group of S is read before the P columns that overwrite part of it)
+            // pass 2: P = 2^arg in bf16 pairs, 32 keys at a time (each group of S is read before
+            // the P columns that overwrite part of it)
             uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
-            uint32_t raw[2][32];
-            umma::ld_32x32b_x32(tmem_s, raw[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                wait_ld(raw[c & 1]);
-                if (c < 3) umma::ld_32x32b_x32(tmem_s + (c + 1) * 32, raw[(c + 1) & 1]);
+            for (int c = 0; c < 2; ++c) {
+                uint32_t raw[32];
+                umma::ld_32x32b_x32(tmem_s + c * 32, raw);
+                wait_ld(raw);
                 float x[32];
-                args(raw[c & 1], c, shift, x);
+                args(raw, c, shift, x);
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -638,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     // O holds the tiles before under the old reference; their last PV finished before
                     // this S was committed, so O can be rescaled now
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c = 0; c < D / 64; ++c) {
                         uint32_t o[32];
                         umma::ld_32x32b_x32(tmem_o + c * 32, o);
                         wait_ld(o);
@@ -649,24 +669,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     umma::wait_st();
                 }
             }
-            // keys of this tile that no row of the CTA sees: zero their V rows (thread r: key row r),
-            // by the first query tile that uses the key tile
+            // keys of this tile that no row of the CTA sees: zero their V rows (thread r: 64 columns
+            // of key row r), by the first query tile that uses the key tile
             const int32_t own = P0 + t0a;
-            const bool gaps = !uni.covers(kbase, kbase + kKeys) || (sc.key_start != nullptr && kbase + kKeys > own);
-            if (gaps && (xq == 0 || !used(0, i))) {
-                const int32_t key = kbase + r;
+            const bool gaps = !uni.covers(ktile, ktile + kKeys) || (sc.key_start != nullptr && ktile + kKeys > own);
+            if (gaps && half < kHalves && (xq == 0 || !used(0, i))) {
+                const int32_t key = ktile + r;
                 bool seen = (key >= uni.a0 && key < uni.a1) || (key >= uni.b0 && key < uni.b1);
                 if (seen && sc.key_start != nullptr && key >= own && !(key >= uni.a0 && key < uni.a1))
                     seen = (seen_own[(key - own) >> 5] >> ((key - own) & 31)) & 1u;
                 const int32_t st = i % kVStages;
                 const bool okv = wait_or_abort(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
                 if (okv && !seen) {
-                    uint8_t* sv = smem + L_::v + st * kTile;
+                    uint8_t* sv = smem + L_::v + st * kTile + half * kHalf;
 #pragma unroll
-                    for (int hf = 0; hf < kHalves; ++hf)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<int4*>(sv + hf * kHalf + r * 128u + c * 16u) = make_int4(0, 0, 0, 0);
+                    for (int c = 0; c < 8; ++c) *reinterpret_cast<int4*>(sv + r * 128u + c * 16u) = make_int4(0, 0, 0, 0);
                 }
                 fence_proxy_async_shared();
             }
@@ -675,13 +692,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             if (lane == 0) mbar_arrive(&p_full[xq]);
         }
         if (ok && cnt > 0) ok = wait_or_abort(&o_done[xq], 0, abort_flag, err);
+        // the halves' sums meet in the query tile's shared memory, which no MMA reads any more; every
+        // softmax thread of the tile comes here, aborted or not
+        float* sums = reinterpret_cast<float*>(smem + xq * kTile);
+        __syncwarp();
+        sums[half * kRows + r] = l_sum;
+        named_barrier(1 + xq, 256);
+        l_sum = sums[r] + sums[kRows + r];
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             umma::fence_after_sync();
             const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-            __nv_bfloat16* orow = out + (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D;
+            __nv_bfloat16* orow = out + (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
                 if (cnt > 0) {
                     umma::ld_32x32b_x32(tmem_o + c * 32, o);
