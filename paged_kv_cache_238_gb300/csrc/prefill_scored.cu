@@ -52,6 +52,8 @@ constexpr float kRescaleThreshold = 8.f;  // log2 units: O is rescaled only when
 constexpr int kLptMaxSeqs = 64;           // sequences ordered longest first inside the kernel
 constexpr float kMaxFixedCap = 51.f;      // 1.5 cap log2(e) <= 112
 
+constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between polls
+
 enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kGeneral = 3 };
 
 template <int D>
@@ -151,8 +153,8 @@ __device__ __forceinline__ uint64_t hold2(float x) {
     asm volatile("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
     return d;
 }
-// Columns 2 e, 2 e + 1 of a group of 32 scores.
-__device__ __forceinline__ uint64_t raw_pair(const uint32_t (&r)[32], int e) {
+// Columns 2 e, 2 e + 1 of a group of 16 scores.
+__device__ __forceinline__ uint64_t raw_pair(const uint32_t (&r)[16], int e) {
     return pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
@@ -179,23 +181,64 @@ __device__ __forceinline__ float capped_exact(float s, const TcScore& sc) {
     return sc.cap_l2 - 2.f * sc.cap_l2 * rcp_approx(1.f + exp2_approx(s * sc.two_k));
 }
 
-// tcgen05.wait::ld tied to the registers it makes valid, so that no use of them moves above it.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+// 32 columns of the warp's tensor-memory lanes, and the wait that makes them valid, as one
+// instruction group: nothing can use the registers before the wait.
+__device__ __forceinline__ void ld_wait_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 16 columns; the wait takes the registers too, so that no use of them moves above it.
+__device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void wait_x16(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-    if (mbar_wait_bounded(bar, parity, abort)) return true;
-    if (!*abort) raise_error(err, PA_DEVERR_WAIT_TIMEOUT);
-    *abort = 1;
-    return false;
+__device__ __forceinline__ void sleep_ns(uint32_t ns) { asm volatile("nanosleep.u32 %0;" ::"r"(ns)); }
+__device__ __forceinline__ int32_t read_flag(uint32_t flag) {
+    int32_t v;
+    asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(flag) : "memory");
+    return v;
+}
+// Bounded wait; kSleep > 0: polls are that many ns apart, so that the many warps that wait leave the
+// issue slots to those that compute (the MMA warp, alone on the critical path, polls at once).
+template <uint32_t kSleep>
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint32_t flag, uint32_t* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int k = 0; k < 64; ++k) {
+            if (kSleep > 0) sleep_ns(kSleep);
+            if (mbar_try_wait(bar, parity)) return true;
+        }
+        if (read_flag(flag)) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_error(err, PA_DEVERR_WAIT_TIMEOUT);
+            asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(flag) : "memory");
+            return false;
+        }
+    }
 }
 
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src, bool zero) {
@@ -240,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     uint64_t* idle = q_full + 1;            // every MMA issued has finished
     uint64_t* mx_full = idle + 1;           // [2][4] both halves' maxima of a tile's 32 rows stored
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L_::misc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
+    const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
 
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
@@ -378,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         row_nxt = page_row(32 + lane);
     }
     if (tid == 0) {
-        *abort_flag = 0;
+        *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
         for (int i = 0; i < L_::num_bars; ++i) mbar_init(&bars[i], 1);
         mbar_init(&p_full[0], 8);
         mbar_init(&p_full[1], 8);
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 row_nxt = page_row(32 * ((j >> 2) + 1) + lane);
             }
             bool ok = true;
-            if (use > 0 && lane == 0) ok = wait_or_abort(&empty[st], (use - 1) & 1u, abort_flag, err);
+            if (use > 0 && lane == 0) ok = wait_or_abort<kSleepProducer>(&empty[st], (use - 1) & 1u, abort_flag, err);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             uint8_t* dst = ring + st * kTile;
@@ -460,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             __syncwarp();
         };
         auto wait_k = [&](int32_t j) {
-            const bool ok = wait_or_abort(&k_full[j % kKStages], static_cast<uint32_t>(j / kKStages) & 1u, abort_flag, err);
+            const bool ok = wait_or_abort<0>(&k_full[j % kKStages], static_cast<uint32_t>(j / kKStages) & 1u, abort_flag, err);
             umma::fence_after_sync();
             return ok;
         };
@@ -470,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             last[x] = n_kv - 1;
             while (last[x] >= 0 && !used(x, last[x])) --last[x];
         }
-        bool ok = wait_or_abort(q_full, 0, abort_flag, err);
+        bool ok = wait_or_abort<0>(q_full, 0, abort_flag, err);
         if (ok && n_kv > 0) {
             ok = wait_k(0);
             if (ok) {
@@ -480,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             }
         }
         auto step_pv = [&](int32_t x, int32_t j) {  // P_x written, S_x read: O_x += P_x V(j)
-            ok = wait_or_abort(&p_full[x], done[x] & 1, abort_flag, err);
+            ok = wait_or_abort<0>(&p_full[x], done[x] & 1, abort_flag, err);
             umma::fence_after_sync();
             if (!ok) return;
             pv(x, j, done[x] > 0);
@@ -489,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         };
         for (int32_t j = 0; j < n_kv && ok; ++j) {
             const bool more = j + 1 < n_kv;
-            ok = wait_or_abort(&v_full[j % kVStages], static_cast<uint32_t>(j / kVStages) & 1u, abort_flag, err);
+            ok = wait_or_abort<0>(&v_full[j % kVStages], static_cast<uint32_t>(j / kVStages) & 1u, abort_flag, err);
             if (ok && used(0, j)) step_pv(0, j);
             if (ok && more) ok = wait_k(j + 1);
             if (ok && used(0, j + 1)) qk(0, j + 1);
@@ -518,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         int32_t cnt = 0;  // key tiles this query tile has used
         for (int32_t i = 0; i < n_kv; ++i) {
             if (!used(xq, i)) continue;
-            ok = wait_or_abort(&s_full[xq], cnt & 1, abort_flag, err);
+            ok = wait_or_abort<kSleepSoftmax>(&s_full[xq], cnt & 1, abort_flag, err);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -534,22 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             const bool mask = !__all_sync(0xffffffffu, whole);
             const bool behind = __any_sync(0xffffffffu, row_valid && kbase + kKeys / 2 - 1 > pos);
             const float d0 = static_cast<float>(kbase - pos);
-            // Bits of the 32 keys of group c that the row sees.
+            // Bits of the 16 keys of group c that the row sees.
             auto visible = [&](int c) -> uint32_t {
-                return span_bits(kbase + c * 32, row.a0, row.a1) | span_bits(kbase + c * 32, row.b0, row.b1);
+                return span_bits(kbase + c * 16, row.a0, row.a1) | span_bits(kbase + c * 16, row.b0, row.b1);
             };
             // Weight arguments (log2 domain) of group c: x = score + shift, in pairs. Straight-line
             // code over the group; what differs by warp is branched on once per group.
-            auto args = [&](const uint32_t(&raw)[32], int c, float shift, float(&x)[32]) {
+            auto args = [&](const uint32_t(&raw)[16], int c, float shift, float(&x)[16]) {
                 if constexpr (MODE == kPlain) {
                     const uint64_t add = pack2(shift, shift);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) unpack2(fma2(raw_pair(raw, e), c1, add), x[2 * e], x[2 * e + 1]);
+                    for (int e = 0; e < 8; ++e) unpack2(fma2(raw_pair(raw, e), c1, add), x[2 * e], x[2 * e + 1]);
                 } else if constexpr (MODE == kCap) {
                     const uint64_t add = pack2(shift, shift);
                     float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const uint64_t s = raw_pair(raw, e), w = mul2(s, s);
                         uint64_t p = fma2(w, tq[4], tq[3]);
                         p = fma2(w, p, tq[2]);
@@ -561,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                         big[e & 3] = max3(big[e & 3], w0, w1);
                     }
                     const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-                    if (__any_sync(0xffffffffu, b > sc.s2_max)) {
+                    if (b > sc.s2_max) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = capped_exact(__uint_as_float(raw[k]), sc) + shift;
+                        for (int k = 0; k < 16; ++k) x[k] = capped_exact(__uint_as_float(raw[k]), sc) + shift;
                     }
                 } else if constexpr (MODE == kDistance) {
                     if (!behind) {  // -slope |p - j| = slope (j - p), stepped along the columns
@@ -571,29 +614,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                         const uint64_t step = pack2(8.f * slope, 8.f * slope);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            away[k] = pack2(fmaf(slope, d0 + (c * 32 + 2 * k), shift), fmaf(slope, d0 + (c * 32 + 2 * k + 1), shift));
+                            away[k] = pack2(fmaf(slope, d0 + (c * 16 + 2 * k), shift), fmaf(slope, d0 + (c * 16 + 2 * k + 1), shift));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < 8; ++e) {
                             unpack2(fma2(raw_pair(raw, e), c1, away[e & 3]), x[2 * e], x[2 * e + 1]);
                             away[e & 3] = add2(away[e & 3], step);
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            x[k] = fmaf(__uint_as_float(raw[k]), sc.c1, fmaf(-slope, fabsf(d0 + (c * 32 + k)), shift));
+                        for (int k = 0; k < 16; ++k)
+                            x[k] = fmaf(__uint_as_float(raw[k]), sc.c1, fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift));
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         const float s = __uint_as_float(raw[k]);
                         const float z = sc.capped ? capped_exact(s, sc) : s * sc.c1;
-                        x[k] = fmaf(-slope, fabsf(d0 + (c * 32 + k)), z) + shift;
+                        x[k] = fmaf(-slope, fabsf(d0 + (c * 16 + k)), z) + shift;
                     }
                 }
                 if (mask) {
                     const uint32_t vis = visible(c);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
+                    for (int k = 0; k < 16; ++k)
                         if (!(vis >> k & 1u)) x[k] = -INFINITY;
                 }
             };
@@ -602,15 +645,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             if constexpr (MODE != kCap) {
                 // pass 1: the tile's maximum over visible keys
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t raw[2][16];
+                ld_x16(tmem_s, raw[0]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t raw[32];
-                    umma::ld_32x32b_x32(tmem_s + c * 32, raw);
-                    wait_ld(raw);
-                    float x[32];
-                    args(raw, c, 0.f, x);
+                for (int c = 0; c < 4; ++c) {
+                    wait_x16(raw[c & 1]);
+                    if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
+                    float x[16];
+                    args(raw[c & 1], c, 0.f, x);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
+                    for (int e = 0; e < 8; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
                 // the row's other half of the keys is another thread's: exchange the maxima, rounded
                 // up to bf16 (any reference at or above the maximum serves, if both take the same)
@@ -618,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 row_max[xq][half][r] = mine;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
-                ok = wait_or_abort(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
+                ok = wait_or_abort<kSleepSoftmax>(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -630,24 +674,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 m_ref = m_new;
                 shift = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
             }
-            // pass 2: P = 2^arg in bf16 pairs, 32 keys at a time (each group of S is read before
+            // pass 2: P = 2^arg in bf16 pairs, 16 keys at a time (each group of S is read before
             // the P columns that overwrite part of it)
             uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t raw[2][16];
+            ld_x16(tmem_s, raw[0]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t raw[32];
-                umma::ld_32x32b_x32(tmem_s + c * 32, raw);
-                wait_ld(raw);
-                float x[32];
-                args(raw, c, shift, x);
-                uint32_t pk[16];
+            for (int c = 0; c < 4; ++c) {
+                wait_x16(raw[c & 1]);
+                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
+                float x[16];
+                args(raw[c & 1], c, shift, x);
+                uint32_t pk[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     const float p0 = exp2_approx(x[2 * e]), p1 = exp2_approx(x[2 * e + 1]);
                     psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
                     pk[e] = pack_bf16x2(p0, p1);
                 }
-                umma::st_32x32b_x16(tmem_s + c * 16, pk);
+                umma::st_32x32b_x8(tmem_s + c * 8, pk);
             }
             umma::wait_st();
             float s0, s1;
@@ -660,8 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
                         uint32_t o[32];
-                        umma::ld_32x32b_x32(tmem_o + c * 32, o);
-                        wait_ld(o);
+                        ld_wait_x32(tmem_o + c * 32, o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
                         umma::st_32x32b_x32(tmem_o + c * 32, o);
@@ -679,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 if (seen && sc.key_start != nullptr && key >= own && !(key >= uni.a0 && key < uni.a1))
                     seen = (seen_own[(key - own) >> 5] >> ((key - own) & 31)) & 1u;
                 const int32_t st = i % kVStages;
-                const bool okv = wait_or_abort(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
+                const bool okv = wait_or_abort<kSleepSoftmax>(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
                 if (okv && !seen) {
                     uint8_t* sv = smem + L_::v + st * kTile + half * kHalf;
 #pragma unroll
@@ -691,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[xq]);
         }
-        if (ok && cnt > 0) ok = wait_or_abort(&o_done[xq], 0, abort_flag, err);
+        if (ok && cnt > 0) ok = wait_or_abort<kSleepSoftmax>(&o_done[xq], 0, abort_flag, err);
         // the halves' sums meet in the query tile's shared memory, which no MMA reads any more; every
         // softmax thread of the tile comes here, aborted or not
         float* sums = reinterpret_cast<float*>(smem + xq * kTile);
@@ -708,8 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
                 if (cnt > 0) {
-                    umma::ld_32x32b_x32(tmem_o + c * 32, o);
-                    wait_ld(o);
+                    ld_wait_x32(tmem_o + c * 32, o);
                 }
                 if (row_valid) {
 #pragma unroll
