@@ -65,7 +65,7 @@ struct Smem {
     static constexpr uint32_t k = q + 2 * tile;
     static constexpr uint32_t v = k + k_stages * tile;
     static constexpr uint32_t bars = v + v_stages * tile;
-    static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 16;
+    static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 20;
     static constexpr uint32_t misc = bars + num_bars * 8;  // tmem base, abort flag
     static constexpr uint32_t total = misc + 16 + 1024;
 };
@@ -73,9 +73,6 @@ struct Smem {
 // Keys that some valid row of one query tile sees: the two spans' unions.
 struct SpanUnion {
     int32_t a0, a1, b0, b1;
-    __device__ __forceinline__ bool touches(int32_t lo, int32_t hi) const {
-        return (a0 < a1 && a0 < hi && a1 > lo) || (b0 < b1 && b0 < hi && b1 > lo);
-    }
     __device__ __forceinline__ bool covers(int32_t lo, int32_t hi) const {
         return (lo >= a0 && hi <= a1) || (lo >= b0 && hi <= b1);
     }
@@ -85,11 +82,14 @@ struct SpanUnion {
 struct TileList {
     int32_t first_a, n_a, first_b, n;
     __device__ __forceinline__ int32_t tile(int32_t i) const { return i < n_a ? first_a + i : first_b + (i - n_a); }
+    __device__ __forceinline__ int32_t position(int32_t t) const {
+        return t < first_a + n_a ? t - first_a : n_a + (t - first_b);
+    }
 };
 
 __device__ __forceinline__ TileList tile_list(const SpanUnion& u) {
     TileList l;
-    l.first_a = u.a0 / kKeys;
+    l.first_a = u.a0 < u.a1 ? u.a0 / kKeys : 0;
     l.n_a = u.a0 < u.a1 ? (u.a1 + kKeys - 1) / kKeys - l.first_a : 0;
     l.first_b = u.b0 / kKeys;
     if (l.n_a > 0) l.first_b = max(l.first_b, l.first_a + l.n_a);
@@ -269,6 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
     constexpr int kHalves = D / 64;
+    // Chains of S -> softmax -> P -> PV -> next S that run independently of one another: one per query
+    // tile, or, when no maximum ties the keys of a row together, one per query tile and half of the
+    // key tile (chain c: query tile c & 1, half c >> 1), so that more MMA and softmax work overlaps.
+    constexpr bool kSplit = MODE == kCap;
+    constexpr int kChains = kSplit ? 4 : 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::bars);
@@ -276,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     uint64_t* k_empty = k_full + kKStages;  // [kKStages] the QKs that read the stage are done
     uint64_t* v_full = k_empty + kKStages;  // [kVStages]
     uint64_t* v_empty = v_full + kVStages;  // [kVStages] the PVs that read the stage are done
-    uint64_t* s_full = v_empty + kVStages;  // [2] S of tile a / b written
-    uint64_t* p_full = s_full + 2;          // [2] P of tile a / b written (8 warps)
-    uint64_t* o_done = p_full + 2;          // [2] last PV of tile a / b finished
+    uint64_t* s_full = v_empty + kVStages;  // [kChains] S of the chain written
+    uint64_t* p_full = s_full + 4;          // [kChains] its P written (each softmax warp of the chain)
+    uint64_t* o_done = p_full + 4;          // [2] last PV of tile a / b finished
     uint64_t* q_full = o_done + 2;          // query tiles in shared memory
     uint64_t* idle = q_full + 1;            // every MMA issued has finished
     uint64_t* mx_full = idle + 1;           // [2][4] both halves' maxima of a tile's 32 rows stored
@@ -375,10 +380,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const SpanUnion uni = join(ux[0], ux[1]);
     const TileList tiles = tile_list(uni);
     const int32_t n_kv = tiles.n;
+    // list positions whose key tile query tile x uses: two ranges
+    int32_t ra0[2], ra_n[2], rb0[2], rb_n[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        ra0[x] = ux[x].a0 / kKeys - tiles.first_a;
+        ra_n[x] = ux[x].a0 < ux[x].a1 ? (ux[x].a1 - 1) / kKeys - tiles.first_a + 1 - ra0[x] : 0;
+        rb0[x] = tiles.position(ux[x].b0 / kKeys);
+        rb_n[x] = ux[x].b0 < ux[x].b1 ? tiles.position((ux[x].b1 - 1) / kKeys) + 1 - rb0[x] : 0;
+    }
     auto used = [&](int32_t x, int32_t i) -> bool {
-        if (i >= n_kv) return false;
-        const int32_t lo = tiles.tile(i) * kKeys;
-        return ux[x].touches(lo, lo + kKeys);
+        return static_cast<uint32_t>(i - ra0[x]) < static_cast<uint32_t>(ra_n[x]) ||
+               static_cast<uint32_t>(i - rb0[x]) < static_cast<uint32_t>(rb_n[x]);
     };
     const int32_t npages = (L + kPageTokens - 1) / kPageTokens;
 
@@ -423,8 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     if (tid == 0) {
         *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
         for (int i = 0; i < L_::num_bars; ++i) mbar_init(&bars[i], 1);
-        mbar_init(&p_full[0], 8);
-        mbar_init(&p_full[1], 8);
+        for (int i = 0; i < kChains; ++i) mbar_init(&p_full[i], kSoftWarps / kChains);
         for (int i = 0; i < 8; ++i) mbar_init(&mx_full[i], 2);
         mbar_init(q_full, kSoftThreads);
         fence_mbarrier_init();
@@ -474,78 +486,83 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             if (lane < 8 * kHalves)  // lane = (column half, page)
                 tma_load_2d(dst + (lane >> 3) * kHalf + (lane & 7) * 2048u, tm, (lane >> 3) * 64, rk, &full[st]);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp && umma::elect_one()) {
         // ======================================= MMA issuer =====================================
-        const bool leader = umma::elect_one();
-        const uint32_t idesc_qk = umma::idesc_bf16_f32(128, 128, 0, 0);  // Q, K both K-major
-        const uint32_t idesc_pv = umma::idesc_bf16_f32(128, D, 0, 1);    // P (TMEM), V MN-major
+        // One thread issues every MMA (a commit tracks those of its own thread) and does all the waiting.
+        constexpr int kChainKeys = kSplit ? 64 : 128;
+        const uint32_t idesc_qk = umma::idesc_bf16_f32(128, kChainKeys, 0, 0);  // Q, K both K-major
+        const uint32_t idesc_pv = umma::idesc_bf16_f32(128, D, 0, 1);           // P (TMEM), V MN-major
         const uint64_t dq0 = umma::smem_desc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t dk0 = umma::smem_desc_sw128(smem_u32(smem + L_::k), 16, 1024);
         const uint64_t dv0 = umma::smem_desc_sw128(smem_u32(smem + L_::v), kHalf, 1024);
-        auto qk = [&](int32_t x, int32_t j) {
+        auto qk = [&](int c, int32_t j) {
+            const int x = c & 1, hf = c >> 1;
             const uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4);
-            const uint64_t dk = dk0 + static_cast<uint64_t>(j % kKStages) * (kTile >> 4);
+            const uint64_t dk = dk0 + static_cast<uint64_t>(j % kKStages) * (kTile >> 4) + hf * (64 * 128 >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                if (leader) umma::mma_bf16(tmem + x * 128, dq + off, dk + off, idesc_qk, ks > 0);
+                umma::mma_bf16(tmem + x * 128 + hf * 64, dq + off, dk + off, idesc_qk, ks > 0);
             }
-            if (leader) umma::commit(&s_full[x]);
-            __syncwarp();
+            umma::commit(&s_full[c]);
         };
-        auto pv = [&](int32_t x, int32_t j, bool acc) {
+        auto pv = [&](int c, int32_t j, bool acc) {
+            const int x = c & 1, hf = c >> 1;
             const uint64_t dv = dv0 + static_cast<uint64_t>(j % kVStages) * (kTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 keys per instruction: 8 P columns
-                if (leader)
-                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                                          dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || kk > 0));
-            __syncwarp();
+            for (int k = 0; k < kChainKeys / 16; ++k) {  // 16 keys per instruction: 8 P columns
+                const int kk = hf * 4 + k;
+                umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                      dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || k > 0));
+            }
         };
         auto wait_k = [&](int32_t j) {
             const bool ok = wait_or_abort<0>(&k_full[j % kKStages], static_cast<uint32_t>(j / kKStages) & 1u, abort_flag, err);
             umma::fence_after_sync();
             return ok;
         };
-        int32_t last[2], done[2] = {0, 0};  // last list position and PVs issued, per query tile
+        int32_t last[2], done[2] = {0, 0};  // last list position, and positions finished, per query tile
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             last[x] = n_kv - 1;
             while (last[x] >= 0 && !used(x, last[x])) --last[x];
         }
         bool ok = wait_or_abort<0>(q_full, 0, abort_flag, err);
+        if (ok && n_kv > 0) ok = wait_k(0);
         if (ok && n_kv > 0) {
-            ok = wait_k(0);
-            if (ok) {
-                if (used(0, 0)) qk(0, 0);
-                if (used(1, 0)) qk(1, 0);
-                if (leader) umma::commit(&k_empty[0]);
-            }
+#pragma unroll
+            for (int c = 0; c < kChains; ++c)
+                if (used(c & 1, 0)) qk(c, 0);
+            umma::commit(&k_empty[0]);
         }
-        auto step_pv = [&](int32_t x, int32_t j) {  // P_x written, S_x read: O_x += P_x V(j)
-            ok = wait_or_abort<0>(&p_full[x], done[x] & 1, abort_flag, err);
-            umma::fence_after_sync();
-            if (!ok) return;
-            pv(x, j, done[x] > 0);
-            ++done[x];
-            if (j == last[x] && leader) umma::commit(&o_done[x]);
-        };
         for (int32_t j = 0; j < n_kv && ok; ++j) {
             const bool more = j + 1 < n_kv;
             ok = wait_or_abort<0>(&v_full[j % kVStages], static_cast<uint32_t>(j / kVStages) & 1u, abort_flag, err);
-            if (ok && used(0, j)) step_pv(0, j);
-            if (ok && more) ok = wait_k(j + 1);
-            if (ok && used(0, j + 1)) qk(0, j + 1);
-            if (ok && used(1, j)) step_pv(1, j);
-            if (ok && leader) umma::commit(&v_empty[j % kVStages]);
-            if (ok && used(1, j + 1)) qk(1, j + 1);
-            if (ok && more && leader) umma::commit(&k_empty[(j + 1) % kKStages]);
-            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < kChains; ++c) {
+                const int x = c & 1;
+                if (ok && used(x, j)) {  // P written, S read: O_x += P V(j)
+                    ok = wait_or_abort<0>(&p_full[c], done[x] & 1, abort_flag, err);
+                    umma::fence_after_sync();
+                    if (ok) {
+                        pv(c, j, done[x] > 0 || c >= 2);
+                        if (c >= kChains - 2) {  // the query tile's last chain
+                            ++done[x];
+                            if (j == last[x]) umma::commit(&o_done[x]);
+                        }
+                    }
+                }
+                if (c == kChains - 1 && ok) umma::commit(&v_empty[j % kVStages]);
+                if (c == 0 && ok && more) ok = wait_k(j + 1);
+                if (ok && used(x, j + 1)) qk(c, j + 1);
+            }
+            if (ok && more) umma::commit(&k_empty[(j + 1) % kKStages]);
         }
-        if (leader) umma::commit(idle);  // arrives once every MMA issued above has finished
-        __syncwarp();
+        umma::commit(idle);  // arrives once every MMA issued above has finished
+        mbar_wait_timeout(idle, 0);
     } else if (softmax_warp) {
         // ==================================== scores and softmax ================================
+        const int32_t chain = kSplit ? half * 2 + xq : xq;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + xq * 128 + half * 64 + lane_off;
         const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (D / 2) + lane_off;
@@ -556,12 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         uint64_t tq[5];  // the polynomial's coefficients, kept in registers
 #pragma unroll
         for (int k = 0; k < 5; ++k) tq[k] = hold2(sc.q[k]);
+        const uint64_t step = pack2(8.f * slope, 8.f * slope);
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         int32_t cnt = 0;  // key tiles this query tile has used
         for (int32_t i = 0; i < n_kv; ++i) {
             if (!used(xq, i)) continue;
-            ok = wait_or_abort<kSleepSoftmax>(&s_full[xq], cnt & 1, abort_flag, err);
+            ok = wait_or_abort<kSleepSoftmax>(&s_full[chain], cnt & 1, abort_flag, err);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -583,61 +601,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             };
             // Weight arguments (log2 domain) of group c: x = score + shift, in pairs. Straight-line
             // code over the group; what differs by warp is branched on once per group.
-            auto args = [&](const uint32_t(&raw)[16], int c, float shift, float(&x)[16]) {
+            // Weight arguments (log2 domain), x = score + shift. A group of 16 keys is straight-line
+            // code: begin_group sets up what its pairs share, pair_args does columns 2 e, 2 e + 1; what
+            // differs by warp is branched on once per group (amend).
+            float big[4];
+            uint64_t away[4];
+            auto begin_group = [&](int c, float shift) {
+                if constexpr (MODE == kCap) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) big[k] = 0.f;
+                } else if constexpr (MODE == kDistance) {  // -slope |p - j| = slope (j - p) for j <= p
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        away[k] = pack2(fmaf(slope, d0 + (c * 16 + 2 * k), shift), fmaf(slope, d0 + (c * 16 + 2 * k + 1), shift));
+                }
+            };
+            auto pair_args = [&](uint64_t s, int c, int e, float shift, float& x0, float& x1) {
                 if constexpr (MODE == kPlain) {
-                    const uint64_t add = pack2(shift, shift);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) unpack2(fma2(raw_pair(raw, e), c1, add), x[2 * e], x[2 * e + 1]);
+                    unpack2(fma2(s, c1, pack2(shift, shift)), x0, x1);
                 } else if constexpr (MODE == kCap) {
-                    const uint64_t add = pack2(shift, shift);
-                    float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint64_t s = raw_pair(raw, e), w = mul2(s, s);
-                        uint64_t p = fma2(w, tq[4], tq[3]);
-                        p = fma2(w, p, tq[2]);
-                        p = fma2(w, p, tq[1]);
-                        p = fma2(w, p, tq[0]);
-                        unpack2(fma2(s, p, add), x[2 * e], x[2 * e + 1]);
-                        float w0, w1;
-                        unpack2(w, w0, w1);
-                        big[e & 3] = max3(big[e & 3], w0, w1);
-                    }
-                    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-                    if (b > sc.s2_max) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = capped_exact(__uint_as_float(raw[k]), sc) + shift;
-                    }
+                    const uint64_t w = mul2(s, s);
+                    uint64_t p = fma2(w, tq[4], tq[3]);
+                    p = fma2(w, p, tq[2]);
+                    p = fma2(w, p, tq[1]);
+                    p = fma2(w, p, tq[0]);
+                    unpack2(fma2(s, p, pack2(shift, shift)), x0, x1);
+                    float w0, w1;
+                    unpack2(w, w0, w1);
+                    big[e & 3] = max3(big[e & 3], w0, w1);
                 } else if constexpr (MODE == kDistance) {
-                    if (!behind) {  // -slope |p - j| = slope (j - p), stepped along the columns
-                        uint64_t away[4];
-                        const uint64_t step = pack2(8.f * slope, 8.f * slope);
+                    unpack2(fma2(s, c1, away[e & 3]), x0, x1);
+                    if (e < 4) away[e & 3] = add2(away[e & 3], step);
+                } else {
+                    float s0, s1;
+                    unpack2(s, s0, s1);
+                    s0 = sc.capped ? capped_exact(s0, sc) : s0 * sc.c1;
+                    s1 = sc.capped ? capped_exact(s1, sc) : s1 * sc.c1;
+                    x0 = fmaf(-slope, fabsf(d0 + (c * 16 + 2 * e)), s0) + shift;
+                    x1 = fmaf(-slope, fabsf(d0 + (c * 16 + 2 * e + 1)), s1) + shift;
+                }
+            };
+            // Scores beyond the polynomial's range, keys behind the row, masked keys.
+            auto amend = [&](const uint32_t(&raw)[16], int c, float shift, float(&x)[16]) {
+                bool redo = false;
+                if constexpr (MODE == kCap) redo = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) > sc.s2_max;
+                if constexpr (MODE == kDistance) redo = behind;
+                if (redo || mask) {
+                    if (redo) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            away[k] = pack2(fmaf(slope, d0 + (c * 16 + 2 * k), shift), fmaf(slope, d0 + (c * 16 + 2 * k + 1), shift));
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            unpack2(fma2(raw_pair(raw, e), c1, away[e & 3]), x[2 * e], x[2 * e + 1]);
-                            away[e & 3] = add2(away[e & 3], step);
+                        for (int k = 0; k < 16; ++k) {
+                            const float s = __uint_as_float(raw[k]);
+                            if constexpr (MODE == kCap) x[k] = capped_exact(s, sc) + shift;
+                            if constexpr (MODE == kDistance)
+                                x[k] = fmaf(s, sc.c1, fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift));
                         }
-                    } else {
+                    }
+                    if (mask) {
+                        const uint32_t vis = visible(c);
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
-                            x[k] = fmaf(__uint_as_float(raw[k]), sc.c1, fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift));
+                            if (!(vis >> k & 1u)) x[k] = -INFINITY;
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float s = __uint_as_float(raw[k]);
-                        const float z = sc.capped ? capped_exact(s, sc) : s * sc.c1;
-                        x[k] = fmaf(-slope, fabsf(d0 + (c * 16 + k)), z) + shift;
-                    }
-                }
-                if (mask) {
-                    const uint32_t vis = visible(c);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (!(vis >> k & 1u)) x[k] = -INFINITY;
                 }
             };
             float alpha = 1.f, shift = -sc.ref;
@@ -652,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     wait_x16(raw[c & 1]);
                     if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
                     float x[16];
-                    args(raw[c & 1], c, 0.f, x);
+                    begin_group(c, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pair_args(raw_pair(raw[c & 1], e), c, e, 0.f, x[2 * e], x[2 * e + 1]);
+                    amend(raw[c & 1], c, 0.f, x);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
@@ -674,30 +701,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 m_ref = m_new;
                 shift = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
             }
-            // pass 2: P = 2^arg in bf16 pairs, 16 keys at a time (each group of S is read before
-            // the P columns that overwrite part of it)
-            uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
-            uint32_t raw[2][16];
-            ld_x16(tmem_s, raw[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                wait_x16(raw[c & 1]);
-                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
-                float x[16];
-                args(raw[c & 1], c, shift, x);
-                uint32_t pk[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float p0 = exp2_approx(x[2 * e]), p1 = exp2_approx(x[2 * e + 1]);
-                    psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
-                    pk[e] = pack_bf16x2(p0, p1);
-                }
-                umma::st_32x32b_x8(tmem_s + c * 8, pk);
-            }
-            umma::wait_st();
-            float s0, s1;
-            unpack2(add2(add2(psum[0], psum[1]), add2(psum[2], psum[3])), s0, s1);
-            l_sum = l_sum * alpha + (s0 + s1);
             if constexpr (MODE != kCap) {
                 if (!first && __any_sync(0xffffffffu, grow)) {
                     // O holds the tiles before under the old reference; their last PV finished before
@@ -713,27 +716,66 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     umma::wait_st();
                 }
             }
-            // keys of this tile that no row of the CTA sees: zero their V rows (thread r: 64 columns
-            // of key row r), by the first query tile that uses the key tile
+            // keys that no row of the CTA sees: zero their V rows, in the chain's part of the key tile, by
+            // the first query tile that uses it (thread r: 64 columns of one key row)
             const int32_t own = P0 + t0a;
             const bool gaps = !uni.covers(ktile, ktile + kKeys) || (sc.key_start != nullptr && ktile + kKeys > own);
-            if (gaps && half < kHalves && (xq == 0 || !used(0, i))) {
-                const int32_t key = ktile + r;
+            const int32_t zrow = kSplit ? half * 64 + (r & 63) : r, zhalf = kSplit ? r >> 6 : half;
+            if (gaps && (xq == 0 || !used(0, i))) {
+                const int32_t key = ktile + zrow;
                 bool seen = (key >= uni.a0 && key < uni.a1) || (key >= uni.b0 && key < uni.b1);
                 if (seen && sc.key_start != nullptr && key >= own && !(key >= uni.a0 && key < uni.a1))
                     seen = (seen_own[(key - own) >> 5] >> ((key - own) & 31)) & 1u;
                 const int32_t st = i % kVStages;
                 const bool okv = wait_or_abort<kSleepSoftmax>(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
-                if (okv && !seen) {
-                    uint8_t* sv = smem + L_::v + st * kTile + half * kHalf;
+                if (okv && !seen && zhalf < kHalves) {
+                    uint8_t* sv = smem + L_::v + st * kTile + zhalf * kHalf;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) *reinterpret_cast<int4*>(sv + r * 128u + c * 16u) = make_int4(0, 0, 0, 0);
+                    for (int c = 0; c < 8; ++c) *reinterpret_cast<int4*>(sv + zrow * 128u + c * 16u) = make_int4(0, 0, 0, 0);
                 }
                 fence_proxy_async_shared();
             }
+            // pass 2: P = 2^arg in bf16 pairs, 16 keys at a time (each group of S is read before
+            // the P columns that overwrite part of it)
+            uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
+            // One group ahead: the arithmetic of group c + 1 (FMA pipes) shares a block of code with
+            // the exponentials of group c (MUFU), so that the two overlap within each warp.
+            uint32_t raw[2][16];
+            float x[2][16];
+            ld_x16(tmem_s, raw[0]);
+            wait_x16(raw[0]);
+            ld_x16(tmem_s + 16, raw[1]);
+            begin_group(0, shift);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pair_args(raw_pair(raw[0], e), 0, e, shift, x[0][2 * e], x[0][2 * e + 1]);
+            amend(raw[0], 0, shift, x[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c < 3) {
+                    wait_x16(raw[(c + 1) & 1]);
+                    if (c < 2) ld_x16(tmem_s + (c + 2) * 16, raw[c & 1]);
+                    begin_group(c + 1, shift);
+                }
+                uint32_t pk[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (c < 3)
+                        pair_args(raw_pair(raw[(c + 1) & 1], e), c + 1, e, shift, x[(c + 1) & 1][2 * e],
+                                  x[(c + 1) & 1][2 * e + 1]);
+                    const float p0 = exp2_approx(x[c & 1][2 * e]), p1 = exp2_approx(x[c & 1][2 * e + 1]);
+                    psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
+                    pk[e] = pack_bf16x2(p0, p1);
+                }
+                umma::st_32x32b_x8(tmem_s + c * 8, pk);
+                if (c < 3) amend(raw[(c + 1) & 1], c + 1, shift, x[(c + 1) & 1]);
+            }
+            umma::wait_st();
             umma::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[xq]);
+            if (lane == 0) mbar_arrive(&p_full[chain]);
+            float s0, s1;
+            unpack2(add2(add2(psum[0], psum[1]), add2(psum[2], psum[3])), s0, s1);
+            l_sum = l_sum * alpha + (s0 + s1);
         }
         if (ok && cnt > 0) ok = wait_or_abort<kSleepSoftmax>(&o_done[xq], 0, abort_flag, err);
         // the halves' sums meet in the query tile's shared memory, which no MMA reads any more; every
@@ -776,7 +818,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         for (int32_t j = max(0, last_j - nst + 1); j <= last_j; ++j)
             mbar_wait_timeout(&full[j % nst], static_cast<uint32_t>(j / nst) & 1u);
     }
-    if (warp == kMmaWarp && lane == 0) mbar_wait_timeout(idle, 0);
     umma::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {
