@@ -22,7 +22,7 @@
 // A capped score lies in [-cap, cap], so the weights 2^(arg - ref) against the fixed reference
 // ref = cap log2(e) / 2 lie in [2^-112, 2^37] for caps up to kMaxFixedCap: no running maximum, no
 // second pass over S and no rescaling of O are needed. tanh is the odd polynomial x Q(x^2) of degree
-// 9, fitted to tanh on |x| <= 0.8 by Remez's minimax method (absolute error 2^-21.5, that times cap
+// 7, fitted to tanh on |x| <= 0.6 by Remez's minimax method (absolute error 2^-20.7, that times cap
 // in the score, below the 2^-9 of the bf16 weights), evaluated on the FMA pipes two elements an
 // instruction; a warp whose 32 scores of a row block hold a larger one takes
 // tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block, exact at every x.
@@ -114,7 +114,7 @@ __device__ __forceinline__ SpanUnion join(const SpanUnion& x, const SpanUnion& y
 // Score constants, log2 domain.
 struct TcScore {
     float c1;       // scale log2 e
-    float q[5];     // s Q(s^2) = cap log2(e) tanh(s scale / cap), coefficients of s, s^3, ..
+    float q[4];     // s Q(s^2) = cap log2(e) tanh(s scale / cap), coefficients of s, s^3, ..
     float s2_max;   // s^2 up to which the polynomial holds
     float two_k;    // 2 log2(e) scale / cap
     float cap_l2;   // cap log2 e
@@ -147,11 +147,11 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
     return d;
 }
-// The pair (x, x), opaque to the compiler so that it stays in registers.
+// The pair (x, x) of a value that every lane holds, through a shuffle: the compiler then keeps it in
+// vector registers instead of moving it out of uniform ones for every group of keys.
 __device__ __forceinline__ uint64_t hold2(float x) {
-    uint64_t d;
-    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
-    return d;
+    const float v = __shfl_sync(0xffffffffu, x, 0);
+    return pack2(v, v);
 }
 // Columns 2 e, 2 e + 1 of a group of 16 scores.
 __device__ __forceinline__ uint64_t raw_pair(const uint32_t (&r)[16], int e) {
@@ -569,10 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         const float slope = (MODE == kDistance || MODE == kGeneral) && sc.slopes && row_valid
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
-        const uint64_t c1 = pack2(sc.c1, sc.c1);
-        uint64_t tq[5];  // the polynomial's coefficients, kept in registers
+        const uint64_t c1 = hold2(sc.c1);
+        const uint64_t ref2 = hold2(-sc.ref);
+        uint64_t tq[4];  // the polynomial's coefficients, kept in registers
 #pragma unroll
-        for (int k = 0; k < 5; ++k) tq[k] = hold2(sc.q[k]);
+        for (int k = 0; k < 4; ++k) tq[k] = hold2(sc.q[k]);
         const uint64_t step = pack2(8.f * slope, 8.f * slope);
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
@@ -621,11 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     unpack2(fma2(s, c1, pack2(shift, shift)), x0, x1);
                 } else if constexpr (MODE == kCap) {
                     const uint64_t w = mul2(s, s);
-                    uint64_t p = fma2(w, tq[4], tq[3]);
-                    p = fma2(w, p, tq[2]);
+                    uint64_t p = fma2(w, tq[3], tq[2]);
                     p = fma2(w, p, tq[1]);
                     p = fma2(w, p, tq[0]);
-                    unpack2(fma2(s, p, pack2(shift, shift)), x0, x1);
+                    unpack2(fma2(s, p, ref2), x0, x1);
                     float w0, w1;
                     unpack2(w, w0, w1);
                     big[e & 3] = max3(big[e & 3], w0, w1);
@@ -826,10 +826,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     }
 }
 
-// Minimax (Remez) coefficients of tanh x = x (t0 + t1 x^2 + .. + t4 x^8) on |x| <= 0.8; absolute
-// error 3.5e-7.
-constexpr double kTanh[5] = {0.999995135, -0.333174266, 0.131862196, -0.0482613134, 0.0114646536};
-constexpr float kTanhRange = 0.8f;
+// Minimax (Remez) coefficients of tanh x = x (t0 + t1 x^2 + t2 x^4 + t3 x^6) on |x| <= 0.6; absolute
+// error 5.9e-7.
+constexpr double kTanh[4] = {0.999991018, -0.332989742, 0.129745541, -0.0396112775};
+constexpr float kTanhRange = 0.6f;
 
 template <int D, int MODE>
 cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t stream) {
@@ -877,7 +877,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
     if (sc.capped) {
         const double k = static_cast<double>(a.scale) / s.cap;
         double c = static_cast<double>(s.cap) * 1.4426950408889634 * k;
-        for (int i = 0; i < 5; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
+        for (int i = 0; i < 4; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
         sc.s2_max = static_cast<float>(kTanhRange * kTanhRange / (k * k));
         sc.two_k = static_cast<float>(2 * 1.4426950408889634 * k);
         sc.cap_l2 = s.cap * kLog2e;
