@@ -551,6 +551,10 @@ PA_API size_t pa_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_he
         return 0;
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return 0;
+    DecodeScoredPlan plan;
+    if (dtype == PA_BF16 &&
+        plan_decode_scored(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &plan))
+        return plan.workspace_bytes;
     return plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
         .workspace_bytes;
 }
@@ -572,13 +576,19 @@ PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache,
     if (st != PA_OK || num_seqs == 0) return st;
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    a.err = dev->err;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DecodeScoredPlan fast;
+    if (dtype == PA_BF16 &&
+        plan_decode_scored(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &fast)) {
+        if (!workspace || workspace_bytes < fast.workspace_bytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+        return launch_decode_scored(a, sa, fast, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     const ScoredSimtPlan plan =
         plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
-    a.err = dev->err;
-    return launch_scored_decode_simt(a, sa, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                                     : PA_ERR_CUDA;
+    return launch_scored_decode_simt(a, sa, plan, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API size_t pa_prefill_scored_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,

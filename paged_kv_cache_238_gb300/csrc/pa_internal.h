@@ -211,6 +211,22 @@ struct ScoreArgs {
     const int32_t* prefix_len;
 };
 
+// The scored calls' workspace begins with this many counters of segments (sequence, kv head, head
+// chunk) whatever the shape, zero between calls: calls of any shapes share a workspace one after
+// another. Partial results follow.
+constexpr int32_t kScoredSegments = 16384;
+constexpr size_t kScoredCounterBytes = kScoredSegments * sizeof(int32_t);
+
+// bf16 decode (decode_scored.cu): batches of sequences, one launch each.
+struct DecodeScoredPlan {
+    int32_t batch, num_ctas, warps, stages;
+    size_t workspace_bytes;
+};
+bool plan_decode_scored(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t max_seq_len, const DeviceInfo& dev, DecodeScoredPlan* plan);
+cudaError_t launch_decode_scored(const DecodeArgs& a, const ScoreArgs& score, const DecodeScoredPlan& plan,
+                                 cudaStream_t stream);
+
 // CUDA-core path (scored_simt.cu): a decode row's visible pages in num_parts partitions of up to
 // part_pages.
 struct ScoredSimtPlan {

@@ -214,6 +214,13 @@ __device__ __forceinline__ void wait_x16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
 __device__ __forceinline__ void sleep_ns(uint32_t ns) { asm volatile("nanosleep.u32 %0;" ::"r"(ns)); }
 __device__ __forceinline__ int32_t read_flag(uint32_t flag) {
     int32_t v;
@@ -766,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
                     pk[e] = pack_bf16x2(p0, p1);
                 }
-                umma::st_32x32b_x8(tmem_s + c * 8, pk);
+                st_x8(tmem_s + c * 8, pk);
                 if (c < 3) amend(raw[(c + 1) & 1], c + 1, shift, x[(c + 1) & 1]);
             }
             umma::wait_st();

@@ -243,7 +243,7 @@ cudaError_t launch_decode_impl(const DecodeArgs& d, const ScoreArgs& score, cons
     a.head_chunks = (d.num_q_heads / d.num_kv_heads + kHeads - 1) / kHeads;
     a.scale = d.scale;
     a.score = score;
-    a.ws_o = static_cast<float*>(d.workspace);
+    a.ws_o = reinterpret_cast<float*>(static_cast<char*>(d.workspace) + kScoredCounterBytes);
     a.ws_ml = a.ws_o + static_cast<size_t>(d.num_seqs) * d.num_q_heads * plan.num_parts * D;
     a.err = d.err;
     const dim3 grid(d.num_seqs, d.num_kv_heads * a.head_chunks, plan.num_parts);
@@ -297,7 +297,9 @@ ScoredSimtPlan plan_scored_simt(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, i
     p.part_pages = static_cast<int32_t>((pages + parts - 1) / parts);
     p.num_parts = (pages + p.part_pages - 1) / p.part_pages;
     p.workspace_bytes =
-        p.num_parts > 1 ? static_cast<size_t>(S) * Hq * p.num_parts * (D + 2) * sizeof(float) : 0;
+        p.num_parts > 1
+            ? kScoredCounterBytes + static_cast<size_t>(S) * Hq * p.num_parts * (D + 2) * sizeof(float)
+            : 0;
     return p;
 }
 
