@@ -33,22 +33,28 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSeqs = 1024;  // sequences of one launch: their spans live in shared memory
 constexpr int kMaxHeads = 16;   // q heads of one segment
+constexpr int kMinSlice = 8;    // pages of a CTA's slice at least
+
+// Pages of one step of a warp: 8 KB of K and V, so that what a step costs besides its pages
+// (waits, reductions, the list) weighs alike at both head dims.
+__host__ __device__ constexpr int step_pages(int D) { return 128 / D; }
 
 __host__ __device__ inline uint32_t up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
-    uint32_t stage, ring, piece0, piece_ml, meta, bars, flags, prefix, spans, total;
+    uint32_t stage, ring, piece0, piece_ml, weight, meta, bars, flags, prefix, spans, total;
 };
 // NW warps, nst stages, hs q heads per segment, S sequences.
 __host__ __device__ inline Layout layout(int NW, int nst, int hs, int D, int S) {
     Layout l;
     uint32_t o = 0;
-    l.stage = up(2u * kPageTokens * D * 2u + static_cast<uint32_t>(hs) * D * 2u, 1024u);  // K, V, query rows
+    l.stage = up(2u * kPageTokens * D * 2u * step_pages(D) + static_cast<uint32_t>(hs) * D * 2u, 1024u);  // pages, query rows
     l.ring = o;      o += static_cast<uint32_t>(NW) * nst * l.stage;
     l.piece0 = o;    o += static_cast<uint32_t>(NW) * hs * D * 4u;       // each warp's first piece
     l.piece_ml = o;  o += static_cast<uint32_t>(NW) * 2u * hs * 8u;      // (max, sum) of both pieces
-    l.meta = o;      o += up(static_cast<uint32_t>(NW) * 2u * 4u, 16u);  // segment of each piece
-    l.bars = o;      o += static_cast<uint32_t>(NW) * nst * 8u;
+    l.weight = o;    o += static_cast<uint32_t>(NW) * 2u * hs * 12u;     // the pieces' weights, and (max, sum) of their run
+    l.meta = up(o, 16u);  o = l.meta + static_cast<uint32_t>(NW) * 2u * 16u;  // segment of each piece
+    l.bars = up(o, 16u);  o = l.bars + static_cast<uint32_t>(NW) * nst * 8u;
     l.flags = o;     o += 32u;
     l.prefix = up(o, 16u);  o = l.prefix + up((S + 1) * 4u, 16u);
     l.spans = o;     o += static_cast<uint32_t>(S) * 16u;
@@ -119,8 +125,10 @@ struct Cursor {
         h = r / np;
         j = r - h * np;
     }
-    __device__ __forceinline__ void advance(const int32_t* prefix, const int4* spans, int32_t S, int32_t nh) {
-        if (++j < np) return;
+    __device__ __forceinline__ void advance(int32_t pages, const int32_t* prefix, const int4* spans, int32_t S,
+                                            int32_t nh) {
+        j += pages;
+        if (j < np) return;
         j = 0;
         if (++h < nh) return;
         h = 0;
@@ -129,39 +137,10 @@ struct Cursor {
     }
 };
 
-// First unit of slice c of C over U units, and the slice that holds unit u.
-__device__ __forceinline__ int32_t slice_start(int64_t U, int64_t C, int64_t c) { return static_cast<int32_t>(c * U / C); }
-__device__ __forceinline__ int32_t slice_owner(int64_t U, int64_t C, int64_t u) {
-    return static_cast<int32_t>(((u + 1) * C + U - 1) / U - 1);
-}
-
-// Joins n pieces of one head, E = 4 consecutive head_dim elements: ml(i) gives piece i's (max, sum),
-// o(i) its elements; `scaled` pieces hold sum-weighted (unnormalised) outputs. Returns the joined
-// (max, sum) and normalised elements.
-template <bool kNormalised, typename Ml, typename O>
-__device__ __forceinline__ float2 join_pieces(int32_t n, Ml ml, O o, float4& r) {
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int32_t i = 0; i < n; ++i) M = fmaxf(M, ml(i).x);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float den = 0.f;
-    r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int32_t i = 0; i < n; ++i) {
-        const float2 p = ml(i);
-        const float e = exp2_approx(p.x - ref);
-        const float w = kNormalised ? e * p.y : e;
-        const float4 v = o(i);
-        den = fmaf(e, p.y, den);
-        r.x = fmaf(w, v.x, r.x);
-        r.y = fmaf(w, v.y, r.y);
-        r.z = fmaf(w, v.z, r.z);
-        r.w = fmaf(w, v.w, r.w);
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    r = den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
-    return make_float2(M, den);
-}
+// A segment's piece: its segment number (-1: none), sequence, segment within the sequence, pages.
+struct Piece {
+    int32_t seg, s, h, np;
+};
 
 // NH: groups of 8 q heads of a segment (up to 8 NH heads).
 template <int D, int NW, int NH>
@@ -170,7 +149,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                          const __grid_constant__ Params a) {
     constexpr uint32_t kPage = kPageTokens * D * 2;
     constexpr uint32_t kHalves = D / 64;
-    constexpr int KS = D / 16, NMT = D / 16;
+    constexpr int KS = D / 16, NMT = D / 16, SP = step_pages(D);
     constexpr int NTH = NW * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,10 +158,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const Layout L = layout(NW, nst, hs, D, S);
     float* piece0 = reinterpret_cast<float*>(smem + L.piece0);
     float2* piece_ml = reinterpret_cast<float2*>(smem + L.piece_ml);
-    int32_t* meta = reinterpret_cast<int32_t*>(smem + L.meta);
+    Piece* meta = reinterpret_cast<Piece*>(smem + L.meta);  // [2 NW]
     uint64_t* bars_all = reinterpret_cast<uint64_t*>(smem + L.bars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.flags);
-    int32_t* cross = reinterpret_cast<int32_t*>(smem + L.flags + 8);  // [2] segments cut by this CTA's slice, [2] last?
+    int32_t* cross = reinterpret_cast<int32_t*>(smem + L.flags + 8);  // [2] pieces of segments cut by the CTA's slice, [2] to join
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.prefix);
     int4* spans = reinterpret_cast<int4*>(smem + L.spans);
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -195,7 +174,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         cross[2] = cross[3] = 0;
     }
     if (lane == 0) {
-        meta[warp * 2] = meta[warp * 2 + 1] = -1;
+        meta[warp * 2].seg = meta[warp * 2 + 1].seg = -1;
         for (int i = 0; i < nst; ++i) mbar_init(&bars_all[warp * nst + i], 1);
         fence_mbarrier_init();
     }
@@ -241,25 +220,27 @@ __global__ void __launch_bounds__(NW * 32, 1)
         if (tid == NTH - 1) prefix[S] = run;
         __syncthreads();
     }
-    const int64_t U = prefix[S], C = gridDim.x;
+    const int32_t U = prefix[S];
+    // slices of equal length, one per CTA: short lists keep to as many CTAs as have kMinSlice pages
+    const int32_t chunk = max((U + static_cast<int32_t>(gridDim.x) - 1) / static_cast<int32_t>(gridDim.x), kMinSlice);
     // rows that see nothing are zero (spread over the CTAs)
     for (int32_t s = blockIdx.x; s < S; s += gridDim.x) {
         if (prefix[s + 1] != prefix[s]) continue;
         uint32_t* z = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(s) * Hq * D);
         for (int32_t i = tid; i < Hq * D / 2; i += NTH) z[i] = 0u;
     }
-    if (U == 0) return;
-    const int32_t u0 = slice_start(U, C, blockIdx.x), u1 = slice_start(U, C, static_cast<int64_t>(blockIdx.x) + 1);
-    if (u0 >= u1) return;  // uniform over the CTA
-    const int64_t n_cta = u1 - u0;
-    const int32_t a_w = u0 + static_cast<int32_t>(warp * n_cta / NW);
-    const int32_t n = u0 + static_cast<int32_t>((warp + 1) * n_cta / NW) - a_w;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * chunk;
+    if (first >= U) return;  // uniform over the CTA
+    const int32_t u0 = static_cast<int32_t>(first), u1 = min(U, u0 + chunk);
+    const int32_t per_warp = (u1 - u0 + NW - 1) / NW;
+    const int32_t a_w = u0 + warp * per_warp, n = max(0, min(u1 - a_w, per_warp));
     uint8_t* ring = smem + L.ring + static_cast<uint32_t>(warp) * nst * L.stage;
     const uint32_t ring_u32 = smem_u32(ring);
     uint64_t* bars = bars_all + warp * nst;
     const int32_t gid = lane >> 2, tig = lane & 3;
 
     if (n > 0) {
+        int32_t t_i = 0, k_i = 0;  // pages and steps issued
         // Pool row of unit a_w + 32 k + lane.
         auto lane_row = [&](int32_t k) -> int32_t {
             if (32 * k + lane >= n) return 0;
@@ -273,54 +254,61 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
             return ((((phys * a.num_kv_heads + c.h / NHC) << a.sub_log2) + (page & ((1 << a.sub_log2) - 1))) * kPageTokens);
         };
-        int32_t kc = 0, id_cur = lane_row(0), id_nxt = n > 32 ? lane_row(1) : 0;
+        int32_t kc = 0, id_cur = lane_row(0), id_nxt = 0;
         // pages are read once per call: let them leave L2 first
         const uint64_t kv_policy = l2_policy_evict_first();
         Cursor wi;
         wi.at(prefix, spans, S, a_w);
-        int32_t consumed = 0, issued = 0;
-        auto issue = [&](int32_t t) {  // warp-uniform
-            if ((t >> 5) == kc + 1) {
+        // Step k_i (pages t_i .. of one segment, up to SP) into stage k_i % nst. Lane 2 i + kv copies the
+        // K (kv = 0) or V of page i, lane 31 the query rows of a segment that begins here.
+        auto issue = [&]() {
+            const int32_t cnt = min(min(SP, wi.np - wi.j), n - t_i), st = k_i % nst;
+            uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
+            const bool seg_first = t_i == 0 || wi.j == 0;
+            const int32_t hk = wi.h / NHC, g0 = (wi.h - hk * NHC) * kMaxHeads;
+            const uint32_t qbytes = static_cast<uint32_t>(min(G - g0, kMaxHeads)) * D * 2u;
+            const int32_t pg = t_i + (lane >> 1);
+            const int32_t r0 = __shfl_sync(0xffffffffu, id_cur, pg & 31), r1 = __shfl_sync(0xffffffffu, id_nxt, pg & 31);
+            const bool go = !*abort_flag;
+            if (lane == 0 && go)
+                mbar_arrive_expect_tx(&bars[st], static_cast<uint32_t>(cnt) * 2u * kPage + (seg_first ? qbytes : 0u));
+            __syncwarp();
+            if (lane < 2 * cnt && go) {
+                const void* tm = (lane & 1) ? static_cast<const void*>(&tm_v) : static_cast<const void*>(&tm_k);
+                uint8_t* dst = stage + static_cast<uint32_t>(lane) * kPage;
+                const int32_t row = (pg >> 5) == kc ? r0 : r1;
+                if constexpr (kHalves == 2) tma_load_3d_hint(dst, tm, 0, row, 0, &bars[st], kv_policy);  // both 64-column halves
+                else tma_load_2d_hint(dst, tm, 0, row, &bars[st], kv_policy);
+            }
+            if (lane == 31 && seg_first && go)
+                bulk_copy_g2s(stage + 2u * kPage * SP, a.q + (static_cast<int64_t>(wi.s) * Hq + hk * G + g0) * D, qbytes,
+                              &bars[st]);
+            wi.advance(cnt, prefix, spans, S, nh);
+            t_i += cnt;
+            ++k_i;
+            if ((t_i >> 5) > kc) {  // the next 32 block ids, fetched while these are used
                 ++kc;
                 id_cur = id_nxt;
                 id_nxt = 32 * (kc + 1) < n ? lane_row(kc + 1) : 0;
             }
-            const int32_t row = __shfl_sync(0xffffffffu, id_cur, t & 31);
-            if (lane == 0 && !*abort_flag) {
-                const int32_t st = t % nst;
-                uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
-                const bool seg_first = t == 0 || wi.j == 0;
-                const int32_t hk = wi.h / NHC, g0 = (wi.h - hk * NHC) * kMaxHeads;
-                const uint32_t qbytes = static_cast<uint32_t>(min(G - g0, kMaxHeads)) * D * 2u;
-                mbar_arrive_expect_tx(&bars[st], 2u * kPage + (seg_first ? qbytes : 0u));
-                if constexpr (kHalves == 2) {  // both 64-column halves in one box
-                    tma_load_3d_hint(stage, &tm_k, 0, row, 0, &bars[st], kv_policy);
-                    tma_load_3d_hint(stage + kPage, &tm_v, 0, row, 0, &bars[st], kv_policy);
-                } else {
-                    tma_load_2d_hint(stage, &tm_k, 0, row, &bars[st], kv_policy);
-                    tma_load_2d_hint(stage + kPage, &tm_v, 0, row, &bars[st], kv_policy);
-                }
-                if (seg_first)
-                    bulk_copy_g2s(stage + 2u * kPage, a.q + (static_cast<int64_t>(wi.s) * Hq + hk * G + g0) * D, qbytes,
-                                  &bars[st]);
-            }
-            wi.advance(prefix, spans, S, nh);
-            issued = t + 1;
         };
-        for (int32_t t = 0; t < min(nst, n); ++t) issue(t);
+        issue();
+        if (n > 32) id_nxt = lane_row(1);
+        for (int32_t i = 1; i < nst && t_i < n; ++i) issue();
 
         Cursor wc;
         wc.at(prefix, spans, S, a_w);
         // Fragment ownership (gid = lane / 4, tig = lane % 4):
         //   qb[f][ks]   Q^T as B: head 8 f + gid, dims 16 ks + 2 tig (+1) and + 8
-        //   sc[f][e]    S^T: key gid + 8 (e / 2), head 8 f + 2 tig + e % 2
+        //   sc[i][f][e] S^T of page i: key gid + 8 (e / 2), head 8 f + 2 tig + e % 2
         //   acc[f][mt]  O^T: head_dim 16 mt + gid + 8 (e / 2), head 8 f + 2 tig + e % 2
         uint32_t qb[NH][KS][2];
         float acc[NH][NMT][4], mh[NH][2], lh[NH][2], slope[NH][2];
         int32_t t_first = 0, ng = 0, head0 = 0;
-        for (int32_t t = 0; t < n; ++t) {
-            const int32_t st = t % nst;
-            const bool landed = mbar_wait_bounded(&bars[st], static_cast<uint32_t>(t / nst) & 1u, abort_flag);
+        int32_t k = 0;  // steps consumed
+        for (int32_t t = 0; t < n;) {
+            const int32_t st = k % nst, cnt = min(min(SP, wc.np - wc.j), n - t);
+            const bool landed = mbar_wait_bounded(&bars[st], static_cast<uint32_t>(k / nst) & 1u, abort_flag);
             if (!__all_sync(0xffffffffu, landed)) {
                 if (lane == 0) {
                     if (!*abort_flag) raise_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
@@ -329,14 +317,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 __syncwarp();
                 break;
             }
-            consumed = t + 1;
+            ++k;
             uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
-            const uint32_t k_u32 = ring_u32 + static_cast<uint32_t>(st) * L.stage, v_u32 = k_u32 + kPage;
+            const uint32_t stage_u32 = ring_u32 + static_cast<uint32_t>(st) * L.stage;
             if (t == 0 || wc.j == 0) {  // a new segment: its query rows came with this page
                 const int32_t hk = wc.h / NHC, g0 = (wc.h - hk * NHC) * kMaxHeads;
                 ng = min(G - g0, kMaxHeads);
                 head0 = hk * G + g0;
-                const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(stage + 2u * kPage);
+                const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(stage + 2u * kPage * SP);
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
                     const bool valid = f * 8 + gid < ng;
@@ -358,47 +346,55 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
                 t_first = t;
             }
-            // keys of the page that the row sees
-            const int32_t key0 = wc.pl.page(wc.j) * kPageTokens, pos = wc.sp.b1 - 1;
-            const bool whole = (key0 >= wc.sp.a0 && key0 + kPageTokens <= wc.sp.a1) ||
-                               (key0 >= wc.sp.b0 && key0 + kPageTokens <= wc.sp.b1);
-            if (!whole) {  // zero the V rows of the others, so that a weight of 0 adds exactly nothing
-                for (int32_t c = lane; c < kPageTokens * 8 * static_cast<int32_t>(kHalves); c += 32) {
-                    const int32_t hf = c / (kPageTokens * 8), rem = c % (kPageTokens * 8), rr = rem >> 3;
-                    if (!wc.sp.sees(key0 + rr))
-                        *reinterpret_cast<int4*>(stage + kPage + hf * 2048u + rr * 128u + (rem & 7) * 16u) =
-                            make_int4(0, 0, 0, 0);
-                }
-                __syncwarp();
-            }
-            // S^T = K Q^T
+            // scores of the step's pages
             const uint32_t mat = lane >> 3, r8 = lane & 7;
-            float sc[NH][4];
+            const int32_t pos = wc.sp.b1 - 1;
+            float sc[SP][NH][4], mx[NH][2];
 #pragma unroll
-            for (int f = 0; f < NH; ++f) sc[f][0] = sc[f][1] = sc[f][2] = sc[f][3] = 0.f;
+            for (int f = 0; f < NH; ++f) mx[f][0] = mx[f][1] = -INFINITY;
+            bool zeroed = false;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t key = r8 + 8u * (mat & 1u), chunk = ks * 2 + (mat >> 1);
-                uint32_t fa[4];
-                ldsm_x4(k_u32 + (chunk >> 3) * 2048u + sw128_offset(key, chunk & 7u), fa[0], fa[1], fa[2], fa[3]);
-#pragma unroll
-                for (int f = 0; f < NH; ++f) mma_16816(sc[f], fa, qb[f][ks][0], qb[f][ks][1]);
-            }
-            // scores, in the log2 domain
-            const bool see0 = whole || wc.sp.sees(key0 + gid), see1 = whole || wc.sp.sees(key0 + gid + 8);
-            const float away0 = fabsf(static_cast<float>(pos - key0 - gid)), away1 = fabsf(static_cast<float>(pos - key0 - gid - 8));
-            float mx[NH][2];
-#pragma unroll
-            for (int f = 0; f < NH; ++f) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = a.cap_l2 > 0.f
-                                        ? a.cap_l2 - 2.f * a.cap_l2 * rcp_approx(1.f + exp2_approx(sc[f][e] * a.two_k))
-                                        : sc[f][e] * a.c1;
-                    sc[f][e] = (e < 2 ? see0 : see1) ? fmaf(-slope[f][e & 1], e < 2 ? away0 : away1, x) : -INFINITY;
+            for (int i = 0; i < SP; ++i) {
+                const uint32_t k_u32 = stage_u32 + 2u * i * kPage;
+                const bool here = i < cnt;  // a missing page: its keys are masked, its K is not meant
+                const int32_t key0 = wc.pl.page(wc.j + (here ? i : 0)) * kPageTokens;
+                const bool whole = here && ((key0 >= wc.sp.a0 && key0 + kPageTokens <= wc.sp.a1) ||
+                                            (key0 >= wc.sp.b0 && key0 + kPageTokens <= wc.sp.b1));
+                if (here && !whole) {  // zero the V rows of keys the row does not see: a weight of 0 adds nothing
+                    uint8_t* v = stage + (2u * i + 1u) * kPage;
+                    for (int32_t c = lane; c < kPageTokens * 8 * static_cast<int32_t>(kHalves); c += 32) {
+                        const int32_t hf = c / (kPageTokens * 8), rem = c % (kPageTokens * 8), rr = rem >> 3;
+                        if (!wc.sp.sees(key0 + rr))
+                            *reinterpret_cast<int4*>(v + hf * 2048u + rr * 128u + (rem & 7) * 16u) = make_int4(0, 0, 0, 0);
+                    }
+                    zeroed = true;
+                    __syncwarp();
                 }
-                mx[f][0] = fmaxf(sc[f][0], sc[f][2]);
-                mx[f][1] = fmaxf(sc[f][1], sc[f][3]);
+                // S^T = K Q^T
+#pragma unroll
+                for (int f = 0; f < NH; ++f) sc[i][f][0] = sc[i][f][1] = sc[i][f][2] = sc[i][f][3] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t key = r8 + 8u * (mat & 1u), c16 = ks * 2 + (mat >> 1);
+                    uint32_t fa[4];
+                    ldsm_x4(k_u32 + (c16 >> 3) * 2048u + sw128_offset(key, c16 & 7u), fa[0], fa[1], fa[2], fa[3]);
+#pragma unroll
+                    for (int f = 0; f < NH; ++f) mma_16816(sc[i][f], fa, qb[f][ks][0], qb[f][ks][1]);
+                }
+                // scores in the log2 domain
+                const bool see0 = here && (whole || wc.sp.sees(key0 + gid)), see1 = here && (whole || wc.sp.sees(key0 + gid + 8));
+                const float away0 = fabsf(static_cast<float>(pos - key0 - gid)), away1 = fabsf(static_cast<float>(pos - key0 - gid - 8));
+#pragma unroll
+                for (int f = 0; f < NH; ++f) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = a.cap_l2 > 0.f ? a.cap_l2 - 2.f * a.cap_l2 * rcp_approx(1.f + exp2_approx(sc[i][f][e] * a.two_k))
+                                                       : sc[i][f][e] * a.c1;
+                        sc[i][f][e] = (e < 2 ? see0 : see1) ? fmaf(-slope[f][e & 1], e < 2 ? away0 : away1, x) : -INFINITY;
+                    }
+                    mx[f][0] = fmaxf(mx[f][0], fmaxf(sc[i][f][0], sc[i][f][2]));
+                    mx[f][1] = fmaxf(mx[f][1], fmaxf(sc[i][f][1], sc[i][f][3]));
+                }
             }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
@@ -407,7 +403,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     mx[f][0] = fmaxf(mx[f][0], __shfl_xor_sync(0xffffffffu, mx[f][0], off));
                     mx[f][1] = fmaxf(mx[f][1], __shfl_xor_sync(0xffffffffu, mx[f][1], off));
                 }
-            uint32_t pb[NH][2];
+            uint32_t pb[SP][NH][2];
 #pragma unroll
             for (int f = 0; f < NH; ++f) {
                 float cc[2], ref[2];
@@ -417,12 +413,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     ref[hh] = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet: weights are 0, not NaN
                     cc[hh] = exp2_approx(mh[f][hh] - ref[hh]);
                     mh[f][hh] = mn;
+                    lh[f][hh] *= cc[hh];
                 }
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(sc[f][e] - ref[e & 1]);
-                lh[f][0] = lh[f][0] * cc[0] + p[0] + p[2];
-                lh[f][1] = lh[f][1] * cc[1] + p[1] + p[3];
 #pragma unroll
                 for (int mt = 0; mt < NMT; ++mt) {
                     acc[f][mt][0] *= cc[0];
@@ -430,20 +422,33 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     acc[f][mt][2] *= cc[0];
                     acc[f][mt][3] *= cc[1];
                 }
-                pb[f][0] = movmatrix_trans(pack_bf16x2(p[0], p[1]));
-                pb[f][1] = movmatrix_trans(pack_bf16x2(p[2], p[3]));
+#pragma unroll
+                for (int i = 0; i < SP; ++i) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = exp2_approx(sc[i][f][e] - ref[e & 1]);
+                    lh[f][0] += p[0] + p[2];
+                    lh[f][1] += p[1] + p[3];
+                    pb[i][f][0] = movmatrix_trans(pack_bf16x2(p[0], p[1]));
+                    pb[i][f][1] = movmatrix_trans(pack_bf16x2(p[2], p[3]));
+                }
             }
             // O^T += V^T P^T
 #pragma unroll
-            for (int mt = 0; mt < NMT; ++mt) {
-                const uint32_t key = r8 + 8u * (mat >> 1), chunk = mt * 2 + (mat & 1u);
-                uint32_t fa[4];
-                ldsm_x4_trans(v_u32 + (chunk >> 3) * 2048u + sw128_offset(key, chunk & 7u), fa[0], fa[1], fa[2], fa[3]);
+            for (int i = 0; i < SP; ++i) {
+                if (i >= cnt) break;
+                const uint32_t v_u32 = stage_u32 + (2u * i + 1u) * kPage;
 #pragma unroll
-                for (int f = 0; f < NH; ++f) mma_16816(acc[f][mt], fa, pb[f][0], pb[f][1]);
+                for (int mt = 0; mt < NMT; ++mt) {
+                    const uint32_t key = r8 + 8u * (mat >> 1), c16 = mt * 2 + (mat & 1u);
+                    uint32_t fa[4];
+                    ldsm_x4_trans(v_u32 + (c16 >> 3) * 2048u + sw128_offset(key, c16 & 7u), fa[0], fa[1], fa[2], fa[3]);
+#pragma unroll
+                    for (int f = 0; f < NH; ++f) mma_16816(acc[f][mt], fa, pb[i][f][0], pb[i][f][1]);
+                }
             }
 
-            if (t == n - 1 || wc.j == wc.np - 1) {  // the warp's last page of this segment
+            if (t + cnt == n || wc.j + cnt == wc.np) {  // the warp's last page of this segment
                 float Lh[NH][2];
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
@@ -486,94 +491,180 @@ __global__ void __launch_bounds__(NW * 32, 1)
                             if (gid == 0) piece_ml[(warp * 2 + slot) * hs + head] = make_float2(mh[f][hh], Lh[f][hh]);
                         }
                     }
-                if (!inside && lane == 0) meta[warp * 2 + slot] = wc.s * nh + wc.h;
+                if (!inside && lane == 0) meta[warp * 2 + slot] = Piece{wc.s * nh + wc.h, wc.s, wc.h, wc.np};
             }
             __syncwarp();
-            if (!whole) fence_proxy_async_shared();  // generic writes before the next copy into the stage
-            if (t + nst < n) issue(t + nst);
-            wc.advance(prefix, spans, S, nh);
+            if (zeroed) fence_proxy_async_shared();  // generic writes before the next copy into the stage
+            if (t_i < n) issue();
+            wc.advance(cnt, prefix, spans, S, nh);
+            t += cnt;
         }
         // after an abort: copies already issued land before the CTA can exit
-        if (consumed < issued && lane == 0)
-            for (int32_t t = consumed; t < issued; ++t) mbar_wait_timeout(&bars[t % nst], static_cast<uint32_t>(t / nst) & 1u);
+        if (k < k_i && lane == 0)
+            for (; k < k_i; ++k) mbar_wait_timeout(&bars[k % nst], static_cast<uint32_t>(k / nst) & 1u);
     }
     __syncthreads();
     if (*abort_flag) return;
 
     // ---- pieces cut between this CTA's warps: runs of equal segments in list order -------------
+    // First every (piece, head) weighs itself against its run: e_i / sum e_k l_k with e_i = 2^(m_i - M)
+    // (pieces hold unnormalised outputs); then all threads add the pieces up.
     constexpr int V4 = D / 4;
+    float* weight = reinterpret_cast<float*>(smem + L.weight);            // [2 NW][hs]
+    float2* run_ml = reinterpret_cast<float2*>(weight + 2 * NW * hs);     // [2 NW][hs] the run's (M, sum), at each piece
+    for (int32_t g = warp; g < hs; g += NW) {  // a warp per head, a lane per piece
+        const int32_t seg = lane < 2 * NW ? meta[lane].seg : -1;
+        const float2 ml = seg >= 0 ? piece_ml[lane * hs + g] : make_float2(-INFINITY, 0.f);
+        float M = -INFINITY, den = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < 2 * NW; ++k) {
+            const int32_t sk = __shfl_sync(0xffffffffu, seg, k);
+            const float mk = __shfl_sync(0xffffffffu, ml.x, k);
+            if (sk == seg) M = fmaxf(M, mk);
+        }
+        const float e = exp2_approx(ml.x - (M == -INFINITY ? 0.f : M)), el = e * ml.y;
+#pragma unroll 4
+        for (int k = 0; k < 2 * NW; ++k) {
+            const int32_t sk = __shfl_sync(0xffffffffu, seg, k);
+            const float lk = __shfl_sync(0xffffffffu, el, k);
+            if (sk == seg) den += lk;
+        }
+        if (seg >= 0) {
+            weight[lane * hs + g] = den == 0.f ? 0.f : e / den;
+            run_ml[lane * hs + g] = make_float2(M, den);
+        }
+    }
+    __syncthreads();
     for (int32_t i0 = 0; i0 < 2 * NW;) {
-        const int32_t seg = meta[i0];
-        if (seg < 0) {
+        const Piece pc = meta[i0];
+        if (pc.seg < 0) {
             ++i0;
             continue;
         }
-        int32_t slot[2 * NW], np_ = 0, i1 = i0;  // the group's pieces
-        for (; i1 < 2 * NW && (meta[i1] == seg || meta[i1] < 0); ++i1)
-            if (meta[i1] == seg) slot[np_++] = i1;
-        i0 = i1;
-        const int32_t s = seg / nh, h = seg - s * nh;
-        const int32_t np = (prefix[s + 1] - prefix[s]) / nh, seg_a = prefix[s] + h * np;
-        const bool complete = seg_a >= u0 && seg_a + np <= u1;
-        const int32_t hk = h / NHC, g0 = (h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
+        int32_t i1 = i0 + 1;  // the run ends where another segment begins
+        while (i1 < 2 * NW && (meta[i1].seg == pc.seg || meta[i1].seg < 0)) ++i1;
+        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np;
+        const bool complete = seg_a >= u0 && seg_a + pc.np <= u1;
+        const int32_t hk = pc.h / NHC, g0 = (pc.h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
         const int32_t cslot = seg_a <= u0 ? 0 : 1;
         for (int32_t i = tid; i < heads * V4; i += NTH) {
             const int32_t g = i / V4, d = (i - g * V4) * 4;
-            float4 r;
-            const float2 ml = join_pieces<false>(
-                np_, [&](int32_t k) { return piece_ml[slot[k] * hs + g]; },
-                [&](int32_t k) {
-                    const float* p = (slot[k] & 1) ? reinterpret_cast<const float*>(
-                                                         smem + L.ring + static_cast<uint32_t>(slot[k] >> 1) * nst * L.stage)
-                                                   : piece0 + static_cast<uint32_t>(slot[k] >> 1) * hs * D;
-                    return *reinterpret_cast<const float4*>(p + g * D + d);
-                },
-                r);
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int32_t k = i0; k < i1; ++k) {
+                if (meta[k].seg < 0) continue;
+                const float* p = (k & 1) ? reinterpret_cast<const float*>(smem + L.ring + static_cast<uint32_t>(k >> 1) * nst * L.stage)
+                                         : piece0 + static_cast<uint32_t>(k >> 1) * hs * D;
+                const float4 v = *reinterpret_cast<const float4*>(p + g * D + d);
+                const float w = weight[k * hs + g];
+                r.x = fmaf(w, v.x, r.x);
+                r.y = fmaf(w, v.y, r.y);
+                r.z = fmaf(w, v.z, r.z);
+                r.w = fmaf(w, v.w, r.w);
+            }
             if (complete) {
-                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(s) * Hq + hk * G + g0 + g) * D + d) =
+                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
                     make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
             } else {
                 const int64_t pg = (static_cast<int64_t>(blockIdx.x) * 2 + cslot) * hs + g;
                 *reinterpret_cast<float4*>(a.piece_o + pg * D + d) = r;
-                if (d == 0) a.piece_ml[pg] = ml;
+                if (d == 0) a.piece_ml[pg] = run_ml[i0 * hs + g];
             }
         }
-        if (!complete && tid == 0) cross[cslot] = seg;
+        if (!complete && tid == 0) cross[cslot] = i0;
+        i0 = i1;
     }
     __syncthreads();
     // ---- segments cut between CTAs: count this CTA's pieces; the last to count joins ------------
     if (tid < 2 && cross[tid] >= 0) {
-        const int32_t seg = cross[tid], s = seg / nh, h = seg - s * nh;
-        const int32_t np = (prefix[s + 1] - prefix[s]) / nh, seg_a = prefix[s] + h * np;
-        const int32_t expected =
-            U >= C ? slice_owner(U, C, seg_a + np - 1) - slice_owner(U, C, seg_a) + 1 : np;  // else one unit per CTA
+        const Piece pc = meta[cross[tid]];
+        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np;
+        const int32_t expected = (seg_a + pc.np - 1) / chunk - seg_a / chunk + 1;
         int32_t old;
-        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counter + seg) : "memory");
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counter + pc.seg) : "memory");
         cross[2 + tid] = old == expected - 1 ? expected : 0;
-        if (old == expected - 1) a.counter[seg] = 0;
+        if (old == expected - 1) a.counter[pc.seg] = 0;
     }
     __syncthreads();
+    // The join: weights of all (CTA piece, head) pairs first, then every thread adds up a share of the
+    // pieces for 4 elements of a head and the shares are added in order. The scratch is the ring, which
+    // nothing uses any more.
+    float2* jml = reinterpret_cast<float2*>(smem + L.ring);                    // [n][heads]
+    float4* share = reinterpret_cast<float4*>(smem + L.ring + 40960u);         // [NTH]
     for (int32_t x = 0; x < 2; ++x) {
         const int32_t n_pieces = cross[2 + x];
-        if (n_pieces == 0) continue;
-        const int32_t seg = cross[x], s = seg / nh, h = seg - s * nh;
-        const int32_t np = (prefix[s + 1] - prefix[s]) / nh, seg_a = prefix[s] + h * np;
-        const int32_t c_first = slice_owner(U, C, seg_a);
-        const int32_t first_slot = seg_a <= slice_start(U, C, c_first) ? 0 : 1;
-        const int32_t hk = h / NHC, g0 = (h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
-        for (int32_t i = tid; i < heads * V4; i += NTH) {
-            const int32_t g = i / V4, d = (i - g * V4) * 4;
-            auto at = [&](int32_t k) -> int64_t {
-                const int64_t c = U >= C ? c_first + k : slice_owner(U, C, seg_a + k);
-                return (c * 2 + (k == 0 ? first_slot : 0)) * hs + g;
-            };
-            float4 r;
-            join_pieces<true>(
-                n_pieces, [&](int32_t k) { return __ldcg(a.piece_ml + at(k)); },
-                [&](int32_t k) { return __ldcg(reinterpret_cast<const float4*>(a.piece_o + at(k) * D + d)); }, r);
-            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(s) * Hq + hk * G + g0 + g) * D + d) =
+        if (n_pieces == 0) continue;  // uniform over the CTA
+        const Piece pc = meta[cross[x]];
+        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np, c_first = seg_a / chunk;
+        const int32_t first_slot = seg_a == c_first * chunk ? 0 : 1;
+        const int32_t hk = pc.h / NHC, g0 = (pc.h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
+        // row of the segment's k-th CTA piece
+        auto piece = [&](int32_t k) -> int64_t {
+            return (static_cast<int64_t>(c_first + k) * 2 + (k == 0 ? first_slot : 0)) * hs;
+        };
+        for (int32_t i = tid; i < n_pieces * heads; i += NTH) {
+            const int32_t k = i / heads;
+            jml[i] = __ldcg(a.piece_ml + piece(k) + (i - k * heads));
+        }
+        __syncthreads();
+        // one warp per head: M and the sum over the pieces, then each piece's weight in place of its sum
+        for (int32_t g = warp; g < heads; g += NW) {
+            float M = -INFINITY;
+            for (int32_t k = lane; k < n_pieces; k += 32) M = fmaxf(M, jml[k * heads + g].x);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            const float ref = M == -INFINITY ? 0.f : M;
+            float den = 0.f;
+            for (int32_t k = lane; k < n_pieces; k += 32)
+                den = fmaf(exp2_approx(jml[k * heads + g].x - ref), jml[k * heads + g].y, den);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+            for (int32_t k = lane; k < n_pieces; k += 32)
+                jml[k * heads + g].y =
+                    den == 0.f ? 0.f : exp2_approx(jml[k * heads + g].x - ref) * jml[k * heads + g].y / den;
+        }
+        __syncthreads();
+        const int32_t cols = heads * V4, shares = max(1, NTH / cols);
+        for (int32_t i = tid; i < cols * shares; i += NTH) {  // one round unless a head chunk has more columns
+            const int32_t sh = i / cols, col = i - sh * cols, g = col / V4, d = (col - g * V4) * 4;
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int32_t k0 = sh; k0 < n_pieces; k0 += 8 * shares) {  // eight loads in flight
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int32_t k = k0 + j * shares;
+                    v[j] = k < n_pieces ? __ldcg(reinterpret_cast<const float4*>(a.piece_o + (piece(k) + g) * D + d))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int32_t k = k0 + j * shares;
+                    const float w = k < n_pieces ? jml[k * heads + g].y : 0.f;
+                    r.x = fmaf(w, v[j].x, r.x);
+                    r.y = fmaf(w, v[j].y, r.y);
+                    r.z = fmaf(w, v[j].z, r.z);
+                    r.w = fmaf(w, v[j].w, r.w);
+                }
+            }
+            if (shares > 1) {
+                share[i] = r;
+            } else {
+                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
+                    make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+            }
+        }
+        __syncthreads();
+        if (shares > 1 && tid < cols) {
+            float4 r = share[tid];
+            for (int32_t k = 1; k < shares; ++k) {
+                const float4 v = share[k * cols + tid];
+                r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
+            }
+            const int32_t g = tid / V4, d = (tid - g * V4) * 4;
+            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
                 make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
         }
+        __syncthreads();  // the scratch serves the other segment next
     }
 }
 
