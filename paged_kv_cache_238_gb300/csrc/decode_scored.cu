@@ -33,7 +33,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSeqs = 1024;  // sequences of one launch: their spans live in shared memory
 constexpr int kMaxHeads = 16;   // q heads of one segment
-constexpr int kMinSlice = 8;    // pages of a CTA's slice at least
+constexpr int kMinSlice = 8;    // units of a CTA's slice at least
+constexpr int kSegmentUnits = 1;  // a segment's start and end weigh as much as this many pages
 
 // Pages of one step of a warp: 8 KB of K and V, so that what a step costs besides its pages
 // (waits, reductions, the list) weighs alike at both head dims.
@@ -107,7 +108,8 @@ __device__ __forceinline__ int32_t find_seq(const int32_t* prefix, int32_t S, in
     return lo;
 }
 
-// Position in the work list: sequence s, its segment h of nh, page j of np.
+// Position in the work list: sequence s, its segment h of nh, unit j: page j of np, or, from np on, one
+// of the kSegmentUnits units without a page that stand for what a segment costs besides its pages.
 struct Cursor {
     int32_t s, h, j, np;
     KeySpans sp;
@@ -121,14 +123,14 @@ struct Cursor {
     __device__ __forceinline__ void at(const int32_t* prefix, const int4* spans, int32_t S, int32_t u) {
         s = find_seq(prefix, S, u);
         load(spans);
-        const int32_t r = u - prefix[s];
-        h = r / np;
-        j = r - h * np;
+        const int32_t r = u - prefix[s], units = np + kSegmentUnits;
+        h = r / units;
+        j = r - h * units;
     }
     __device__ __forceinline__ void advance(int32_t pages, const int32_t* prefix, const int4* spans, int32_t S,
                                             int32_t nh) {
         j += pages;
-        if (j < np) return;
+        if (j < np + kSegmentUnits) return;
         j = 0;
         if (++h < nh) return;
         h = 0;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             const KeySpans sp = key_spans(len, len - 1, a.score.key_start ? __ldg(a.score.key_start + s) : 0,
                                           a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window);
             spans[s] = make_int4(sp.a0, sp.a1, sp.b0, sp.b1);
-            const int32_t units = page_list(sp).n * nh;
+            const int32_t pages = page_list(sp).n, units = pages > 0 ? (pages + kSegmentUnits) * nh : 0;
             prefix[s] = units;
             local += units;
         }
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (32 * k + lane >= n) return 0;
             Cursor c;
             c.at(prefix, spans, S, a_w + 32 * k + lane);
+            if (c.j >= c.np) return 0;
             const int32_t page = c.pl.page(c.j);
             int32_t phys = __ldg(a.block_table + static_cast<int64_t>(c.s) * a.max_blocks + (page >> a.sub_log2));
             if (phys < 0 || phys >= a.num_blocks) {
@@ -261,10 +264,27 @@ __global__ void __launch_bounds__(NW * 32, 1)
         wi.at(prefix, spans, S, a_w);
         // Step k_i (pages t_i .. of one segment, up to SP) into stage k_i % nst. Lane 2 i + kv copies the
         // K (kv = 0) or V of page i, lane 31 the query rows of a segment that begins here.
+        bool q_due = true;  // the segment's query rows have not been copied yet
+        auto next_block_ids = [&]() {
+            if ((t_i >> 5) > kc) {  // the next 32 block ids, fetched while these are used
+                ++kc;
+                id_cur = id_nxt;
+                id_nxt = 32 * (kc + 1) < n ? lane_row(kc + 1) : 0;
+            }
+        };
+        auto skip = [&]() {  // to the next page of the part
+            while (t_i < n && wi.j >= wi.np) {
+                const int32_t none = min(wi.np + kSegmentUnits - wi.j, n - t_i);
+                wi.advance(none, prefix, spans, S, nh);
+                t_i += none;
+                q_due = true;
+                next_block_ids();
+            }
+        };
         auto issue = [&]() {
             const int32_t cnt = min(min(SP, wi.np - wi.j), n - t_i), st = k_i % nst;
             uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
-            const bool seg_first = t_i == 0 || wi.j == 0;
+            const bool seg_first = q_due;
             const int32_t hk = wi.h / NHC, g0 = (wi.h - hk * NHC) * kMaxHeads;
             const uint32_t qbytes = static_cast<uint32_t>(min(G - g0, kMaxHeads)) * D * 2u;
             const int32_t pg = t_i + (lane >> 1);
@@ -286,15 +306,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
             wi.advance(cnt, prefix, spans, S, nh);
             t_i += cnt;
             ++k_i;
-            if ((t_i >> 5) > kc) {  // the next 32 block ids, fetched while these are used
-                ++kc;
-                id_cur = id_nxt;
-                id_nxt = 32 * (kc + 1) < n ? lane_row(kc + 1) : 0;
-            }
+            q_due = false;
+            next_block_ids();
+            skip();
         };
-        issue();
         if (n > 32) id_nxt = lane_row(1);
-        for (int32_t i = 1; i < nst && t_i < n; ++i) issue();
+        skip();
+        for (int32_t i = 0; i < nst && t_i < n; ++i) issue();
 
         Cursor wc;
         wc.at(prefix, spans, S, a_w);
@@ -304,9 +322,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
         //   acc[f][mt]  O^T: head_dim 16 mt + gid + 8 (e / 2), head 8 f + 2 tig + e % 2
         uint32_t qb[NH][KS][2];
         float acc[NH][NMT][4], mh[NH][2], lh[NH][2], slope[NH][2];
-        int32_t t_first = 0, ng = 0, head0 = 0;
+        int32_t ng = 0, head0 = 0;
+        bool cut_left = false;
         int32_t k = 0;  // steps consumed
+        bool first_page = true;  // of a segment in this part
         for (int32_t t = 0; t < n;) {
+            if (wc.j >= wc.np) {  // units without a page
+                const int32_t none = min(wc.np + kSegmentUnits - wc.j, n - t);
+                wc.advance(none, prefix, spans, S, nh);
+                t += none;
+                first_page = true;
+                continue;
+            }
             const int32_t st = k % nst, cnt = min(min(SP, wc.np - wc.j), n - t);
             const bool landed = mbar_wait_bounded(&bars[st], static_cast<uint32_t>(k / nst) & 1u, abort_flag);
             if (!__all_sync(0xffffffffu, landed)) {
@@ -320,7 +347,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
             ++k;
             uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
             const uint32_t stage_u32 = ring_u32 + static_cast<uint32_t>(st) * L.stage;
-            if (t == 0 || wc.j == 0) {  // a new segment: its query rows came with this page
+            if (first_page) {  // a new segment: its query rows came with this step
+                first_page = false;
                 const int32_t hk = wc.h / NHC, g0 = (wc.h - hk * NHC) * kMaxHeads;
                 ng = min(G - g0, kMaxHeads);
                 head0 = hk * G + g0;
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         slope[f][hh] = a.score.slopes && head < ng ? __ldg(a.score.slopes + head0 + head) * kLog2e : 0.f;
                     }
                 }
-                t_first = t;
+                cut_left = wc.j > 0;
             }
             // scores of the step's pages
             const uint32_t mat = lane >> 3, r8 = lane & 7;
@@ -462,9 +490,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         Lh[f][0] += __shfl_xor_sync(0xffffffffu, Lh[f][0], off);
                         Lh[f][1] += __shfl_xor_sync(0xffffffffu, Lh[f][1], off);
                     }
-                const int32_t seg_a = prefix[wc.s] + wc.h * wc.np;
-                const bool inside = seg_a >= a_w && seg_a + wc.np <= a_w + n;
-                const int slot = t_first == 0 ? 0 : 1;  // a cut piece: the part's first segment or its last
+                const bool inside = !cut_left && wc.j + cnt == wc.np;
+                const int slot = cut_left ? 0 : 1;  // a piece cut on the left is the part's first, else its last
                 __syncwarp();                           // slot 1 reuses the ring, idle after the last page
                 float* pa_acc = slot == 0 ? piece0 + static_cast<uint32_t>(warp) * hs * D : reinterpret_cast<float*>(ring);
                 __nv_bfloat16* o = a.out + (static_cast<int64_t>(wc.s) * Hq + head0) * D;
@@ -535,19 +562,26 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
     }
     __syncthreads();
-    for (int32_t i0 = 0; i0 < 2 * NW;) {
+    // Runs begin at the pieces whose predecessor belongs to another segment; the warps share the runs,
+    // and several warps share a run where there are few.
+    uint32_t starts;
+    {
+        const int32_t seg = lane < 2 * NW ? meta[lane].seg : -1;
+        const uint32_t held = __ballot_sync(0xffffffffu, seg >= 0);
+        const uint32_t before = held & ((1u << lane) - 1u);
+        const int32_t prev = __shfl_sync(0xffffffffu, seg, before ? 31 - __clz(before) : lane);
+        starts = __ballot_sync(0xffffffffu, seg >= 0 && (before == 0u || prev != seg));
+    }
+    const int32_t runs = __popc(starts);
+    for (int32_t run = runs > 0 ? warp % runs : 0; run < runs; run += NW) {
+        const int32_t i0 = __fns(starts, 0, run + 1), i1 = run + 1 < runs ? __fns(starts, 0, run + 2) : 2 * NW;
+        const int32_t shares = runs < NW ? (NW - 1 - run) / runs + 1 : 1, mine = runs < NW ? warp / runs : 0;
         const Piece pc = meta[i0];
-        if (pc.seg < 0) {
-            ++i0;
-            continue;
-        }
-        int32_t i1 = i0 + 1;  // the run ends where another segment begins
-        while (i1 < 2 * NW && (meta[i1].seg == pc.seg || meta[i1].seg < 0)) ++i1;
-        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np;
+        const int32_t seg_a = prefix[pc.s] + pc.h * (pc.np + kSegmentUnits);
         const bool complete = seg_a >= u0 && seg_a + pc.np <= u1;
         const int32_t hk = pc.h / NHC, g0 = (pc.h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
         const int32_t cslot = seg_a <= u0 ? 0 : 1;
-        for (int32_t i = tid; i < heads * V4; i += NTH) {
+        for (int32_t i = mine * 32 + lane; i < heads * V4; i += shares * 32) {
             const int32_t g = i / V4, d = (i - g * V4) * 4;
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
@@ -571,14 +605,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 if (d == 0) a.piece_ml[pg] = run_ml[i0 * hs + g];
             }
         }
-        if (!complete && tid == 0) cross[cslot] = i0;
-        i0 = i1;
+        if (!complete && mine == 0 && lane == 0) cross[cslot] = i0;
     }
     __syncthreads();
     // ---- segments cut between CTAs: count this CTA's pieces; the last to count joins ------------
     if (tid < 2 && cross[tid] >= 0) {
         const Piece pc = meta[cross[tid]];
-        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np;
+        const int32_t seg_a = prefix[pc.s] + pc.h * (pc.np + kSegmentUnits);
         const int32_t expected = (seg_a + pc.np - 1) / chunk - seg_a / chunk + 1;
         int32_t old;
         asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(a.counter + pc.seg) : "memory");
@@ -586,83 +619,64 @@ __global__ void __launch_bounds__(NW * 32, 1)
         if (old == expected - 1) a.counter[pc.seg] = 0;
     }
     __syncthreads();
-    // The join: weights of all (CTA piece, head) pairs first, then every thread adds up a share of the
-    // pieces for 4 elements of a head and the shares are added in order. The scratch is the ring, which
-    // nothing uses any more.
-    float2* jml = reinterpret_cast<float2*>(smem + L.ring);                    // [n][heads]
-    float4* share = reinterpret_cast<float4*>(smem + L.ring + 40960u);         // [NTH]
+    // The join: a thread adds up a share of the pieces for 4 elements of a head, eight pieces' loads in
+    // flight, and the shares are joined in order. The scratch is the ring, which nothing uses any more.
+    float4* share_o = reinterpret_cast<float4*>(smem + L.ring);               // [NTH]
+    float2* share_ml = reinterpret_cast<float2*>(smem + L.ring + 16u * NTH);  // [NTH]
     for (int32_t x = 0; x < 2; ++x) {
         const int32_t n_pieces = cross[2 + x];
         if (n_pieces == 0) continue;  // uniform over the CTA
         const Piece pc = meta[cross[x]];
-        const int32_t seg_a = prefix[pc.s] + pc.h * pc.np, c_first = seg_a / chunk;
+        const int32_t seg_a = prefix[pc.s] + pc.h * (pc.np + kSegmentUnits), c_first = seg_a / chunk;
         const int32_t first_slot = seg_a == c_first * chunk ? 0 : 1;
         const int32_t hk = pc.h / NHC, g0 = (pc.h - hk * NHC) * kMaxHeads, heads = min(G - g0, kMaxHeads);
-        // row of the segment's k-th CTA piece
-        auto piece = [&](int32_t k) -> int64_t {
-            return (static_cast<int64_t>(c_first + k) * 2 + (k == 0 ? first_slot : 0)) * hs;
+        const int32_t cols = heads * V4, shares = max(1, min(NTH / cols, n_pieces));
+        auto add = [](float& M, float& den, float4& r, const float2 ml, const float4 v, float l) {
+            // one piece (or share) more: its weight is l 2^(m - M), its sum ml.y 2^(m - M)
+            const float Mn = fmaxf(M, ml.x), ref = Mn == -INFINITY ? 0.f : Mn;
+            const float f = exp2_approx(M - ref), e = exp2_approx(ml.x - ref), w = e * l;
+            M = Mn;
+            den = fmaf(den, f, e * ml.y);
+            r = make_float4(fmaf(w, v.x, r.x * f), fmaf(w, v.y, r.y * f), fmaf(w, v.z, r.z * f), fmaf(w, v.w, r.w * f));
         };
-        for (int32_t i = tid; i < n_pieces * heads; i += NTH) {
-            const int32_t k = i / heads;
-            jml[i] = __ldcg(a.piece_ml + piece(k) + (i - k * heads));
-        }
-        __syncthreads();
-        // one warp per head: M and the sum over the pieces, then each piece's weight in place of its sum
-        for (int32_t g = warp; g < heads; g += NW) {
-            float M = -INFINITY;
-            for (int32_t k = lane; k < n_pieces; k += 32) M = fmaxf(M, jml[k * heads + g].x);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            const float ref = M == -INFINITY ? 0.f : M;
-            float den = 0.f;
-            for (int32_t k = lane; k < n_pieces; k += 32)
-                den = fmaf(exp2_approx(jml[k * heads + g].x - ref), jml[k * heads + g].y, den);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-            for (int32_t k = lane; k < n_pieces; k += 32)
-                jml[k * heads + g].y =
-                    den == 0.f ? 0.f : exp2_approx(jml[k * heads + g].x - ref) * jml[k * heads + g].y / den;
-        }
-        __syncthreads();
-        const int32_t cols = heads * V4, shares = max(1, NTH / cols);
+        auto put = [&](int32_t g, int32_t d, float den, const float4 r) {
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
+                make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+        };
         for (int32_t i = tid; i < cols * shares; i += NTH) {  // one round unless a head chunk has more columns
             const int32_t sh = i / cols, col = i - sh * cols, g = col / V4, d = (col - g * V4) * 4;
+            float M = -INFINITY, den = 0.f;
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int32_t k0 = sh; k0 < n_pieces; k0 += 8 * shares) {  // eight loads in flight
+#pragma unroll 1
+            for (int32_t k0 = sh; k0 < n_pieces; k0 += 8 * shares) {
                 float4 v[8];
+                float2 ml[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int32_t k = k0 + j * shares;
-                    v[j] = k < n_pieces ? __ldcg(reinterpret_cast<const float4*>(a.piece_o + (piece(k) + g) * D + d))
+                    const int64_t pg = (static_cast<int64_t>(c_first + k) * 2 + (k == 0 ? first_slot : 0)) * hs + g;
+                    ml[j] = k < n_pieces ? __ldcg(a.piece_ml + pg) : make_float2(-INFINITY, 0.f);
+                    v[j] = k < n_pieces ? __ldcg(reinterpret_cast<const float4*>(a.piece_o + pg * D + d))
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int32_t k = k0 + j * shares;
-                    const float w = k < n_pieces ? jml[k * heads + g].y : 0.f;
-                    r.x = fmaf(w, v[j].x, r.x);
-                    r.y = fmaf(w, v[j].y, r.y);
-                    r.z = fmaf(w, v[j].z, r.z);
-                    r.w = fmaf(w, v[j].w, r.w);
-                }
+                for (int j = 0; j < 8; ++j) add(M, den, r, ml[j], v[j], ml[j].y);  // pieces are normalised
             }
-            if (shares > 1) {
-                share[i] = r;
+            if (shares == 1) {
+                put(g, d, den, r);
             } else {
-                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
-                    make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+                share_o[i] = r;
+                share_ml[i] = make_float2(M, den);
             }
         }
         __syncthreads();
         if (shares > 1 && tid < cols) {
-            float4 r = share[tid];
-            for (int32_t k = 1; k < shares; ++k) {
-                const float4 v = share[k * cols + tid];
-                r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
-            }
-            const int32_t g = tid / V4, d = (tid - g * V4) * 4;
-            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
-                make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+            float M = -INFINITY, den = 0.f;
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int32_t k = 0; k < shares; ++k) add(M, den, r, share_ml[k * cols + tid], share_o[k * cols + tid], 1.f);
+            const int32_t g = tid / V4;
+            put(g, (tid - g * V4) * 4, den, r);
         }
         __syncthreads();  // the scratch serves the other segment next
     }
