@@ -461,6 +461,21 @@ def _need(what: str, t, dtype, shape, device: int) -> None:
         raise ValueError(f"{what}: shape {tuple(t.shape)} where {tuple(shape)} is needed (-1: any size)")
 
 
+def _fits(t, dtype, shape, device: int) -> bool:
+    """_need's conditions as one expression, for tensors whose whole shape is known: what a serving
+    loop pays for the checks of each call. (A tensor that is not CUDA's has a negative device.)"""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The stream's handle; without one, torch's current stream of the device, read without making
+    the Python object that _stream makes (1.5 us of a call that takes 10)."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _need_current(device: int) -> None:
     import torch
     if device != torch.cuda.current_device():
@@ -482,6 +497,8 @@ class Score:
 
     def _check(self, H_q: int, rows: int, S: int, device: int) -> None:
         import torch
+        if self.alibi_slopes is self.key_start is self.prefix_len is None:
+            return
         if self.alibi_slopes is not None:
             _need("alibi_slopes", self.alibi_slopes, torch.float32, (H_q,), device)
         if self.key_start is not None:
@@ -491,25 +508,36 @@ class Score:
 
 
 def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace):
-    """Shape and type checks shared by the scored calls; returns (rows, H_q, D, NB, H_kv, BS, S, dtype code)."""
+    """Shape and type checks shared by the scored calls; returns (T, H_q, D, NB, H_kv, BS, S, max_blocks,
+    device, dtype code, workspace bytes)."""
     import torch
-    code = _dtype_code(q)
-    dev = q.get_device()
-    _need("q", q, q.dtype, (-1, -1, -1), dev)
-    T, H_q, D = q.shape
-    _need("out", out, q.dtype, (T, H_q, D), dev)
-    _need("k_cache", k_cache, q.dtype, (-1, -1, -1, D), dev)
-    NB, H_kv, BS, _ = k_cache.shape
-    _need("v_cache", v_cache, q.dtype, (NB, H_kv, BS, D), dev)
-    _need("seq_lens", seq_lens, torch.int32, (-1,), dev)
-    S = seq_lens.shape[0]
-    _need("block_table", block_table, torch.int32, (S, -1), dev)
+    dt, i32, dev = q.dtype, torch.int32, q.get_device()
+    code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(q)
+    if not (dev >= 0 and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2 and q.is_contiguous()):
+        _need("q", q, dt, (-1, -1, -1), dev)
+        _need("k_cache", k_cache, dt, (-1, -1, -1, -1), dev)
+        _need("block_table", block_table, i32, (-1, -1), dev)
+    T, H_q, D = q_shape = q.shape
+    NB, H_kv, BS, _ = pool_shape = k_cache.shape
+    S, mb = table_shape = block_table.shape
+    if not (D == pool_shape[3] and _fits(out, dt, q_shape, dev) and _fits(k_cache, dt, pool_shape, dev) and
+            _fits(v_cache, dt, pool_shape, dev) and _fits(seq_lens, i32, (S,), dev) and
+            _fits(block_table, i32, table_shape, dev)):
+        _need("out", out, dt, (T, H_q, D), dev)
+        _need("k_cache", k_cache, dt, (-1, -1, -1, D), dev)
+        _need("v_cache", v_cache, dt, (NB, H_kv, BS, D), dev)
+        _need("seq_lens", seq_lens, i32, (-1,), dev)
+        _need("block_table", block_table, i32, (seq_lens.shape[0], -1), dev)
     if score is not None:
         score._check(H_q, T, S, dev)
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != dev):
-        raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
-    _need_current(dev)
-    return T, H_q, D, NB, H_kv, BS, S, code
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
+        ws_bytes = workspace.nbytes
+    if dev != torch._C._cuda_getDevice():
+        _need_current(dev)
+    return T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes
 
 
 def pa_decode_scored_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -524,14 +552,16 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_table, seq_lens, max_seq_le
     """pa_decode with scored attention (C ABI pa_decode_scored). out, q: [S, H_q, D]; score: a
     Score or None; workspace: zeroed uint8 CUDA tensor of pa_decode_scored_workspace_size(...)
     bytes (None when that is 0); the rest as for pa_decode, any block size."""
-    T, H_q, D, NB, H_kv, BS, S, code = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace)
+    T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens,
+                                                                       score, workspace)
     if T != S:
         raise ValueError(f"decode takes one query row per sequence: {T} rows, {S} sequences")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("pa_decode_scored", load().pa_decode_scored(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), S,
-        int(max_seq_len), H_q, H_kv, D, NB, BS, float(scale), None if score is None else score._desc, code,
-        _ptr(workspace), ws_bytes, _stream(stream)))
+    st = (_lib or load()).pa_decode_scored(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        seq_lens.data_ptr(), S, int(max_seq_len), H_q, H_kv, D, NB, BS, scale, None if score is None else score._desc,
+        code, _ptr(workspace), ws_bytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_decode_scored", st)
 
 
 def pa_prefill_scored_workspace_size(num_seqs: int, max_chunk_len: int, num_q_heads: int, num_kv_heads: int,
@@ -548,13 +578,16 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
     query_start_loc: [S + 1] int32; score: a Score (key_start per row of q) or None; workspace: as
     for pa_decode_scored, of pa_prefill_scored_workspace_size(...) bytes."""
     import torch
-    T, H_q, D, NB, H_kv, BS, S, code = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace)
-    _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), q.get_device())
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("pa_prefill_scored", load().pa_prefill_scored(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        _ptr(query_start_loc), S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS, float(scale),
-        None if score is None else score._desc, code, _ptr(workspace), ws_bytes, _stream(stream)))
+    T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes = _check_scored(out, q, k_cache, v_cache, block_table, seq_lens,
+                                                                       score, workspace)
+    if not _fits(query_start_loc, torch.int32, (S + 1,), dev):
+        _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), dev)
+    st = (_lib or load()).pa_prefill_scored(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS,
+        scale, None if score is None else score._desc, code, _ptr(workspace), ws_bytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_prefill_scored", st)
 
 
 class PoolList:
@@ -600,7 +633,7 @@ def pa_move_blocks(pools, block_pairs, tokens=None, block_table=None, seq_lens=N
     NB, H_kv, BS, D = pools.shape
     _check("pa_move_blocks", load().pa_move_blocks(
         pools._ptrs, len(pools.pools), H_kv, D, NB, BS, pools.dtype_code, _ptr(block_pairs), n, _ptr(tokens),
-        _ptr(block_table), mb, _ptr(seq_lens) if block_table is not None else None, S, _stream(stream)))
+        _ptr(block_table), mb, _ptr(seq_lens) if block_table is not None else None, S, _raw_stream(stream, dev)))
 
 
 def pa_sha256(data: bytes) -> bytes:
