@@ -12,6 +12,8 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtas = 2432;   // copying CTAs below which a block is shared among several
+constexpr int kInFlight = 8;  // 16-byte loads a thread issues before their stores
 
 struct Pools {
     int4* p[kMoveMaxPools];
@@ -21,7 +23,7 @@ __global__ void __launch_bounds__(kThreads) move_blocks_kernel(const __grid_cons
                                                                const __grid_constant__ MoveArgs a) {
     const int2* pairs = reinterpret_cast<const int2*>(a.pairs);
     if (static_cast<int32_t>(blockIdx.x) >= a.num_pairs) {  // block-table rewrite
-        if (blockIdx.y != 0) return;
+        if (blockIdx.y != 0 || blockIdx.z != 0) return;
         const int32_t ctas = static_cast<int32_t>(gridDim.x) - a.num_pairs;
         const int64_t entries = static_cast<int64_t>(a.num_seqs) * a.max_blocks;
         for (int64_t i = (static_cast<int64_t>(blockIdx.x) - a.num_pairs) * kThreads + threadIdx.x; i < entries;
@@ -42,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) move_blocks_kernel(const __grid_cons
         return;
     }
     const int2 pr = __ldg(pairs + blockIdx.x);
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
         if (pr.x < 0 || pr.x >= a.num_blocks || pr.y < 0 || pr.y >= a.num_blocks) raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
         if (a.block_table != nullptr && blockIdx.x > 0 && __ldg(&pairs[blockIdx.x - 1].x) >= pr.x)
             raise_error(a.err, PA_DEVERR_PAIR_ORDER);
@@ -51,14 +53,26 @@ __global__ void __launch_bounds__(kThreads) move_blocks_kernel(const __grid_cons
     int4* pool = pools.p[blockIdx.y];
     const int4* src = pool + static_cast<int64_t>(pr.x) * a.block_chunks;
     int4* dst = pool + static_cast<int64_t>(pr.y) * a.block_chunks;
-    if (a.tokens == nullptr) {
-        for (int32_t c = threadIdx.x; c < a.block_chunks; c += kThreads) dst[c] = src[c];
-        return;
+    // runs of n chunks, one per head (whole blocks: one run); this CTA's share of all of them
+    const int32_t head = a.tokens ? a.block_size * a.row_chunks : a.block_chunks;
+    const int32_t n = a.tokens ? min(max(__ldg(a.tokens + blockIdx.x), 0), a.block_size) * a.row_chunks : head;
+    const int32_t total = a.block_chunks / head * n;
+    const int32_t share = (total + static_cast<int32_t>(gridDim.z) - 1) / static_cast<int32_t>(gridDim.z);
+    const int32_t end = min(total, static_cast<int32_t>(blockIdx.z + 1) * share);
+    int32_t c = static_cast<int32_t>(blockIdx.z) * share + threadIdx.x;
+    for (; c < end; c += kInFlight * kThreads) {
+        int4 v[kInFlight];
+        int32_t at[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int32_t i = c + k * kThreads, h = i / n;
+            at[k] = h * head + (i - h * n);
+            if (i < end) v[k] = src[at[k]];
+        }
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k)
+            if (c + k * kThreads < end) dst[at[k]] = v[k];
     }
-    const int32_t n = min(max(__ldg(a.tokens + blockIdx.x), 0), a.block_size) * a.row_chunks;  // chunks per head
-    const int32_t head = a.block_size * a.row_chunks;
-    for (int32_t h = 0; h * head < a.block_chunks; ++h)
-        for (int32_t c = threadIdx.x; c < n; c += kThreads) dst[h * head + c] = src[h * head + c];
 }
 
 }  // namespace
@@ -73,7 +87,11 @@ cudaError_t launch_move_blocks(const MoveArgs& a, void* const* pools, int32_t nu
         const int64_t entries = m.block_table ? static_cast<int64_t>(m.num_seqs) * m.max_blocks : 0;
         const int64_t table_ctas = (entries + kThreads - 1) / kThreads < 512 ? (entries + kThreads - 1) / kThreads : 512;
         if (m.num_pairs + table_ctas == 0) return cudaSuccess;
-        const dim3 grid(static_cast<unsigned>(m.num_pairs + table_ctas), n > 0 ? n : 1);
+        // few blocks: each goes to several CTAs, of at least kInFlight chunks a thread
+        const int64_t whole = static_cast<int64_t>(m.num_pairs) * n, most = m.block_chunks / (kThreads * kInFlight);
+        int64_t shares = whole > 0 ? (kCtas + whole - 1) / whole : 1;
+        if (shares > most) shares = most;
+        const dim3 grid(static_cast<unsigned>(m.num_pairs + table_ctas), n > 0 ? n : 1, shares > 1 ? static_cast<unsigned>(shares) : 1);
         move_blocks_kernel<<<grid, kThreads, 0, stream>>>(ps, m);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -634,7 +634,7 @@ PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t n
     const int64_t row_bytes = static_cast<int64_t>(head_dim) * elem_bytes(dtype);
     if (row_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
     const int64_t chunks = row_bytes / 16 * num_kv_heads * block_size;
-    if (chunks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (chunks > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;  // the copies count chunks in 32 bits, with room to step past the end
     if (block_table && (num_seqs < 0 || max_blocks_per_seq <= 0 || !seq_lens || !aligned4(block_table) || !aligned4(seq_lens)))
         return PA_ERR_INVALID_ARG;
     if (n_pairs == 0) return PA_OK;
