@@ -499,12 +499,11 @@ class Score:
         import torch
         if self.alibi_slopes is self.key_start is self.prefix_len is None:
             return
-        if self.alibi_slopes is not None:
-            _need("alibi_slopes", self.alibi_slopes, torch.float32, (H_q,), device)
-        if self.key_start is not None:
-            _need("key_start", self.key_start, torch.int32, (rows,), device)
-        if self.prefix_len is not None:
-            _need("prefix_len", self.prefix_len, torch.int32, (S,), device)
+        for name, t, dtype, n in (("alibi_slopes", self.alibi_slopes, torch.float32, H_q),
+                                  ("key_start", self.key_start, torch.int32, rows),
+                                  ("prefix_len", self.prefix_len, torch.int32, S)):
+            if t is not None and not _fits(t, dtype, (n,), device):
+                _need(name, t, dtype, (n,), device)
 
 
 def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace):

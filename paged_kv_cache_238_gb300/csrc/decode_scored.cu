@@ -738,8 +738,7 @@ cudaError_t launch_impl(const DecodeArgs& d, const ScoreArgs& score, const Decod
         if (score.key_start) a.score.key_start = score.key_start + s0;
         if (score.prefix_len) a.score.prefix_len = score.prefix_len + s0;
         const Layout l = layout(NW, plan.stages, hs, D, S);
-        e = cudaFuncSetAttribute(decode_scored_kernel<D, NW, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(l.total));
+        e = allow_smem<decode_scored_kernel<D, NW, NH>>(static_cast<int>(l.total));
         if (e != cudaSuccess) return e;
         cfg.dynamicSmemBytes = l.total;
         e = cudaLaunchKernelEx(&cfg, decode_scored_kernel<D, NW, NH>, tm_k, tm_v, a);

@@ -298,6 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
 
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // launched while the kernel before drains: nothing is read before it is done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
     __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_seq;
     __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
@@ -846,18 +849,26 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t st
     if (e != cudaSuccess) return e;
     e = encode_bf16_2d_sw128(&tm_v, a.v_cache, D, rows, 64, kPageTokens);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(prefill_scored_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(Smem<D>::total));
+    e = allow_smem<prefill_scored_kernel<D, MODE>>(static_cast<int>(Smem<D>::total));
     if (e != cudaSuccess) return e;
     const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
     const dim3 grid((a.max_chunk_len + 2 * TT - 1) / (2 * TT), a.num_kv_heads, a.num_seqs);
-    prefill_scored_kernel<D, MODE><<<grid, kThreads, Smem<D>::total, stream>>>(
-        tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(a.q), a.block_table,
-        a.max_blocks_per_seq, a.seq_lens, a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens,
-        a.max_chunk_len, sc, a.err);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<D>::total;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_scored_kernel<D, MODE>, tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out),
+                              static_cast<const __nv_bfloat16*>(a.q), a.block_table, a.max_blocks_per_seq, a.seq_lens,
+                              a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens, a.max_chunk_len,
+                              sc, a.err);
 }
 
 template <int D>

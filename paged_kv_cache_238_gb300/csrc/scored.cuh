@@ -8,9 +8,31 @@
 // (the window part), so a kernel walks only their pages.
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "pa_device.cuh"
 
 namespace pa {
+
+// Lets a kernel use this much dynamic shared memory on the current device. The runtime is asked once
+// per kernel, device and larger size, not once per launch (it takes part of a microsecond).
+template <auto* Kernel>
+cudaError_t allow_smem(int bytes) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> allowed[kDevices];
+    static std::mutex mutex;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (allowed[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) allowed[dev].store(bytes, std::memory_order_release);
+    return e;
+}
 
 struct KeySpans {
     int32_t a0, a1, b0, b1;

@@ -2,11 +2,13 @@
 //
 // A CTA takes up to R rows (R = 4 or 16) that share a kv head: the q heads of a decode row, or the
 // q heads of R / G consecutive tokens of a chunk, so that each K and V element it reads serves all of
-// them. Its eight warps take the 16-token pages that some row sees in turn. Scores: a lane holds one
-// key and every other row (two lanes a key), so a score is one thread's dot product, q coming from
-// shared memory by broadcast, and the page's maximum takes four shuffles a row. Then lanes change
-// roles, through shared memory: a lane holds head_dim / 32 columns of the output of all R rows and
-// walks the page's keys. The softmax runs online per warp in the log2 domain; the warps' (max, sum,
+// them. Its eight warps take the 16-token pages that some row sees in turn; each has room for one K and
+// one V page, and the next K page is on its way while the V page is used, and the other way round.
+// Scores: a lane multiplies 4 keys by 8 rows (R = 4: by 4) over a fourth (an eighth) of the columns, so
+// that a value out of shared memory serves 4 or 8 products; a reduction that also scatters leaves each
+// lane the scores of one key with half of the rows, and the page's maximum takes four shuffles a row.
+// Then lanes change roles, through shared memory: a lane holds head_dim / 32 columns of the output of
+// all R rows and walks the page's keys. Products run as packed pairs (two elements an instruction). The softmax runs online per warp in the log2 domain; the warps' (max, sum,
 // output) meet in shared memory, and partitions of a decode row's pages in the workspace, where the
 // last CTA to arrive merges them by the same rule:
 //   M = max_p m_p,  w_p = l_p 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p.
@@ -23,27 +25,72 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewRows = 4, kManyRows = 16;  // R: rows of a CTA
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr float kLag = 8.f;  // log2 units
 constexpr int32_t kFar = 0x7fffffff;
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const uint16_t* p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xffff0000u));
+__device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-// E consecutive elements (2 or 4).
-__device__ __forceinline__ void load_n(const float* p, float (&x)[2]) {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-    x[0] = v.x, x[1] = v.y;
+// Four consecutive elements as two packed pairs.
+struct Pairs {
+    uint64_t lo, hi;
+};
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
 }
-__device__ __forceinline__ void load_n(const uint16_t* p, float (&x)[2]) {
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p));
-    x[0] = __uint_as_float(v << 16), x[1] = __uint_as_float(v & 0xffff0000u);
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pairs load4(const float* p) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    return Pairs{v.x, v.y};
+}
+__device__ __forceinline__ Pairs load4(const uint16_t* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return Pairs{pack2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)),
+                 pack2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u))};
+}
+// E consecutive elements (2 or 4), each twice.
+__device__ __forceinline__ void load_twice(const float* p, uint64_t (&x)[2]) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = pack2(v.x, v.x), x[1] = pack2(v.y, v.y);
+}
+__device__ __forceinline__ void load_twice(const uint16_t* p, uint64_t (&x)[2]) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    const float lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xffff0000u);
+    x[0] = pack2(lo, lo), x[1] = pack2(hi, hi);
 }
 template <typename T>
-__device__ __forceinline__ void load_n(const T* p, float (&x)[4]) {
-    const float4 v = load4(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+__device__ __forceinline__ void load_twice(const T* p, uint64_t (&x)[4]) {
+    const Pairs v = load4(p);
+    float f[4];
+    unpack2(v.lo, f[0], f[1]);
+    unpack2(v.hi, f[2], f[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = pack2(f[e], f[e]);
+}
+
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {  // all but the N groups committed last have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename T>
@@ -71,16 +118,21 @@ struct SimtArgs {
     uint32_t* err;
 };
 
-// Shared memory, in floats: the rows' q while pages are walked, then the warps' outputs.
-template <int D, int R>
+// Shared memory in bytes: q, weights and pages while pages are walked, then the warps' outputs.
+template <typename T, int D, int R>
 struct Smem {
-    static constexpr int q_stride = D + 4;  // two rows in a broadcast lie in different banks
+    static constexpr int pad = 16 / sizeof(T);  // rows 16 bytes apart in bank: a lane reads its own row
+    static constexpr int q_stride = D + 4;      // two rows in a broadcast lie in different banks
     static constexpr int q = 0;
-    static constexpr int p = q + R * q_stride;             // [kWarps][16 keys][R]
-    static constexpr int corr = p + kWarps * 16 * R;       // [kWarps][R]
-    static constexpr int o = 0;                            // [kWarps][R][D]
-    static constexpr int walk = corr + kWarps * R, join = o + kWarps * R * D;
-    static constexpr int bytes = 4 * (walk > join ? walk : join);
+    static constexpr int p = q + 4 * R * q_stride;                // [kWarps][16 keys][R]
+    static constexpr int p_stride = R == 4 ? 4 : R + 4;           // lanes store their keys' weights in different banks
+    static constexpr int corr = p + 4 * kWarps * 16 * p_stride;  // [kWarps][R]
+    static constexpr int page = corr + 4 * kWarps * R;     // [kWarps] K page, V page
+    static constexpr int k_stride = D + pad;
+    static constexpr int k_bytes = 16 * k_stride * static_cast<int>(sizeof(T));
+    static constexpr int page_bytes = k_bytes + 16 * D * static_cast<int>(sizeof(T));
+    static constexpr int walk = page + kWarps * page_bytes, join = 4 * kWarps * R * D;
+    static constexpr int bytes = walk > join ? walk : join;
 };
 
 template <typename T, int D, int R>
@@ -89,13 +141,12 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
                                                                const T* __restrict__ v_cache,
                                                                const __grid_constant__ SimtArgs a) {
     constexpr int E = D / 32, RL = R / 2;
-    using L = Smem<D, R>;
+    using L = Smem<T, D, R>;
     extern __shared__ float4 smem4[];
-    float* sm = reinterpret_cast<float*>(smem4);
+    char* sm = reinterpret_cast<char*>(smem4);
     __shared__ KeySpans spans[R];
     __shared__ float slopes[R];
     __shared__ int32_t where[R];      // the rows' positions
-    __shared__ KeySpans hull, inner;  // keys that some row sees (and what lies between them), that all rows see
     __shared__ float jm[kWarps][R], jl[kWarps][R], jM[R], jden[R];
     __shared__ int32_t last_part;
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -127,181 +178,241 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
         n_tok = min(a.tokens, chunk - t0);
     }
     const int32_t n_rows = n_tok * heads;
-    if (warp == 0) {
-        KeySpans sp{0, 0, 0, 0};
-        const bool valid = lane < n_rows;
-        if (valid) {
-            const int32_t tt = lane / heads, row = row0 + tt;
-            sp = key_spans(len, pos0 + tt, a.score.key_start ? __ldg(a.score.key_start + row) : 0,
-                           a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window);
-            slopes[lane] = a.score.slopes ? __ldg(a.score.slopes + h0 + (lane - tt * heads)) * kLog2e : 0.f;
-            where[lane] = pos0 + tt;
-        } else if (lane < R) {
-            slopes[lane] = 0.f;
-            where[lane] = 0;
-        }
-        if (lane < R) spans[lane] = sp;
-        const bool in_a = sp.a0 < sp.a1, in_b = sp.b0 < sp.b1;
-        const int32_t ha0 = __reduce_min_sync(~0u, in_a ? sp.a0 : kFar), ha1 = __reduce_max_sync(~0u, in_a ? sp.a1 : 0);
-        const int32_t hb0 = __reduce_min_sync(~0u, in_b ? sp.b0 : kFar), hb1 = __reduce_max_sync(~0u, in_b ? sp.b1 : 0);
-        const int32_t ia0 = __reduce_max_sync(~0u, valid ? sp.a0 : 0), ia1 = __reduce_min_sync(~0u, valid ? sp.a1 : kFar);
-        const int32_t ib0 = __reduce_max_sync(~0u, valid ? sp.b0 : 0), ib1 = __reduce_min_sync(~0u, valid ? sp.b1 : kFar);
-        if (lane == 0) {
-            hull = KeySpans{ha0 < ha1 ? ha0 : 0, ha0 < ha1 ? ha1 : 0, hb0 < hb1 ? hb0 : 0, hb0 < hb1 ? hb1 : 0};
-            inner = KeySpans{ia0, ia1, ib0, ib1};
-        }
+    // every warp works out the rows' spans, so that its first pages can be on their way before the rows' q
+    KeySpans sp{0, 0, 0, 0};
+    const bool valid = lane < n_rows;
+    if (valid) {
+        const int32_t tt = lane / heads;
+        sp = key_spans(len, pos0 + tt, a.score.key_start ? __ldg(a.score.key_start + row0 + tt) : 0,
+                       a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window);
     }
-    // ---- q, scaled, rows without a query zero ---------------------------------------------------
-    for (int32_t i = tid; i < R * D / 4; i += kThreads) {
-        const int32_t r = i / (D / 4), c = i - r * (D / 4);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n_rows) {
-            const int32_t tt = r / heads;
-            v = load4(q + (static_cast<int64_t>(row0 + tt) * a.num_q_heads + h0 + (r - tt * heads)) * D + c * 4);
-            v.x *= a.scale, v.y *= a.scale, v.z *= a.scale, v.w *= a.scale;
-        }
-        *reinterpret_cast<float4*>(sm + L::q + r * L::q_stride + c * 4) = v;
+    if (warp == 0 && lane < R) {
+        const int32_t tt = lane / heads;
+        spans[lane] = sp;
+        slopes[lane] = valid && a.score.slopes ? __ldg(a.score.slopes + h0 + (lane - tt * heads)) * kLog2e : 0.f;
+        where[lane] = pos0 + tt;
     }
-    __syncthreads();
-
+    const bool in_a = sp.a0 < sp.a1, in_b = sp.b0 < sp.b1;
+    KeySpans hull, inner;  // keys that some row sees, with what lies between them; keys that all rows see
+    hull.a0 = __reduce_min_sync(~0u, in_a ? sp.a0 : kFar);
+    hull.a1 = __reduce_max_sync(~0u, in_a ? sp.a1 : 0);
+    hull.b0 = __reduce_min_sync(~0u, in_b ? sp.b0 : kFar);
+    hull.b1 = __reduce_max_sync(~0u, in_b ? sp.b1 : 0);
+    if (hull.a0 == kFar) hull.a0 = 0;
+    if (hull.b0 == kFar) hull.b0 = 0;
+    inner.a0 = __reduce_max_sync(~0u, valid ? sp.a0 : 0);
+    inner.a1 = __reduce_min_sync(~0u, valid ? sp.a1 : kFar);
+    inner.b0 = __reduce_max_sync(~0u, valid ? sp.b0 : 0);
+    inner.b1 = __reduce_min_sync(~0u, valid ? sp.b1 : kFar);
     const PageList pl = page_list(hull);
     const int32_t parts = (pl.n + a.part_pages - 1) / a.part_pages, part = blockIdx.z;
     if (part >= max(parts, 1)) return;  // uniform over the CTA
-    const int32_t end = min(pl.n, (part + 1) * a.part_pages);
-    const int32_t key = lane & 15, hh = lane >> 4;  // this lane's key of a page; its rows are 2 i + hh
+    const int32_t end = min(pl.n, (part + 1) * a.part_pages), first = part * a.part_pages + warp;
     const int32_t* table = a.block_table + static_cast<int64_t>(s) * a.max_blocks;
-    float* ps = sm + L::p + warp * 16 * R;    // [key][hh RL + i]: the weights
-    float* corr = sm + L::corr + warp * R;    // [hh RL + i]: what the outputs so far are scaled by
-    float m[RL], l[RL], acc[R][E];            // acc[hh RL + i]
+    T* k_page = reinterpret_cast<T*>(sm + L::page + warp * L::page_bytes);
+    T* v_page = k_page + 16 * L::k_stride;
+    auto block_of = [&](int32_t i) { return i < end ? __ldg(table + (pl.page(i) >> a.sub_log2)) : 0; };
+    auto in_pool = [&](int32_t block) { return block >= 0 && block < a.num_blocks; };
+    // copy list page i of this warp, in this block, from a cache: 16 rows of D elements
+    auto fetch = [&](const T* cache, T* dst, int32_t stride, int32_t i, int32_t block) {
+        if (i < end && in_pool(block)) {
+            const int64_t row = ((static_cast<int64_t>(block) * a.num_kv_heads + hk) << a.sub_log2) +
+                                (pl.page(i) & ((1 << a.sub_log2) - 1));
+            const T* src = cache + row * (kPageTokens * D);
+            constexpr int kN = 16 / sizeof(T), kChunks = D / kN;  // 16-byte chunks of a row
+#pragma unroll
+            for (int c = lane; c < 16 * kChunks; c += 32) cp_async16(dst + c / kChunks * stride + c % kChunks * kN, src + c * kN);
+        }
+        cp_async_commit();
+    };
+    int32_t block = block_of(first), block_next = block_of(first + kWarps);
+    fetch(k_cache, k_page, L::k_stride, first, block);
+    fetch(v_cache, v_page, D, first, block);
+    // ---- q, scaled, rows without a query zero ---------------------------------------------------
+    for (int32_t i = tid; i < R * D / 4; i += kThreads) {
+        const int32_t r = i / (D / 4), c = i - r * (D / 4);
+        Pairs v{0ull, 0ull};
+        if (r < n_rows) {
+            const int32_t tt = r / heads;
+            v = load4(q + (static_cast<int64_t>(row0 + tt) * a.num_q_heads + h0 + (r - tt * heads)) * D + c * 4);
+            const uint64_t scale = pack2(a.scale, a.scale);
+            v.lo = mul2(v.lo, scale), v.hi = mul2(v.hi, scale);
+        }
+        *reinterpret_cast<Pairs*>(sm + L::q + 4 * (r * L::q_stride + c * 4)) = v;
+    }
+    __syncthreads();
+
+    const int32_t key = lane & 15, hh = lane >> 4;  // the key of a page whose scores end here, with rows hh RL + i
+    // products: keys key & ~3 .., RT rows from qrow, the ds-th of DS parts of the columns
+    constexpr int RT = R == 4 ? 4 : R / 2, DS = R == 4 ? 8 : 4;
+    const int32_t qrow = R == 4 ? 0 : hh * RL, ds = R == 4 ? (lane & 3) + 4 * hh : lane & 3;
+    float* ps = reinterpret_cast<float*>(sm + L::p) + warp * 16 * L::p_stride;  // [key][row]: the weights
+    float* corr = reinterpret_cast<float*>(sm + L::corr) + warp * R;  // [row]: what the outputs so far are scaled by
+    float m[RL], l[RL];
+    uint64_t acc[R / 2][E];  // outputs of rows 2 r, 2 r + 1
 #pragma unroll
     for (int i = 0; i < RL; ++i) m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R / 2; ++r)
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
-    int32_t i0 = part * a.part_pages + warp;
-    int32_t phys = i0 < end ? __ldg(table + (pl.page(i0) >> a.sub_log2)) : 0;
-    for (; i0 < end; i0 += kWarps) {
-        const int32_t page = pl.page(i0), block = phys, j0 = page * kPageTokens, j = j0 + key;
-        if (i0 + kWarps < end) phys = __ldg(table + (pl.page(i0 + kWarps) >> a.sub_log2));
-        if (block < 0 || block >= a.num_blocks) {
-            raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
-            continue;
-        }
-        const int64_t base = ((((static_cast<int64_t>(block) * a.num_kv_heads + hk) << a.sub_log2) +
-                               (page & ((1 << a.sub_log2) - 1))) * kPageTokens) * D;
-        // ---- scores of (key, rows 2 i + hh) ----
-        float z[RL];
-#pragma unroll
-        for (int i = 0; i < RL; ++i) z[i] = 0.f;
-        const T* kp = k_cache + base + key * D;
-        const float* qs = sm + L::q + hh * L::q_stride;
-#pragma unroll
-        for (int c0 = 0; c0 < D / 4; c0 += 8) {
-            float4 kv[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) kv[c] = load4(kp + (c0 + c) * 4);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-                for (int i = 0; i < RL; ++i) {
-                    const float4 qv = *reinterpret_cast<const float4*>(qs + 2 * i * L::q_stride + (c0 + c) * 4);
-                    z[i] = fmaf(qv.x, kv[c].x, z[i]);
-                    z[i] = fmaf(qv.y, kv[c].y, z[i]);
-                    z[i] = fmaf(qv.z, kv[c].z, z[i]);
-                    z[i] = fmaf(qv.w, kv[c].w, z[i]);
-                }
-        }
-        const bool whole = (j0 >= inner.a0 && j0 + kPageTokens <= inner.a1) || (j0 >= inner.b0 && j0 + kPageTokens <= inner.b1);
-        uint32_t seen = 0xffffu;  // keys of the page that some row sees
-#pragma unroll
-        for (int i = 0; i < RL; ++i) {
-            if (a.score.cap > 0.f) z[i] = a.score.cap * tanhf(z[i] / a.score.cap);
-            z[i] *= kLog2e;
-            if (a.score.slopes) z[i] -= slopes[2 * i + hh] * static_cast<float>(abs(where[2 * i + hh] - j));
-        }
-        if (!whole) {
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < RL; ++i) {
-                const bool sees = spans[2 * i + hh].sees(j);
-                any |= sees;
-                if (!sees) z[i] = -INFINITY;
-            }
-            seen = __ballot_sync(0xffffffffu, any);
-            seen = (seen | seen >> 16) & 0xffffu;
-            if (seen == 0u) continue;
-        }
-        // ---- weights against the rows' running maxima ----
-        bool grow = false;
-        float mn[RL];
-#pragma unroll
-        for (int i = 0; i < RL; ++i) mn[i] = z[i];
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-#pragma unroll
-            for (int i = 0; i < RL; ++i) mn[i] = fmaxf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], off));
-#pragma unroll
-        for (int i = 0; i < RL; ++i) {
-            grow |= mn[i] > m[i];
-            mn[i] = fmaxf(mn[i], m[i]);
-            const float ref = mn[i] == -INFINITY ? 0.f : mn[i];  // nothing finite yet: weights are 0, not NaN
-            z[i] = exp2f(z[i] - ref);
-        }
-        const bool rescale = __any_sync(0xffffffffu, grow);
-        if (rescale) {
-#pragma unroll
-            for (int i = 0; i < RL; ++i) {
-                const float f = exp2f(m[i] - (mn[i] == -INFINITY ? 0.f : mn[i]));
-                l[i] *= f;
-                m[i] = mn[i];
-                if (key == 0) corr[hh * RL + i] = f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < RL; ++i) {
-            l[i] += z[i];
-            ps[key * R + hh * RL + i] = z[i];
-        }
+        for (int e = 0; e < E; ++e) acc[r][e] = 0ull;
+    for (int32_t i0 = first; i0 < end; i0 += kWarps) {
+        const int32_t j0 = pl.page(i0) * kPageTokens, j = j0 + key;
+        uint32_t seen = 0u;  // keys of the page that some row sees
+        if (in_pool(block)) seen = 0xffffu;
+        else if (lane == 0) raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
+        cp_async_wait<1>();
         __syncwarp();
-        if (rescale) {
+        // ---- scores of (key, rows hh RL + i) ----
+        float z[RL];
+        if (seen) {
+            uint64_t z2[4][RT];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float f = corr[r];
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[r][e] *= f;
-            }
-        }
-        // ---- outputs: columns lane E .. of all rows ----
-        const T* vp = v_cache + base + lane * E;
+                for (int i = 0; i < RT; ++i) z2[k][i] = 0ull;
 #pragma unroll
-        for (int k0 = 0; k0 < kPageTokens; k0 += 8) {
-            float vv[8][E];
+            for (int c = 0; c < D / 4 / DS; ++c) {
+                const int col = (c * DS + ds) * 4;
+                Pairs kv[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (seen >> (k0 + k) & 1u) load_n(vp + (k0 + k) * D, vv[k]);
-                else
+                for (int k = 0; k < 4; ++k) kv[k] = load4(k_page + ((key & 12) + k) * L::k_stride + col);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) vv[k][e] = 0.f;
-            }
+                for (int i = 0; i < RT; ++i) {
+                    const Pairs qv = load4(reinterpret_cast<const float*>(sm + L::q) + (qrow + i) * L::q_stride + col);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int r = 0; r < R; r += 4) {
-                    const float4 w = *reinterpret_cast<const float4*>(ps + (k0 + k) * R + r);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        acc[r][e] = fmaf(w.x, vv[k][e], acc[r][e]);
-                        acc[r + 1][e] = fmaf(w.y, vv[k][e], acc[r + 1][e]);
-                        acc[r + 2][e] = fmaf(w.z, vv[k][e], acc[r + 2][e]);
-                        acc[r + 3][e] = fmaf(w.w, vv[k][e], acc[r + 3][e]);
+                    for (int k = 0; k < 4; ++k) {
+                        z2[k][i] = fma2(qv.lo, kv[k].lo, z2[k][i]);
+                        z2[k][i] = fma2(qv.hi, kv[k].hi, z2[k][i]);
                     }
                 }
+            }
+            // sum over the column parts: lanes that differ in bits 1, 0 (keys) and, R = 4, 4 (rows)
+            float y[4][RT];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    float lo, hi;
+                    unpack2(z2[k][i], lo, hi);
+                    y[k][i] = lo + hi;
+                }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const bool up = lane & 2, odd = lane & 1;
+                const float s0 = up ? y[0][i] : y[2][i], s1 = up ? y[1][i] : y[3][i];
+                const float k0 = (up ? y[2][i] : y[0][i]) + __shfl_xor_sync(0xffffffffu, s0, 2);
+                const float k1 = (up ? y[3][i] : y[1][i]) + __shfl_xor_sync(0xffffffffu, s1, 2);
+                y[0][i] = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+            }
+#pragma unroll
+            for (int i = 0; i < RL; ++i) {
+                z[i] = y[0][i];
+                if constexpr (RT > RL)
+                    z[i] = (hh ? y[0][i + RL] : y[0][i]) + __shfl_xor_sync(0xffffffffu, hh ? y[0][i] : y[0][i + RL], 16);
+            }
         }
+        __syncwarp();  // the K page has been read
+        const int32_t block_after = block_of(i0 + 2 * kWarps);
+        fetch(k_cache, k_page, L::k_stride, i0 + kWarps, block_next);
+        const bool whole = (j0 >= inner.a0 && j0 + kPageTokens <= inner.a1) || (j0 >= inner.b0 && j0 + kPageTokens <= inner.b1);
+        if (seen) {
+            if (a.score.cap > 0.f) {
+#pragma unroll
+                for (int i = 0; i < RL; ++i) z[i] = a.score.cap * tanhf(z[i] / a.score.cap);
+            }
+#pragma unroll
+            for (int i = 0; i < RL; ++i) z[i] *= kLog2e;
+            if (a.score.slopes) {
+#pragma unroll
+                for (int i = 0; i < RL; ++i) z[i] -= slopes[hh * RL + i] * static_cast<float>(abs(where[hh * RL + i] - j));
+            }
+            if (!whole) {
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < RL; ++i) {
+                    const bool sees = spans[hh * RL + i].sees(j);
+                    any |= sees;
+                    if (!sees) z[i] = -INFINITY;
+                }
+                seen = __ballot_sync(0xffffffffu, any);
+                seen = (seen | seen >> 16) & 0xffffu;
+            }
+        }
+        bool rescale = false;
+        if (seen) {
+            // ---- weights against the rows' references: maxima of earlier pages, kept until one is
+            // exceeded by more than kLag (the weights then stay below 2^kLag, and most pages rescale nothing)
+            float mx[RL];
+            bool grow = false;
+#pragma unroll
+            for (int i = 0; i < RL; ++i) mx[i] = z[i];
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+                for (int i = 0; i < RL; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+#pragma unroll
+            for (int i = 0; i < RL; ++i) grow |= mx[i] > m[i] + kLag;
+            rescale = __any_sync(0xffffffffu, grow);
+            if (rescale) {
+#pragma unroll
+                for (int i = 0; i < RL; ++i) {
+                    const float up = fmaxf(mx[i], m[i]);
+                    const float f = exp2_approx(m[i] - (up == -INFINITY ? 0.f : up));
+                    l[i] *= f;
+                    m[i] = up;
+                    if (key == 0) corr[hh * RL + i] = f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RL; ++i)  // nothing finite yet: weights are 0, not NaN
+                z[i] = exp2_approx(z[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+#pragma unroll
+            for (int i = 0; i < RL; i += 2) {
+                l[i] += z[i];
+                l[i + 1] += z[i + 1];
+                *reinterpret_cast<float2*>(ps + key * L::p_stride + hh * RL + i) = make_float2(z[i], z[i + 1]);
+            }
+        }
+        cp_async_wait<1>();
         __syncwarp();
+        if (seen) {
+            if (seen != 0xffffu) {  // keys that no row sees: their weights are 0, their V may be anything
+                for (uint32_t w = ~seen & 0xffffu; w != 0u; w &= w - 1)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v_page[(__ffs(w) - 1) * D + lane * E + e] = T(0);
+            }
+            if (rescale) {
+#pragma unroll
+                for (int r = 0; r < R / 2; ++r) {
+                    const uint64_t f = *reinterpret_cast<const uint64_t*>(corr + 2 * r);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[r][e] = mul2(acc[r][e], f);
+                }
+            }
+            // ---- outputs: columns lane E .. of all rows (each lane reads what it zeroed itself) ----
+#pragma unroll
+            for (int k = 0; k < kPageTokens; ++k) {
+                uint64_t vv[E];
+                load_twice(v_page + k * D + lane * E, vv);
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const Pairs w = load4(ps + k * L::p_stride + r);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        acc[r / 2][e] = fma2(w.lo, vv[e], acc[r / 2][e]);
+                        acc[r / 2 + 1][e] = fma2(w.hi, vv[e], acc[r / 2 + 1][e]);
+                    }
+                }
+            }
+        }
+        __syncwarp();  // the V page and the weights have been read
+        fetch(v_cache, v_page, D, i0 + kWarps, block_next);
+        block = block_next;
+        block_next = block_after;
     }
 
-    // ---- the warps' parts meet; row order hh RL + i -> row 2 i + hh -------------------------------
+    // ---- the warps' parts meet -------------------------------
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1)
 #pragma unroll
@@ -309,10 +420,11 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
     if (key == 0)
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
-            jm[warp][2 * i + hh] = m[i];
-            jl[warp][2 * i + hh] = l[i];
+            jm[warp][hh * RL + i] = m[i];
+            jl[warp][hh * RL + i] = l[i];
         }
-    __syncthreads();  // q and the weights are done with
+    cp_async_wait<0>();
+    __syncthreads();  // q, weights and pages are done with
     if (tid < R) {
         float M = -INFINITY, den = 0.f;
 #pragma unroll
@@ -320,25 +432,29 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(jm[w][tid] - ref);  // a warp without keys: m = -inf, weight 0
+            const float f = exp2_approx(jm[w][tid] - ref);  // a warp without keys: m = -inf, weight 0
             den = fmaf(jl[w][tid], f, den);
             jm[w][tid] = f;
         }
         jM[tid] = M;
         jden[tid] = den;
     }
+    float* const joined = reinterpret_cast<float*>(sm);  // [kWarps][R][D]
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        float* o = sm + L::o + (warp * R + (i % RL) * 2 + i / RL) * D + lane * E;
+    for (int i = 0; i < R; i += 2)
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = acc[i][e];
-    }
+        for (int e = 0; e < E; ++e) {
+            float x0, x1;
+            unpack2(acc[i / 2][e], x0, x1);
+            joined[(warp * R + i) * D + lane * E + e] = x0;
+            joined[(warp * R + i + 1) * D + lane * E + e] = x1;
+        }
     __syncthreads();
     for (int32_t i = tid; i < n_rows * D; i += kThreads) {
         const int32_t r = i / D, d = i - r * D;
         float num = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) num = fmaf(sm[L::o + (w * R + r) * D + d], jm[w][r], num);
+        for (int w = 0; w < kWarps; ++w) num = fmaf(joined[(w * R + r) * D + d], jm[w][r], num);
         const float o = jden[r] == 0.f ? 0.f : num / jden[r];
         const int32_t tt = r / heads;
         const int64_t head = static_cast<int64_t>(row0 + tt) * a.num_q_heads + h0 + (r - tt * heads);
@@ -372,7 +488,7 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
         float num = 0.f, den = 0.f;
         for (int32_t p = 0; p < parts; ++p) {
             const float2 v = __ldcg(ml + p);
-            const float w = v.y * exp2f(v.x - ref);
+            const float w = v.y * exp2_approx(v.x - ref);
             num = fmaf(w, __ldcg(a.ws_o + (slot0 + p) * D + d), num);
             den += w;
         }
@@ -383,9 +499,9 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
 template <typename T, int D, int R>
 cudaError_t launch_rows(void* out, const void* q, const void* k, const void* v, const SimtArgs& a, dim3 grid,
                         cudaStream_t stream) {
-    constexpr int bytes = Smem<D, R>::bytes;
-    if (bytes > 40960) {
-        const cudaError_t e = cudaFuncSetAttribute(scored_simt_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int bytes = Smem<T, D, R>::bytes;
+    if (bytes > 40960) {  // with the static part, beyond what every kernel may use
+        const cudaError_t e = allow_smem<scored_simt_kernel<T, D, R>>(bytes);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr[1];
@@ -451,7 +567,7 @@ int32_t scored_simt_head_chunks(int32_t group) {
 // Partitions so that (sequence, kv head, head chunk, partition) items fill the SMs about twice, of
 // at least kMinPages pages each.
 ScoredSimtPlan plan_scored_simt(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len, int num_sms) {
-    constexpr int64_t kMinPages = 2 * kWarps;
+    constexpr int64_t kMinPages = 32;
     ScoredSimtPlan p{};
     const int64_t items = static_cast<int64_t>(S) * Hkv * scored_simt_head_chunks(Hq / Hkv);
     const int32_t pages = max_seq_len / kPageTokens + 2;
