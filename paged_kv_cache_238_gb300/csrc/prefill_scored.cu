@@ -298,9 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
 
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // launched while the kernel before drains: nothing is read before it is done
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
     __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_seq;
     __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
@@ -795,28 +792,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         sums[half * kRows + r] = l_sum;
         named_barrier(1 + xq, 256);
         l_sum = sums[r] + sums[kRows + r];
+        named_barrier(1 + xq, 256);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             umma::fence_after_sync();
             const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-            __nv_bfloat16* orow = out + (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2);
+            // this warp's rows x D / 2 columns through its own part of the tile's Q, so that the stores go
+            // out whole lines at a time (a row's 16-byte pieces in different banks, lane by lane)
+            constexpr int kPieces = D / 16;
+            uint8_t* stage = smem + xq * kTile + (half * 4 + quad) * (32 * D);
+            const int32_t turn = D == 128 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
-                if (cnt > 0) {
-                    ld_wait_x32(tmem_o + c * 32, o);
-                }
-                if (row_valid) {
+                if (cnt > 0) ld_wait_x32(tmem_o + c * 32, o);
 #pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4) {
-                        float f[8];
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    float f[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = l_sum == 0.f ? 0.f : __uint_as_float(o[v4 * 8 + k]) * inv;
-                        *reinterpret_cast<uint4*>(orow + c * 32 + v4 * 8) =
-                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                       pack_bf16x2(f[6], f[7]));
-                    }
+                    for (int k = 0; k < 8; ++k) f[k] = l_sum == 0.f ? 0.f : __uint_as_float(o[v4 * 8 + k]) * inv;
+                    *reinterpret_cast<uint4*>(stage + lane * D + ((c * 4 + v4) ^ turn) * 16) =
+                        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                   pack_bf16x2(f[6], f[7]));
                 }
+            }
+            __syncwarp();
+            const int64_t row_off =
+                row_valid ? (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2) : -1;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int32_t i = k * 32 + lane, rr = i / kPieces, c = i % kPieces;
+                const int64_t off = __shfl_sync(0xffffffffu, row_off, rr);
+                const int32_t t = D == 128 ? rr & 7 : (rr >> 1) & 3;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * D + (c ^ t) * 16);
+                if (off >= 0) *reinterpret_cast<uint4*>(out + off + c * 8) = v;
             }
         }
     }
@@ -855,20 +864,11 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t st
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
     const dim3 grid((a.max_chunk_len + 2 * TT - 1) / (2 * TT), a.num_kv_heads, a.num_seqs);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem<D>::total;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefill_scored_kernel<D, MODE>, tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out),
-                              static_cast<const __nv_bfloat16*>(a.q), a.block_table, a.max_blocks_per_seq, a.seq_lens,
-                              a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens, a.max_chunk_len,
-                              sc, a.err);
+    prefill_scored_kernel<D, MODE><<<grid, kThreads, Smem<D>::total, stream>>>(
+        tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(a.q), a.block_table,
+        a.max_blocks_per_seq, a.seq_lens, a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens,
+        a.max_chunk_len, sc, a.err);
+    return cudaGetLastError();
 }
 
 template <int D>
