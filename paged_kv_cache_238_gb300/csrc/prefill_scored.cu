@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     // Chains of S -> softmax -> P -> PV -> next S that run independently of one another: one per query
     // tile, or, when no maximum ties the keys of a row together, one per query tile and half of the
     // key tile (chain c: query tile c & 1, half c >> 1), so that more MMA and softmax work overlaps.
-    constexpr bool kSplit = MODE == kCap;
+    constexpr bool kSplit = MODE == kCap || D == 64;
+    constexpr bool kOwnO = kSplit && MODE != kCap;  // each half of the keys has its own O and maximum
     constexpr int kChains = kSplit ? 4 : 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
             for (int k = 0; k < kChainKeys / 16; ++k) {  // 16 keys per instruction: 8 P columns
                 const int kk = hf * 4 + k;
-                umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                umma::mma_bf16_tmem_a(tmem + 256 + x * 128 + (kOwnO ? hf * D : 0), tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                                       dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || k > 0));
             }
         };
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     ok = wait_or_abort<0>(&p_full[c], done[x] & 1, abort_flag, err);
                     umma::fence_after_sync();
                     if (ok) {
-                        pv(c, j, done[x] > 0 || c >= 2);
+                        pv(c, j, done[x] > 0 || (!kOwnO && c >= 2));
                         if (c >= kChains - 2) {  // the query tile's last chain
                             ++done[x];
                             if (j == last[x]) umma::commit(&o_done[x]);
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         const int32_t chain = kSplit ? half * 2 + xq : xq;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + xq * 128 + half * 64 + lane_off;
-        const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (D / 2) + lane_off;
+        const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (kOwnO ? D : D / 2) + lane_off;  // columns it rescales
         const float slope = (MODE == kDistance || MODE == kGeneral) && sc.slopes && row_valid
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
@@ -690,18 +691,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
-                // the row's other half of the keys is another thread's: exchange the maxima, rounded
-                // up to bf16 (any reference at or above the maximum serves, if both take the same)
-                const __nv_bfloat16 mine = __float2bfloat16_ru(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                row_max[xq][half][r] = mine;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
-                ok = wait_or_abort<kSleepSoftmax>(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if constexpr (!kOwnO) {
+                    // the row's other half of the keys is another thread's: exchange the maxima, rounded
+                    // up to bf16 (any reference at or above the maximum serves, if both take the same)
+                    const __nv_bfloat16 mine = __float2bfloat16_ru(top);
+                    row_max[xq][half][r] = mine;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
+                    ok = wait_or_abort<kSleepSoftmax>(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    top = fmaxf(__bfloat162float(mine), __bfloat162float(row_max[xq][half ^ 1][r]));
                 }
-                const float top = fmaxf(__bfloat162float(mine), __bfloat162float(row_max[xq][half ^ 1][r]));
                 grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
                 const float m_new = grow ? top : m_ref;
                 alpha = grow ? exp2_approx(m_ref - m_new) : 1.f;
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     // O holds the tiles before under the old reference; their last PV finished before
                     // this S was committed, so O can be rescaled now
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
+                    for (int c = 0; c < (kOwnO ? D : D / 2) / 32; ++c) {
                         uint32_t o[32];
                         ld_wait_x32(tmem_o + c * 32, o);
 #pragma unroll
@@ -790,8 +794,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         float* sums = reinterpret_cast<float*>(smem + xq * kTile);
         __syncwarp();
         sums[half * kRows + r] = l_sum;
+        if (kOwnO) sums[(2 + half) * kRows + r] = m_ref;
         named_barrier(1 + xq, 256);
-        l_sum = sums[r] + sums[kRows + r];
+        float w0 = 1.f, w1 = 1.f;  // weights of the halves' outputs: 1 under a common reference
+        if (kOwnO) {
+            const float m0 = sums[2 * kRows + r], m1 = sums[3 * kRows + r], top = fmaxf(m0, m1);
+            w0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - top);
+            w1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - top);
+        }
+        l_sum = w0 * sums[r] + w1 * sums[kRows + r];
         named_barrier(1 + xq, 256);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
@@ -805,7 +816,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
-                if (cnt > 0) ld_wait_x32(tmem_o + c * 32, o);
+                const uint32_t cols = tmem + 256 + xq * 128 + half * (D / 2) + c * 32 + lane_off;
+                if (cnt > 0) ld_wait_x32(cols, o);
+                if (kOwnO && cnt > 0) {
+                    uint32_t o1[32];
+                    ld_wait_x32(cols + D, o1);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(fmaf(w0, __uint_as_float(o[k]), w1 * __uint_as_float(o1[k])));
+                }
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     float f[8];
