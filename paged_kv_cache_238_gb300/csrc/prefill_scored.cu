@@ -300,28 +300,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
-    __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_seq;
+    __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_prefix;
+    __shared__ int4 lpt_seq;  // its number, first row of q, rows, length
     __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
     __shared__ uint32_t seen_own[8];  // documents: the CTA's own positions that some row sees
     __shared__ __nv_bfloat16 row_max[2][2][kRows];  // per query tile and half of the keys: the rows' maxima
-    int32_t seq = blockIdx.z;
+    int32_t seq = blockIdx.z, q0, C, L, prefix = 0;
     const int32_t n_seqs = gridDim.z;
     if (n_seqs > 1 && n_seqs <= kLptMaxSeqs) {
-        if (tid < n_seqs) lpt_len[tid] = __ldg(seq_lens + tid);
-        __syncthreads();
+        // every sequence's numbers are read at once, so that the chosen one's need no second trip to memory
+        int32_t start = 0, n = 0, len = 0, pre = 0;
         if (tid < n_seqs) {
-            const int32_t mine = lpt_len[tid];
-            int32_t rank = 0;
-            for (int32_t u = 0; u < n_seqs; ++u) rank += (lpt_len[u] > mine || (lpt_len[u] == mine && u < tid)) ? 1 : 0;
-            if (rank == seq) lpt_seq = tid;
+            len = __ldg(seq_lens + tid);
+            start = __ldg(query_start_loc + tid);
+            n = __ldg(query_start_loc + tid + 1) - start;
+            if (sc.prefix_len) pre = __ldg(sc.prefix_len + tid);
+            lpt_len[tid] = len;
         }
         __syncthreads();
-        seq = lpt_seq;
+        if (tid < n_seqs) {
+            int32_t rank = 0;
+#pragma unroll 8
+            for (int32_t u = 0; u < n_seqs; ++u) rank += (lpt_len[u] > len || (lpt_len[u] == len && u < tid)) ? 1 : 0;
+            if (rank == seq) lpt_seq = make_int4(tid, start, n, len), lpt_prefix = pre;
+        }
+        __syncthreads();
+        const int4 chosen = lpt_seq;
+        seq = chosen.x, q0 = chosen.y, C = chosen.z, L = chosen.w, prefix = lpt_prefix;
+    } else {
+        q0 = __ldg(query_start_loc + seq);
+        C = __ldg(query_start_loc + seq + 1) - q0;
+        L = __ldg(seq_lens + seq);
+        if (sc.prefix_len) prefix = __ldg(sc.prefix_len + seq);
     }
     const int32_t h = blockIdx.y, TT = kRows / G, Hq = G * num_kv_heads;
     const int32_t pair = gridDim.x - 1 - blockIdx.x;  // the longest pairs start first
-    const int32_t q0 = __ldg(query_start_loc + seq), C = __ldg(query_start_loc + seq + 1) - q0;
-    const int32_t L = __ldg(seq_lens + seq);
     if (C < 0 || C > max_chunk || C > L || L > cap_tokens) {
         if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
         return;
@@ -329,17 +342,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const int32_t t0a = 2 * pair * TT, t0b = t0a + TT;
     if (t0a >= C) return;  // uniform over the CTA
     const int32_t P0 = L - C;
-    const int32_t prefix = sc.prefix_len ? __ldg(sc.prefix_len + seq) : 0;
 
-    // ---- rows of the softmax threads, and the keys each query tile sees ------------------------
+    // ---- rows of the softmax threads --------------------------------------------------------------
     const bool softmax_warp = warp < kSoftWarps;
     const int32_t xq = (warp >> 2) & 1, half = (warp >> 3) & 1;  // query tile and key half of a softmax warp
     const int32_t quad = warp & 3;                                // its TMEM lane quadrant
     const int32_t r = quad * 32 + lane;
-    const int32_t tl = r / G, g = r - tl * G;
+    const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // x / G = x inv_G / 2^16 for x, G <= 128
+    const int32_t tl = static_cast<int32_t>(r * inv_G >> 16), g = r - tl * G;
     const int32_t t_row = (xq ? t0b : t0a) + tl;
     const bool row_valid = softmax_warp && tl < TT && t_row < C;
     const int32_t pos = P0 + t_row;
+    // ---- query tiles: 16-byte copies into the swizzled K-major layout; rows without a query zero
+    if (softmax_warp) {
+        const int32_t ti = half * 128 + (tid & 127);
+        uint8_t* sq = smem + xq * kTile;
+        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+        const int32_t t0 = xq ? t0b : t0a;
+#pragma unroll
+        for (int k = 0; k < kRows * kChunks / 256; ++k) {
+            const int32_t i = ti + k * 256;
+            const int32_t rr = i / kChunks, c16 = i % kChunks;
+            const int32_t tt = static_cast<int32_t>(rr * inv_G >> 16), t = t0 + tt;
+            const bool in = tt < TT && t < C;
+            const __nv_bfloat16* src =
+                in ? q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D + c16 * 8 : q;
+            cp_async16(sq + (c16 >> 3) * kHalf + sw128_offset(rr, c16 & 7), src, !in);
+        }
+    }
+    // ---- keys that the rows see ------------------------------------------------------------------
     KeySpans row{0, 0, 0, 0};
     if (row_valid)
         row = key_spans(L, pos, sc.key_start ? __ldg(sc.key_start + q0 + t_row) : 0, prefix, sc.window);
@@ -403,23 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     };
     const int32_t npages = (L + kPageTokens - 1) / kPageTokens;
 
-    // ---- query tiles: 16-byte copies into the swizzled K-major layout; rows without a query zero
-    if (softmax_warp) {
-        const int32_t ti = half * 128 + (tid & 127);
-        uint8_t* sq = smem + xq * kTile;
-        constexpr int kChunks = D / 8;  // 16-byte chunks of a row
-        const int32_t t0 = xq ? t0b : t0a;
-#pragma unroll
-        for (int k = 0; k < kRows * kChunks / 256; ++k) {
-            const int32_t i = ti + k * 256;
-            const int32_t rr = i / kChunks, c16 = i % kChunks;
-            const int32_t tt = rr / G, t = t0 + tt;
-            const bool in = tt < TT && t < C;
-            const __nv_bfloat16* src =
-                in ? q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D + c16 * 8 : q;
-            cp_async16(sq + (c16 >> 3) * kHalf + sw128_offset(rr, c16 & 7), src, !in);
-        }
-    }
     // Pool row of list page 8 i + s (page s of the i-th key tile); lane l of a producer warp holds
     // page 32 w + l of window w, fetched one window ahead.
     auto page_row = [&](int32_t lp) -> int32_t {
