@@ -619,7 +619,7 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = prefill_scored_tc_ok(a, dev->info) ? launch_prefill_scored_tc(a, sa, s)
+    const cudaError_t e = prefill_scored_tc_ok(a, dev->info) ? launch_prefill_scored_tc(a, sa, dev->info.num_sms, s)
                                                              : launch_scored_prefill_simt(a, sa, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

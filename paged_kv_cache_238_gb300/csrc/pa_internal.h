@@ -242,7 +242,7 @@ cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& sc
 
 // Tensor-core prefill (prefill_scored.cu): bf16, up to 128 q heads per kv head.
 bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev);
-cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& score, cudaStream_t stream);
+cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& score, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
 // move_blocks (page copies in every layer's pools, block tables rewritten)

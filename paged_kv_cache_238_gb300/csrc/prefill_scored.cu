@@ -49,7 +49,11 @@ constexpr int kThreads = 32 * (kVWarp + 1);
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 bf16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units: O is rescaled only when the maximum grows by more
-constexpr int kLptMaxSeqs = 64;           // sequences ordered longest first inside the kernel
+constexpr int kRankMax = 256;             // entries that each CTA ranks by their work
+// Grids of up to this many CTAs an SM (CTAs without tokens counted) are ordered pair by pair. Measured at
+// 512 CTAs of 1 to 16 key tiles: 58 us, against 65 ordered by sequence; at 864 CTAs of 1 to 3 key
+// tiles, 504 of them without tokens: 49 us against 43, as ranking costs each CTA 0.6 us.
+constexpr int kFewWaves = 4;
 constexpr float kMaxFixedCap = 51.f;      // 1.5 cap log2(e) <= 112
 
 constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between polls
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ query_start_loc,
     int32_t num_kv_heads, int32_t G, int32_t num_blocks, int32_t sub_log2, int32_t cap_tokens, int32_t max_chunk,
-    const __grid_constant__ TcScore sc, uint32_t* err) {
+    int32_t sub, uint32_t inv_sub,    const __grid_constant__ TcScore sc, uint32_t* err) {
     using L_ = Smem<D>;
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
@@ -299,42 +303,59 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
 
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // Up to 64 sequences go in order of decreasing length, so that the longest CTAs start first.
-    __shared__ int32_t lpt_len[kLptMaxSeqs], lpt_prefix;
-    __shared__ int4 lpt_seq;  // its number, first row of q, rows, length
+    __shared__ int4 chosen[2];  // the item's sequence, pair, first row of q, rows; length, prefix
     __shared__ int32_t red[2][4];    // per query tile: min a0, max a1, min b0, max b1
     __shared__ uint32_t seen_own[8];  // documents: the CTA's own positions that some row sees
-    __shared__ __nv_bfloat16 row_max[2][2][kRows];  // per query tile and half of the keys: the rows' maxima
-    int32_t seq = blockIdx.z, q0, C, L, prefix = 0;
-    const int32_t n_seqs = gridDim.z;
-    if (n_seqs > 1 && n_seqs <= kLptMaxSeqs) {
-        // every sequence's numbers are read at once, so that the chosen one's need no second trip to memory
-        int32_t start = 0, n = 0, len = 0, pre = 0;
-        if (tid < n_seqs) {
-            len = __ldg(seq_lens + tid);
-            start = __ldg(query_start_loc + tid);
-            n = __ldg(query_start_loc + tid + 1) - start;
-            if (sc.prefix_len) pre = __ldg(sc.prefix_len + tid);
-            lpt_len[tid] = len;
-        }
-        __syncthreads();
-        if (tid < n_seqs) {
-            int32_t rank = 0;
-#pragma unroll 8
-            for (int32_t u = 0; u < n_seqs; ++u) rank += (lpt_len[u] > len || (lpt_len[u] == len && u < tid)) ? 1 : 0;
-            if (rank == seq) lpt_seq = make_int4(tid, start, n, len), lpt_prefix = pre;
-        }
-        __syncthreads();
-        const int4 chosen = lpt_seq;
-        seq = chosen.x, q0 = chosen.y, C = chosen.z, L = chosen.w, prefix = lpt_prefix;
-    } else {
+    __shared__ union {  // one after the other
+        alignas(16) uint32_t rank_key[kRankMax];  // the items' work
+        __nv_bfloat16 row_max[2][2][kRows];       // per query tile and half of the keys: the rows' maxima
+    } shared;
+    // A CTA's entry: one pair of query tiles of a sequence (sub = the pairs of a chunk) or, sub = 1, a
+    // whole sequence, whose pairs and heads follow one another. Entries with the most keys come first:
+    // work that a long CTA leaves to the end of the grid keeps one SM busy and the others idle.
+    const int32_t TT = kRows / G, Hq = G * num_kv_heads;
+    const int32_t place = blockIdx.z, n_entries = gridDim.z, h = blockIdx.y;
+    int32_t seq, pair, q0, C, L, prefix = 0;
+    auto entry = [&](int32_t i) {
+        seq = sub > 1 ? static_cast<int32_t>(i * inv_sub >> 16) : i;  // i / sub, for i < 256 exact
+        pair = sub - 1 - (i - seq * sub);                              // a sequence's last tokens come first
         q0 = __ldg(query_start_loc + seq);
         C = __ldg(query_start_loc + seq + 1) - q0;
         L = __ldg(seq_lens + seq);
         if (sc.prefix_len) prefix = __ldg(sc.prefix_len + seq);
+    };
+    if (n_entries > 1 && n_entries <= kRankMax) {
+        uint32_t mine = 0;
+        if (tid < n_entries) {
+            entry(tid);
+            const int32_t first = 2 * pair * TT, rows = sub > 1 ? min(2 * TT, C - first) : C;
+            int32_t keys = L - C + first + rows;  // up to the last row's own
+            if (sc.window > 0) keys = min(keys, sc.window + rows + min(max(prefix, 0), L));
+            if (rows <= 0) keys = 0;
+            // 24 bits of keys (all of them up to 2^24 tokens), and the number: no two alike
+            mine = static_cast<uint32_t>(max(keys, 0)) >> max(8 - __clz(cap_tokens), 0) << 8 | (kRankMax - 1 - tid);
+        }
+        if (tid < kRankMax) shared.rank_key[tid] = mine;
+        __syncthreads();
+        if (tid < n_entries) {
+            int32_t rank = 0;
+#pragma unroll 4
+            for (int32_t u = 0; u < n_entries; u += 4) {
+                const uint4 k = *reinterpret_cast<const uint4*>(shared.rank_key + u);
+                rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+            }
+            if (rank == place) {
+                chosen[0] = make_int4(seq, pair, q0, C);
+                chosen[1] = make_int4(L, prefix, 0, 0);
+            }
+        }
+        __syncthreads();
+        const int4 c0 = chosen[0], c1 = chosen[1];
+        seq = c0.x, pair = c0.y, q0 = c0.z, C = c0.w, L = c1.x, prefix = c1.y;
+    } else {
+        entry(place);
     }
-    const int32_t h = blockIdx.y, TT = kRows / G, Hq = G * num_kv_heads;
-    const int32_t pair = gridDim.x - 1 - blockIdx.x;  // the longest pairs start first
+    if (sub == 1) pair = gridDim.x - 1 - blockIdx.x;
     if (C < 0 || C > max_chunk || C > L || L > cap_tokens) {
         if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
         return;
@@ -710,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     // the row's other half of the keys is another thread's: exchange the maxima, rounded
                     // up to bf16 (any reference at or above the maximum serves, if both take the same)
                     const __nv_bfloat16 mine = __float2bfloat16_ru(top);
-                    row_max[xq][half][r] = mine;
+                    shared.row_max[xq][half][r] = mine;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
                     ok = wait_or_abort<kSleepSoftmax>(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
@@ -718,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                         ok = false;
                         break;
                     }
-                    top = fmaxf(__bfloat162float(mine), __bfloat162float(row_max[xq][half ^ 1][r]));
+                    top = fmaxf(__bfloat162float(mine), __bfloat162float(shared.row_max[xq][half ^ 1][r]));
                 }
                 grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
                 const float m_new = grow ? top : m_ref;
@@ -884,7 +905,7 @@ constexpr double kTanh[4] = {0.999991018, -0.332989742, 0.129745541, -0.03961127
 constexpr float kTanhRange = 0.6f;
 
 template <int D, int MODE>
-cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t stream) {
+cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, int num_sms, cudaStream_t stream) {
     alignas(64) CUtensorMap tm_k, tm_v;
     const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.num_kv_heads * a.block_size;
     cudaError_t e = encode_bf16_2d_sw128(&tm_k, a.k_cache, D, rows, 64, kPageTokens);
@@ -896,21 +917,26 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, cudaStream_t st
     const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
-    const dim3 grid((a.max_chunk_len + 2 * TT - 1) / (2 * TT), a.num_kv_heads, a.num_seqs);
+    const int32_t pairs = (a.max_chunk_len + 2 * TT - 1) / (2 * TT);
+    // Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
+    const int64_t entries = static_cast<int64_t>(pairs) * a.num_seqs;
+    const bool by_pair = entries <= kRankMax && entries * a.num_kv_heads <= kFewWaves * num_sms;
+    const int32_t sub = by_pair ? pairs : 1;
+    const dim3 grid(by_pair ? 1 : pairs, a.num_kv_heads, a.num_seqs * sub);
     prefill_scored_kernel<D, MODE><<<grid, kThreads, Smem<D>::total, stream>>>(
         tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(a.q), a.block_table,
         a.max_blocks_per_seq, a.seq_lens, a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens,
-        a.max_chunk_len, sc, a.err);
+        a.max_chunk_len, sub, 65536u / sub + 1, sc, a.err);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, cudaStream_t stream) {
+cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, int num_sms, cudaStream_t stream) {
     switch (mode) {
-        case kPlain: return launch_impl<D, kPlain>(a, sc, stream);
-        case kCap: return launch_impl<D, kCap>(a, sc, stream);
-        case kDistance: return launch_impl<D, kDistance>(a, sc, stream);
-        default: return launch_impl<D, kGeneral>(a, sc, stream);
+        case kPlain: return launch_impl<D, kPlain>(a, sc, num_sms, stream);
+        case kCap: return launch_impl<D, kCap>(a, sc, num_sms, stream);
+        case kDistance: return launch_impl<D, kDistance>(a, sc, num_sms, stream);
+        default: return launch_impl<D, kGeneral>(a, sc, num_sms, stream);
     }
 }
 
@@ -921,7 +947,7 @@ bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
            a.num_kv_heads <= 65535 && static_cast<int>(Smem<128>::total) <= dev.max_smem_optin;
 }
 
-cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, cudaStream_t stream) {
+cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, int num_sms, cudaStream_t stream) {
     TcScore sc{};
     sc.c1 = a.scale * kLog2e;
     sc.capped = s.cap > 0.f;
@@ -940,7 +966,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
     sc.prefix_len = s.prefix_len;
     const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
                                  : (!s.slopes && s.cap <= kMaxFixedCap ? kCap : kGeneral);
-    return a.head_dim == 128 ? pick<128>(a, sc, mode, stream) : pick<64>(a, sc, mode, stream);
+    return a.head_dim == 128 ? pick<128>(a, sc, mode, num_sms, stream) : pick<64>(a, sc, mode, num_sms, stream);
 }
 
 }  // namespace pa
