@@ -555,7 +555,7 @@ PA_API size_t pa_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_he
     if (dtype == PA_BF16 &&
         plan_decode_scored(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &plan))
         return plan.workspace_bytes;
-    return plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
+    return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
         .workspace_bytes;
 }
 
@@ -585,7 +585,7 @@ PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache,
         return launch_decode_scored(a, sa, fast, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const ScoredSimtPlan plan =
-        plan_scored_simt(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
+        plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
     return launch_scored_decode_simt(a, sa, plan, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -594,9 +594,19 @@ PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache,
 PA_API size_t pa_prefill_scored_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
                                                int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
                                                pa_dtype dtype) {
-    (void)num_seqs; (void)max_chunk_len; (void)num_q_heads; (void)num_kv_heads; (void)head_dim; (void)max_seq_len;
-    (void)dtype;
-    return 0;
+    if (check_attention_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, 1, max_seq_len / 16 + 1, max_seq_len,
+                              dtype, PA_BLOCK_SIZE) != PA_OK || max_chunk_len <= 0 ||
+        static_cast<int64_t>(num_seqs) * max_chunk_len > 0x7fffffffLL)
+        return 0;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return 0;
+    PrefillArgs a{};
+    a.dtype = dtype, a.num_seqs = num_seqs, a.num_q_heads = num_q_heads, a.num_kv_heads = num_kv_heads;
+    if (prefill_scored_tc_ok(a, dev->info))
+        return plan_prefill_scored(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                   dev->info.num_sms).workspace_bytes;
+    return plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                            dev->info.num_sms).workspace_bytes;
 }
 
 PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -605,7 +615,6 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
                                    int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                    int32_t num_blocks, int32_t block_size, float scale, const pa_score* score,
                                    pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    (void)workspace; (void)workspace_bytes;
     PrefillArgs a;
     pa_status st = prepare_prefill(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens,
                                    query_start_loc, num_seqs, max_chunk_len, max_seq_len, num_q_heads, num_kv_heads,
@@ -619,8 +628,19 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = prefill_scored_tc_ok(a, dev->info) ? launch_prefill_scored_tc(a, sa, dev->info.num_sms, s)
-                                                             : launch_scored_prefill_simt(a, sa, s);
+    auto room = [&](size_t bytes) {
+        return bytes == 0 || (workspace && workspace_bytes >= bytes && aligned16(workspace));
+    };
+    if (!prefill_scored_tc_ok(a, dev->info)) {
+        const ScoredSimtPlan plan = plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                     max_seq_len, dev->info.num_sms);
+        if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
+        return launch_scored_prefill_simt(a, sa, plan, workspace, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
+    const PrefillScoredPlan plan = plan_prefill_scored(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                       max_seq_len, dev->info.num_sms);
+    if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
+    const cudaError_t e = launch_prefill_scored_tc(a, sa, plan, workspace, dev->info.num_sms, s);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

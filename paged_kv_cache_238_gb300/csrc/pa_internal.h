@@ -227,22 +227,31 @@ bool plan_decode_scored(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_he
 cudaError_t launch_decode_scored(const DecodeArgs& a, const ScoreArgs& score, const DecodeScoredPlan& plan,
                                  cudaStream_t stream);
 
-// CUDA-core path (scored_simt.cu): a decode row's visible pages in num_parts partitions of up to
-// part_pages.
+// CUDA-core path (scored_simt.cu): CTAs of up to `rows` rows of a kv head, from `tokens` tokens; their
+// visible pages in up to num_parts partitions of part_pages.
 struct ScoredSimtPlan {
-    int32_t part_pages, num_parts;
+    int32_t rows, head_chunks, tokens, groups, grid_x, part_pages, num_parts;
     size_t workspace_bytes;
 };
 int32_t scored_simt_head_chunks(int32_t group);
-ScoredSimtPlan plan_scored_simt(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                int32_t max_seq_len, int num_sms);
+ScoredSimtPlan plan_scored_simt(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t max_seq_len, int num_sms);
 cudaError_t launch_scored_decode_simt(const DecodeArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
                                       cudaStream_t stream);
-cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& score, cudaStream_t stream);
+cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
+                                       void* workspace, cudaStream_t stream);
 
 // Tensor-core prefill (prefill_scored.cu): bf16, up to 128 q heads per kv head.
 bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev);
-cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& score, int num_sms, cudaStream_t stream);
+// Runs into which a CTA's key list is split when the grid is small, and what their results take.
+struct PrefillScoredPlan {
+    int32_t parts;
+    size_t workspace_bytes;
+};
+PrefillScoredPlan plan_prefill_scored(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t max_seq_len, int num_sms);
+cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& score, const PrefillScoredPlan& plan,
+                                     void* workspace, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
 // move_blocks (page copies in every layer's pools, block tables rewritten)

@@ -33,6 +33,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
 #include "scored.cuh"
@@ -54,6 +56,11 @@ constexpr int kRankMax = 256;             // entries that each CTA ranks by thei
 // 512 CTAs of 1 to 16 key tiles: 58 us, against 65 ordered by sequence; at 864 CTAs of 1 to 3 key
 // tiles, 504 of them without tokens: 49 us against 43, as ranking costs each CTA 0.6 us.
 constexpr int kFewWaves = 4;
+constexpr size_t kSplitRowBytes = kRankMax * 16 * 16;  // Split::rows, in a workspace
+// Key tiles of a run, at least, when a list is split. Measured, 16 rows of one sequence on 4096 keys, 8 kv
+// heads of 128: 15.8 us with 2, 17.7 with 4, 25.7 with 8, 63.8 not split; 256 rows on 32768 keys: 149 us, not
+// split 531.
+constexpr int kMinPartTiles = 2;
 constexpr float kMaxFixedCap = 51.f;      // 1.5 cap log2(e) <= 112
 
 constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between polls
@@ -85,9 +92,13 @@ struct SpanUnion {
 // Key tiles walked by the CTA: n_a from first_a, the rest from first_b.
 struct TileList {
     int32_t first_a, n_a, first_b, n;
-    __device__ __forceinline__ int32_t tile(int32_t i) const { return i < n_a ? first_a + i : first_b + (i - n_a); }
+    int32_t base = 0;  // list position that the CTA's part begins with; positions below count from it
+    __device__ __forceinline__ int32_t tile(int32_t i) const {
+        i += base;
+        return i < n_a ? first_a + i : first_b + (i - n_a);
+    }
     __device__ __forceinline__ int32_t position(int32_t t) const {
-        return t < first_a + n_a ? t - first_a : n_a + (t - first_b);
+        return (t < first_a + n_a ? t - first_a : n_a + (t - first_b)) - base;
     }
 };
 
@@ -114,6 +125,15 @@ __device__ __forceinline__ SpanUnion join(const SpanUnion& x, const SpanUnion& y
     }
     return u;
 }
+
+// Few CTAs with long key lists: each list in up to `parts` runs, one CTA each. Their outputs (fp32, not
+// yet divided by the sums) and (reference, sum) of every row go to the workspace for the merge kernel.
+struct Split {
+    int32_t parts;
+    int4* rows;  // per CTA of the unsplit grid: first row of q, rows of tile a, of tile b, runs (0: nothing to merge)
+    float4* o;   // [CTA][parts][D / 4][2 * kRows]
+    float2* ml;  // [CTA][parts][2 * kRows]
+};
 
 // Score constants, log2 domain.
 struct TcScore {
@@ -269,13 +289,13 @@ __device__ __forceinline__ uint32_t span_bits(int32_t base, int32_t lo, int32_t 
     return (h == 32 ? 0xffffffffu : (1u << h) - 1u) & ~(l == 32 ? 0xffffffffu : (1u << l) - 1u);
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ query_start_loc,
     int32_t num_kv_heads, int32_t G, int32_t num_blocks, int32_t sub_log2, int32_t cap_tokens, int32_t max_chunk,
-    int32_t sub, uint32_t inv_sub,    const __grid_constant__ TcScore sc, uint32_t* err) {
+    int32_t sub, uint32_t inv_sub, const __grid_constant__ Split split,    const __grid_constant__ TcScore sc, uint32_t* err) {
     using L_ = Smem<D>;
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
@@ -355,7 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     } else {
         entry(place);
     }
-    if (sub == 1) pair = gridDim.x - 1 - blockIdx.x;
+    if (sub == 1) pair = SPLIT ? 0 : gridDim.x - 1 - blockIdx.x;
+    const int32_t cta = place * num_kv_heads + h;
+    if (SPLIT && tid == 0 && blockIdx.x == 0) split.rows[cta] = make_int4(0, 0, 0, 0);
     if (C < 0 || C > max_chunk || C > L || L > cap_tokens) {
         if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
         return;
@@ -438,14 +460,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         for (int x = 0; x < 2; ++x) ux[x] = SpanUnion{red[x][0], red[x][1], red[x][2], red[x][3]};
     }
     const SpanUnion uni = join(ux[0], ux[1]);
-    const TileList tiles = tile_list(uni);
-    const int32_t n_kv = tiles.n;
+    TileList tiles = tile_list(uni);
+    int32_t n_kv = tiles.n, n_parts = 1;
+    if constexpr (SPLIT) {  // this CTA takes one of up to split.parts equal runs of the list
+        const int32_t most = max(min(split.parts, n_kv / kMinPartTiles), 1), share = max((n_kv + most - 1) / most, 1);
+        n_parts = max((n_kv + share - 1) / share, 1);
+        if (static_cast<int32_t>(blockIdx.x) >= n_parts) {  // uniform over the CTA
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            return;
+        }
+        tiles.base = blockIdx.x * share;
+        n_kv = min(share, n_kv - tiles.base);
+        if (tid == 0 && blockIdx.x == 0 && n_parts > 1)
+            split.rows[cta] = make_int4(q0 + t0a, min(TT, C - t0a) * G, max(min(TT, C - t0b), 0) * G, n_parts);
+    }
     // list positions whose key tile query tile x uses: two ranges
     int32_t ra0[2], ra_n[2], rb0[2], rb_n[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        ra0[x] = ux[x].a0 / kKeys - tiles.first_a;
-        ra_n[x] = ux[x].a0 < ux[x].a1 ? (ux[x].a1 - 1) / kKeys - tiles.first_a + 1 - ra0[x] : 0;
+        ra0[x] = ux[x].a0 / kKeys - tiles.first_a - tiles.base;
+        ra_n[x] = ux[x].a0 < ux[x].a1 ? (ux[x].a1 - 1) / kKeys - tiles.first_a - tiles.base + 1 - ra0[x] : 0;
         rb0[x] = tiles.position(ux[x].b0 / kKeys);
         rb_n[x] = ux[x].b0 < ux[x].b1 ? tiles.position((ux[x].b1 - 1) / kKeys) + 1 - rb0[x] : 0;
     }
@@ -832,15 +866,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         if (kOwnO) sums[(2 + half) * kRows + r] = m_ref;
         named_barrier(1 + xq, 256);
         float w0 = 1.f, w1 = 1.f;  // weights of the halves' outputs: 1 under a common reference
+        float top = MODE == kCap ? 0.f : m_ref;
         if (kOwnO) {
-            const float m0 = sums[2 * kRows + r], m1 = sums[3 * kRows + r], top = fmaxf(m0, m1);
+            const float m0 = sums[2 * kRows + r], m1 = sums[3 * kRows + r];
+            top = fmaxf(m0, m1);
             w0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - top);
             w1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - top);
         }
         l_sum = w0 * sums[r] + w1 * sums[kRows + r];
         named_barrier(1 + xq, 256);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
+        // columns half (D / 2) + 32 c .. of the row's output, before the division; 0 where no key was used
+        auto load_output = [&](int c, uint32_t(&o)[32]) {
+            const uint32_t cols = tmem + 256 + xq * 128 + half * (D / 2) + c * 32 + lane_off;
+            if (cnt == 0) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = 0u;
+                return;
+            }
+            ld_wait_x32(cols, o);
+            if constexpr (kOwnO) {
+                uint32_t o1[32];
+                ld_wait_x32(cols + D, o1);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    o[k] = __float_as_uint(fmaf(w0, __uint_as_float(o[k]), w1 * __uint_as_float(o1[k])));
+            }
+        };
+        if (SPLIT && n_parts > 1) {
+            if (ok) {
+                umma::fence_after_sync();
+                const int64_t run = static_cast<int64_t>(cta) * split.parts + blockIdx.x;
+                if (half == 0) split.ml[run * (2 * kRows) + xq * kRows + r] = make_float2(top, l_sum);
+                float4* po = split.o + (run * (D / 4) + half * (D / 8)) * (2 * kRows) + xq * kRows + r;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t o[32];
+                    load_output(c, o);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        po[(c * 8 + v) * (2 * kRows)] =
+                            make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                        __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                }
+            }
+        } else if (ok) {
             umma::fence_after_sync();
             const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
             // this warp's rows x D / 2 columns through its own part of the tile's Q, so that the stores go
@@ -851,15 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
-                const uint32_t cols = tmem + 256 + xq * 128 + half * (D / 2) + c * 32 + lane_off;
-                if (cnt > 0) ld_wait_x32(cols, o);
-                if (kOwnO && cnt > 0) {
-                    uint32_t o1[32];
-                    ld_wait_x32(cols + D, o1);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        o[k] = __float_as_uint(fmaf(w0, __uint_as_float(o[k]), w1 * __uint_as_float(o1[k])));
-                }
+                load_output(c, o);
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     float f[8];
@@ -899,20 +961,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     }
 }
 
+// Merges the runs of split key lists: M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l. Grid: four
+// columns of head_dim x CTA of the unsplit grid; a thread has one row of the CTA's two tiles.
+template <int D>
+__global__ void __launch_bounds__(2 * kRows) prefill_scored_merge_kernel(__nv_bfloat16* __restrict__ out,
+                                                                         const __grid_constant__ Split split,
+                                                                         int32_t num_kv_heads, int32_t G) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t c4 = blockIdx.x, cta = blockIdx.y, R = threadIdx.x;
+    const int4 rows = split.rows[cta];
+    const int32_t rr = R & (kRows - 1), n = R < kRows ? rows.y : rows.z;
+    if (rows.w == 0 || rr >= n) return;
+    const float2* ml = split.ml + static_cast<int64_t>(cta) * split.parts * (2 * kRows) + R;
+    const float4* po = split.o + (static_cast<int64_t>(cta) * split.parts * (D / 4) + c4) * (2 * kRows) + R;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int32_t p = 0; p < rows.w; ++p) M = fmaxf(M, ml[p * (2 * kRows)].x);
+    const float ref = M == -INFINITY ? 0.f : M;  // no visible key in any run: weights are 0
+#pragma unroll 8
+    for (int32_t p = 0; p < rows.w; ++p) {
+        const float2 x = ml[p * (2 * kRows)];
+        const float4 o = po[static_cast<int64_t>(p) * (D / 4) * (2 * kRows)];
+        const float w = exp2_approx(x.x - ref);
+        den = fmaf(w, x.y, den);
+        acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const int32_t h = cta % num_kv_heads, TT = kRows / G, tt = rr / G, t = (R < kRows ? 0 : TT) + tt;
+    __nv_bfloat16* to = out + (static_cast<int64_t>(rows.x + t) * G * num_kv_heads + h * G + (rr - tt * G)) * D + c4 * 4;
+    *reinterpret_cast<uint2*>(to) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
 // Minimax (Remez) coefficients of tanh x = x (t0 + t1 x^2 + t2 x^4 + t3 x^6) on |x| <= 0.6; absolute
 // error 5.9e-7.
 constexpr double kTanh[4] = {0.999991018, -0.332989742, 0.129745541, -0.0396112775};
 constexpr float kTanhRange = 0.6f;
 
-template <int D, int MODE>
-cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, int num_sms, cudaStream_t stream) {
+// Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
+bool few_waves(int64_t entries, int32_t num_kv_heads, int num_sms) {
+    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * num_sms;
+}
+
+template <int D, int MODE, bool SPLIT>
+cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillScoredPlan& plan,
+                        void* workspace, int num_sms, cudaStream_t stream) {
     alignas(64) CUtensorMap tm_k, tm_v;
     const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.num_kv_heads * a.block_size;
     cudaError_t e = encode_bf16_2d_sw128(&tm_k, a.k_cache, D, rows, 64, kPageTokens);
     if (e != cudaSuccess) return e;
     e = encode_bf16_2d_sw128(&tm_v, a.v_cache, D, rows, 64, kPageTokens);
     if (e != cudaSuccess) return e;
-    e = allow_smem<prefill_scored_kernel<D, MODE>>(static_cast<int>(Smem<D>::total));
+    e = allow_smem<prefill_scored_kernel<D, MODE, SPLIT>>(static_cast<int>(Smem<D>::total));
     if (e != cudaSuccess) return e;
     const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
@@ -920,34 +1022,75 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, int num_sms, cu
     const int32_t pairs = (a.max_chunk_len + 2 * TT - 1) / (2 * TT);
     // Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
     const int64_t entries = static_cast<int64_t>(pairs) * a.num_seqs;
-    const bool by_pair = entries <= kRankMax && entries * a.num_kv_heads <= kFewWaves * num_sms;
+    const bool by_pair = few_waves(entries, a.num_kv_heads, num_sms);
     const int32_t sub = by_pair ? pairs : 1;
-    const dim3 grid(by_pair ? 1 : pairs, a.num_kv_heads, a.num_seqs * sub);
-    prefill_scored_kernel<D, MODE><<<grid, kThreads, Smem<D>::total, stream>>>(
-        tm_k, tm_v, static_cast<__nv_bfloat16*>(a.out), static_cast<const __nv_bfloat16*>(a.q), a.block_table,
-        a.max_blocks_per_seq, a.seq_lens, a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens,
-        a.max_chunk_len, sub, 65536u / sub + 1, sc, a.err);
-    return cudaGetLastError();
+    const dim3 grid(SPLIT ? plan.parts : by_pair ? 1 : pairs, a.num_kv_heads, a.num_seqs * sub);
+    Split split{};
+    if (SPLIT) {
+        char* ws = static_cast<char*>(workspace);
+        split.parts = plan.parts;
+        split.rows = reinterpret_cast<int4*>(ws + kScoredCounterBytes);
+        split.o = reinterpret_cast<float4*>(ws + kScoredCounterBytes + kSplitRowBytes);
+        split.ml = reinterpret_cast<float2*>(split.o + entries * a.num_kv_heads * plan.parts * (D / 4) * (2 * kRows));
+    }
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+    prefill_scored_kernel<D, MODE, SPLIT><<<grid, kThreads, Smem<D>::total, stream>>>(
+        tm_k, tm_v, out, static_cast<const __nv_bfloat16*>(a.q), a.block_table, a.max_blocks_per_seq, a.seq_lens,
+        a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens, a.max_chunk_len, sub, 65536u / sub + 1,
+        split, sc, a.err);
+    e = cudaGetLastError();
+    if (!SPLIT || e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];  // the merge's CTAs may be set up while the last runs end
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 4, static_cast<unsigned>(entries * a.num_kv_heads));
+    cfg.blockDim = dim3(2 * kRows);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_scored_merge_kernel<D>, out, split, a.num_kv_heads, G);
 }
 
 template <int D>
-cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, int num_sms, cudaStream_t stream) {
+cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, const PrefillScoredPlan& plan, void* workspace,
+                 int num_sms, cudaStream_t stream) {
+    auto run = [&](auto m) {
+        return plan.parts > 1 ? launch_impl<D, m, true>(a, sc, plan, workspace, num_sms, stream)
+                              : launch_impl<D, m, false>(a, sc, plan, workspace, num_sms, stream);
+    };
     switch (mode) {
-        case kPlain: return launch_impl<D, kPlain>(a, sc, num_sms, stream);
-        case kCap: return launch_impl<D, kCap>(a, sc, num_sms, stream);
-        case kDistance: return launch_impl<D, kDistance>(a, sc, num_sms, stream);
-        default: return launch_impl<D, kGeneral>(a, sc, num_sms, stream);
+        case kPlain: return run(std::integral_constant<int, kPlain>{});
+        case kCap: return run(std::integral_constant<int, kCap>{});
+        case kDistance: return run(std::integral_constant<int, kDistance>{});
+        default: return run(std::integral_constant<int, kGeneral>{});
     }
 }
 
 }  // namespace
+
+PrefillScoredPlan plan_prefill_scored(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_len,
+                                      int num_sms) {
+    PrefillScoredPlan plan{1, 0};
+    const int64_t most = static_cast<int64_t>(max_len / kKeys + 1) / kMinPartTiles;  // runs of the longest list
+    if (Hq / Hkv > kRows || most < 2) return plan;
+    // room for a wave of CTAs, whatever the chunks: a workspace serves every call up to its max_len
+    plan.workspace_bytes = kScoredCounterBytes + kSplitRowBytes + static_cast<size_t>(num_sms) * (2 * kRows) * (D * 4 + 8);
+    if (S < 1 || max_chunk < 1) return plan;
+    const int32_t TT = kRows / (Hq / Hkv);
+    const int64_t entries = (static_cast<int64_t>(max_chunk) + 2 * TT - 1) / (2 * TT) * S;
+    if (few_waves(entries, Hkv, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
+        plan.parts = static_cast<int32_t>(max(min(num_sms / (entries * Hkv), most), static_cast<int64_t>(1)));
+    return plan;
+}
 
 bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
     return a.dtype == PA_BF16 && a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
            a.num_kv_heads <= 65535 && static_cast<int>(Smem<128>::total) <= dev.max_smem_optin;
 }
 
-cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, int num_sms, cudaStream_t stream) {
+cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, const PrefillScoredPlan& plan,
+                                     void* workspace, int num_sms, cudaStream_t stream) {
     TcScore sc{};
     sc.c1 = a.scale * kLog2e;
     sc.capped = s.cap > 0.f;
@@ -966,7 +1109,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, i
     sc.prefix_len = s.prefix_len;
     const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
                                  : (!s.slopes && s.cap <= kMaxFixedCap ? kCap : kGeneral);
-    return a.head_dim == 128 ? pick<128>(a, sc, mode, num_sms, stream) : pick<64>(a, sc, mode, num_sms, stream);
+    return a.head_dim == 128 ? pick<128>(a, sc, mode, plan, workspace, num_sms, stream) : pick<64>(a, sc, mode, plan, workspace, num_sms, stream);
 }
 
 }  // namespace pa

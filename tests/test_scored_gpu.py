@@ -390,3 +390,66 @@ def test_windowed_generation_gives_pages_back_and_shrinks_the_pool():
     held = [b for b in bm.block_ids(1) if b]
     assert len(held) <= 1 + window // BS + 2 and max(held) < 12
     bm.close()
+
+
+SPLIT_CHUNKS = [(4099, 3), (2600, 70), (130, 5), (0, 0), (700, 1), (257, 257)]
+
+
+@pytest.mark.parametrize("kind", CHUNK_KINDS)
+@pytest.mark.parametrize("H_q,H_kv,D,BS,dtype", [(8, 2, 128, 16, "bf16"), (3, 1, 64, 128, "bf16"), (2, 1, 64, 16, "f32")])
+def test_prefill_key_lists_split_among_ctas(kind, H_q, H_kv, D, BS, dtype):
+    """Few rows on long contexts: the keys of a row group go to several CTAs, of sequences that are
+    long enough; short ones, and those without rows, lie between them."""
+    lens, chunks = zip(*SPLIT_CHUNKS)
+    c = Case(26, lens, H_q, H_kv, D, BS, dtype, chunks=chunks, **chunk_scores(kind, H_q, SPLIT_CHUNKS))
+    d = check(c, kind)
+    first = d.out.clone()
+    for _ in range(3):  # the workspace needs nothing between calls; results do not depend on who ends last
+        d.out.fill_(float("nan"))
+        assert torch.equal(d.run(), first)
+
+
+def test_prefill_split_workspace_serves_other_shapes():
+    """One workspace, sized for the largest: calls that split, that do not and whose sequences lost their rows."""
+    shapes = [[(3000, 2), (2500, 2)], [(40, 40)], [(2500, 2), (0, 0)], [(900, 100)], [(3000, 1)]]
+    cases = [Case(27 + i, [L for L, _ in p], 4, 2, 64, 16, "bf16", chunks=[C for _, C in p], cap=30.0)
+             for i, p in enumerate(shapes)]
+    n = B.pa_prefill_scored_workspace_size(2, 100, 4, 2, 64, 3000, torch.bfloat16)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for c in cases + cases[::-1]:
+        d = OnDevice(c)
+        assert d.ws is None or d.ws.numel() <= n
+        d.ws = ws
+        ref, tol = c.reference()
+        assert (np.abs(to_f64(d.run()) - ref) <= tol).all()
+    dec = OnDevice(Case(33, [1500, 3], 4, 2, 64, 16, "bf16"))  # the counters at its start are as they were
+    dec.ws[:65536].copy_(ws[:65536])
+    ref, tol = dec.c.reference()
+    assert (np.abs(to_f64(dec.run()) - ref) <= tol).all()
+
+
+def test_prefill_split_is_captured_and_replayed():
+    c = Case(34, [2100, 3500], 8, 2, 128, 16, "bf16", chunks=[4, 9], slopes=alibi(8))
+    d = OnDevice(c)
+    d.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d.run()
+    ref, tol = c.reference()
+    for _ in range(3):
+        d.out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (np.abs(to_f64(d.out) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_split_refuses_a_small_workspace(dtype):
+    c = Case(35, [3000], 4, 1, 64, 16, dtype, chunks=[2])
+    d = OnDevice(c)
+    assert d.ws is not None
+    for ws in (None, d.ws[:-16], d.ws[8:]):
+        d.ws = ws
+        with pytest.raises(B.PaError):
+            d.run()
