@@ -463,7 +463,10 @@ PA_API pa_status pa_decode_scored(void* out, const void* q, const void* k_cache,
  * pa_prefill_scored: pa_prefill_chunk_bs with scored attention; chunk row r of sequence i sits at
  * position seq_lens[i] - C_i + r. A chunk longer than max_chunk_len or than its sequence sets
  * PA_DEVERR_LEN_RANGE and leaves its rows unwritten. workspace: as for pa_decode_scored, sized by
- * pa_prefill_scored_workspace_size (may be NULL when that is 0). Supported: as pa_decode_scored.
+ * pa_prefill_scored_workspace_size (may be NULL when that is 0, which it is for short contexts); a
+ * size found for some num_seqs and max_chunk_len serves every call with the same heads, head_dim and
+ * dtype up to its max_seq_len. Calls with few rows on long contexts split their keys among the SMs and
+ * join the parts there. Supported: as pa_decode_scored.
  */
 PA_API size_t pa_prefill_scored_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
                                                int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,

@@ -21,6 +21,10 @@
 // CTA meet in shared memory after one barrier, joined by all its threads; segments cut between CTAs
 // leave one piece per CTA in the workspace, and the CTA that counts the last one joins them and
 // puts the counter back to zero.
+//
+// Bound: HBM. 8 sequences of 20000 to 32768 keys, 64 q / 8 kv heads of 128, cap 30: 131 us, 6.5 TB/s, 96 % of
+// the measured copy rate; 64 sequences of 500 to 16384 keys in a window of 4096: 110 us (94 %). Small batches
+// are a chain of latencies (lengths, list, first pages, joins): 4 sequences of up to 700 keys 10.6 us.
 #include <cuda.h>
 #include <math.h>
 
@@ -33,8 +37,14 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSeqs = 1024;  // sequences of one launch: their spans live in shared memory
 constexpr int kMaxHeads = 16;   // q heads of one segment
-constexpr int kMinSlice = 8;    // units of a CTA's slice at least
-constexpr int kSegmentUnits = 1;  // a segment's start and end weigh as much as this many pages
+// Units of a CTA's slice, at least. Measured, 4 sequences of up to 700 keys, 8 kv heads of 128: 9.7 us with 4 or 2,
+// 10.6 with 8, 14.3 with 32; 2 sequences of 1000 keys, one kv head: 9.8 with 4 or 8, 11.3 with 2, 14.2 with 1.
+constexpr int kMinSlice = 4;
+// One kv head of 128: 500 pages take 12.7, 14.2, 16.2, 20.3 us in 24, 48, 96, 125 pieces, 1250 pages 17.7, 16.7,
+// 18.8, 22.2 us in 24, 48, 96, 152, 6250 pages 47.5, 31.9, 27.1, 27.4 us: best near sqrt(1.5 n) pieces.
+constexpr float kJoinWeight = 1.f / 1.5f;
+constexpr int kSegmentUnits = 1;  // a segment's start and end weigh as much as this many pages (96 sequences of 16
+                                  // to 2048 keys, 16 heads of 64: 39.9 us, 52.3 when they weighed nothing)
 
 // Pages of one step of a warp: 8 KB of K and V, so that what a step costs besides its pages
 // (waits, reductions, the list) weighs alike at both head dims.
@@ -223,8 +233,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
         __syncthreads();
     }
     const int32_t U = prefix[S];
-    // slices of equal length, one per CTA: short lists keep to as many CTAs as have kMinSlice pages
-    const int32_t chunk = max((U + static_cast<int32_t>(gridDim.x) - 1) / static_cast<int32_t>(gridDim.x), kMinSlice);
+    // slices of equal length, one per CTA, but not below kMinSlice, nor below where the time that n / chunk
+    // pieces of a segment of n units take to join outweighs the shorter slices (about sqrt(n / 1.5))
+    const float n_mean = static_cast<float>(U) / static_cast<float>(S * a.num_kv_heads * NHC);
+    const int32_t chunk = max(max((U + static_cast<int32_t>(gridDim.x) - 1) / static_cast<int32_t>(gridDim.x), kMinSlice),
+                              static_cast<int32_t>(sqrtf(n_mean * kJoinWeight)));
     // rows that see nothing are zero (spread over the CTAs)
     for (int32_t s = blockIdx.x; s < S; s += gridDim.x) {
         if (prefix[s + 1] != prefix[s]) continue;

@@ -2,9 +2,13 @@
 // block tables to follow them. Pure data movement, bound by HBM: each moved byte is read and
 // written once.
 //
-// Grid: x = pair (the last rows of CTAs after the pairs rewrite the table), y = pool. A block of
-// all kv heads is contiguous, so a whole-block copy is one run of 16-byte chunks; with `tokens` the
-// copy is a run per head. A table entry finds its pair by binary search over the ascending src ids.
+// Grid: x = pair (the last rows of CTAs after the pairs rewrite the table), y = pool, z = share of a
+// block. A block of all kv heads is contiguous, so a whole-block copy is one run of 16-byte chunks; with
+// `tokens` the copy is a run per head. A thread sends for eight chunks before it stores them, and blocks
+// go to several CTAs where there are few: one chunk at a time and a CTA per block took 36 us for 6
+// half-full blocks of 256 KB in 64 pools, this 14.6 (6.6 TB/s read and written); 960 blocks of 32 KB in 64
+// pools: 565 us (7.1 TB/s, a plain copy of the same bytes 593). A table entry finds its pair by binary
+// search over the ascending src ids.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 

@@ -14,18 +14,36 @@
 //   warps 0-15 - scores and softmax, two threads per query row, each on 64 of the tile's 128 keys
 //                (four warps a scheduler to cover the arithmetic's and tensor memory's latencies).
 //
+// Chains of S -> softmax -> P -> P V -> next S run independently of one another: where a row's keys need
+// no common maximum there are four, one per query tile and half of the key tile (64 keys), else two.
+//
 // Scores. Four variants of the score arithmetic (Mode), all in the log2 domain:
 //   plain      arg = s c1;                       online maximum, two passes over S
-//   cap        arg = s Q(s^2) - ref;             no maximum: see below, one pass over S
+//   cap        arg = s Q(s^2) - ref;             no maximum: see below, one pass over S, four chains
 //   distance   arg = s c1 - slope |p - j|;       online maximum, two passes
-//   general    both, or a cap beyond the fixed reference's range
+//   both       arg = s Q(s^2) - slope |p - j| - ref(row);  as cap
+//   general    caps beyond the range of the fixed reference
+// At head_dim 64 tensor memory has room for an output per half of the keys: the modes with maxima then
+// run four chains too, each half with its own maximum and output, merged at the end (8 sequences of 100
+// to 1000 new rows on up to 2500 keys, 16 heads: 65.7 us, two chains 67.8).
 // A capped score lies in [-cap, cap], so the weights 2^(arg - ref) against the fixed reference
 // ref = cap log2(e) / 2 lie in [2^-112, 2^37] for caps up to kMaxFixedCap: no running maximum, no
 // second pass over S and no rescaling of O are needed. tanh is the odd polynomial x Q(x^2) of degree
 // 7, fitted to tanh on |x| <= 0.6 by Remez's minimax method (absolute error 2^-20.7, that times cap
 // in the score, below the 2^-9 of the bf16 weights), evaluated on the FMA pipes two elements an
 // instruction; a warp whose 32 scores of a row block hold a larger one takes
-// tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block, exact at every x.
+// tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block, exact at every x. P is rounded to bf16, the
+// type in which the tensor cores multiply it by V (fp32 accumulation; the sums add the fp32 weights).
+//
+// Bound: the tensor cores, then the exponentials. 16 sequences of 512 new rows on 512 to 4608 keys, 32 q /
+// 8 kv heads of 128, cap 50: 293 us, 1.06 PFLOP/s over visible pairs (54 % of the measured bf16 rate; a key
+// tile takes 1.8 us against 1.35 of MMA time, its 64-wide S products being bound by shared memory), of
+// which 20 % goes to each CTA's start (3 us), first S (1.5) and end (3.5). Forms that were slower: one
+// persistent CTA per SM over equal cuts of all key tiles (399), key tiles sent for before the CTA's first
+// barrier (304), raw maxima in pass one (no gain).
+//
+// Few rows on many keys: the key list is split (Split) so that a wave of CTAs shares it, and a second
+// kernel merges their outputs.
 //
 // V rows of keys that no row of the CTA sees are zeroed in shared memory before P V (their pool
 // cells may hold anything); their scores are masked. Every wait is bounded; a timeout sets
@@ -61,11 +79,14 @@ constexpr size_t kSplitRowBytes = kRankMax * 16 * 16;  // Split::rows, in a work
 // heads of 128: 15.8 us with 2, 17.7 with 4, 25.7 with 8, 63.8 not split; 256 rows on 32768 keys: 149 us, not
 // split 531.
 constexpr int kMinPartTiles = 2;
-constexpr float kMaxFixedCap = 51.f;      // 1.5 cap log2(e) <= 112
+// Caps with a fixed reference: 1.5 cap log2(e) <= 112. Measured, 16 sequences of 512 new rows on 2512 keys, 32 q / 8
+// kv heads of 128: cap 50 298 us, not capped 332, cap 52 (general) 821.
+constexpr float kMaxFixedCap = 51.f;
+constexpr float kTopWeight = 48.f;  // with a distance bias: the largest weight's exponent
 
 constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between polls
 
-enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kGeneral = 3 };
+enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kCapDistance = 3, kGeneral = 4 };
 
 template <int D>
 struct Smem {
@@ -303,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     // Chains of S -> softmax -> P -> PV -> next S that run independently of one another: one per query
     // tile, or, when no maximum ties the keys of a row together, one per query tile and half of the
     // key tile (chain c: query tile c & 1, half c >> 1), so that more MMA and softmax work overlaps.
-    constexpr bool kSplit = MODE == kCap || D == 64;
-    constexpr bool kOwnO = kSplit && MODE != kCap;  // each half of the keys has its own O and maximum
+    constexpr bool kFixed = MODE == kCap || MODE == kCapDistance;  // fixed reference
+    constexpr bool kSplit = kFixed || D == 64;
+    constexpr bool kOwnO = kSplit && !kFixed;  // each half of the keys has its own O and maximum
     constexpr int kChains = kSplit ? 4 : 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -643,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + xq * 128 + half * 64 + lane_off;
         const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (kOwnO ? D : D / 2) + lane_off;  // columns it rescales
-        const float slope = (MODE == kDistance || MODE == kGeneral) && sc.slopes && row_valid
+        const float slope = (MODE != kPlain && MODE != kCap) && sc.slopes && row_valid
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
         const uint64_t c1 = hold2(sc.c1);
@@ -652,6 +674,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) tq[k] = hold2(sc.q[k]);
         const uint64_t step = pack2(8.f * slope, 8.f * slope);
+        // fixed reference; under a distance bias, taken from the row's largest bias, so that the weight of the
+        // key that has it lies in the range of the capped scores
+        float fixed_shift = -sc.ref;
+        if constexpr (MODE == kCapDistance) {
+            const bool in_a = row.a0 < row.a1, in_b = row.b0 < row.b1;
+            const int32_t lo = in_a ? row.a0 : row.b0, hi = (in_b ? row.b1 : row.a1) - 1;  // ends of what the row sees
+            int32_t near = 0;  // b holds the row's own key, or is empty
+            if (!in_b) near = max(max(lo - pos, pos - hi), 0);
+            fixed_shift += slope * static_cast<float>(slope >= 0.f ? near : max(abs(pos - lo), abs(hi - pos)));
+        }
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         int32_t cnt = 0;  // key tiles this query tile has used
@@ -677,18 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             auto visible = [&](int c) -> uint32_t {
                 return span_bits(kbase + c * 16, row.a0, row.a1) | span_bits(kbase + c * 16, row.b0, row.b1);
             };
-            // Weight arguments (log2 domain) of group c: x = score + shift, in pairs. Straight-line
-            // code over the group; what differs by warp is branched on once per group.
             // Weight arguments (log2 domain), x = score + shift. A group of 16 keys is straight-line
             // code: begin_group sets up what its pairs share, pair_args does columns 2 e, 2 e + 1; what
             // differs by warp is branched on once per group (amend).
             float big[4];
             uint64_t away[4];
             auto begin_group = [&](int c, float shift) {
-                if constexpr (MODE == kCap) {
+                if constexpr (kFixed) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) big[k] = 0.f;
-                } else if constexpr (MODE == kDistance) {  // -slope |p - j| = slope (j - p) for j <= p
+                }
+                if constexpr (MODE == kDistance || MODE == kCapDistance) {  // -slope |p - j| = slope (j - p) for j <= p
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         away[k] = pack2(fmaf(slope, d0 + (c * 16 + 2 * k), shift), fmaf(slope, d0 + (c * 16 + 2 * k + 1), shift));
@@ -697,12 +728,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             auto pair_args = [&](uint64_t s, int c, int e, float shift, float& x0, float& x1) {
                 if constexpr (MODE == kPlain) {
                     unpack2(fma2(s, c1, pack2(shift, shift)), x0, x1);
-                } else if constexpr (MODE == kCap) {
+                } else if constexpr (kFixed) {
                     const uint64_t w = mul2(s, s);
                     uint64_t p = fma2(w, tq[3], tq[2]);
                     p = fma2(w, p, tq[1]);
                     p = fma2(w, p, tq[0]);
-                    unpack2(fma2(s, p, ref2), x0, x1);
+                    if constexpr (MODE == kCap) {
+                        unpack2(fma2(s, p, ref2), x0, x1);
+                    } else {
+                        unpack2(fma2(s, p, away[e & 3]), x0, x1);
+                        if (e < 4) away[e & 3] = add2(away[e & 3], step);
+                    }
                     float w0, w1;
                     unpack2(w, w0, w1);
                     big[e & 3] = max3(big[e & 3], w0, w1);
@@ -721,14 +757,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             // Scores beyond the polynomial's range, keys behind the row, masked keys.
             auto amend = [&](const uint32_t(&raw)[16], int c, float shift, float(&x)[16]) {
                 bool redo = false;
-                if constexpr (MODE == kCap) redo = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) > sc.s2_max;
-                if constexpr (MODE == kDistance) redo = behind;
+                if constexpr (kFixed) redo = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) > sc.s2_max;
+                if constexpr (MODE == kDistance || MODE == kCapDistance) redo = redo || behind;
                 if (redo || mask) {
                     if (redo) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float s = __uint_as_float(raw[k]);
                             if constexpr (MODE == kCap) x[k] = capped_exact(s, sc) + shift;
+                            if constexpr (MODE == kCapDistance)
+                                x[k] = capped_exact(s, sc) + fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift);
                             if constexpr (MODE == kDistance)
                                 x[k] = fmaf(s, sc.c1, fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift));
                         }
@@ -741,9 +779,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                     }
                 }
             };
-            float alpha = 1.f, shift = -sc.ref;
+            float alpha = 1.f, shift = fixed_shift;
             bool grow = false;
-            if constexpr (MODE != kCap) {
+            if constexpr (!kFixed) {
                 // pass 1: the tile's maximum over visible keys
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 uint32_t raw[2][16];
@@ -781,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
                 m_ref = m_new;
                 shift = m_new == -INFINITY ? 0.f : -m_new;  // nothing visible yet: weights are 0
             }
-            if constexpr (MODE != kCap) {
+            if constexpr (!kFixed) {
                 if (!first && __any_sync(0xffffffffu, grow)) {
                     // O holds the tiles before under the old reference; their last PV finished before
                     // this S was committed, so O can be rescaled now
@@ -866,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         if (kOwnO) sums[(2 + half) * kRows + r] = m_ref;
         named_barrier(1 + xq, 256);
         float w0 = 1.f, w1 = 1.f;  // weights of the halves' outputs: 1 under a common reference
-        float top = MODE == kCap ? 0.f : m_ref;
+        float top = kFixed ? 0.f : m_ref;
         if (kOwnO) {
             const float m0 = sums[2 * kRows + r], m1 = sums[3 * kRows + r];
             top = fmaxf(m0, m1);
@@ -1063,6 +1101,7 @@ cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, const Prefi
         case kPlain: return run(std::integral_constant<int, kPlain>{});
         case kCap: return run(std::integral_constant<int, kCap>{});
         case kDistance: return run(std::integral_constant<int, kDistance>{});
+        case kCapDistance: return run(std::integral_constant<int, kCapDistance>{});
         default: return run(std::integral_constant<int, kGeneral>{});
     }
 }
@@ -1101,14 +1140,14 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
         sc.s2_max = static_cast<float>(kTanhRange * kTanhRange / (k * k));
         sc.two_k = static_cast<float>(2 * 1.4426950408889634 * k);
         sc.cap_l2 = s.cap * kLog2e;
-        sc.ref = 0.5f * sc.cap_l2;
+        sc.ref = s.slopes ? sc.cap_l2 - kTopWeight : 0.5f * sc.cap_l2;
     }
     sc.window = s.window;
     sc.slopes = s.slopes;
     sc.key_start = s.key_start;
     sc.prefix_len = s.prefix_len;
     const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
-                                 : (!s.slopes && s.cap <= kMaxFixedCap ? kCap : kGeneral);
+                                 : s.cap > kMaxFixedCap ? kGeneral : s.slopes ? kCapDistance : kCap;
     return a.head_dim == 128 ? pick<128>(a, sc, mode, plan, workspace, num_sms, stream) : pick<64>(a, sc, mode, plan, workspace, num_sms, stream);
 }
 

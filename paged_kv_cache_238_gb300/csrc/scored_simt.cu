@@ -14,6 +14,11 @@
 //   M = max_p m_p,  w_p = l_p 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p.
 // The pages are those of the rows' visible spans only, so a window or a document start costs no
 // reads outside them. A page that a span cuts is read; its keys that no row sees are skipped in V.
+//
+// Bound: for a few rows the chain launch, lengths, block ids, pages, join (about 5 us: 24 sequences of up
+// to 777 keys, 12 q / 4 kv heads of 64 in fp32: 5.8 us); for chunks the fp32 pipes (two products of a
+// page take 2000 of 3100 cycles, one page and two warps per scheduler: 4 sequences of 17 to 96 rows in a
+// window of 256 keys: 15.7 us). Loads of K and V straight into registers, a key per lane, took 27 us.
 #include <math.h>
 
 #include <type_traits>

@@ -453,3 +453,26 @@ def test_prefill_split_refuses_a_small_workspace(dtype):
         d.ws = ws
         with pytest.raises(B.PaError):
             d.run()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (6, 1, 64)])
+@pytest.mark.parametrize("cap,slope", [(51.0, 1.0), (51.0, -0.02), (20.0, 30.0), (3.0, 0.01), (60.0, None), (60.0, 0.5),
+                                       (300.0, -0.01)])
+def test_prefill_caps_with_and_without_a_bias(H_q, H_kv, D, cap, slope):
+    """Caps on both sides of the fixed reference's limit; slopes from none over steep to negative (the bias
+    then grows with the distance); rows that see only keys far behind or before them."""
+    pairs = [(300, 200), (150, 150), (700, 5), (64, 64)]
+    lens, chunks = zip(*pairs)
+    pos = [p for L, C in pairs for p in range(L - C, L)]
+    slopes = None if slope is None else [slope * 2.0 ** -(h % 5) for h in range(H_q)]
+    common = dict(cap=cap, sharp=8.0, slopes=slopes)
+    check(Case(41, lens, H_q, H_kv, D, 16, "bf16", chunks=chunks, **common))
+    # every third row sees the prefix alone (from inside it, before it or behind it), some of them nothing
+    start = [p + 1 if i % 3 == 0 else 0 for i, p in enumerate(pos)]
+    check(Case(42, lens, H_q, H_kv, D, 16, "bf16", chunks=chunks, key_start=start, prefix=[250, 40, 100, 64], **common))
+
+
+def test_decode_one_kv_head_on_a_long_context():
+    """A segment that all CTAs could share goes to a limited number of them."""
+    check(Case(43, [9001], 8, 1, 128, 16, "bf16", cap=20.0))
+    check(Case(44, [5000, 40], 4, 1, 64, 64, "bf16", window=3000))
