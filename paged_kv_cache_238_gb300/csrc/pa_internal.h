@@ -230,7 +230,7 @@ cudaError_t launch_decode_scored(const DecodeArgs& a, const ScoreArgs& score, co
 // CUDA-core path (scored_simt.cu): CTAs of up to `rows` rows of a kv head, from `tokens` tokens; their
 // visible pages in up to num_parts partitions of part_pages.
 struct ScoredSimtPlan {
-    int32_t rows, head_chunks, tokens, groups, grid_x, part_pages, num_parts;
+    int32_t rows, warps, head_chunks, tokens, groups, grid_x, part_pages, num_parts;
     size_t workspace_bytes;
 };
 int32_t scored_simt_head_chunks(int32_t group);

@@ -2,7 +2,7 @@
 //
 // A CTA takes up to R rows (R = 4 or 16) that share a kv head: the q heads of a decode row, or the
 // q heads of R / G consecutive tokens of a chunk, so that each K and V element it reads serves all of
-// them. Its eight warps take the 16-token pages that some row sees in turn; each has room for one K and
+// them. Its warps (8 or 4) take the 16-token pages that some row sees in turn; each has room for one K and
 // one V page, and the next K page is on its way while the V page is used, and the other way round.
 // Scores: a lane multiplies 4 keys by 8 rows (R = 4: by 4) over a fourth (an eighth) of the columns, so
 // that a value out of shared memory serves 4 or 8 products; a reduction that also scatters leaves each
@@ -31,7 +31,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewRows = 4, kManyRows = 16;  // R: rows of a CTA
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMaxParts = 128;  // partitions: the merge holds their weights in shared memory
 constexpr float kLag = 8.f;  // log2 units
 constexpr int32_t kFar = 0x7fffffff;
 
@@ -126,7 +126,7 @@ struct SimtArgs {
 };
 
 // Shared memory in bytes: q, weights and pages while pages are walked, then the warps' outputs.
-template <typename T, int D, int R>
+template <typename T, int D, int R, int kWarps>
 struct Smem {
     static constexpr int pad = 16 / sizeof(T);  // rows 16 bytes apart in bank: a lane reads its own row
     static constexpr int q_stride = D + 4;      // two rows in a broadcast lie in different banks
@@ -140,15 +140,16 @@ struct Smem {
     static constexpr int page_bytes = k_bytes + 16 * D * static_cast<int>(sizeof(T));
     static constexpr int walk = page + kWarps * page_bytes, join = 4 * kWarps * R * D;
     static constexpr int bytes = walk > join ? walk : join;
+    static_assert(kMaxParts * R * 8 <= bytes, "the merge's weights");
 };
 
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ out, const T* __restrict__ q,
+template <typename T, int D, int R, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict__ out, const T* __restrict__ q,
                                                                const T* __restrict__ k_cache,
                                                                const T* __restrict__ v_cache,
                                                                const __grid_constant__ SimtArgs a) {
-    constexpr int E = D / 32, RL = R / 2;
-    using L = Smem<T, D, R>;
+    constexpr int E = D / 32, RL = R / 2, kThreads = 32 * kWarps;
+    using L = Smem<T, D, R, kWarps>;
     extern __shared__ float4 smem4[];
     char* sm = reinterpret_cast<char*>(smem4);
     __shared__ KeySpans spans[R];
@@ -486,32 +487,52 @@ __global__ void __launch_bounds__(kThreads) scored_simt_kernel(T* __restrict__ o
     }
     __syncthreads();
     if (!last_part) return;
-    for (int32_t i = tid; i < n_rows * D; i += kThreads) {
-        const int32_t r = i / D, d = i - r * D;
-        const int32_t tt = r / heads;
-        const int64_t head = static_cast<int64_t>(row0 + tt) * a.num_q_heads + h0 + (r - tt * heads);
-        const int64_t slot0 = (static_cast<int64_t>(cta) * R + r) * a.num_parts;
-        const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + slot0;
-        float M = -INFINITY;
-        for (int32_t p = 0; p < parts; ++p) M = fmaxf(M, __ldcg(ml + p).x);
+    // the partitions' (max, sum) of every row, then their weights, in shared memory: [part][row]
+    float2* const w = reinterpret_cast<float2*>(sm);
+    const int64_t slot0 = static_cast<int64_t>(cta) * R * a.num_parts;
+    for (int32_t i = tid; i < parts * R; i += kThreads) {
+        const int32_t p = i / R, r = i - p * R;
+        if (r < n_rows) w[i] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + slot0 + r * a.num_parts + p);
+    }
+    __syncthreads();
+    if (tid < n_rows) {
+        float M = -INFINITY, den = 0.f;
+        for (int32_t p = 0; p < parts; ++p) M = fmaxf(M, w[p * R + tid].x);
         const float ref = M == -INFINITY ? 0.f : M;
-        float num = 0.f, den = 0.f;
         for (int32_t p = 0; p < parts; ++p) {
-            const float2 v = __ldcg(ml + p);
-            const float w = v.y * exp2_approx(v.x - ref);
-            num = fmaf(w, __ldcg(a.ws_o + (slot0 + p) * D + d), num);
-            den += w;
+            const float2 v = w[p * R + tid];
+            const float f = v.y * exp2_approx(v.x - ref);
+            den += f;
+            w[p * R + tid].x = f;
         }
-        out[head * D + d] = narrow<T>(den == 0.f ? 0.f : num / den);
+        jden[tid] = den == 0.f ? 0.f : 1.f / den;
+    }
+    __syncthreads();
+    for (int32_t i = tid; i < n_rows * (D / 4); i += kThreads) {
+        const int32_t r = i / (D / 4), c = i - r * (D / 4);
+        const float4* o = reinterpret_cast<const float4*>(a.ws_o + (slot0 + r * a.num_parts) * D) + c;
+        float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int32_t p = 0; p < parts; ++p) {
+            const float4 v = __ldcg(o + p * (D / 4));
+            const float f = w[p * R + r].x;
+            acc4.x = fmaf(f, v.x, acc4.x), acc4.y = fmaf(f, v.y, acc4.y);
+            acc4.z = fmaf(f, v.z, acc4.z), acc4.w = fmaf(f, v.w, acc4.w);
+        }
+        const int32_t tt = r / heads;
+        T* to = out + (static_cast<int64_t>(row0 + tt) * a.num_q_heads + h0 + (r - tt * heads)) * D + c * 4;
+        const float inv = jden[r];
+        to[0] = narrow<T>(acc4.x * inv), to[1] = narrow<T>(acc4.y * inv);
+        to[2] = narrow<T>(acc4.z * inv), to[3] = narrow<T>(acc4.w * inv);
     }
 }
 
-template <typename T, int D, int R>
+template <typename T, int D, int R, int kWarps>
 cudaError_t launch_rows(void* out, const void* q, const void* k, const void* v, const SimtArgs& a, dim3 grid,
                         cudaStream_t stream) {
-    constexpr int bytes = Smem<T, D, R>::bytes;
+    constexpr int bytes = Smem<T, D, R, kWarps>::bytes;
     if (bytes > 40960) {  // with the static part, beyond what every kernel may use
-        const cudaError_t e = allow_smem<scored_simt_kernel<T, D, R>>(bytes);
+        const cudaError_t e = allow_smem<scored_simt_kernel<T, D, R, kWarps>>(bytes);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr[1];
@@ -519,12 +540,12 @@ cudaError_t launch_rows(void* out, const void* q, const void* k, const void* v, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_simt_kernel<T, D, R>, static_cast<T*>(out), static_cast<const T*>(q),
+    return cudaLaunchKernelEx(&cfg, scored_simt_kernel<T, D, R, kWarps>, static_cast<T*>(out), static_cast<const T*>(q),
                               static_cast<const T*>(k), static_cast<const T*>(v), a);
 }
 
@@ -542,8 +563,9 @@ cudaError_t launch_impl(void* out, const void* q, const void* k, const void* v, 
         a.ws_ml = a.ws_o + static_cast<size_t>(p.grid_x) * a.num_kv_heads * p.head_chunks * p.rows * p.num_parts * D;
     }
     const dim3 grid(p.grid_x, a.num_kv_heads * a.head_chunks, a.num_parts);
-    return p.rows == kFewRows ? launch_rows<T, D, kFewRows>(out, q, k, v, a, grid, stream)
-                              : launch_rows<T, D, kManyRows>(out, q, k, v, a, grid, stream);
+    if (p.rows == kFewRows) return launch_rows<T, D, kFewRows, 8>(out, q, k, v, a, grid, stream);
+    return p.warps == 8 ? launch_rows<T, D, kManyRows, 8>(out, q, k, v, a, grid, stream)
+                        : launch_rows<T, D, kManyRows, 4>(out, q, k, v, a, grid, stream);
 }
 
 template <typename A>
@@ -582,27 +604,33 @@ int32_t scored_simt_head_chunks(int32_t group) {
     return group <= kFewRows ? 1 : (group + kManyRows - 1) / kManyRows;
 }
 
-// max_chunk 0: decode. Partitions so that the CTAs fill the SMs about twice, of at least kMinPages pages
-// each. Measured, 24 sequences of up to 777 keys, 4 kv heads of 64 in fp32: 9.1 us with 32 or 64 pages,
+// max_chunk 0: decode. Partitions so that the CTAs fill the SMs once (two CTAs of 4 rows, one of 16 on an SM),
+// of at least kMinPages pages each. Measured, 24 sequences of up to 777 keys, 4 kv heads of 64 in fp32: 9.1 us with 32 or 64 pages,
 // 10.7 with 8 or 16.
 ScoredSimtPlan plan_scored_simt(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len,
                                 int num_sms) {
     constexpr int64_t kMinPages = 32;
     ScoredSimtPlan p{};
     const int32_t G = Hq / Hkv;
+    // (24 sequences, 12 q / 4 kv heads of 64 in fp32: 5.8 us with 4 rows, 8.0 with 16; chunks of 17 to 96 rows, 8 q / 2
+    // kv heads: 17.1 with 4, 15.7 with 16)
     p.rows = static_cast<int64_t>(G) * (max_chunk > 0 ? max_chunk : 1) <= kFewRows ? kFewRows : kManyRows;
     p.head_chunks = (G + p.rows - 1) / p.rows;
     p.tokens = G < p.rows ? p.rows / G : 1;
     p.groups = max_chunk > 0 ? (max_chunk + p.tokens - 1) / p.tokens : 1;
     p.grid_x = S * p.groups;
     const int64_t ctas = static_cast<int64_t>(p.grid_x) * Hkv * p.head_chunks, pages = max_seq_len / kPageTokens + 2;
-    int64_t parts = ctas > 0 ? (2LL * num_sms + ctas - 1) / ctas : 1;
-    parts = max(min(parts, pages / kMinPages), static_cast<int64_t>(1));
+    int64_t parts = ctas > 0 ? (p.rows == kFewRows ? 2LL : 1LL) * num_sms / ctas : 1;
+    parts = max(min(min(parts, pages / kMinPages), static_cast<int64_t>(kMaxParts)), static_cast<int64_t>(1));
     p.part_pages = static_cast<int32_t>((pages + parts - 1) / parts);
     p.num_parts = static_cast<int32_t>((pages + p.part_pages - 1) / p.part_pages);
-    // room for any number of rows: fewer than 4 num_sms CTAs are split
+    // A CTA of 8 warps and 16 rows has an SM to itself; of 4 warps two fit, and hide each other's start and end.
+    // Measured in fp32: 4 x 1024 rows, 16 q / 4 kv heads of 128: 659 us with 8, 541 with 4; 192 CTAs, 12 pages a
+    // warp: 24.9 and 20.1; 192 CTAs of which 114 have rows (chunks of 17 to 96): 15.7 and 22.4.
+    p.warps = p.rows == kFewRows || ctas * p.num_parts <= 2 * num_sms ? 8 : 4;
+    // room for any number of rows: split grids have 2 num_sms CTAs at most
     if (pages >= 2 * kMinPages)
-        p.workspace_bytes = kScoredCounterBytes + static_cast<size_t>(4 * num_sms) * kManyRows * (D + 2) * sizeof(float);
+        p.workspace_bytes = kScoredCounterBytes + static_cast<size_t>(2 * num_sms) * kManyRows * (D + 2) * sizeof(float);
     return p;
 }
 

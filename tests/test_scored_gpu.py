@@ -476,3 +476,12 @@ def test_decode_one_kv_head_on_a_long_context():
     """A segment that all CTAs could share goes to a limited number of them."""
     check(Case(43, [9001], 8, 1, 128, 16, "bf16", cap=20.0))
     check(Case(44, [5000, 40], 4, 1, 64, 64, "bf16", window=3000))
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,dtype", [(8, 1, 64, "f32"), (3, 1, 128, "f32"), (130, 1, 64, "bf16")])
+def test_general_path_in_many_partitions(H_q, H_kv, D, dtype):
+    """One sequence, few rows, fp32 (and a group that the tensor cores do not take): as many partitions as there are."""
+    check(Case(45, [40011], H_q, H_kv, D, 16, dtype))
+    if H_q < 100:
+        check(Case(46, [40011], H_q, H_kv, D, 16, dtype, chunks=[1], prefix=[100], window=30000))
+        check(Case(47, [9000, 50], H_q, H_kv, D, 16, dtype, chunks=[2, 50], cap=10.0))
