@@ -245,7 +245,7 @@ cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& sc
 bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev);
 // Runs into which a CTA's key list is split when the grid is small, and what their results take.
 struct PrefillScoredPlan {
-    int32_t parts;
+    int32_t parts, tiles;  // tiles: query tiles of a CTA
     size_t workspace_bytes;
 };
 PrefillScoredPlan plan_prefill_scored(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,

@@ -2,10 +2,11 @@
 // heads per kv head): attention of a chunk of new rows over the paged pool with scores that are
 // capped by a tanh, biased by distance or masked (window, visible prefix, document start).
 //
-// One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head): row r of a tile is
-// token r / G, q head r % G of the G heads that share the kv head, so every K/V tile is read once
-// for both. Keys come in tiles of 128, and only the tiles that hold a key some row of the CTA sees
-// (TileList: the prefix's tiles, then the window's):
+// One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head), or one tile on short
+// contexts and of short chunks (short_keys): row r of a tile is token r / G, q head r % G of the G heads
+// that share the kv head, so every K/V tile is read once for both. Keys come in tiles of 128, and only
+// the tiles that hold a key some row of the CTA sees (TileList: the prefix's tiles, then the window's).
+// Of a CTA of two tiles (one tile: 8 softmax warps, then the same three):
 //   warp 16    - K producer, warp 18 - V producer: block ids 32 pages ahead, TMA copies of 16-token
 //                pages (128-byte swizzle) into rings of key tiles;
 //   warp 17    - tensor-memory owner and MMA issuer: S = Q K^T, O += P V with P from tensor memory,
@@ -63,10 +64,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
-constexpr int kSoftWarps = 16;  // warps 0-15: scores and softmax
-constexpr int kKWarp = 16, kMmaWarp = 17, kVWarp = 18;
-constexpr int kThreads = 32 * (kVWarp + 1);
-constexpr int kSoftThreads = 32 * kSoftWarps;
+// Warps of a CTA of NQ query tiles: softmax, K producer, MMA issuer, V producer.
+template <int NQ>
+struct Warps {
+    static constexpr int soft = 8 * NQ, k = soft, mma = soft + 1, v = soft + 2, threads = 32 * (soft + 3);
+};
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 bf16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units: O is rescaled only when the maximum grows by more
 constexpr int kRankMax = 256;             // entries that each CTA ranks by their work
@@ -79,6 +81,12 @@ constexpr size_t kSplitRowBytes = kRankMax * 16 * 16;  // Split::rows, in a work
 // heads of 128: 15.8 us with 2, 17.7 with 4, 25.7 with 8, 63.8 not split; 256 rows on 32768 keys: 149 us, not
 // split 531.
 constexpr int kMinPartTiles = 2;
+// Query tiles of a CTA: one, with two CTAs on an SM that cover each other's start and end, where one tile holds
+// a chunk (64 chunks of 20 rows, 32 q / 8 kv heads of 128: on 30 keys 24.3 us against 38.1 with two tiles, on 2020
+// keys 109 against 149) or the contexts are short (16 chunks of 300, 16 heads of 64: 33.1 against 40.0; 12 chunks
+// of 100 on 120 keys, heads of 128: 12.8 against 19.0); else two, which share each K and V tile (16 chunks of 512
+// on up to 4608 keys: 293 us, with one tile 419; the two meet near 1000 keys at head_dim 64, 200 at 128).
+__host__ __device__ constexpr int short_keys(int D) { return D == 64 ? 768 : 192; }
 // Caps with a fixed reference: 1.5 cap log2(e) <= 112. Measured, 16 sequences of 512 new rows on 2512 keys, 32 q / 8
 // kv heads of 128: cap 50 298 us, not capped 332, cap 52 (general) 821.
 constexpr float kMaxFixedCap = 51.f;
@@ -88,13 +96,13 @@ constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between poll
 
 enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kCapDistance = 3, kGeneral = 4 };
 
-template <int D>
+template <int D, int NQ>
 struct Smem {
-    static constexpr int k_stages = D == 128 ? 3 : 4;
-    static constexpr int v_stages = D == 128 ? 2 : 4;
+    static constexpr int k_stages = NQ == 1 ? 128 / D : D == 128 ? 3 : 4;
+    static constexpr int v_stages = NQ == 1 ? 128 / D : D == 128 ? 2 : 4;
     static constexpr uint32_t tile = (D / 64) * kHalf;  // 128 x D bf16
-    static constexpr uint32_t q = 0;                    // query tiles a, b
-    static constexpr uint32_t k = q + 2 * tile;
+    static constexpr uint32_t q = 0;                    // query tiles
+    static constexpr uint32_t k = q + NQ * tile;
     static constexpr uint32_t v = k + k_stages * tile;
     static constexpr uint32_t bars = v + v_stages * tile;
     static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 20;
@@ -310,14 +318,17 @@ __device__ __forceinline__ uint32_t span_bits(int32_t base, int32_t lo, int32_t 
     return (h == 32 ? 0xffffffffu : (1u << h) - 1u) & ~(l == 32 ? 0xffffffffu : (1u << l) - 1u);
 }
 
-template <int D, int MODE, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
+template <int D, int MODE, int NQ, bool SPLIT>
+__global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ query_start_loc,
     int32_t num_kv_heads, int32_t G, int32_t num_blocks, int32_t sub_log2, int32_t cap_tokens, int32_t max_chunk,
     int32_t sub, uint32_t inv_sub, const __grid_constant__ Split split,    const __grid_constant__ TcScore sc, uint32_t* err) {
-    using L_ = Smem<D>;
+    using L_ = Smem<D, NQ>;
+    constexpr int kSoftWarps = Warps<NQ>::soft, kKWarp = Warps<NQ>::k, kMmaWarp = Warps<NQ>::mma, kVWarp = Warps<NQ>::v;
+    constexpr int kSoftThreads = 32 * kSoftWarps;
+    constexpr uint32_t kO = NQ * 128;  // first tensor-memory column of O
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
     constexpr int kHalves = D / 64;
@@ -327,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     constexpr bool kFixed = MODE == kCap || MODE == kCapDistance;  // fixed reference
     constexpr bool kSplit = kFixed || D == 64;
     constexpr bool kOwnO = kSplit && !kFixed;  // each half of the keys has its own O and maximum
-    constexpr int kChains = kSplit ? 4 : 2;
+    constexpr int kChains = kSplit ? 2 * NQ : NQ;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::bars);
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         uint32_t mine = 0;
         if (tid < n_entries) {
             entry(tid);
-            const int32_t first = 2 * pair * TT, rows = sub > 1 ? min(2 * TT, C - first) : C;
+            const int32_t first = NQ * pair * TT, rows = sub > 1 ? min(NQ * TT, C - first) : C;
             int32_t keys = L - C + first + rows;  // up to the last row's own
             if (sc.window > 0) keys = min(keys, sc.window + rows + min(max(prefix, 0), L));
             if (rows <= 0) keys = 0;
@@ -404,13 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
         return;
     }
-    const int32_t t0a = 2 * pair * TT, t0b = t0a + TT;
+    const int32_t t0a = NQ * pair * TT, t0b = t0a + TT;
     if (t0a >= C) return;  // uniform over the CTA
     const int32_t P0 = L - C;
 
     // ---- rows of the softmax threads --------------------------------------------------------------
     const bool softmax_warp = warp < kSoftWarps;
-    const int32_t xq = (warp >> 2) & 1, half = (warp >> 3) & 1;  // query tile and key half of a softmax warp
+    const int32_t xq = NQ == 2 ? (warp >> 2) & 1 : 0, half = (NQ == 2 ? warp >> 3 : warp >> 2) & 1;  // query tile and key half of a softmax warp
     const int32_t quad = warp & 3;                                // its TMEM lane quadrant
     const int32_t r = quad * 32 + lane;
     const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // x / G = x inv_G / 2^16 for x, G <= 128
@@ -439,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     KeySpans row{0, 0, 0, 0};
     if (row_valid)
         row = key_spans(L, pos, sc.key_start ? __ldg(sc.key_start + q0 + t_row) : 0, prefix, sc.window);
-    SpanUnion ux[2];
+    SpanUnion ux[NQ];
     if (sc.key_start == nullptr) {  // rows' spans move with their position: the first and the last row tell
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NQ; ++x) {
             const int32_t t0 = x ? t0b : t0a, t1 = min(t0 + TT, C);
             if (t0 >= t1) {
                 ux[x] = SpanUnion{0, 0, 0, 0};
@@ -479,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         }
         __syncthreads();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ux[x] = SpanUnion{red[x][0], red[x][1], red[x][2], red[x][3]};
+        for (int x = 0; x < NQ; ++x) ux[x] = SpanUnion{red[x][0], red[x][1], red[x][2], red[x][3]};
     }
-    const SpanUnion uni = join(ux[0], ux[1]);
+    const SpanUnion uni = join(ux[0], ux[NQ - 1]);
     TileList tiles = tile_list(uni);
     int32_t n_kv = tiles.n, n_parts = 1;
     if constexpr (SPLIT) {  // this CTA takes one of up to split.parts equal runs of the list
@@ -497,9 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             split.rows[cta] = make_int4(q0 + t0a, min(TT, C - t0a) * G, max(min(TT, C - t0b), 0) * G, n_parts);
     }
     // list positions whose key tile query tile x uses: two ranges
-    int32_t ra0[2], ra_n[2], rb0[2], rb_n[2];
+    int32_t ra0[NQ], ra_n[NQ], rb0[NQ], rb_n[NQ];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NQ; ++x) {
         ra0[x] = ux[x].a0 / kKeys - tiles.first_a - tiles.base;
         ra_n[x] = ux[x].a0 < ux[x].a1 ? (ux[x].a1 - 1) / kKeys - tiles.first_a - tiles.base + 1 - ra0[x] : 0;
         rb0[x] = tiles.position(ux[x].b0 / kKeys);
@@ -541,14 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
-        umma::tmem_alloc(tmem_holder, 512);
+        umma::tmem_alloc(tmem_holder, 2 * kO);
         umma::tmem_relinquish();
     }
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, bf16 pairs,
-    // overwrites the first 32 of the half's 64 columns once read), O of tile x at 256 + 128 x
+    // overwrites the first 32 of the half's 64 columns once read), O of tile x at kO + 128 x
     const uint32_t tmem = *tmem_holder;
     if (softmax_warp) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         const uint64_t dk0 = umma::smem_desc_sw128(smem_u32(smem + L_::k), 16, 1024);
         const uint64_t dv0 = umma::smem_desc_sw128(smem_u32(smem + L_::v), kHalf, 1024);
         auto qk = [&](int c, int32_t j) {
-            const int x = c & 1, hf = c >> 1;
+            const int x = c % NQ, hf = c / NQ;
             const uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4);
             const uint64_t dk = dk0 + static_cast<uint64_t>(j % kKStages) * (kTile >> 4) + hf * (64 * 128 >> 4);
 #pragma unroll
@@ -606,12 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             umma::commit(&s_full[c]);
         };
         auto pv = [&](int c, int32_t j, bool acc) {
-            const int x = c & 1, hf = c >> 1;
+            const int x = c % NQ, hf = c / NQ;
             const uint64_t dv = dv0 + static_cast<uint64_t>(j % kVStages) * (kTile >> 4);
 #pragma unroll
             for (int k = 0; k < kChainKeys / 16; ++k) {  // 16 keys per instruction: 8 P columns
                 const int kk = hf * 4 + k;
-                umma::mma_bf16_tmem_a(tmem + 256 + x * 128 + (kOwnO ? hf * D : 0), tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                umma::mma_bf16_tmem_a(tmem + kO + x * 128 + (kOwnO ? hf * D : 0), tmem + x * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                                       dv + static_cast<uint64_t>(kk * (2048 >> 4)), idesc_pv, (acc || k > 0));
             }
         };
@@ -620,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             umma::fence_after_sync();
             return ok;
         };
-        int32_t last[2], done[2] = {0, 0};  // last list position, and positions finished, per query tile
+        int32_t last[NQ], done[NQ] = {};  // last list position, and positions finished, per query tile
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NQ; ++x) {
             last[x] = n_kv - 1;
             while (last[x] >= 0 && !used(x, last[x])) --last[x];
         }
@@ -631,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         if (ok && n_kv > 0) {
 #pragma unroll
             for (int c = 0; c < kChains; ++c)
-                if (used(c & 1, 0)) qk(c, 0);
+                if (used(c % NQ, 0)) qk(c, 0);
             umma::commit(&k_empty[0]);
         }
         for (int32_t j = 0; j < n_kv && ok; ++j) {
@@ -639,13 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
             ok = wait_or_abort<0>(&v_full[j % kVStages], static_cast<uint32_t>(j / kVStages) & 1u, abort_flag, err);
 #pragma unroll
             for (int c = 0; c < kChains; ++c) {
-                const int x = c & 1;
+                const int x = c % NQ;
                 if (ok && used(x, j)) {  // P written, S read: O_x += P V(j)
                     ok = wait_or_abort<0>(&p_full[c], done[x] & 1, abort_flag, err);
                     umma::fence_after_sync();
                     if (ok) {
-                        pv(c, j, done[x] > 0 || (!kOwnO && c >= 2));
-                        if (c >= kChains - 2) {  // the query tile's last chain
+                        pv(c, j, done[x] > 0 || (!kOwnO && c >= NQ));
+                        if (c >= kChains - NQ) {  // the query tile's last chain
                             ++done[x];
                             if (j == last[x]) umma::commit(&o_done[x]);
                         }
@@ -661,10 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         mbar_wait_timeout(idle, 0);
     } else if (softmax_warp) {
         // ==================================== scores and softmax ================================
-        const int32_t chain = kSplit ? half * 2 + xq : xq;
+        const int32_t chain = kSplit ? half * NQ + xq : xq;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + xq * 128 + half * 64 + lane_off;
-        const uint32_t tmem_o = tmem + 256 + xq * 128 + half * (kOwnO ? D : D / 2) + lane_off;  // columns it rescales
+        const uint32_t tmem_o = tmem + kO + xq * 128 + half * (kOwnO ? D : D / 2) + lane_off;  // columns it rescales
         const float slope = (MODE != kPlain && MODE != kCap) && sc.slopes && row_valid
                                 ? __ldg(sc.slopes + h * G + g) * kLog2e
                                 : 0.f;
@@ -916,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
         ok = __all_sync(0xffffffffu, ok);
         // columns half (D / 2) + 32 c .. of the row's output, before the division; 0 where no key was used
         auto load_output = [&](int c, uint32_t(&o)[32]) {
-            const uint32_t cols = tmem + 256 + xq * 128 + half * (D / 2) + c * 32 + lane_off;
+            const uint32_t cols = tmem + kO + xq * 128 + half * (D / 2) + c * 32 + lane_off;
             if (cnt == 0) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
@@ -995,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_scored_kernel(
     __syncthreads();
     if (warp == kMmaWarp) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, 512);
+        umma::tmem_dealloc(tmem, 2 * kO);
     }
 }
 
@@ -1039,11 +1050,12 @@ constexpr double kTanh[4] = {0.999991018, -0.332989742, 0.129745541, -0.03961127
 constexpr float kTanhRange = 0.6f;
 
 // Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
-bool few_waves(int64_t entries, int32_t num_kv_heads, int num_sms) {
-    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * num_sms;
+// tiles: query tiles of a CTA; of one tile, two CTAs share an SM.
+bool few_waves(int64_t entries, int32_t num_kv_heads, int tiles, int num_sms) {
+    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * (3 - tiles) * num_sms;
 }
 
-template <int D, int MODE, bool SPLIT>
+template <int D, int MODE, int NQ, bool SPLIT>
 cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillScoredPlan& plan,
                         void* workspace, int num_sms, cudaStream_t stream) {
     alignas(64) CUtensorMap tm_k, tm_v;
@@ -1052,15 +1064,15 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillSc
     if (e != cudaSuccess) return e;
     e = encode_bf16_2d_sw128(&tm_v, a.v_cache, D, rows, 64, kPageTokens);
     if (e != cudaSuccess) return e;
-    e = allow_smem<prefill_scored_kernel<D, MODE, SPLIT>>(static_cast<int>(Smem<D>::total));
+    e = allow_smem<prefill_scored_kernel<D, MODE, NQ, SPLIT>>(static_cast<int>(Smem<D, NQ>::total));
     if (e != cudaSuccess) return e;
     const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
-    const int32_t pairs = (a.max_chunk_len + 2 * TT - 1) / (2 * TT);
+    const int32_t pairs = (a.max_chunk_len + NQ * TT - 1) / (NQ * TT);
     // Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
     const int64_t entries = static_cast<int64_t>(pairs) * a.num_seqs;
-    const bool by_pair = few_waves(entries, a.num_kv_heads, num_sms);
+    const bool by_pair = few_waves(entries, a.num_kv_heads, NQ, num_sms);
     const int32_t sub = by_pair ? pairs : 1;
     const dim3 grid(SPLIT ? plan.parts : by_pair ? 1 : pairs, a.num_kv_heads, a.num_seqs * sub);
     Split split{};
@@ -1072,7 +1084,7 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillSc
         split.ml = reinterpret_cast<float2*>(split.o + entries * a.num_kv_heads * plan.parts * (D / 4) * (2 * kRows));
     }
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-    prefill_scored_kernel<D, MODE, SPLIT><<<grid, kThreads, Smem<D>::total, stream>>>(
+    prefill_scored_kernel<D, MODE, NQ, SPLIT><<<grid, Warps<NQ>::threads, Smem<D, NQ>::total, stream>>>(
         tm_k, tm_v, out, static_cast<const __nv_bfloat16*>(a.q), a.block_table, a.max_blocks_per_seq, a.seq_lens,
         a.query_start_loc, a.num_kv_heads, G, a.num_blocks, sub_log2, cap_tokens, a.max_chunk_len, sub, 65536u / sub + 1,
         split, sc, a.err);
@@ -1094,8 +1106,9 @@ template <int D>
 cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, const PrefillScoredPlan& plan, void* workspace,
                  int num_sms, cudaStream_t stream) {
     auto run = [&](auto m) {
-        return plan.parts > 1 ? launch_impl<D, m, true>(a, sc, plan, workspace, num_sms, stream)
-                              : launch_impl<D, m, false>(a, sc, plan, workspace, num_sms, stream);
+        if (plan.parts > 1) return launch_impl<D, m, 2, true>(a, sc, plan, workspace, num_sms, stream);
+        return plan.tiles == 1 ? launch_impl<D, m, 1, false>(a, sc, plan, workspace, num_sms, stream)
+                               : launch_impl<D, m, 2, false>(a, sc, plan, workspace, num_sms, stream);
     };
     switch (mode) {
         case kPlain: return run(std::integral_constant<int, kPlain>{});
@@ -1110,22 +1123,24 @@ cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, const Prefi
 
 PrefillScoredPlan plan_prefill_scored(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_len,
                                       int num_sms) {
-    PrefillScoredPlan plan{1, 0};
+    PrefillScoredPlan plan{1, 2, 0};
+    if (Hq / Hkv > kRows) return plan;
+    const int32_t TT = kRows / (Hq / Hkv);
+    if (max_chunk <= TT || max_len <= short_keys(D)) plan.tiles = 1;
     const int64_t most = static_cast<int64_t>(max_len / kKeys + 1) / kMinPartTiles;  // runs of the longest list
-    if (Hq / Hkv > kRows || most < 2) return plan;
+    if (most < 2) return plan;
     // room for a wave of CTAs, whatever the chunks: a workspace serves every call up to its max_len
     plan.workspace_bytes = kScoredCounterBytes + kSplitRowBytes + static_cast<size_t>(num_sms) * (2 * kRows) * (D * 4 + 8);
     if (S < 1 || max_chunk < 1) return plan;
-    const int32_t TT = kRows / (Hq / Hkv);
     const int64_t entries = (static_cast<int64_t>(max_chunk) + 2 * TT - 1) / (2 * TT) * S;
-    if (few_waves(entries, Hkv, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
+    if (few_waves(entries, Hkv, 2, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
         plan.parts = static_cast<int32_t>(max(min(num_sms / (entries * Hkv), most), static_cast<int64_t>(1)));
     return plan;
 }
 
 bool prefill_scored_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
     return a.dtype == PA_BF16 && a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
-           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128>::total) <= dev.max_smem_optin;
+           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128, 2>::total) <= dev.max_smem_optin;
 }
 
 cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, const PrefillScoredPlan& plan,

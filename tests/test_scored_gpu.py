@@ -485,3 +485,19 @@ def test_general_path_in_many_partitions(H_q, H_kv, D, dtype):
     if H_q < 100:
         check(Case(46, [40011], H_q, H_kv, D, 16, dtype, chunks=[1], prefix=[100], window=30000))
         check(Case(47, [9000, 50], H_q, H_kv, D, 16, dtype, chunks=[2, 50], cap=10.0))
+
+
+WIDE_CHUNKS = {  # name: (keys, rows), H_q, H_kv: what a CTA of the bf16 kernel takes
+    "two tiles": ([(900, 300), (805, 200), (20, 20)], 40, 40),
+    "one tile of a short chunk": ([(1 + 41 * i % 700, 1 + i % 40 if 1 + 41 * i % 700 > 40 else 1) for i in range(40)], 8, 4),
+    "one tile of short contexts": ([(190, 190), (130, 2), (64, 64), (129, 100), (1, 1), (0, 0)], 12, 4),
+}
+
+
+@pytest.mark.parametrize("kind", CHUNK_KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name", list(WIDE_CHUNKS))
+def test_prefill_tiles_of_a_cta(name, D, kind):
+    pairs, H_q, H_kv = WIDE_CHUNKS[name]
+    lens, chunks = zip(*pairs)
+    check(Case(48, lens, H_q, H_kv, D, 32, "bf16", chunks=chunks, **chunk_scores(kind, H_q, pairs)), f"{name} {kind}")
