@@ -667,7 +667,7 @@ PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t n
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     MoveArgs a{block_pairs, tokens, block_table, seq_lens, n_pairs, num_blocks, block_size, block_table ? num_seqs : 0,
-               max_blocks_per_seq, static_cast<int32_t>(row_bytes / 16), static_cast<int32_t>(chunks), dev->err};
+               max_blocks_per_seq, static_cast<int32_t>(row_bytes / 16), static_cast<int32_t>(chunks), 1, dev->err};
     return launch_move_blocks(a, pools, num_pools, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                                       : PA_ERR_CUDA;
 }

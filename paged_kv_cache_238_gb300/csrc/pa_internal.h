@@ -264,6 +264,7 @@ struct MoveArgs {
     const int32_t* seq_lens;
     int32_t num_pairs, num_blocks, block_size, num_seqs, max_blocks;
     int32_t row_chunks, block_chunks;  // 16-byte chunks of a token's row, of a block
+    int32_t group;                     // pairs of a CTA (set by the launcher)
     uint32_t* err;
 };
 cudaError_t launch_move_blocks(const MoveArgs& a, void* const* pools, int32_t num_pools, cudaStream_t stream);

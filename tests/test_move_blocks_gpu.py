@@ -123,3 +123,40 @@ def test_offsets_past_32_bits():
     pool[2] = 5.0
     B.pa_move_blocks([pool], i32([(NB - 1, 1), (2, NB - 2)]))
     assert (pool[1] == 3).all() and (pool[NB - 2] == 5).all()
+
+
+@pytest.mark.parametrize("H,BS,D,dtype", [(1, 16, 8, torch.bfloat16), (1, 16, 64, torch.bfloat16), (3, 16, 64, torch.bfloat16),
+                                          (2, 32, 128, torch.float32)])
+@pytest.mark.parametrize("partial", [False, True])
+def test_many_small_blocks(H, BS, D, dtype, partial):
+    """Several pairs to a CTA: more pairs than one CTA takes, the last group not full, ids that are equal or out of range."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n = 333
+    NB = 2 * n + 5
+    pools = [torch.randn(NB, H, BS, D, generator=g, device="cuda").to(dtype) for _ in range(3)]
+    order = np.random.default_rng(5).permutation(NB)
+    pairs = [(int(order[i]), int(order[n + i])) for i in range(n)]
+    pairs[7] = (pairs[7][0], pairs[7][0])
+    tokens = [(5 * i) % (BS + 3) - 1 for i in range(n)] if partial else None
+    want = expected(pools, pairs, tokens)
+    B.pa_move_blocks(pools, i32(pairs), tokens=None if tokens is None else i32(tokens))
+    for p, w in zip(pools, want):
+        assert np.array_equal(bits(p), w)
+    before = [p.clone() for p in pools]
+    bad = [(0, NB)] * 200 + [(-1, 3)] * 100 + [(2, 4)]
+    B.pa_move_blocks(pools, i32(bad))
+    assert B.pa_get_device_errors(clear=True) == B.PA_DEVERR_BLOCK_RANGE
+    for p, b in zip(pools, before):
+        b[4] = b[2]
+        assert torch.equal(p, b)
+
+
+@pytest.mark.parametrize("H", [1, 8])
+def test_tables_without_pools(H):
+    table, lens = i32([[3, 5, 9, 0], [5, 3, 2, 9]]), i32([40, 64])
+    pairs = i32([(3, 1), (9, 4)])
+    status = B.load().pa_move_blocks(None, 0, H, 128, 16, 16, B.PA_BF16, pairs.data_ptr(), 2, None, table.data_ptr(), 4,
+                                     lens.data_ptr(), 2, None)
+    assert status == B.PA_OK
+    torch.cuda.synchronize()
+    assert table.tolist() == [[1, 5, 4, 0], [5, 1, 2, 4]]
