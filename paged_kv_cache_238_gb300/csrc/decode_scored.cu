@@ -722,7 +722,7 @@ cudaError_t launch_impl(const DecodeArgs& d, const ScoreArgs& score, const Decod
     a.nst = plan.stages;
     a.c1 = d.scale * kLog2e;
     if (score.cap > 0.f) {
-        a.two_k = static_cast<float>(2 * 1.4426950408889634 * d.scale / score.cap);
+        a.two_k = static_cast<float>(fmin(fmax(2 * 1.4426950408889634 * d.scale / score.cap, -3e38), 3e38));
         a.cap_l2 = score.cap * kLog2e;
     }
     char* ws = static_cast<char*>(d.workspace);

@@ -1153,7 +1153,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
         double c = static_cast<double>(s.cap) * 1.4426950408889634 * k;
         for (int i = 0; i < 4; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
         sc.s2_max = static_cast<float>(kTanhRange * kTanhRange / (k * k));
-        sc.two_k = static_cast<float>(2 * 1.4426950408889634 * k);
+        sc.two_k = static_cast<float>(fmin(fmax(2 * 1.4426950408889634 * k, -3e38), 3e38));
         sc.cap_l2 = s.cap * kLog2e;
         sc.ref = s.slopes ? sc.cap_l2 - kTopWeight : 0.5f * sc.cap_l2;
     }
@@ -1162,7 +1162,8 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
     sc.key_start = s.key_start;
     sc.prefix_len = s.prefix_len;
     const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
-                                 : s.cap > kMaxFixedCap ? kGeneral : s.slopes ? kCapDistance : kCap;
+                                 : s.cap > kMaxFixedCap || !isfinite(sc.q[3]) ? kGeneral  // (tiny caps: no polynomial)
+                                 : s.slopes ? kCapDistance : kCap;
     return a.head_dim == 128 ? pick<128>(a, sc, mode, plan, workspace, num_sms, stream) : pick<64>(a, sc, mode, plan, workspace, num_sms, stream);
 }
 

@@ -501,3 +501,13 @@ def test_prefill_tiles_of_a_cta(name, D, kind):
     pairs, H_q, H_kv = WIDE_CHUNKS[name]
     lens, chunks = zip(*pairs)
     check(Case(48, lens, H_q, H_kv, D, 32, "bf16", chunks=chunks, **chunk_scores(kind, H_q, pairs)), f"{name} {kind}")
+
+
+@pytest.mark.parametrize("sharp", [0.0, 1.0])
+@pytest.mark.parametrize("cap", [1e-6, 1e-30, 1e-38])
+def test_tiny_caps(cap, sharp):
+    """Caps so small that the scale over them overflows: every score is 0 or the cap, also where q.k is 0."""
+    for slopes in (None, alibi(4)):
+        check(Case(49, [300, 40], 4, 2, 64, 16, "bf16", chunks=[150, 40], cap=cap, sharp=sharp, slopes=slopes))
+        check(Case(49, [300, 40], 4, 2, 128, 16, "bf16", cap=cap, sharp=sharp, slopes=slopes))
+        check(Case(49, [300, 40], 4, 2, 64, 16, "f32", chunks=[15, 4], cap=cap, sharp=sharp, slopes=slopes))
