@@ -499,11 +499,15 @@ class Score:
         import torch
         if self.alibi_slopes is self.key_start is self.prefix_len is None:
             return
-        for name, t, dtype, n in (("alibi_slopes", self.alibi_slopes, torch.float32, H_q),
-                                  ("key_start", self.key_start, torch.int32, rows),
-                                  ("prefix_len", self.prefix_len, torch.int32, S)):
-            if t is not None and not _fits(t, dtype, (n,), device):
-                _need(name, t, dtype, (n,), device)
+        t = self.alibi_slopes
+        if t is not None and not _fits(t, torch.float32, (H_q,), device):
+            _need("alibi_slopes", t, torch.float32, (H_q,), device)
+        t = self.key_start
+        if t is not None and not _fits(t, torch.int32, (rows,), device):
+            _need("key_start", t, torch.int32, (rows,), device)
+        t = self.prefix_len
+        if t is not None and not _fits(t, torch.int32, (S,), device):
+            _need("prefix_len", t, torch.int32, (S,), device)
 
 
 def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace):
@@ -518,10 +522,15 @@ def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, worksp
         _need("block_table", block_table, i32, (-1, -1), dev)
     T, H_q, D = q_shape = q.shape
     NB, H_kv, BS, _ = pool_shape = k_cache.shape
-    S, mb = table_shape = block_table.shape
-    if not (D == pool_shape[3] and _fits(out, dt, q_shape, dev) and _fits(k_cache, dt, pool_shape, dev) and
-            _fits(v_cache, dt, pool_shape, dev) and _fits(seq_lens, i32, (S,), dev) and
-            _fits(block_table, i32, table_shape, dev)):
+    S, mb = block_table.shape
+    # written out, not as calls of _fits: a call takes as long as the comparisons
+    if not (D == pool_shape[3] and
+            out.dtype is dt and out.shape == q_shape and out.get_device() == dev and out.is_contiguous() and
+            k_cache.dtype is dt and k_cache.get_device() == dev and k_cache.is_contiguous() and
+            v_cache.dtype is dt and v_cache.shape == pool_shape and v_cache.get_device() == dev and
+            v_cache.is_contiguous() and block_table.dtype is i32 and block_table.get_device() == dev and
+            block_table.is_contiguous() and seq_lens.dtype is i32 and seq_lens.shape == (S,) and
+            seq_lens.get_device() == dev and seq_lens.is_contiguous()):
         _need("out", out, dt, (T, H_q, D), dev)
         _need("k_cache", k_cache, dt, (-1, -1, -1, D), dev)
         _need("v_cache", v_cache, dt, (NB, H_kv, BS, D), dev)
