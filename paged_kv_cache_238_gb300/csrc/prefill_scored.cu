@@ -906,9 +906,11 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             unpack2(add2(add2(psum[0], psum[1]), add2(psum[2], psum[3])), s0, s1);
             l_sum = l_sum * alpha + (s0 + s1);
         }
-        if (ok && cnt > 0) ok = wait_or_abort<kSleepSoftmax>(&o_done[xq], 0, abort_flag, err);
-        // the halves' sums meet in the query tile's shared memory, which no MMA reads any more; every
-        // softmax thread of the tile comes here, aborted or not
+        // The halves' sums meet in the query tile's shared memory, which no MMA reads any more and no thread's
+        // copy still writes: o_done says both, as the MMAs waited for the copies. A query tile that no key tile of
+        // the CTA uses (rows that see nothing, a run of keys that only the other tile sees) has no MMAs and
+        // waits for all the copies itself. Every softmax thread of the tile comes here, aborted or not.
+        if (ok) ok = wait_or_abort<kSleepSoftmax>(cnt > 0 ? &o_done[xq] : q_full, 0, abort_flag, err);
         float* sums = reinterpret_cast<float*>(smem + xq * kTile);
         __syncwarp();
         sums[half * kRows + r] = l_sum;

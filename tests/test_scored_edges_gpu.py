@@ -1,0 +1,53 @@
+"""Scored attention at its edges on the GPU, against the fp64 definition and the tolerance of
+scored_reference.py (or a tighter one, derived beside its test)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from paged_kv_cache_238_gb300 import binding as B  # noqa: E402
+
+from scored_reference import Case, alibi  # noqa: E402
+from test_scored_gpu import check  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    B.pa_get_device_errors(clear=True)
+    yield
+    assert B.pa_get_device_errors(clear=True) == 0, "a kernel raised a device error"
+
+
+FORMS = {  # a name for each arithmetic of the scores
+    "plain": {}, "cap": dict(cap=20.0, sharp=6.0), "distance": dict(slopes=alibi(2)),
+    "cap distance": dict(cap=20.0, sharp=6.0, slopes=alibi(2)), "large cap": dict(cap=100.0, sharp=6.0)}
+
+
+def repeats(c, what, times=20):
+    """Right, and the same bits every time."""
+    d = check(c, what)
+    first = d.out.clone()
+    for _ in range(times):
+        d.out.fill_(float("nan"))
+        assert torch.equal(d.run(), first), what
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_query_tiles_without_keys(D, form):
+    """A query tile of 128 rows that uses no key tile of its CTA: its rows see nothing (documents that begin
+    behind them), or it belongs to a run of keys that only the other query tile of the CTA sees. 2 heads
+    with a kv head each: a query tile is 128 tokens."""
+    kw = FORMS[form]
+    L, C = 700, 256
+    for empty in (range(0, 128), range(128, 256), range(0, 256)):
+        start = [L if r in empty else 0 for r in range(C)]
+        repeats(Case(61, [L], 2, 2, D, 16, "bf16", chunks=[C], key_start=start, **kw), f"{form} {empty}")
+    # 256 rows from position 3840 under a window of 600: key tiles 25 to 31 in runs of three, three and one
+    # (rows 3840 to 3967 see nothing of the last); a window of 900 gives other runs
+    for window in (600, 900, 130):
+        repeats(Case(62, [4096], 2, 2, D, 16, "bf16", chunks=[C], window=window, **kw), f"{form} window {window}")
