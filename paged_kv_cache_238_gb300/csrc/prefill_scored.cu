@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                 }
                 if (c == kChains - 1 && ok) umma::commit(&v_empty[j % kVStages]);
                 if (c == 0 && ok && more) ok = wait_k(j + 1);
-                if (ok && used(x, j + 1)) qk(c, j + 1);
+                if (ok && more && used(x, j + 1)) qk(c, j + 1);  // (used() knows the whole list, not where a run ends)
             }
             if (ok && more) umma::commit(&k_empty[(j + 1) % kKStages]);
         }

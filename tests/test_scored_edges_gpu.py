@@ -51,3 +51,16 @@ def test_query_tiles_without_keys(D, form):
     # (rows 3840 to 3967 see nothing of the last); a window of 900 gives other runs
     for window in (600, 900, 130):
         repeats(Case(62, [4096], 2, 2, D, 16, "bf16", chunks=[C], window=window, **kw), f"{form} window {window}")
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("H_q,H_kv,D", [(2, 2, 64), (2, 2, 128), (8, 1, 128)])
+def test_ends_of_split_runs(H_q, H_kv, D, form):
+    """Key lists cut into runs of two and more key tiles at every offset of the first visible key: nothing past a
+    run's end is multiplied, and the next run's tiles are not lost."""
+    kw = dict(FORMS[form])
+    if "slopes" in kw:
+        kw["slopes"] = alibi(H_q)
+    for L, C, window in ((640, 5, 0), (641, 130, 0), (1279, 16, 0), (3000, 40, 1111), (2047, 129, 1500)):
+        repeats(Case(63, [L, 300], H_q, H_kv, D, 32, "bf16", chunks=[C, 3], window=window, **kw),
+                f"{form} {L} {C} {window}", times=3)
