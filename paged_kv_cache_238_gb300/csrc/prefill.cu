@@ -237,11 +237,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(
 
     if (tid == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < TcSmem::kNumBars; ++i) mbar_init(&bars[i], 1);
-        mbar_init(&p_full[0], 4);
-        mbar_init(&p_full[1], 4);
-        mbar_init(q_full, kSoftmaxThreads);
-        mbar_init(ml_full, kSoftmaxThreads);
+        for (int i = 0; i < TcSmem::kNumBars; ++i) {  // each once: an object in use must not be initialised again
+            uint64_t* bar = bars + i;
+            const bool p = bar >= p_full && bar < p_full + 2;
+            mbar_init(bar, p ? 4 : bar == q_full || bar == ml_full ? kSoftmaxThreads : 1);
+        }
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {

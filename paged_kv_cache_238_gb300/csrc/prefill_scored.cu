@@ -545,10 +545,11 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
     }
     if (tid == 0) {
         *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
-        for (int i = 0; i < L_::num_bars; ++i) mbar_init(&bars[i], 1);
-        for (int i = 0; i < kChains; ++i) mbar_init(&p_full[i], kSoftWarps / kChains);
-        for (int i = 0; i < 8; ++i) mbar_init(&mx_full[i], 2);
-        mbar_init(q_full, kSoftThreads);
+        for (int i = 0; i < L_::num_bars; ++i) {  // each once: an object in use must not be initialised again
+            uint64_t* bar = bars + i;
+            const bool p = bar >= p_full && bar < p_full + kChains;
+            mbar_init(bar, p ? kSoftWarps / kChains : bar >= mx_full ? 2 : bar == q_full ? kSoftThreads : 1);
+        }
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
