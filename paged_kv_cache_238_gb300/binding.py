@@ -486,28 +486,77 @@ class Score:
     """How scored attention scores a key (C ABI pa_score): scores capped at +-softcap by a tanh
     (0: not), a linear distance bias of alibi_slopes [H_q] fp32 per query head, a sliding window
     of `window` keys (0: none), key_start int32 per query row (the first key the row sees) and
-    prefix_len [S] int32 (keys that every row of the sequence sees). Keeps its tensors alive."""
+    prefix_len [S] int32 (keys that every row of the sequence sees). Keeps its tensors alive. Each
+    argument may be assigned between calls: a call takes what is there when it is made."""
 
-    __slots__ = ("softcap", "window", "alibi_slopes", "key_start", "prefix_len", "_desc")
+    __slots__ = ("_softcap", "_window", "_alibi_slopes", "_key_start", "_prefix_len", "_desc")
 
     def __init__(self, softcap: float = 0.0, alibi_slopes=None, window: int = 0, key_start=None, prefix_len=None):
-        self.softcap, self.window = float(softcap), int(window)
+        self._desc = ScoreDesc()
+        self.softcap, self.window = softcap, window
         self.alibi_slopes, self.key_start, self.prefix_len = alibi_slopes, key_start, prefix_len
-        self._desc = ScoreDesc(self.softcap, self.window, _ptr(alibi_slopes), _ptr(key_start), _ptr(prefix_len))
+
+    @property
+    def softcap(self) -> float:
+        return self._softcap
+
+    @softcap.setter
+    def softcap(self, value) -> None:
+        self._softcap = self._desc.softcap = float(value)
+
+    @property
+    def window(self) -> int:
+        return self._window
+
+    @window.setter
+    def window(self, value) -> None:
+        self._window = self._desc.window = int(value)
+
+    @property
+    def alibi_slopes(self):
+        return self._alibi_slopes
+
+    @alibi_slopes.setter
+    def alibi_slopes(self, t) -> None:
+        self._alibi_slopes, self._desc.alibi_slopes = t, _ptr(t)
+
+    @property
+    def key_start(self):
+        return self._key_start
+
+    @key_start.setter
+    def key_start(self, t) -> None:
+        self._key_start, self._desc.key_start = t, _ptr(t)
+
+    @property
+    def prefix_len(self):
+        return self._prefix_len
+
+    @prefix_len.setter
+    def prefix_len(self, t) -> None:
+        self._prefix_len, self._desc.prefix_len = t, _ptr(t)
 
     def _check(self, H_q: int, rows: int, S: int, device: int) -> None:
+        """Checks the tensors of a call, and takes their addresses: one may have got other storage since it
+        was assigned."""
         import torch
-        if self.alibi_slopes is self.key_start is self.prefix_len is None:
+        if self._alibi_slopes is self._key_start is self._prefix_len is None:
             return
-        t = self.alibi_slopes
-        if t is not None and not _fits(t, torch.float32, (H_q,), device):
-            _need("alibi_slopes", t, torch.float32, (H_q,), device)
-        t = self.key_start
-        if t is not None and not _fits(t, torch.int32, (rows,), device):
-            _need("key_start", t, torch.int32, (rows,), device)
-        t = self.prefix_len
-        if t is not None and not _fits(t, torch.int32, (S,), device):
-            _need("prefix_len", t, torch.int32, (S,), device)
+        t, desc = self._alibi_slopes, self._desc
+        if t is not None:
+            if not _fits(t, torch.float32, (H_q,), device):
+                _need("alibi_slopes", t, torch.float32, (H_q,), device)
+            desc.alibi_slopes = t.data_ptr()
+        t = self._key_start
+        if t is not None:
+            if not _fits(t, torch.int32, (rows,), device):
+                _need("key_start", t, torch.int32, (rows,), device)
+            desc.key_start = t.data_ptr()
+        t = self._prefix_len
+        if t is not None:
+            if not _fits(t, torch.int32, (S,), device):
+                _need("prefix_len", t, torch.int32, (S,), device)
+            desc.prefix_len = t.data_ptr()
 
 
 def _check_scored(out, q, k_cache, v_cache, block_table, seq_lens, score, workspace):

@@ -10,7 +10,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 from paged_kv_cache_238_gb300 import binding as B  # noqa: E402
 
 from scored_reference import Case, alibi  # noqa: E402
-from test_scored_gpu import check  # noqa: E402
+from test_scored_gpu import OnDevice, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,32 @@ def test_ends_of_split_runs(H_q, H_kv, D, form):
     for L, C, window in ((640, 5, 0), (641, 130, 0), (1279, 16, 0), (3000, 40, 1111), (2047, 129, 1500)):
         repeats(Case(63, [L, 300], H_q, H_kv, D, 32, "bf16", chunks=[C, 3], window=window, **kw),
                 f"{form} {L} {C} {window}", times=3)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_score_assigned_between_calls(decode):
+    """A serving loop's Score: key_start and prefix_len of the step, a window, a cap assigned after it was made, and
+    tensors whose storage changes, against a Score made for each call."""
+    lens, chunks = [300, 90, 17], None if decode else [60, 90, 5]
+    rows = 3 if decode else sum(chunks)
+    gen = torch.Generator().manual_seed(5)
+    d = OnDevice(Case(64, lens, 4, 2, 64, 16, "bf16", chunks=chunks, prefix=[300, 90, 17], free_invisible=False))
+    i32 = lambda hi, n: torch.randint(0, hi, (n,), generator=gen, dtype=torch.int32).cuda()  # noqa: E731
+    kept = B.Score()
+    for step in range(6):
+        args = dict(softcap=[0.0, 20.0, 100.0][step % 3], window=[0, 40, 7][step % 3], key_start=i32(60, rows),
+                    prefix_len=i32(90, 3) if step != 4 else None,
+                    alibi_slopes=torch.rand(4, generator=gen).cuda() if step % 2 else None)
+        d.score = B.Score(**args)
+        want = d.run().clone()
+        for name, value in args.items():
+            setattr(kept, name, value)
+        if step == 5:  # other storage under the same tensors
+            for t in (kept.key_start, kept.prefix_len, kept.alibi_slopes):
+                fresh = t.clone()
+                old = t.data
+                t.data = fresh
+                old.fill_(0)
+        d.score = kept
+        d.out.fill_(float("nan"))
+        assert torch.equal(d.run(), want), step
