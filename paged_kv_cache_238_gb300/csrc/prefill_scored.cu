@@ -229,6 +229,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// Floats as integers of the same order (no NaN), and back.
+__device__ __forceinline__ int32_t ordered(float x) {
+    const int32_t b = __float_as_int(x);
+    return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int32_t b) { return __int_as_float(b ^ (b >> 31 & 0x7fffffff)); }
+
 // cap log2(e) tanh(s scale / cap) at any s.
 __device__ __forceinline__ float capped_exact(float s, const TcScore& sc) {
     return sc.cap_l2 - 2.f * sc.cap_l2 * rcp_approx(1.f + exp2_approx(s * sc.two_k));
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
     __shared__ uint32_t seen_own[8];  // documents: the CTA's own positions that some row sees
     __shared__ union {  // one after the other
         alignas(16) uint32_t rank_key[kRankMax];  // the items' work
-        __nv_bfloat16 row_max[2][2][kRows];       // per query tile and half of the keys: the rows' maxima
+        int32_t row_top[2][kRows];                // per query tile: the rows' largest score so far, as an ordered integer
     } shared;
     // A CTA's entry: one pair of query tiles of a sequence (sub = the pairs of a chunk) or, sub = 1, a
     // whole sequence, whose pairs and heads follow one another. Entries with the most keys come first:
@@ -552,6 +559,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
         }
         fence_mbarrier_init();
     }
+    if (!kSplit && softmax_warp && half == 0) shared.row_top[xq][r] = ordered(-INFINITY);  // (the ranking is over)
     if (warp == kMmaWarp) {
         umma::tmem_alloc(tmem_holder, 2 * kO);
         umma::tmem_relinquish();
@@ -812,10 +820,12 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                 }
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if constexpr (!kOwnO) {
-                    // the row's other half of the keys is another thread's: exchange the maxima, rounded
-                    // up to bf16 (any reference at or above the maximum serves, if both take the same)
-                    const __nv_bfloat16 mine = __float2bfloat16_ru(top);
-                    shared.row_max[xq][half][r] = mine;
+                    // The row's other half of the keys is another thread's: both raise the row's maximum so far and
+                    // read it. It is exact: rounded to fewer bits, a reference could lie so far above large
+                    // scores that every weight of the row is 0. (The maximum so far exceeds m_ref + threshold just
+                    // where the tile's does, and nobody raises it for the next tile before both have read
+                    // it: the next S waits for both halves' P.)
+                    atomicMax(&shared.row_top[xq][r], ordered(top));
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mx_full[xq * 4 + quad]);
                     ok = wait_or_abort<kSleepSoftmax>(&mx_full[xq * 4 + quad], (cnt - 1) & 1, abort_flag, err);
@@ -823,7 +833,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                         ok = false;
                         break;
                     }
-                    top = fmaxf(__bfloat162float(mine), __bfloat162float(shared.row_max[xq][half ^ 1][r]));
+                    top = unordered(*const_cast<volatile int32_t*>(&shared.row_top[xq][r]));
                 }
                 grow = top > m_ref + kRescaleThreshold;  // first visible keys: m_ref = -inf
                 const float m_new = grow ? top : m_ref;

@@ -8,8 +8,10 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 from paged_kv_cache_238_gb300 import binding as B  # noqa: E402
+from paged_kv_cache_238_gb300 import workloads as W  # noqa: E402
 
-from scored_reference import Case, alibi  # noqa: E402
+from helpers import to_f64  # noqa: E402
+from scored_reference import Case, U, alibi  # noqa: E402
 from test_scored_gpu import OnDevice, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +95,63 @@ def test_score_assigned_between_calls(decode):
         d.score = kept
         d.out.fill_(float("nan"))
         assert torch.equal(d.run(), want), step
+
+
+def outputs(c, score_error):
+    """(out, tolerance) from fp64, where score_error(z) bounds the error of a row's visible scores z
+    (capped, before the bias) and bias: the tolerance of scored_reference.py with that bound in place of its dz."""
+    G = c.H_q // c.H_kv
+    q = W.as_f64(c.q)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    half = 2.0 ** -8 if c.dtype == "bf16" else U
+    for s, seen in enumerate(c.seen):
+        L, C = int(c.lens[s]), int(c.chunks[s])
+        for h in range(c.H_q):
+            K, V = c.keys[s][:, h // G], c.vals[s][:, h // G]
+            for r in range(C):
+                vis = np.flatnonzero(seen[r])
+                if len(vis) == 0:
+                    continue
+                row = q[c.qsl[s] + r, h]
+                z = K[vis] @ row * c.scale
+                mag = (np.abs(K[vis]) @ np.abs(row)).max() * c.scale
+                if c.cap:
+                    z = c.cap * np.tanh(z / c.cap)
+                bias = 0.0 if c.slopes is None else float(c.slopes[h]) * np.abs(L - C + r - vis)
+                dz = score_error(mag, z, bias)
+                z = z - bias
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                o, A = w @ V[vis], w @ np.abs(V[vis])
+                rel = 2 * (dz + 2.0 ** -21) * (1 + dz) + 2 * (len(vis) + 16) * U + (2.0 ** -8 if c.dtype == "bf16" else 0.0)
+                out[c.qsl[s] + r, h] = o
+                tol[c.qsl[s] + r, h] = rel * A + half * (np.abs(o) + rel * A)
+    return out, tol
+
+
+def within(c, score_error, what):
+    got = to_f64(OnDevice(c).run())
+    ref, tol = outputs(c, score_error)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} outside, worst {np.nanmax(np.abs(got - ref) - tol)}"
+
+
+def one_product(c, amplitude):
+    """Queries with one element: scores are exact products of a power of two and a bf16 (or fp32) number."""
+    q = np.zeros(W.as_f64(c.q).shape, dtype=np.float32)
+    q[..., 3] = amplitude
+    c.q = W.f32_to_bf16_bits(q) if c.dtype == "bf16" else q
+    return c
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,dtype", [(8, 2, 128, "bf16"), (4, 2, 64, "bf16"), (4, 2, 128, "f32")])
+@pytest.mark.parametrize("form", ["product", "negative product", "slope", "product and slope"])
+def test_scores_of_many_thousands(H_q, H_kv, D, dtype, form):
+    """Scores up to 10^5 either way, where 8 bits do not resolve what separates two weights. The dot products are
+    exact, so a score is off by its later roundings alone: dz = 8 u max(|z|, |bias|) (below 0.1 here)."""
+    error = lambda mag, z, bias: 8 * U * max(np.abs(z).max(), np.abs(bias).max())  # noqa: E731
+    size = {"product": 2.0 ** 18, "negative product": -2.0 ** 17, "slope": 1.0, "product and slope": 2.0 ** 14}[form]
+    slopes = [-30.0 * 2.0 ** -(h % 3) for h in range(H_q)] if "slope" in form else None
+    for lens, chunks in (([300, 64, 1], [100, 64, 1]), ([2500, 130], [40, 130]), ([1500, 900, 33], None)):
+        c = Case(65, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, slopes=slopes)
+        within(one_product(c, size), error, f"{form} {lens}")
