@@ -13,7 +13,7 @@
 // The arithmetic runs transposed: S^T = K Q^T puts the page's 16 keys in the 16 rows of
 // m16n8k16 and 8 q heads in its columns, then O^T += V^T P^T with P^T brought into place by a
 // register transpose; the softmax runs online in the log2 domain. Scores are transformed between
-// the two (tanh x = 1 - 2 / (1 + 2^(2 x log2 e)), a distance bias, masks); V rows of keys the row
+// the two (a tanh, by scored.cuh, a distance bias, masks); V rows of keys the row
 // does not see are zeroed in shared memory.
 //
 // Joins, all by M = max m_i, w_i = l_i 2^(m_i - M), out = sum w_i o_i / sum w_i in a fixed order:
@@ -88,17 +88,6 @@ struct Params {
     float2* piece_ml;  // [C][2][hs]
     uint32_t* err;
 };
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void bulk_copy_g2s(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile(
@@ -425,14 +414,40 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 // scores in the log2 domain
                 const bool see0 = here && (whole || wc.sp.sees(key0 + gid)), see1 = here && (whole || wc.sp.sees(key0 + gid + 8));
                 const float away0 = fabsf(static_cast<float>(pos - key0 - gid)), away1 = fabsf(static_cast<float>(pos - key0 - gid - 8));
+                if (a.cap_l2 > 0.f) {  // the polynomial for all, the identity where a score is beyond it
+                    float x[NH][4], big = 0.f;
+#pragma unroll
+                    for (int f = 0; f < NH; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = sc[i][f][e] * a.two_k;
+                            x[f][e] = capped_near(sc[i][f][e], y * y, a.c1);
+                            big = fmaxf(big, y * y);
+                        }
+                    if (__any_sync(0xffffffffu, big > kTanhY2)) {
+#pragma unroll
+                        for (int f = 0; f < NH; ++f)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float y = sc[i][f][e] * a.two_k;
+                                if (y * y > kTanhY2) x[f][e] = capped_far(y, a.cap_l2);
+                            }
+                    }
+#pragma unroll
+                    for (int f = 0; f < NH; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i][f][e] = x[f][e];
+                } else {
+#pragma unroll
+                    for (int f = 0; f < NH; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i][f][e] *= a.c1;
+                }
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = a.cap_l2 > 0.f ? a.cap_l2 - 2.f * a.cap_l2 * rcp_approx(1.f + exp2_approx(sc[i][f][e] * a.two_k))
-                                                       : sc[i][f][e] * a.c1;
-                        sc[i][f][e] = (e < 2 ? see0 : see1) ? fmaf(-slope[f][e & 1], e < 2 ? away0 : away1, x) : -INFINITY;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        sc[i][f][e] = (e < 2 ? see0 : see1) ? fmaf(-slope[f][e & 1], e < 2 ? away0 : away1, sc[i][f][e]) : -INFINITY;
                     mx[f][0] = fmaxf(mx[f][0], fmaxf(sc[i][f][0], sc[i][f][2]));
                     mx[f][1] = fmaxf(mx[f][1], fmaxf(sc[i][f][1], sc[i][f][3]));
                 }
@@ -723,7 +738,7 @@ cudaError_t launch_impl(const DecodeArgs& d, const ScoreArgs& score, const Decod
     a.c1 = d.scale * kLog2e;
     if (score.cap > 0.f) {
         a.two_k = static_cast<float>(fmin(fmax(2 * 1.4426950408889634 * d.scale / score.cap, -3e38), 3e38));
-        a.cap_l2 = score.cap * kLog2e;
+        a.cap_l2 = fminf(score.cap * kLog2e, kLargestCapL2);
     }
     char* ws = static_cast<char*>(d.workspace);
     a.counter = reinterpret_cast<int32_t*>(ws);

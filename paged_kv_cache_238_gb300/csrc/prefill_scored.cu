@@ -18,12 +18,13 @@
 // Chains of S -> softmax -> P -> P V -> next S run independently of one another: where a row's keys need
 // no common maximum there are four, one per query tile and half of the key tile (64 keys), else two.
 //
-// Scores. Four variants of the score arithmetic (Mode), all in the log2 domain:
+// Scores. Variants of the score arithmetic (Mode), all in the log2 domain:
 //   plain      arg = s c1;                       online maximum, two passes over S
 //   cap        arg = s Q(s^2) - ref;             no maximum: see below, one pass over S, four chains
 //   distance   arg = s c1 - slope |p - j|;       online maximum, two passes
 //   both       arg = s Q(s^2) - slope |p - j| - ref(row);  as cap
-//   general    caps beyond the range of the fixed reference
+//   general    caps beyond the range of the fixed reference: online maximum, two passes, tanh by the identity
+//   large cap  caps above kMaxIdentityCap: as general, small scores by the polynomial of scored.cuh
 // At head_dim 64 tensor memory has room for an output per half of the keys: the modes with maxima then
 // run four chains too, each half with its own maximum and output, merged at the end (8 sequences of 100
 // to 1000 new rows on up to 2500 keys, 16 heads: 65.7 us, two chains 67.8).
@@ -33,7 +34,7 @@
 // 7, fitted to tanh on |x| <= 0.6 by Remez's minimax method (absolute error 2^-20.7, that times cap
 // in the score, below the 2^-9 of the bf16 weights), evaluated on the FMA pipes two elements an
 // instruction; a warp whose 32 scores of a row block hold a larger one takes
-// tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block, exact at every x. P is rounded to bf16, the
+// tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block (absolute error 2^-20). P is rounded to bf16, the
 // type in which the tensor cores multiply it by V (fp32 accumulation; the sums add the fp32 weights).
 //
 // Bound: the tensor cores, then the exponentials. 16 sequences of 512 new rows on 512 to 4608 keys, 32 q /
@@ -88,13 +89,18 @@ constexpr int kMinPartTiles = 2;
 // on up to 4608 keys: 293 us, with one tile 419; the two meet near 1000 keys at head_dim 64, 200 at 128).
 __host__ __device__ constexpr int short_keys(int D) { return D == 64 ? 768 : 192; }
 // Caps with a fixed reference: 1.5 cap log2(e) <= 112. Measured, 16 sequences of 512 new rows on 2512 keys, 32 q / 8
-// kv heads of 128: cap 50 298 us, not capped 332, cap 52 (general) 821.
+// kv heads of 128: cap 50 298 us, not capped 332, cap 52 (general) 728.
 constexpr float kMaxFixedCap = 51.f;
 constexpr float kTopWeight = 48.f;  // with a distance bias: the largest weight's exponent
 
 constexpr uint32_t kSleepProducer = 200, kSleepSoftmax = 40;  // ns between polls
 
-enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kCapDistance = 3, kGeneral = 4 };
+// Caps up to which the identity alone serves: its error, 2^-20 cap, is then an eighth of the rounding of a weight to
+// bf16. Measured, 16 sequences of 512 new rows on 2512 keys, 32 q / 8 kv heads of 128, scores of a few units: 728 us,
+// with the polynomial for small scores 890; with scores that reach the cap 748 and 1419.
+constexpr float kMaxIdentityCap = 256.f;
+
+enum Mode : int { kPlain = 0, kCap = 1, kDistance = 2, kCapDistance = 3, kGeneral = 4, kLargeCap = 5 };
 
 template <int D, int NQ>
 struct Smem {
@@ -172,23 +178,12 @@ struct TcScore {
     float two_k;    // 2 log2(e) scale / cap
     float cap_l2;   // cap log2 e
     float ref;      // fixed reference
-    bool capped;
     int32_t window;
     const float* slopes;
     const int32_t* key_start;
     const int32_t* prefix_len;
 };
 
-__device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -235,11 +230,6 @@ __device__ __forceinline__ int32_t ordered(float x) {
     return b ^ (b >> 31 & 0x7fffffff);
 }
 __device__ __forceinline__ float unordered(int32_t b) { return __int_as_float(b ^ (b >> 31 & 0x7fffffff)); }
-
-// cap log2(e) tanh(s scale / cap) at any s.
-__device__ __forceinline__ float capped_exact(float s, const TcScore& sc) {
-    return sc.cap_l2 - 2.f * sc.cap_l2 * rcp_approx(1.f + exp2_approx(s * sc.two_k));
-}
 
 // 32 columns of the warp's tensor-memory lanes, and the wait that makes them valid, as one
 // instruction group: nothing can use the registers before the wait.
@@ -735,7 +725,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             float big[4];
             uint64_t away[4];
             auto begin_group = [&](int c, float shift) {
-                if constexpr (kFixed) {
+                if constexpr (kFixed || MODE == kLargeCap) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) big[k] = 0.f;
                 }
@@ -768,8 +758,15 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                 } else {
                     float s0, s1;
                     unpack2(s, s0, s1);
-                    s0 = sc.capped ? capped_exact(s0, sc) : s0 * sc.c1;
-                    s1 = sc.capped ? capped_exact(s1, sc) : s1 * sc.c1;
+                    const float y0 = s0 * sc.two_k, y1 = s1 * sc.two_k;
+                    if constexpr (MODE == kGeneral) {
+                        s0 = capped_far(y0, sc.cap_l2);
+                        s1 = capped_far(y1, sc.cap_l2);
+                    } else {
+                        s0 = capped_near(s0, y0 * y0, sc.c1);
+                        s1 = capped_near(s1, y1 * y1, sc.c1);
+                        big[e & 3] = max3(big[e & 3], y0 * y0, y1 * y1);
+                    }
                     x0 = fmaf(-slope, fabsf(d0 + (c * 16 + 2 * e)), s0) + shift;
                     x1 = fmaf(-slope, fabsf(d0 + (c * 16 + 2 * e + 1)), s1) + shift;
                 }
@@ -777,16 +774,21 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             // Scores beyond the polynomial's range, keys behind the row, masked keys.
             auto amend = [&](const uint32_t(&raw)[16], int c, float shift, float(&x)[16]) {
                 bool redo = false;
-                if constexpr (kFixed) redo = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) > sc.s2_max;
+                if constexpr (kFixed || MODE == kLargeCap)
+                    redo = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) > (kFixed ? sc.s2_max : kTanhY2);
                 if constexpr (MODE == kDistance || MODE == kCapDistance) redo = redo || behind;
                 if (redo || mask) {
                     if (redo) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float s = __uint_as_float(raw[k]);
-                            if constexpr (MODE == kCap) x[k] = capped_exact(s, sc) + shift;
+                            if constexpr (MODE == kCap) x[k] = capped_far(s * sc.two_k, sc.cap_l2) + shift;
                             if constexpr (MODE == kCapDistance)
-                                x[k] = capped_exact(s, sc) + fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift);
+                                x[k] = capped_far(s * sc.two_k, sc.cap_l2) + fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift);
+                            if constexpr (MODE == kLargeCap) {
+                                const float y = s * sc.two_k;
+                                if (y * y > kTanhY2) x[k] = fmaf(-slope, fabsf(d0 + (c * 16 + k)), capped_far(y, sc.cap_l2)) + shift;
+                            }
                             if constexpr (MODE == kDistance)
                                 x[k] = fmaf(s, sc.c1, fmaf(-slope, fabsf(d0 + (c * 16 + k)), shift));
                         }
@@ -1128,7 +1130,8 @@ cudaError_t pick(const PrefillArgs& a, const TcScore& sc, Mode mode, const Prefi
         case kCap: return run(std::integral_constant<int, kCap>{});
         case kDistance: return run(std::integral_constant<int, kDistance>{});
         case kCapDistance: return run(std::integral_constant<int, kCapDistance>{});
-        default: return run(std::integral_constant<int, kGeneral>{});
+        case kGeneral: return run(std::integral_constant<int, kGeneral>{});
+        default: return run(std::integral_constant<int, kLargeCap>{});
     }
 }
 
@@ -1160,21 +1163,22 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
                                      void* workspace, int num_sms, cudaStream_t stream) {
     TcScore sc{};
     sc.c1 = a.scale * kLog2e;
-    sc.capped = s.cap > 0.f;
-    if (sc.capped) {
+    const bool capped = s.cap > 0.f;
+    if (capped) {
         const double k = static_cast<double>(a.scale) / s.cap;
         double c = static_cast<double>(s.cap) * 1.4426950408889634 * k;
         for (int i = 0; i < 4; ++i, c *= k * k) sc.q[i] = static_cast<float>(c * kTanh[i]);
         sc.s2_max = static_cast<float>(kTanhRange * kTanhRange / (k * k));
         sc.two_k = static_cast<float>(fmin(fmax(2 * 1.4426950408889634 * k, -3e38), 3e38));
-        sc.cap_l2 = s.cap * kLog2e;
+        sc.cap_l2 = fminf(s.cap * kLog2e, kLargestCapL2);
         sc.ref = s.slopes ? sc.cap_l2 - kTopWeight : 0.5f * sc.cap_l2;
     }
     sc.window = s.window;
     sc.slopes = s.slopes;
     sc.key_start = s.key_start;
     sc.prefix_len = s.prefix_len;
-    const Mode mode = !sc.capped ? (s.slopes ? kDistance : kPlain)
+    const Mode mode = !capped ? (s.slopes ? kDistance : kPlain)
+                                 : s.cap > kMaxIdentityCap ? kLargeCap
                                  : s.cap > kMaxFixedCap || !isfinite(sc.q[3]) ? kGeneral  // (tiny caps: no polynomial)
                                  : s.slopes ? kCapDistance : kCap;
     return a.head_dim == 128 ? pick<128>(a, sc, mode, plan, workspace, num_sms, stream) : pick<64>(a, sc, mode, plan, workspace, num_sms, stream);

@@ -34,6 +34,34 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Capped scores, cap log2(e) tanh(u) with u = s scale / cap, from y = 2 u log2(e) = s two_k and c1 = scale log2(e).
+// Two forms, of which neither serves every cap: near u = 0 the identity cancels (an error of 2^-21 cap,
+// whatever the score), and far from it a polynomial does not hold.
+//   |u| <= 0.6  s c1 (1 + y^2 P(y^2)): tanh(u) / u fitted in its relative error (6.5e-8, minimax over a fine grid by
+//               linear programming, the leading 1 held), so that a cap far above the scores leaves them alone;
+//   beyond      cap (1 - 2 / (1 + 2^y)): relative error below 2^-20, and an absolute one below 2^-20 cap anywhere.
+constexpr float kTanhP0 = -0.0400365926f, kTanhP1 = 0.00192027225f, kTanhP2 = -9.02627071e-05f, kTanhP3 = 3.21615289e-06f;
+constexpr float kTanhY2 = 2.997171f;       // y^2 up to which the polynomial holds, (1.2 log2 e)^2
+constexpr float kLargestCapL2 = 1.6e38f;  // cap log2(e) is held where twice of it is finite
+__device__ __forceinline__ float capped_near(float s, float y2, float c1) {
+    const float t = s * c1;
+    return fmaf(t * y2, fmaf(y2, fmaf(y2, fmaf(y2, kTanhP3, kTanhP2), kTanhP1), kTanhP0), t);
+}
+__device__ __forceinline__ float capped_far(float y, float cap_l2) {
+    return fmaf(-2.f * cap_l2, rcp_approx(1.f + exp2_approx(y)), cap_l2);
+}
+
 struct KeySpans {
     int32_t a0, a1, b0, b1;
     __device__ __forceinline__ bool sees(int32_t j) const { return (j >= a0 && j < a1) || (j >= b0 && j < b1); }

@@ -35,11 +35,6 @@ constexpr int kMaxParts = 128;  // partitions: the merge holds their weights in 
 constexpr float kLag = 8.f;  // log2 units
 constexpr int32_t kFar = 0x7fffffff;
 
-__device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Four consecutive elements as two packed pairs.
 struct Pairs {
     uint64_t lo, hi;

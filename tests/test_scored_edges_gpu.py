@@ -155,3 +155,39 @@ def test_scores_of_many_thousands(H_q, H_kv, D, dtype, form):
     for lens, chunks in (([300, 64, 1], [100, 64, 1]), ([2500, 130], [40, 130]), ([1500, 900, 33], None)):
         c = Case(65, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, slopes=slopes)
         within(one_product(c, size), error, f"{form} {lens}")
+
+
+# A capped score may be off by 2^-20 of itself (not of the cap) besides the dot product and the later roundings.
+CAP_ERROR = {
+    "drawn": lambda D: lambda mag, z, bias: ((D + 16) * U * mag + 8 * U * max(np.abs(z).max(), np.abs(bias).max())
+                                             + 2.0 ** -20 * np.abs(z).max()),
+    "exact": lambda D: lambda mag, z, bias: (8 * U * max(np.abs(z).max(), np.abs(bias).max())
+                                             + 2.0 ** -20 * np.abs(z).max())}
+
+
+def small_cap_error(cap):
+    """bf16 prefill takes caps up to 256 by forms of the tanh whose error is 2^-20 of the cap: 2^-12 at most, an
+    eighth of what rounding the weights to bf16 may move."""
+    return 2.0 ** -20 * cap if cap <= 256 else 0.0
+
+
+@pytest.mark.parametrize("cap", [60.0, 256.0, 300.0, 1e4, 1e6, 1e9, 1e30, 2.5e38, 2.99e38])
+@pytest.mark.parametrize("H_q,H_kv,D,dtype", [(8, 2, 128, "bf16"), (4, 2, 64, "bf16"), (4, 2, 128, "f32")])
+def test_large_caps(H_q, H_kv, D, dtype, cap):
+    """Caps far above the scores leave them as they are, up to the largest cap that the calls take."""
+    for slopes in (None, [0.5 * 2.0 ** -(h % 4) for h in range(H_q)]):
+        for lens, chunks in (([300, 64, 1], [100, 64, 1]), ([1500, 40], [30, 40]), ([700, 300, 33, 1], None)):
+            c = Case(66, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, cap=cap, slopes=slopes, sharp=4.0)
+            within(c, lambda *z: CAP_ERROR["drawn"](D)(*z) + small_cap_error(cap), f"cap {cap} {lens}")
+
+
+@pytest.mark.parametrize("cap,amplitude", [(40.0, 2.0 ** 8), (100.0, 2.0 ** 9), (256.0, 2.0 ** 11), (300.0, 2.0 ** 11),
+                                           (1e4, 2.0 ** 16), (1e6, 2.0 ** 22)])
+@pytest.mark.parametrize("H_q,H_kv,D,dtype", [(8, 2, 128, "bf16"), (4, 2, 64, "bf16"), (4, 2, 128, "f32")])
+def test_scores_around_a_cap(H_q, H_kv, D, dtype, cap, amplitude):
+    """Scores from none over the place where one form of the tanh gives way to the other to several caps."""
+    error = CAP_ERROR["exact"](D)
+    bound = lambda mag, z, bias: error(mag, z, bias) + small_cap_error(cap)  # noqa: E731
+    for lens, chunks in (([300, 64, 1], [100, 64, 1]), ([1500, 40], [30, 40]), ([700, 300, 33, 1], None)):
+        c = one_product(Case(67, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, cap=cap), amplitude)
+        within(c, bound, f"cap {cap} {lens}")
