@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             entry(tid);
             const int32_t first = NQ * pair * TT, rows = sub > 1 ? min(NQ * TT, C - first) : C;
             int32_t keys = L - C + first + rows;  // up to the last row's own
-            if (sc.window > 0) keys = min(keys, sc.window + rows + min(max(prefix, 0), L));
+            if (sc.window > 0) keys = min(keys, min(sc.window, cap_tokens) + rows + min(max(prefix, 0), cap_tokens));
             if (rows <= 0) keys = 0;
             // 24 bits of keys (all of them up to 2^24 tokens), and the number: no two alike
             mine = static_cast<uint32_t>(max(keys, 0)) >> max(8 - __clz(cap_tokens), 0) << 8 | (kRankMax - 1 - tid);

@@ -191,3 +191,34 @@ def test_scores_around_a_cap(H_q, H_kv, D, dtype, cap, amplitude):
     for lens, chunks in (([300, 64, 1], [100, 64, 1]), ([1500, 40], [30, 40]), ([700, 300, 33, 1], None)):
         c = one_product(Case(67, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, cap=cap), amplitude)
         within(c, bound, f"cap {cap} {lens}")
+
+
+INT_MAX, INT_MIN = 2 ** 31 - 1, -2 ** 31
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "bf16"), (64, "f32")])
+def test_arguments_at_the_ends_of_their_range(D, dtype, form):
+    """A window, a prefix and document starts near 2^31 mean all keys, or none."""
+    for lens, chunks in (([300, 64, 1, 200], [200, 64, 1, 9]), ([2500, 130], [3, 130]), ([700, 300, 33, 1], None)):
+        rows = len(lens) if chunks is None else sum(chunks)
+        make = lambda **kw: OnDevice(Case(68, lens, 2, 2, D, 16, dtype, chunks=chunks, free_invisible=False,  # noqa: E731
+                                          **FORMS[form], **kw))
+        want = make().run().clone()
+        for window in (INT_MAX, INT_MAX - 1, INT_MAX - 200, max(lens)):
+            assert torch.equal(make(window=window).run(), want), window
+        for none in (0, -1, INT_MIN):
+            assert torch.equal(make(prefix=[none] * len(lens)).run(), want), none
+            assert torch.equal(make(key_start=[none] * rows).run(), want), none
+        whole = make(prefix=lens).run().clone()
+        for every in (INT_MAX, INT_MAX - 1, max(lens)):
+            assert torch.equal(make(prefix=[every] * len(lens)).run(), whole), every
+            assert torch.equal(make(prefix=[every] * len(lens), window=INT_MAX).run(), whole), every
+        for start in (INT_MAX, INT_MAX - 1, max(lens)):
+            d = make(key_start=[start if r % 3 == 1 else 0 for r in range(rows)], prefix=lens, window=INT_MAX)
+            got = d.run()
+            assert torch.equal(got[1::3], torch.zeros_like(got[1::3])), start
+            # The other rows by the definition: their last bits may depend on the empty rows beside them, as
+            # the CUDA-core kernel takes new references for all rows of a warp when one row's maximum grows.
+            ref, tol = d.c.reference()
+            assert (np.abs(to_f64(got) - ref) <= tol).all(), start
