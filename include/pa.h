@@ -407,11 +407,14 @@ PA_API pa_status pa_step(const pa_step_desc* step, void* stream);
  *   z_j = z_j - alibi_slopes[h] * |p - j|            when alibi_slopes is given
  *   key j is visible when  j < L,  j >= key_start,  and
  *       ( j < prefix_len  or  ( j <= p  and  (window == 0 or j > p - window) ) )
+ *   or, with prefix_causal = 1,  when  j < L,  j >= key_start,  j <= p,  and
+ *       ( j < prefix_len  or  window == 0  or  j > p - window )
  *   out = sum over visible j of softmax(z)_j v_j;  an all-zero row when no key is visible
  * softcap bounds the scores; alibi_slopes is a linear distance bias; window a sliding window that
  * counts the row's own key; prefix_len names the first keys of a sequence that every row of it
- * sees, rows before them included (prompts whose prefix is attended in both directions, and
- * first tokens that stay visible under a window); key_start the first key a row may see (a
+ * sees: rows before them included (prompts whose prefix is attended in both directions), or, with
+ * prefix_causal, only rows at or behind them (the first tokens of a causal model that stay visible
+ * under a window). The two differ for prefill rows inside the prefix only. key_start the first key a row may see (a
  * document mask for packed documents: the position where the row's document starts).
  *   softcap       0 (none) or a positive finite number
  *   alibi_slopes  NULL or [num_q_heads] fp32
@@ -419,6 +422,7 @@ PA_API pa_status pa_step(const pa_step_desc* step, void* stream);
  *   key_start     NULL or int32 per query row: [num_seqs] for decode, [total_query_tokens] for
  *                 prefill; a negative entry counts as 0, one past the row's keys leaves it empty
  *   prefix_len    NULL or [num_seqs] int32; clamped to [0, seq_lens[i]]
+ *   prefix_causal 0 or 1; without prefix_len it changes nothing
  * All arrays are device arrays, 4-byte aligned. A NULL descriptor, or one of zeros, gives plain
  * causal attention.
  *
@@ -436,6 +440,7 @@ typedef struct {
     const float* alibi_slopes;
     const int32_t* key_start;
     const int32_t* prefix_len;
+    int32_t prefix_causal;
 } pa_score;
 
 /*

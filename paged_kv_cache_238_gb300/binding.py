@@ -70,7 +70,7 @@ class StepDesc(ctypes.Structure):
 class ScoreDesc(ctypes.Structure):
     """Mirror of pa_score in include/pa.h (same fields, same order, C layout)."""
     _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", ctypes.c_void_p),
-                ("key_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+                ("key_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("prefix_causal", ctypes.c_int32)]
 
 
 class PaError(RuntimeError):
@@ -486,14 +486,17 @@ class Score:
     """How scored attention scores a key (C ABI pa_score): scores capped at +-softcap by a tanh
     (0: not), a linear distance bias of alibi_slopes [H_q] fp32 per query head, a sliding window
     of `window` keys (0: none), key_start int32 per query row (the first key the row sees) and
-    prefix_len [S] int32 (keys that every row of the sequence sees). Keeps its tensors alive. Each
-    argument may be assigned between calls: a call takes what is there when it is made."""
+    prefix_len [S] int32 (keys that every row of the sequence sees: those before them too, a prefix
+    attended in both directions, unless prefix_causal, for the first tokens of a causal model that
+    stay visible under a window). Keeps its tensors alive. Each argument may be assigned between
+    calls: a call takes what is there when it is made."""
 
-    __slots__ = ("_softcap", "_window", "_alibi_slopes", "_key_start", "_prefix_len", "_desc")
+    __slots__ = ("_softcap", "_window", "_alibi_slopes", "_key_start", "_prefix_len", "_prefix_causal", "_desc")
 
-    def __init__(self, softcap: float = 0.0, alibi_slopes=None, window: int = 0, key_start=None, prefix_len=None):
+    def __init__(self, softcap: float = 0.0, alibi_slopes=None, window: int = 0, key_start=None, prefix_len=None,
+                 prefix_causal: bool = False):
         self._desc = ScoreDesc()
-        self.softcap, self.window = softcap, window
+        self.softcap, self.window, self.prefix_causal = softcap, window, prefix_causal
         self.alibi_slopes, self.key_start, self.prefix_len = alibi_slopes, key_start, prefix_len
 
     @property
@@ -511,6 +514,15 @@ class Score:
     @window.setter
     def window(self, value) -> None:
         self._window = self._desc.window = int(value)
+
+    @property
+    def prefix_causal(self) -> bool:
+        return self._prefix_causal
+
+    @prefix_causal.setter
+    def prefix_causal(self, value) -> None:
+        self._prefix_causal = bool(value)
+        self._desc.prefix_causal = int(self._prefix_causal)
 
     @property
     def alibi_slopes(self):

@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 len = len < 0 ? 0 : a.cap_tokens;
             }
             const KeySpans sp = key_spans(len, len - 1, a.score.key_start ? __ldg(a.score.key_start + s) : 0,
-                                          a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window);
+                                          a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window,
+                                          false);  // (the last row sees the whole prefix either way)
             spans[s] = make_int4(sp.a0, sp.a1, sp.b0, sp.b1);
             const int32_t pages = page_list(sp).n, units = pages > 0 ? (pages + kSegmentUnits) * nh : 0;
             prefix[s] = units;

@@ -531,9 +531,11 @@ pa_status prepare_score(const pa_score* score, ScoreArgs* a) {
     *a = ScoreArgs{};
     if (!score) return PA_OK;
     if (!(score->softcap >= 0.f) || score->softcap > 3.0e38f || score->window < 0) return PA_ERR_INVALID_ARG;
+    if (score->prefix_causal != 0 && score->prefix_causal != 1) return PA_ERR_INVALID_ARG;
     if (!aligned4(score->alibi_slopes) || !aligned4(score->key_start) || !aligned4(score->prefix_len))
         return PA_ERR_INVALID_ARG;
-    *a = ScoreArgs{score->softcap, score->window, score->alibi_slopes, score->key_start, score->prefix_len};
+    *a = ScoreArgs{score->softcap,   score->window,     score->alibi_slopes,
+                   score->key_start, score->prefix_len, score->prefix_causal != 0};
     return PA_OK;
 }
 

@@ -209,6 +209,7 @@ struct ScoreArgs {
     const float* slopes;
     const int32_t* key_start;
     const int32_t* prefix_len;
+    bool causal;  // rows inside the prefix see no key behind themselves
 };
 
 // The scored calls' workspace begins with this many counters of segments (sequence, kv head, head

@@ -182,6 +182,7 @@ struct TcScore {
     const float* slopes;
     const int32_t* key_start;
     const int32_t* prefix_len;
+    bool causal;  // rows inside the prefix see no key behind themselves
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
     // ---- keys that the rows see ------------------------------------------------------------------
     KeySpans row{0, 0, 0, 0};
     if (row_valid)
-        row = key_spans(L, pos, sc.key_start ? __ldg(sc.key_start + q0 + t_row) : 0, prefix, sc.window);
+        row = key_spans(L, pos, sc.key_start ? __ldg(sc.key_start + q0 + t_row) : 0, prefix, sc.window, sc.causal);
     SpanUnion ux[NQ];
     if (sc.key_start == nullptr) {  // rows' spans move with their position: the first and the last row tell
 #pragma unroll
@@ -456,9 +457,9 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                 ux[x] = SpanUnion{0, 0, 0, 0};
                 continue;
             }
-            const KeySpans f = key_spans(L, P0 + t0, 0, prefix, sc.window);
-            const KeySpans l = key_spans(L, P0 + t1 - 1, 0, prefix, sc.window);
-            ux[x] = SpanUnion{f.a0, f.a1, f.b0, l.b1};
+            const KeySpans f = key_spans(L, P0 + t0, 0, prefix, sc.window, sc.causal);
+            const KeySpans l = key_spans(L, P0 + t1 - 1, 0, prefix, sc.window, sc.causal);
+            ux[x] = SpanUnion{f.a0, l.a1, f.b0, l.b1};
         }
     } else {
         if (tid < 8) {
@@ -478,11 +479,16 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                 atomicMin(&red[xq][2], b0);
                 atomicMax(&red[xq][3], b1);
             }
-            if (in_b && g == 0) {
+            if (g == 0) {
                 // the CTA's own positions P0 + t0a + i that this row sees; a key before them that
-                // any row's window span reaches past is seen by the row with the lowest start
-                const int32_t own = P0 + t0a, lo = max(row.b0 - own, 0), hi = row.b1 - own;
-                for (int32_t w = lo >> 5; w * 32 < hi; ++w) atomicOr(&seen_own[w], span_bits(w * 32, lo, hi));
+                // any row's span reaches past is seen by the row with the lowest start
+                const int32_t own = P0 + t0a;
+                int32_t lo = max(row.a0 - own, 0), hi = in_a ? min(row.a1 - own, 256) : 0;
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    for (int32_t w = lo >> 5; w * 32 < hi; ++w) atomicOr(&seen_own[w], span_bits(w * 32, lo, hi));
+                    lo = max(row.b0 - own, 0), hi = in_b ? row.b1 - own : 0;
+                }
             }
         }
         __syncthreads();
@@ -866,7 +872,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             if (gaps && (xq == 0 || !used(0, i))) {
                 const int32_t key = ktile + zrow;
                 bool seen = (key >= uni.a0 && key < uni.a1) || (key >= uni.b0 && key < uni.b1);
-                if (seen && sc.key_start != nullptr && key >= own && !(key >= uni.a0 && key < uni.a1))
+                if (seen && sc.key_start != nullptr && static_cast<uint32_t>(key - own) < 256u)  // (behind: the prefix)
                     seen = (seen_own[(key - own) >> 5] >> ((key - own) & 31)) & 1u;
                 const int32_t st = i % kVStages;
                 const bool okv = wait_or_abort<kSleepSoftmax>(&v_full[st], static_cast<uint32_t>(i / kVStages) & 1u, abort_flag, err);
@@ -1177,6 +1183,7 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& s, c
     sc.slopes = s.slopes;
     sc.key_start = s.key_start;
     sc.prefix_len = s.prefix_len;
+    sc.causal = s.causal;
     const Mode mode = !capped ? (s.slopes ? kDistance : kPlain)
                                  : s.cap > kMaxIdentityCap ? kLargeCap
                                  : s.cap > kMaxFixedCap || !isfinite(sc.q[3]) ? kGeneral  // (tiny caps: no polynomial)

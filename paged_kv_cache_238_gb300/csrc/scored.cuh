@@ -2,7 +2,8 @@
 // query row sees.
 //
 //   z = scale q.k;  z = cap tanh(z / cap);  z -= slope |p - j|
-//   visible(j) = j < L and j >= key_start and (j < prefix or (j <= p and j > p - window))
+//   visible(j) = j < L and j >= key_start and (j < prefix or (j <= p and j > p - window)),
+//                causal prefix: (j <= p and (j < prefix or j > p - window))
 //
 // The visible keys are two spans without a common key, [a0, a1) (the prefix part) and [b0, b1)
 // (the window part), so a kernel walks only their pages.
@@ -67,13 +68,14 @@ struct KeySpans {
     __device__ __forceinline__ bool sees(int32_t j) const { return (j >= a0 && j < a1) || (j >= b0 && j < b1); }
 };
 
-// Spans of a row at position p of a sequence with len keys (p < len).
+// Spans of a row at position p of a sequence with len keys (p < len). A row inside a causal prefix sees the prefix up
+// to itself, and its window part is empty. Over the rows of a sequence, prefix parts lie before window parts.
 __device__ __forceinline__ KeySpans key_spans(int32_t len, int32_t p, int32_t key_start, int32_t prefix,
-                                              int32_t window) {
+                                              int32_t window, bool causal) {
     KeySpans s;
     const int32_t start = max(key_start, 0);
     s.a0 = start;
-    s.a1 = max(start, min(prefix, len));
+    s.a1 = max(start, min(prefix, causal ? p + 1 : len));
     s.b0 = max(start, window > 0 ? p + 1 - window : 0);
     if (s.a1 > s.a0) s.b0 = max(s.b0, s.a1);
     s.b1 = max(s.b0, p + 1);

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
     if (valid) {
         const int32_t tt = lane / heads;
         sp = key_spans(len, pos0 + tt, a.score.key_start ? __ldg(a.score.key_start + row0 + tt) : 0,
-                       a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window);
+                       a.score.prefix_len ? __ldg(a.score.prefix_len + s) : 0, a.score.window, a.score.causal);
     }
     if (warp == 0 && lane < R) {
         const int32_t tt = lane / heads;

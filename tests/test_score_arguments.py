@@ -38,3 +38,22 @@ def test_construction_and_assignment_agree():
 def test_misspelt_arguments_are_refused():
     with pytest.raises(AttributeError):
         B.Score().windows = 3
+
+
+def test_causal_prefix_argument():
+    score = B.Score()
+    assert score.prefix_causal is False and score._desc.prefix_causal == 0
+    score.prefix_causal = True
+    assert score.prefix_causal is True and score._desc.prefix_causal == 1
+    assert B.Score(prefix_causal=True)._desc.prefix_causal == 1
+
+
+@pytest.mark.parametrize("value", [-1, 2, 1 << 30])
+def test_calls_refuse_other_values_of_the_causal_flag(value):
+    from test_scored_abi import FAKE
+    desc = B.ScoreDesc(prefix_causal=value)
+    lib = B.load()
+    assert lib.pa_decode_scored(FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 2, 64, 8, 2, 128, 16, 16, 0.1, desc, B.PA_BF16, FAKE,
+                                1 << 30, None) == B.PA_ERR_INVALID_ARG
+    assert lib.pa_prefill_scored(FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, FAKE, 2, 16, 64, 8, 2, 128, 16, 16, 0.1, desc,
+                                 B.PA_BF16, FAKE, 1 << 30, None) == B.PA_ERR_INVALID_ARG

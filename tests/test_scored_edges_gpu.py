@@ -222,3 +222,73 @@ def test_arguments_at_the_ends_of_their_range(D, dtype, form):
             # the CUDA-core kernel takes new references for all rows of a warp when one row's maximum grows.
             ref, tol = d.c.reference()
             assert (np.abs(to_f64(got) - ref) <= tol).all(), start
+
+
+def causal(c):
+    """The case under a causal prefix: rows see no key behind themselves; cells and pages that no row then sees
+    hold NaN and the null block."""
+    nan = np.float32(np.nan) if c.dtype == "f32" else np.uint16(0x7fc0)
+    for s, (L, C) in enumerate(zip(c.lens.tolist(), c.chunks.tolist())):
+        j, seen = np.arange(L), np.zeros((C, L), dtype=bool)
+        for r in range(C):
+            p = L - C + r
+            start = 0 if c.key_start is None else int(c.key_start[c.qsl[s] + r])
+            seen[r] = (j <= p) & (j >= start) & ((j < int(c.prefix[s])) | (c.window == 0) | (j > p - c.window))
+        assert not (seen & ~c.seen[s]).any()
+        c.seen[s] = seen
+        any_row = seen.any(axis=0)
+        for b in range(-(-L // c.BS)):
+            page, mine = c.table[s, b], any_row[b * c.BS:(b + 1) * c.BS]
+            if not mine.any():
+                c.table[s, b] = 0
+            for o in np.flatnonzero(~mine):
+                c.k_cache[page, :, o] = nan
+                c.v_cache[page, :, o] = nan
+    return c
+
+
+CAUSAL_CHUNKS = {
+    "chunks": ([(129, 129), (300, 300), (257, 128), (40, 7), (16, 16), (1, 1), (0, 0), (700, 256)],
+               [30, 200, 180, 38, 16, 1, 5, 600]),
+    "few rows on long contexts": ([(4099, 3), (2600, 70), (700, 1), (257, 257)], [4098, 2570, 100, 40]),
+    "one tile of short contexts": ([(190, 190), (130, 2), (64, 64)], [100, 129, 4])}
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("H_q,H_kv,D,BS,dtype", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 64, "bf16"), (4, 2, 64, 16, "f32")])
+@pytest.mark.parametrize("name", list(CAUSAL_CHUNKS))
+def test_first_tokens_of_a_causal_model_stay_visible(name, H_q, H_kv, D, BS, dtype, form):
+    """prefix_causal: rows inside the prefix see what is before them, rows behind it the prefix and their window."""
+    pairs, prefix = CAUSAL_CHUNKS[name]
+    lens, chunks = zip(*pairs)
+    kw = dict(FORMS[form])
+    if "slopes" in kw:
+        kw["slopes"] = alibi(H_q)
+    pos = [p for L, C in pairs for p in range(L - C, L)]
+    documents = [p + 1 if i % 17 == 16 else p // 90 * 90 for i, p in enumerate(pos)]
+    for window, starts in ((0, None), (50, None), (1, None), (50, documents), (0, documents)):
+        c = causal(Case(69, lens, H_q, H_kv, D, BS, dtype, chunks=chunks, prefix=prefix, window=window, key_start=starts, **kw))
+        d = OnDevice(c)
+        d.score.prefix_causal = True
+        ref, tol = c.reference()
+        got = to_f64(d.run())
+        assert (np.abs(got - ref) <= tol).all(), (window, starts is None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_causal_prefix_prefill_agrees_with_decode_step_by_step(dtype):
+    """Each row of a prompt's prefill is what decode gives for the sequence that ends there, first tokens of the
+    prompt included (within both calls' tolerances)."""
+    L, window, sinks = 120, 24, 5
+    c = causal(Case(70, [L], 4, 2, 64, 16, dtype, chunks=[L], cap=20.0, prefix=[sinks], window=window))
+    d = OnDevice(c)
+    d.score.prefix_causal = True
+    rows = to_f64(d.run())
+    ref, tol = c.reference()
+    for p in (0, 1, sinks - 1, sinks, sinks + 1, window, L - 1):
+        q, out = d.q[p:p + 1].contiguous(), torch.empty_like(d.q[:1])
+        n = B.pa_decode_scored_workspace_size(1, 4, 2, 64, p + 1, q.dtype)
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None
+        B.pa_decode_scored(out, q, d.k, d.v, d.table, torch.tensor([p + 1], dtype=torch.int32, device="cuda"), p + 1, c.scale,
+                           d.score, ws)
+        assert (np.abs(to_f64(out)[0] - rows[p]) <= 2 * tol[p]).all(), p
