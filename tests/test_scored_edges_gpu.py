@@ -102,7 +102,7 @@ def outputs(c, score_error):
     (capped, before the bias) and bias: the tolerance of scored_reference.py with that bound in place of its dz."""
     G = c.H_q // c.H_kv
     q = W.as_f64(c.q)
-    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    out, tol = np.zeros((len(q), c.H_q, c.D)), np.zeros((len(q), c.H_q, c.D))
     half = 2.0 ** -8 if c.dtype == "bf16" else U
     for s, seen in enumerate(c.seen):
         L, C = int(c.lens[s]), int(c.chunks[s])
@@ -292,3 +292,130 @@ def test_causal_prefix_prefill_agrees_with_decode_step_by_step(dtype):
         B.pa_decode_scored(out, q, d.k, d.v, d.table, torch.tensor([p + 1], dtype=torch.int32, device="cuda"), p + 1, c.scale,
                            d.score, ws)
         assert (np.abs(to_f64(out)[0] - rows[p]) <= 2 * tol[p]).all(), p
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("H_q,H_kv,dtype", [(4, 2, "f32"), (130, 1, "bf16")])
+def test_offsets_past_32_bits_on_the_cuda_cores(H_q, H_kv, dtype, decode):
+    """fp32, and groups that the tensor cores do not take: K and V are read through element offsets, which pass
+    2^32 here. (bf16 decode takes any group on the tensor cores: there the pool's rows are coordinates.)"""
+    D, BS = 128, 16
+    c = Case(71, [200, 77], H_q, H_kv, D, BS, dtype, chunks=None if decode else [6, 77], cap=20.0)
+    d = OnDevice(c)
+    NB, per_block = c.k_cache.shape[0], H_kv * BS * D
+    far = (1 << 32) // per_block + 1000
+    assert far + NB < 1 << 25
+    pools = []
+    for small in (d.k, d.v):
+        big = torch.empty((far + NB, H_kv, BS, D), dtype=small.dtype, device="cuda")
+        big[:NB] = float("nan")      # where a 32-bit offset would land
+        big[far - (1 << 32) // per_block:][:NB] = float("nan")
+        big[far:] = small
+        pools.append(big)
+    d.k, d.v = pools
+    d.table = d.table + far
+    ref, tol = c.reference()
+    assert (np.abs(to_f64(d.run()) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,dtype", [(8, 2, 128, "bf16"), (4, 2, 64, "bf16"), (4, 2, 128, "f32")])
+@pytest.mark.parametrize("form", ["plain", "cap", "distance", "cap distance", "large cap", "larger cap"])
+@pytest.mark.parametrize("decode", [True, False])
+def test_infinite_and_nan_scores(H_q, H_kv, D, dtype, form, decode):
+    """Visible keys with an infinite or NaN score. A cap takes infinite scores to its ends; without one a row that
+    sees +inf, as one that sees NaN, is NaN, and -inf weighs nothing. Other rows are not touched."""
+    kw = dict(cap=1000.0) if form == "larger cap" else dict(FORMS[form], sharp=1.0)
+    if "slopes" in kw:
+        kw["slopes"] = alibi(H_q)
+    lens, chunks = [400, 200, 300], None if decode else [150, 200, 3]
+    for value in (np.inf, -np.inf, np.nan):
+        c = one_product(Case(72, lens, H_q, H_kv, D, 16, dtype, chunks=chunks, **kw), 4.0)
+        d = OnDevice(c)
+        for s, j in ((0, 299), (1, 60)):  # sequence 2 has none
+            d.k[c.table[s, j // 16], :, j % 16, 3] = float(value)
+            c.keys[s] = c.keys[s].copy()
+            c.keys[s][j, :, 3] = value
+        capped = c.cap > 0
+        got = to_f64(d.run())
+        bad = np.zeros(got.shape[0], dtype=bool)
+        if np.isnan(value) or (value > 0 and not capped):
+            for s, j in ((0, 299), (1, 60)):
+                bad[c.qsl[s]:c.qsl[s + 1]] = c.seen[s][:, j]
+        assert bad.any() == (np.isnan(value) or (value > 0 and not capped))
+        assert np.isnan(got[bad]).all(), (form, value)
+        # the others by the definition; what they may be off does not depend on the infinite score, which is exact
+        # after the cap (its dz is that of a score of the cap's size)
+        error = lambda mag, z, bias: (8 * U * max(np.abs(z[np.isfinite(z)]).max(), np.abs(bias).max())  # noqa: E731
+                                      + (D + 16) * U * (mag if np.isfinite(mag) else 4.0 * 8.0) + 2.0 ** -20 * c.cap)
+        with np.errstate(invalid="ignore", over="ignore"):
+            ref, tol = outputs(zero_times_infinity(c), error)
+        assert (np.abs(got - ref) <= tol)[~bad].all(), (form, value)
+
+
+def zero_times_infinity(c):
+    """The case with queries of one element cut down to it, so that fp64 forms no 0 x inf either."""
+    k = [keys[..., 3:4] for keys in c.keys]
+    cut = Case.__new__(Case)
+    cut.__dict__.update(c.__dict__)
+    cut.keys = k
+    q = W.as_f64(c.q)[..., 3:4]
+    cut.q = q.astype(np.float32) if c.dtype == "f32" else W.f32_to_bf16_bits(q.astype(np.float32))
+    return cut
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_threads_with_a_stream_and_a_workspace_each(dtype, decode):
+    """Calls of several threads at once, each with its stream and workspace, equal the same calls alone."""
+    import threading
+    calls, want = [], []
+    for i, lens in enumerate(([2000, 33], [700, 700], [3001], [50] * 20)):
+        chunks = None if decode else [min(9, L) for L in lens]
+        calls.append(OnDevice(Case(73 + i, lens, 4, 2, 64, 16, dtype, chunks=chunks, cap=[0.0, 20.0, 100.0, 400.0][i])))
+        want.append(calls[-1].run().clone())
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(25):
+                calls[i].out.fill_(float("nan"))
+                calls[i].run()
+                stream.synchronize()
+                if not torch.equal(calls[i].out, want[i]):
+                    failed.append(i)
+                    return
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
+def test_tensors_that_are_not_contiguous_or_elsewhere_are_refused():
+    c = Case(77, [300, 40], 4, 2, 64, 16, "bf16", cap=20.0, slopes=alibi(4), prefix=[3, 4], key_start=[0, 1])
+    wide = lambda t: torch.stack([t, t], dim=-1)[..., 0]  # noqa: E731
+    for name in ("out", "q", "k", "v", "table", "lens"):
+        for change in (wide, lambda t: t.cpu()):
+            d = OnDevice(c)
+            setattr(d, name, change(getattr(d, name)))
+            with pytest.raises(ValueError):
+                d.run()
+    for name in ("alibi_slopes", "prefix_len", "key_start"):
+        for change in (wide, lambda t: t.cpu(), lambda t: t[:1]):
+            d = OnDevice(c)
+            setattr(d.score, name, change(getattr(d.score, name)))
+            with pytest.raises(ValueError):
+                d.run()
+        d = OnDevice(c)
+        setattr(d.score, name, getattr(d.score, name).double())
+        with pytest.raises(TypeError):
+            d.run()
+    d = OnDevice(c)
+    for ws in (d.ws[::2], d.ws.cpu()):
+        d.ws = ws
+        with pytest.raises(ValueError):
+            d.run()
