@@ -793,7 +793,7 @@ bool plan_decode_scored(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t m
     const int64_t nh = static_cast<int64_t>(Hkv) * ((G + kMaxHeads - 1) / kMaxHeads);
     // sequences of one launch: their segments have counters, and units are counted in 32 bits
     int64_t batch = kScoredSegments / nh;
-    const int64_t by_units = 0x7fffffffLL / (nh * (max_seq_len / kPageTokens + 2));
+    const int64_t by_units = 0x70000000LL / (nh * (max_seq_len / kPageTokens + 2));  // (room for a slice past the end)
     if (by_units < batch) batch = by_units;
     if (batch > kMaxSeqs) batch = kMaxSeqs;
     if (batch < 1 || S < 1) return false;
