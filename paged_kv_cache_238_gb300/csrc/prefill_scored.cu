@@ -190,12 +190,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// Packed fp32 pairs: one instruction for two elements.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
 // The pair (x, x) of a value that every lane holds, through a shuffle: the compiler then keeps it in
 // vector registers instead of moving it out of uniform ones for every group of keys.
 __device__ __forceinline__ uint64_t hold2(float x) {
@@ -205,19 +199,6 @@ __device__ __forceinline__ uint64_t hold2(float x) {
 // Columns 2 e, 2 e + 1 of a group of 16 scores.
 __device__ __forceinline__ uint64_t raw_pair(const uint32_t (&r)[16], int e) {
     return pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -322,7 +303,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
     __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ block_table,
     int32_t max_blocks, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ query_start_loc,
     int32_t num_kv_heads, int32_t G, int32_t num_blocks, int32_t sub_log2, int32_t cap_tokens, int32_t max_chunk,
-    int32_t sub, uint32_t inv_sub, const __grid_constant__ Split split,    const __grid_constant__ TcScore sc, uint32_t* err) {
+    int32_t sub, uint32_t inv_sub, const __grid_constant__ Split split, const __grid_constant__ TcScore sc, uint32_t* err) {
     using L_ = Smem<D, NQ>;
     constexpr int kSoftWarps = Warps<NQ>::soft, kKWarp = Warps<NQ>::k, kMmaWarp = Warps<NQ>::mma, kVWarp = Warps<NQ>::v;
     constexpr int kSoftThreads = 32 * kSoftWarps;
@@ -1070,7 +1051,7 @@ __global__ void __launch_bounds__(2 * kRows) prefill_scored_merge_kernel(__nv_bf
 constexpr double kTanh[4] = {0.999991018, -0.332989742, 0.129745541, -0.0396112775};
 constexpr float kTanhRange = 0.6f;
 
-// Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
+// Grids of few waves are ordered pair by pair, others sequence by sequence (kFewWaves).
 // tiles: query tiles of a CTA; of one tile, two CTAs share an SM.
 bool few_waves(int64_t entries, int32_t num_kv_heads, int tiles, int num_sms) {
     return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * (3 - tiles) * num_sms;
@@ -1091,7 +1072,6 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillSc
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
     const int32_t pairs = (a.max_chunk_len + NQ * TT - 1) / (NQ * TT);
-    // Grids of few waves are ordered pair by pair, others sequence by sequence (see kFewWaves).
     const int64_t entries = static_cast<int64_t>(pairs) * a.num_seqs;
     const bool by_pair = few_waves(entries, a.num_kv_heads, NQ, num_sms);
     const int32_t sub = by_pair ? pairs : 1;
