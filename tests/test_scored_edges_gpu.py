@@ -419,3 +419,21 @@ def test_tensors_that_are_not_contiguous_or_elsewhere_are_refused():
         d.ws = ws
         with pytest.raises(ValueError):
             d.run()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_a_row_that_sees_one_key_is_its_value(form, H_q, H_kv, D):
+    """One visible key has weight 1 whatever its score: the output is its V, bit for bit (the two roundings of a
+    quotient p v / p in fp32 are far below half a step of bf16). Prefill in contexts of up to 192 keys, decode
+    everywhere."""
+    kw = dict(FORMS[form])
+    if "slopes" in kw:
+        kw["slopes"] = alibi(H_q)
+    for lens, chunks in (([1, 190, 64, 17], [1, 190, 9, 17]), ([1, 1500, 33, 777], None)):
+        c = Case(78, lens, H_q, H_kv, D, 16, "bf16", chunks=chunks, window=1, **kw)
+        got = to_f64(OnDevice(c).run())
+        for s, (L, C) in enumerate(zip(lens, chunks or [1] * len(lens))):
+            for r in range(C):
+                v = c.vals[s][L - C + r]  # [H_kv, D]
+                assert np.array_equal(got[c.qsl[s] + r], np.repeat(v, H_q // H_kv, axis=0)), (form, L, r)
