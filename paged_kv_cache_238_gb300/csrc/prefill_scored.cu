@@ -79,7 +79,7 @@ constexpr int kRankMax = 256;             // entries that each CTA ranks by thei
 constexpr int kFewWaves = 4;
 constexpr size_t kSplitRowBytes = kRankMax * 16 * 16;  // Split::rows, in a workspace
 // Key tiles of a run, at least, when a list is split. Measured, 16 rows of one sequence on 4096 keys, 8 kv
-// heads of 128: 15.8 us with 2, 17.7 with 4, 25.7 with 8, 63.8 not split; 256 rows on 32768 keys: 149 us, not
+// heads of 128: 16.4 us with 2, 17.7 with 4, 25.7 with 8, 63.8 not split; 256 rows on 32768 keys: 154 us, not
 // split 531.
 constexpr int kMinPartTiles = 2;
 // Query tiles of a CTA: one, with two CTAs on an SM that cover each other's start and end, where one tile holds
@@ -89,7 +89,7 @@ constexpr int kMinPartTiles = 2;
 // on up to 4608 keys: 293 us, with one tile 419; the two meet near 1000 keys at head_dim 64, 200 at 128).
 __host__ __device__ constexpr int short_keys(int D) { return D == 64 ? 768 : 192; }
 // Caps with a fixed reference: 1.5 cap log2(e) <= 112. Measured, 16 sequences of 512 new rows on 2512 keys, 32 q / 8
-// kv heads of 128: cap 50 298 us, not capped 332, cap 52 (general) 728.
+// kv heads of 128: cap 50 302 us, not capped 330, cap 52 (general) 720.
 constexpr float kMaxFixedCap = 51.f;
 constexpr float kTopWeight = 48.f;  // with a distance bias: the largest weight's exponent
 
