@@ -414,8 +414,8 @@ PA_API pa_status pa_step(const pa_step_desc* step, void* stream);
  * counts the row's own key; prefix_len names the first keys of a sequence that every row of it
  * sees: rows before them included (prompts whose prefix is attended in both directions), or, with
  * prefix_causal, only rows at or behind them (the first tokens of a causal model that stay visible
- * under a window). The two differ for prefill rows inside the prefix only. key_start the first key a row may see (a
- * document mask for packed documents: the position where the row's document starts).
+ * under a window). The two differ for prefill rows inside the prefix only. key_start is the first
+ * key a row may see (a document mask for packed documents: where the row's document starts).
  *   softcap       0 (none) or a positive finite number
  *   alibi_slopes  NULL or [num_q_heads] fp32
  *   window        0 (none) or a positive number of keys

@@ -499,6 +499,10 @@ class Score:
         self.softcap, self.window, self.prefix_causal = softcap, window, prefix_causal
         self.alibi_slopes, self.key_start, self.prefix_len = alibi_slopes, key_start, prefix_len
 
+    def __reduce__(self):  # a copy has a descriptor of its own
+        return Score, (self._softcap, self._alibi_slopes, self._window, self._key_start, self._prefix_len,
+                       self._prefix_causal)
+
     @property
     def softcap(self) -> float:
         return self._softcap

@@ -57,3 +57,16 @@ def test_calls_refuse_other_values_of_the_causal_flag(value):
                                 1 << 30, None) == B.PA_ERR_INVALID_ARG
     assert lib.pa_prefill_scored(FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, FAKE, 2, 16, 64, 8, 2, 128, 16, 16, 0.1, desc,
                                  B.PA_BF16, FAKE, 1 << 30, None) == B.PA_ERR_INVALID_ARG
+
+
+def test_copies_are_apart():
+    """A copied Score that is changed leaves the first one as it was."""
+    import copy
+    a, b = torch.ones(4), torch.zeros(4)
+    first = B.Score(softcap=20.0, alibi_slopes=a, window=5, prefix_causal=True)
+    for second in (copy.copy(first), copy.deepcopy(first)):
+        assert (second.softcap, second.window, second.prefix_causal) == (20.0, 5, True)
+        assert torch.equal(second.alibi_slopes, a)
+        second.window, second.softcap, second.alibi_slopes, second.prefix_causal = 9, 0.0, b, False
+        assert fields(first) == (20.0, 5, a.data_ptr(), None, None) and first._desc.prefix_causal == 1
+    assert copy.copy(first).alibi_slopes is a
