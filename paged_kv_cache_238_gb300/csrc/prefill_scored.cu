@@ -35,7 +35,7 @@
 // in the score, below the 2^-9 of the bf16 weights), evaluated on the FMA pipes two elements an
 // instruction; a warp whose 32 scores of a row block hold a larger one takes
 // tanh x = 1 - 2 / (1 + 2^(2 x log2 e)) for that block (absolute error 2^-20). P is rounded to bf16, the
-// type in which the tensor cores multiply it by V (fp32 accumulation; the sums add the fp32 weights, but see kRoundedSums).
+// type in which the tensor cores multiply it by V (fp32 accumulation; the sums add the fp32 weights).
 //
 // Bound: the tensor cores, then the exponentials. 16 sequences of 512 new rows on 512 to 4608 keys, 32 q /
 // 8 kv heads of 128, cap 50: 293 us, 1.06 PFLOP/s over visible pairs (54 % of the measured bf16 rate; a key
@@ -318,11 +318,6 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
     constexpr bool kSplit = kFixed || D == 64;
     constexpr bool kOwnO = kSplit && !kFixed;  // each half of the keys has its own O and maximum
     constexpr int kChains = kSplit ? 2 * NQ : NQ;
-    // Against a fixed reference even the largest weight of a row is rounded to bf16 for P V (against its maximum it is 1),
-    // which a row that sees one key, or is ruled by one, shows in full: 2^-9 of V. Where contexts may be that short
-    // the sums add the rounded weights too, and the rounding cancels there. In two tiles, where most
-    // rows see many keys, this would take 5 % (16 chunks of 512 rows on up to 4608 keys: 301 and 318 us).
-    constexpr bool kRoundedSums = kFixed && NQ == 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::bars);
@@ -898,7 +893,7 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                                   x[(c + 1) & 1][2 * e + 1]);
                     const float p0 = exp2_approx(x[c & 1][2 * e]), p1 = exp2_approx(x[c & 1][2 * e + 1]);
                     pk[e] = pack_bf16x2(p0, p1);
-                    psum[e & 3] = add2(psum[e & 3], kRoundedSums ? bf16_pair(pk[e]) : pack2(p0, p1));
+                    psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
                 }
                 st_x8(tmem_s + c * 8, pk);
                 if (c < 3) amend(raw[(c + 1) & 1], c + 1, shift, x[(c + 1) & 1]);
@@ -930,6 +925,8 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
             w1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - top);
         }
         l_sum = w0 * sums[r] + w1 * sums[kRows + r];
+        // A row that sees one key is its V: its sum is the one weight, which P V took rounded to bf16.
+        if (row.a1 - row.a0 + (row.b1 - row.b0) == 1) l_sum = __bfloat162float(__float2bfloat16_rn(l_sum));
         named_barrier(1 + xq, 256);
         ok = __all_sync(0xffffffffu, ok);
         // columns half (D / 2) + 32 c .. of the row's output, before the division; 0 where no key was used

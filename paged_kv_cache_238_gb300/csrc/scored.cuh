@@ -65,10 +65,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The two bf16 of a word as fp32.
-__device__ __forceinline__ uint64_t bf16_pair(uint32_t v) {
-    return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
 
 // Capped scores, cap log2(e) tanh(u) with u = s scale / cap, from y = 2 u log2(e) = s two_k and c1 = scale log2(e).
 // Two forms, of which neither serves every cap: near u = 0 the identity cancels (an error of 2^-21 cap,

@@ -425,15 +425,25 @@ def test_tensors_that_are_not_contiguous_or_elsewhere_are_refused():
 @pytest.mark.parametrize("form", list(FORMS))
 def test_a_row_that_sees_one_key_is_its_value(form, H_q, H_kv, D):
     """One visible key has weight 1 whatever its score: the output is its V, bit for bit (the two roundings of a
-    quotient p v / p in fp32 are far below half a step of bf16). Prefill in contexts of up to 192 keys, decode
-    everywhere."""
+    quotient p v / p in fp32 are far below half a step of bf16)."""
     kw = dict(FORMS[form])
     if "slopes" in kw:
         kw["slopes"] = alibi(H_q)
-    for lens, chunks in (([1, 190, 64, 17], [1, 190, 9, 17]), ([1, 1500, 33, 777], None)):
+    for lens, chunks in (([1, 190, 64, 17], [1, 190, 9, 17]), ([1200, 300, 1], [200, 300, 1]), ([3000], [4]),
+                         ([1, 1500, 33, 777], None)):
         c = Case(78, lens, H_q, H_kv, D, 16, "bf16", chunks=chunks, window=1, **kw)
         got = to_f64(OnDevice(c).run())
         for s, (L, C) in enumerate(zip(lens, chunks or [1] * len(lens))):
             for r in range(C):
                 v = c.vals[s][L - C + r]  # [H_kv, D]
                 assert np.array_equal(got[c.qsl[s] + r], np.repeat(v, H_q // H_kv, axis=0)), (form, L, r)
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(32, 2, 64), (32, 4, 128)])
+@pytest.mark.parametrize("cap", [5.0, 30.0, 51.0])
+def test_rows_of_two_and_three_keys(cap, H_q, H_kv, D):
+    """Few weights of one size, where an error of the sums does not average out against those of P V."""
+    for seed in range(6):
+        for window in (2, 3):
+            check(Case(90 + seed, [189, 8, 17, 77, 13], H_q, H_kv, D, 16, "bf16", chunks=[149, 8, 7, 47, 1], window=window,
+                       cap=cap), f"{cap} {window} {seed}")
