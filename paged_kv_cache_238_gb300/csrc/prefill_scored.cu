@@ -892,8 +892,8 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
                         pair_args(raw_pair(raw[(c + 1) & 1], e), c + 1, e, shift, x[(c + 1) & 1][2 * e],
                                   x[(c + 1) & 1][2 * e + 1]);
                     const float p0 = exp2_approx(x[c & 1][2 * e]), p1 = exp2_approx(x[c & 1][2 * e + 1]);
-                    pk[e] = pack_bf16x2(p0, p1);
                     psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
+                    pk[e] = pack_bf16x2(p0, p1);
                 }
                 st_x8(tmem_s + c * 8, pk);
                 if (c < 3) amend(raw[(c + 1) & 1], c + 1, shift, x[(c + 1) & 1]);
