@@ -74,7 +74,9 @@ typedef enum {
 
 typedef enum {
     PA_F32 = 0,               /* fp32 Q/K/V/out, fp32 arithmetic (no TF32)              */
-    PA_BF16 = 1               /* bf16 Q/K/V/out, fp32 accumulation                      */
+    PA_BF16 = 1,              /* bf16 Q/K/V/out, fp32 accumulation                      */
+    PA_FP4 = 2                /* a pool held in 4 bits ("4-bit pools" below): accepted only
+                                 where an entry point says so                           */
 } pa_dtype;
 
 /* Bits of the device error word. */
@@ -88,6 +90,8 @@ typedef enum {
                                            with row 0's prefix blocks (results invalid)   */
 #define PA_DEVERR_PAIR_ORDER   0x40u /* pa_move_blocks: src ids not strictly ascending while a
                                         block table is rewritten (the table is unspecified)  */
+#define PA_DEVERR_POSITION     0x80u /* pa_rotate_and_cache: a position outside the table of angles (the
+                                        token is left out)                                   */
 
 /*
  * pa_reshape_and_cache: write the K/V rows of num_tokens new tokens into their slots.
@@ -484,6 +488,114 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
                                    pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * 4-bit pools: K and V held in 4 bits and a shared scale, 9/32 of the bytes of bf16. A value is
+ *   code * scale * factor
+ * with the code in e2m1 (+-{0, 0.5, 1, 1.5, 2, 3, 4, 6}: bit 3 the sign, bits 0-2 the magnitude's
+ * index), the scale in e4m3, shared by 16 consecutive dims of a token's head row, and the pool's
+ * factor k_scale or v_scale: a power of two between 2^-24 and 2^24 that the caller keeps with the
+ * pool and passes to every call (1 serves values whose groups have a largest magnitude between
+ * 0.01 and 2688).
+ *   k_cache, v_cache   [num_blocks][num_kv_heads][BS / 16] pages of 9 * head_dim bytes, 16-byte
+ *                      aligned: 16 tokens' rows of head_dim / 2 bytes of codes (dim 2 i in the low
+ *                      half of byte i), then 16 tokens' rows of head_dim / 16 scales
+ *   storing x          y = x / factor;  scale = e4m3(max over the group |y| / 6), nearest, ties to
+ *                      even, at most 448;  code = e2m1(y / scale), nearest, ties to even, magnitude
+ *                      at most 6;  all codes 0 when the scale is 0. Infinities saturate; a NaN takes
+ *                      no part in the maximum and is stored as some number.
+ * Such pools take pa_rotate_and_cache, pa_decode_fp4, pa_prefill_fp4 and pa_gather_fp4; pa_move_blocks
+ * (whole blocks) and pa_bm_num_blocks_for_memory with dtype PA_FP4; and every block-manager call.
+ * head_dim 64 or 128. No counterpart on the source pages.
+ */
+
+/*
+ * pa_rotate_and_cache: new tokens on their way into the pool. For token t at position
+ * p = positions[t], with c_i = cos_sin[p][i] and s_i = cos_sin[p][rotary_dim / 2 + i]:
+ *   interleaved 0   (x_i, x_(i + rotary_dim/2)) -> (x_i c_i - x_(i + rotary_dim/2) s_i,
+ *                                                   x_(i + rotary_dim/2) c_i + x_i s_i)
+ *   interleaved 1   (x_2i, x_(2i+1))            -> the same with these two
+ * for i < rotary_dim / 2; dims from rotary_dim on stay. Every head of q[t] rotated goes to q_out[t];
+ * every kv head of k[t] rotated and of v[t] goes to slot slot_mapping[t] of the pools, as
+ * pa_reshape_and_cache writes them (a negative slot: q_out only).
+ * The rotation is computed in fp32 and rounded once to dtype. Into a 4-bit pool k is first rounded to
+ * dtype (from a sum of about 45 bits), then stored: the bytes are those of rotating first and
+ * storing what that gave.
+ *   q_out, q      [num_tokens] rows of [num_q_heads][head_dim], q_out_stride and q_stride elements
+ *                 apart; q_out may be q itself (same stride). Both NULL with num_q_heads 0.
+ *   k, v          [num_tokens] rows of [num_kv_heads][head_dim], k_stride and v_stride apart
+ *                 (views of a packed projection, for example). Rows must be 16-byte aligned: strides
+ *                 are multiples of 16 bytes and at least a row (one token: any stride).
+ *   positions     [num_tokens] int64 in [0, num_positions); another one sets PA_DEVERR_POSITION, and
+ *                 the token is left out (q_out row and slot keep what they held)
+ *   cos_sin       [num_positions][rotary_dim] fp32
+ *   rotary_dim    a multiple of 16 up to head_dim (another positive value: PA_ERR_UNSUPPORTED)
+ *   slot_mapping  [num_tokens] int64, under pa_reshape_and_cache's rules
+ *   cache_dtype   dtype, or PA_FP4; k_scale and v_scale are read for PA_FP4 only
+ * Supported: bf16 or fp32, head_dim 64 or 128, block sizes 16, 32, 64 and 128. int64 arrays are 8-byte
+ * aligned.
+ */
+typedef struct {
+    void* q_out;
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;
+    const int64_t* positions;
+    const float* cos_sin;
+    int32_t num_positions, rotary_dim, interleaved;
+    void* k_cache;
+    void* v_cache;
+    const int64_t* slot_mapping;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size;
+    pa_dtype dtype, cache_dtype;
+    float k_scale, v_scale;
+} pa_rotate;
+
+PA_API pa_status pa_rotate_and_cache(const pa_rotate* rotate, void* stream);
+
+/*
+ * pa_decode_fp4: pa_decode_bs over 4-bit pools: K_i[j] and V_i[j] are the values described above.
+ * q and out are dtype (bf16 or fp32); any number of q heads per kv head. Products with bf16 queries run
+ * on the tensor cores in fp16, which holds the pool's values exactly: each q head's row is scaled by a
+ * power of two to fp16 (elements 2^-24 below the row's largest magnitude are lost), weights are rounded
+ * to fp16; sums and softmax statistics are fp32. fp32 queries compute in fp32 throughout.
+ * workspace: >= pa_decode_fp4_workspace_size(...) bytes, under the rules of pa_decode_scored's.
+ */
+PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t max_seq_len, pa_dtype dtype);
+PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale, float k_scale,
+                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_prefill_fp4: pa_prefill_chunk_bs over 4-bit pools, with pa_decode_fp4's values and arithmetic. A
+ * chunk longer than max_chunk_len or than its sequence sets PA_DEVERR_LEN_RANGE and leaves its rows
+ * unwritten. workspace: >= pa_prefill_fp4_workspace_size(...) bytes, under the rules of
+ * pa_prefill_scored's (may be NULL when that is 0).
+ */
+PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                                            pa_dtype dtype);
+PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
+                                int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, float scale, float k_scale, float v_scale,
+                                pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_gather_fp4: rows of 4-bit pools as values, e.g. to move a sequence into another pool:
+ * k_out[i] and v_out[i] ([num_slots][num_kv_heads][head_dim], dtype bf16 or fp32, which hold the
+ * values exactly) are what slot slots[i] (int64) holds. A negative slot gives a row of zeros; one
+ * outside the pool too, and sets PA_DEVERR_SLOT_RANGE. Slots may repeat.
+ */
+PA_API pa_status pa_gather_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int64_t* slots, int32_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t num_blocks, int32_t block_size, float k_scale, float v_scale, pa_dtype dtype,
+                               void* stream);
+
+/*
  * pa_get_device_errors: read the device error word of the current device (PA_DEVERR_*
  * bits OR-ed by the kernels since the last clear) into *errors, and clear it when
  * `clear` is non-zero. Synchronises the current device. The library owns the word.
@@ -630,7 +742,8 @@ PA_API pa_status pa_bm_block_info(const pa_block_manager* bm, int32_t block_id, 
  * is sized once from a utilisation fraction of free memory); -1 on a bad argument. */
 PA_API int64_t pa_bm_num_blocks_for_memory(size_t free_bytes, double utilization, int32_t num_layers,
                                            int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype);
-/* The same for blocks of block_size tokens (16, 32, 64 or 128; -1 otherwise). */
+/* The same for blocks of block_size tokens (16, 32, 64 or 128; -1 otherwise). dtype of both: PA_FP4 for 4-bit
+ * pools (head_dim then a multiple of 64). */
 PA_API int64_t pa_bm_num_blocks_for_memory_bs(size_t free_bytes, double utilization, int32_t num_layers,
                                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                               pa_dtype dtype);
@@ -662,6 +775,8 @@ PA_API pa_status pa_copy_blocks_bs(void* k_cache, void* v_cache, const int32_t* 
  *   pools        host array of num_pools device pointers, each [num_blocks][num_kv_heads]
  *                [block_size][head_dim], 16-byte aligned (K and V pools alike); the array is read
  *                during the call only
+ *   dtype        the pools' type; PA_FP4 for 4-bit pools, whose blocks move whole (`tokens` NULL, else
+ *                PA_ERR_UNSUPPORTED)
  *   tokens       NULL (whole blocks) or device int32 [n_pairs]: only the first tokens[i] tokens of
  *                each head's page are copied (the filled part of a partly filled block); clamped
  *                to [0, block_size]

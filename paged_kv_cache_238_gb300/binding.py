@@ -14,11 +14,12 @@ from typing import Optional
 from . import _build
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_NO_SPACE = 0, 1, 2, 3, 4
-PA_F32, PA_BF16 = 0, 1
+PA_F32, PA_BF16, PA_FP4 = 0, 1, 2
 PA_DEVERR_SLOT_RANGE, PA_DEVERR_BLOCK_RANGE, PA_DEVERR_LEN_RANGE, PA_DEVERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 PA_DEVERR_APPEND_SLOT = 0x10
 PA_DEVERR_PREFIX_MISMATCH = 0x20
 PA_DEVERR_PAIR_ORDER = 0x40
+PA_DEVERR_POSITION = 0x80
 PA_DECODE_TABLES_READY = 0x1
 PA_DECODE_POOL_READY = 0x2
 PA_DRILL_OFF, PA_DRILL_DECODE_STAGE, PA_DRILL_PREFILL_K_TILE = 0, 1, 2
@@ -35,7 +36,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode", "pa
             "pa_bm_num_blocks_for_memory_bs", "pa_debug_set_wait_drill", "pa_decode_shared_prefix_workspace_size",
             "pa_decode_shared_prefix", "pa_debug_decode_slices", "pa_decode_scored_workspace_size",
             "pa_decode_scored", "pa_prefill_scored_workspace_size", "pa_prefill_scored", "pa_move_blocks",
-            "pa_bm_release_behind", "pa_bm_resize")
+            "pa_bm_release_behind", "pa_bm_resize", "pa_rotate_and_cache", "pa_decode_fp4_workspace_size", "pa_decode_fp4",
+            "pa_prefill_fp4_workspace_size", "pa_prefill_fp4", "pa_gather_fp4")
 #: block sizes the *_bs entry points accept
 BLOCK_SIZES = (16, 32, 64, 128)
 #: size of the library's fixed scratch used by pa_decode_noalloc
@@ -71,6 +73,19 @@ class ScoreDesc(ctypes.Structure):
     """Mirror of pa_score in include/pa.h (same fields, same order, C layout)."""
     _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", ctypes.c_void_p),
                 ("key_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("prefix_causal", ctypes.c_int32)]
+
+
+class RotateDesc(ctypes.Structure):
+    """Mirror of pa_rotate in include/pa.h (same fields, same order, C layout)."""
+    _fields_ = [("q_out", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("num_positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("slot_mapping", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
 
 
 class PaError(RuntimeError):
@@ -149,6 +164,15 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
                                                          sz, vp]),
                     ("pa_move_blocks", ctypes.c_int, [vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, i32, vp, vp, i32,
                                                       vp, i32, vp]),
+                    ("pa_rotate_and_cache", ctypes.c_int, [ctypes.POINTER(RotateDesc), vp]),
+                    ("pa_decode_fp4_workspace_size", sz, [i32, i32, i32, i32, i32, ctypes.c_int]),
+                    ("pa_decode_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                                     f32, f32, f32, ctypes.c_int, vp, sz, vp]),
+                    ("pa_prefill_fp4_workspace_size", sz, [i32, i32, i32, i32, i32, i32, ctypes.c_int]),
+                    ("pa_prefill_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                                      i32, f32, f32, f32, ctypes.c_int, vp, sz, vp]),
+                    ("pa_gather_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, f32, ctypes.c_int,
+                                                     vp]),
                     ("pa_bm_release_behind", ctypes.c_int, [vp, i64, i32, i32, pi32]),
                     ("pa_bm_resize", ctypes.c_int, [vp, i32, pi32, pi32, i32, pi32]),
                     ("pa_bm_create_bs", ctypes.c_int, [i32, i32, i32, ctypes.c_char_p, ctypes.POINTER(vp)]),
@@ -665,20 +689,23 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_table, seq_lens, query_sta
 
 class PoolList:
     """The pools that pa_move_blocks copies in: tensors [NB, H_kv, BS, D] of one shape, dtype and
-    device (the K and V pool of every layer), checked once. Keeps them alive."""
+    device (the K and V pool of every layer), checked once; 4-bit pools as uint8 [NB, H_kv, BS, 9 D / 16].
+    Keeps them alive."""
 
     def __init__(self, pools):
         self.pools = list(pools)
         if not self.pools:
             raise ValueError("PoolList needs at least one pool")
         first = self.pools[0]
-        self.dtype_code = _dtype_code(first)
+        self.dtype_code = PA_FP4 if _is_fp4(first) else _dtype_code(first)
         self.device = first.get_device()
         for i, p in enumerate(self.pools):
             _need(f"pools[{i}]", p, first.dtype, (-1, -1, -1, -1), self.device)
             if p.shape != first.shape:
                 raise ValueError(f"pools[{i}]: shape {tuple(p.shape)} where {tuple(first.shape)} is needed")
         self.shape = tuple(int(n) for n in first.shape)
+        if self.dtype_code == PA_FP4:
+            self.shape = self.shape[:3] + (_fp4_head_dim(first),)
         self._ptrs = (ctypes.c_void_p * len(self.pools))(*[p.data_ptr() for p in self.pools])
 
 
@@ -709,6 +736,211 @@ def pa_move_blocks(pools, block_pairs, tokens=None, block_table=None, seq_lens=N
         _ptr(block_table), mb, _ptr(seq_lens) if block_table is not None else None, S, _raw_stream(stream, dev)))
 
 
+# ------------------------------------------------------------------------------------------
+# rotation into the cache, 4-bit pools
+# ------------------------------------------------------------------------------------------
+
+#: row bytes of a 4-bit pool -> head_dim
+_FP4_ROWS = {36: 64, 72: 128}
+
+
+def _is_fp4(pool) -> bool:
+    import torch
+    return pool.dtype is torch.uint8
+
+
+def _fp4_head_dim(pool) -> int:
+    D = _FP4_ROWS.get(pool.shape[-1])
+    if D is None:
+        raise ValueError(f"a 4-bit pool has rows of 36 (head_dim 64) or 72 bytes (128), not {pool.shape[-1]}")
+    return D
+
+
+def fp4_pool_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int):
+    """Shape of a 4-bit pool, a uint8 tensor (pages of 16 tokens: codes, then scales; include/pa.h)."""
+    return num_blocks, num_kv_heads, block_size, head_dim * 9 // 16
+
+
+def _token_rows(what: str, t, dtype, tokens: int, D: int, device: int) -> int:
+    """A CUDA tensor [tokens, heads, D] whose rows of heads are contiguous; returns the elements between tokens."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{what}: on device {t.get_device()}, the others on device {device} (libpa takes CUDA tensors)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: {t.dtype} where {dtype} is needed")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != D:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} where {(tokens, -1, D)} is needed (-1: any size)")
+    step, head, one = t.stride()
+    if one != 1 or (head != D and t.shape[1] > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return step
+
+
+def pa_rotate_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved: bool = False,
+                        k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """New tokens rotated and written (C ABI pa_rotate_and_cache): q [T, H_q, D] rotated by positions
+    [T] int64 into q_out (which may be q), k and v [T, H_kv, D], k rotated, into slot_mapping [T] int64 of
+    the pools. q, k, v and q_out may be views with any distance between tokens. cos_sin: fp32
+    [positions, rotary_dim], cosines then sines. Pools in q's type, or 4-bit (uint8) with the factors k_scale
+    and v_scale. Without q: q = q_out = None."""
+    import torch
+    dt, dev, i64 = k.dtype, k.get_device(), torch.int64
+    code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(k)
+    fp4 = k_cache.dtype is torch.uint8
+    if k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2:
+        raise ValueError("k is [T, H_kv, D], the pools have four dimensions, cos_sin two")
+    T, H_kv, D = k.shape
+    NB, _, BS, _ = pool = k_cache.shape
+    want, row = (torch.uint8, D * 9 // 16) if fp4 else (dt, D)
+    if not (pool[1] == H_kv and pool[3] == row and k_cache.dtype is want and k_cache.get_device() == dev and
+            k_cache.is_contiguous() and v_cache.dtype is want and v_cache.shape == pool and v_cache.get_device() == dev and
+            v_cache.is_contiguous() and cos_sin.dtype is torch.float32 and cos_sin.get_device() == dev and
+            cos_sin.is_contiguous() and positions.dtype is i64 and positions.shape == (T,) and
+            positions.get_device() == dev and positions.is_contiguous() and slot_mapping.dtype is i64 and
+            slot_mapping.shape == (T,) and slot_mapping.get_device() == dev and slot_mapping.is_contiguous() and dev >= 0):
+        _need("k_cache", k_cache, want, (-1, H_kv, -1, row), dev)
+        _need("v_cache", v_cache, want, tuple(pool), dev)
+        _need("cos_sin", cos_sin, torch.float32, (-1, -1), dev)
+        _need("positions", positions, i64, (T,), dev)
+        _need("slot_mapping", slot_mapping, i64, (T,), dev)
+    if dev != torch._C._cuda_getDevice():
+        _need_current(dev)
+    d = RotateDesc()
+    if q is not None:
+        H_q = q.shape[1] if q.dim() == 3 else -1
+        d.q_stride, d.q_out_stride = _token_rows("q", q, dt, T, D, dev), _token_rows("q_out", q_out, dt, T, D, dev)
+        if q_out.shape[1] != H_q:
+            raise ValueError(f"q_out: shape {tuple(q_out.shape)} where {tuple(q.shape)} is needed")
+        d.q, d.q_out, d.num_q_heads = q.data_ptr(), q_out.data_ptr(), H_q
+    d.k_stride, d.v_stride = _token_rows("k", k, dt, T, D, dev), _token_rows("v", v, dt, T, D, dev)
+    if v.shape[1] != H_kv:
+        raise ValueError(f"v: shape {tuple(v.shape)} where {tuple(k.shape)} is needed")
+    d.k, d.v, d.positions, d.cos_sin = k.data_ptr(), v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr()
+    d.num_positions, d.rotary_dim = cos_sin.shape
+    d.interleaved = 1 if interleaved else 0
+    d.k_cache, d.v_cache, d.slot_mapping = k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr()
+    d.num_tokens, d.num_kv_heads, d.head_dim, d.num_blocks, d.block_size = T, H_kv, D, NB, BS
+    d.dtype, d.cache_dtype, d.k_scale, d.v_scale = code, PA_FP4 if fp4 else code, k_scale, v_scale
+    st = (_lib or load()).pa_rotate_and_cache(d, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_rotate_and_cache", st)
+
+
+def _check_fp4(out, q, k_cache, v_cache, block_table, seq_lens, workspace):
+    """Shape and type checks shared by the attention calls over 4-bit pools; returns (T, H_q, D, NB, H_kv, BS, S,
+    max_blocks, device, dtype code, workspace bytes)."""
+    import torch
+    dt, i32, u8, dev = q.dtype, torch.int32, torch.uint8, q.get_device()
+    code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(q)
+    if not (dev >= 0 and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2 and q.is_contiguous()):
+        _need("q", q, dt, (-1, -1, -1), dev)
+        _need("k_cache", k_cache, u8, (-1, -1, -1, -1), dev)
+        _need("block_table", block_table, i32, (-1, -1), dev)
+    T, H_q, D = q_shape = q.shape
+    NB, H_kv, BS, row = pool_shape = k_cache.shape
+    S, mb = block_table.shape
+    # written out, not as calls of _fits: a call takes as long as the comparisons
+    if not (row * 16 == D * 9 and
+            out.dtype is dt and out.shape == q_shape and out.get_device() == dev and out.is_contiguous() and
+            k_cache.dtype is u8 and k_cache.get_device() == dev and k_cache.is_contiguous() and
+            v_cache.dtype is u8 and v_cache.shape == pool_shape and v_cache.get_device() == dev and
+            v_cache.is_contiguous() and block_table.dtype is i32 and block_table.get_device() == dev and
+            block_table.is_contiguous() and seq_lens.dtype is i32 and seq_lens.shape == (S,) and
+            seq_lens.get_device() == dev and seq_lens.is_contiguous()):
+        _need("out", out, dt, (T, H_q, D), dev)
+        _need("k_cache", k_cache, u8, (-1, -1, -1, D * 9 // 16), dev)
+        _need("v_cache", v_cache, u8, tuple(pool_shape), dev)
+        _need("seq_lens", seq_lens, i32, (-1,), dev)
+        _need("block_table", block_table, i32, (seq_lens.shape[0], -1), dev)
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA tensor on the other tensors' device is needed")
+        ws_bytes = workspace.nbytes
+    if dev != torch._C._cuda_getDevice():
+        _need_current(dev)
+    return T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes
+
+
+def pa_decode_fp4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seq_len: int,
+                                 dtype) -> int:
+    import torch
+    code = dtype if isinstance(dtype, int) else (PA_F32 if dtype == torch.float32 else PA_BF16)
+    return int(load().pa_decode_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, code))
+
+
+def pa_decode_fp4(out, q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, scale: float, workspace=None,
+                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """pa_decode over 4-bit pools (C ABI pa_decode_fp4). out, q: [S, H_q, D]; k_cache, v_cache: uint8
+    [NB, H_kv, BS, 9 D / 16], with their factors; workspace: zeroed uint8 CUDA tensor of
+    pa_decode_fp4_workspace_size(...) bytes (None when that is 0); the rest as for pa_decode."""
+    T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes = _check_fp4(out, q, k_cache, v_cache, block_table, seq_lens,
+                                                                    workspace)
+    if T != S:
+        raise ValueError(f"decode takes one query row per sequence: {T} rows, {S} sequences")
+    st = (_lib or load()).pa_decode_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        seq_lens.data_ptr(), S, int(max_seq_len), H_q, H_kv, D, NB, BS, scale, k_scale, v_scale, code, _ptr(workspace),
+        ws_bytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_decode_fp4", st)
+
+
+def pa_prefill_fp4_workspace_size(num_seqs: int, max_chunk_len: int, num_q_heads: int, num_kv_heads: int,
+                                  head_dim: int, max_seq_len: int, dtype) -> int:
+    import torch
+    code = dtype if isinstance(dtype, int) else (PA_F32 if dtype == torch.float32 else PA_BF16)
+    return int(load().pa_prefill_fp4_workspace_size(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                    max_seq_len, code))
+
+
+def pa_prefill_fp4(out, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_chunk_len: int,
+                   max_seq_len: int, scale: float, workspace=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                   stream=None) -> None:
+    """pa_prefill_chunk over 4-bit pools (C ABI pa_prefill_fp4). out, q: [T_q, H_q, D]; query_start_loc: [S + 1]
+    int32; pools and workspace as for pa_decode_fp4, of pa_prefill_fp4_workspace_size(...) bytes."""
+    import torch
+    T, H_q, D, NB, H_kv, BS, S, mb, dev, code, ws_bytes = _check_fp4(out, q, k_cache, v_cache, block_table, seq_lens,
+                                                                    workspace)
+    if not _fits(query_start_loc, torch.int32, (S + 1,), dev):
+        _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), dev)
+    st = (_lib or load()).pa_prefill_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        seq_lens.data_ptr(), query_start_loc.data_ptr(), S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS,
+        scale, k_scale, v_scale, code, _ptr(workspace), ws_bytes, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_prefill_fp4", st)
+
+
+def pa_gather_fp4(k_out, v_out, k_cache, v_cache, slots, k_scale: float = 1.0, v_scale: float = 1.0,
+                  stream=None) -> None:
+    """Rows of 4-bit pools as values (C ABI pa_gather_fp4): k_out, v_out [n, H_kv, D] bf16 or fp32 of slots [n]
+    int64; a negative slot gives zeros."""
+    import torch
+    dev, dt, u8 = k_out.get_device(), k_out.dtype, torch.uint8
+    code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(k_out)
+    if k_out.dim() != 3 or k_cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("k_out is [n, H_kv, D], the pools have four dimensions, slots one")
+    n, H_kv, D = k_out.shape
+    NB, _, BS, _ = pool = k_cache.shape
+    if not (dev >= 0 and k_out.is_contiguous() and v_out.dtype is dt and v_out.shape == k_out.shape and
+            v_out.get_device() == dev and v_out.is_contiguous() and k_cache.dtype is u8 and pool[1] == H_kv and
+            pool[3] * 16 == D * 9 and k_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.dtype is u8 and
+            v_cache.shape == pool and v_cache.get_device() == dev and v_cache.is_contiguous() and
+            slots.dtype is torch.int64 and slots.shape == (n,) and slots.get_device() == dev and slots.is_contiguous()):
+        _need("k_out", k_out, dt, (-1, -1, -1), dev)
+        _need("v_out", v_out, dt, (n, H_kv, D), dev)
+        _need("k_cache", k_cache, u8, (-1, H_kv, -1, D * 9 // 16), dev)
+        _need("v_cache", v_cache, u8, tuple(pool), dev)
+        _need("slots", slots, torch.int64, (n,), dev)
+    if dev != torch._C._cuda_getDevice():
+        _need_current(dev)
+    st = (_lib or load()).pa_gather_fp4(
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), n, H_kv, D, NB, BS,
+        k_scale, v_scale, code, _raw_stream(stream, dev))
+    if st != PA_OK:
+        _check("pa_gather_fp4", st)
+
+
 def pa_sha256(data: bytes) -> bytes:
     out = (ctypes.c_uint8 * 32)()
     buf = (ctypes.c_uint8 * max(1, len(data))).from_buffer_copy(data or b"\0")
@@ -718,8 +950,10 @@ def pa_sha256(data: bytes) -> bytes:
 
 def pa_bm_num_blocks_for_memory(free_bytes: int, utilization: float, num_layers: int, num_kv_heads: int,
                                 head_dim: int, dtype, block_size: int = BLOCK_SIZE) -> int:
+    """dtype: torch.float32, torch.bfloat16, or torch.uint8 for 4-bit pools."""
     import torch
-    code = dtype if isinstance(dtype, int) else (PA_F32 if dtype == torch.float32 else PA_BF16)
+    codes = {torch.float32: PA_F32, torch.uint8: PA_FP4}
+    code = dtype if isinstance(dtype, int) else codes.get(dtype, PA_BF16)
     if block_size == BLOCK_SIZE:
         return int(load().pa_bm_num_blocks_for_memory(free_bytes, utilization, num_layers, num_kv_heads, head_dim,
                                                       code))

@@ -614,9 +614,10 @@ PA_API int64_t pa_bm_num_blocks_for_memory_bs(size_t free_bytes, double utilizat
                                               pa_dtype dtype) {
     if (num_layers <= 0 || num_kv_heads <= 0 || head_dim <= 0 || !(utilization > 0.0) || utilization > 1.0) return -1;
     if (!pa::bm::block_size_valid(block_size)) return -1;
-    const int64_t el = dtype == PA_F32 ? 4 : (dtype == PA_BF16 ? 2 : 0);
-    if (el == 0) return -1;
-    const int64_t per_block = static_cast<int64_t>(num_layers) * 2 * num_kv_heads * block_size * head_dim * el;
+    if (dtype == PA_FP4 && head_dim % 64 != 0) return -1;
+    const int64_t el16 = dtype == PA_F32 ? 64 : dtype == PA_BF16 ? 32 : dtype == PA_FP4 ? 9 : 0;  // bytes of 16 elements
+    if (el16 == 0) return -1;
+    const int64_t per_block = static_cast<int64_t>(num_layers) * 2 * num_kv_heads * block_size / 16 * head_dim * el16;
     const int64_t usable = static_cast<int64_t>(static_cast<double>(free_bytes) * utilization);
     return usable / per_block;
 }

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <math.h>
 
 #include <atomic>
 #include <mutex>
@@ -646,16 +647,163 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// The factor of a 4-bit pool: a power of two between 2^-24 and 2^24.
+static bool factor_ok(float f) {
+    int e = 0;
+    return f > 0.f && f < 3e7f && frexpf(f, &e) == 0.5f && e >= -23 && e <= 25;
+}
+
+PA_API pa_status pa_rotate_and_cache(const pa_rotate* r, void* stream) {
+    if (!r) return PA_ERR_INVALID_ARG;
+    if (r->num_tokens < 0 || r->num_q_heads < 0 || r->num_kv_heads <= 0 || r->num_blocks <= 0 || r->num_positions < 0 ||
+        r->rotary_dim <= 0 || r->rotary_dim > r->head_dim || (r->interleaved != 0 && r->interleaved != 1))
+        return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(r->block_size)) return r->block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    if (!dtype_ok(r->dtype) || (r->cache_dtype != r->dtype && r->cache_dtype != PA_FP4)) return PA_ERR_INVALID_ARG;
+    if ((r->head_dim != 64 && r->head_dim != 128) || r->rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    const bool fp4 = r->cache_dtype == PA_FP4;
+    if (fp4 && (!factor_ok(r->k_scale) || !factor_ok(r->v_scale))) return PA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(r->num_blocks) * r->num_kv_heads * r->block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (r->num_tokens == 0) return PA_OK;
+    if (!r->k || !r->v || !r->k_cache || !r->v_cache || !r->positions || !r->cos_sin || !r->slot_mapping ||
+        (r->num_q_heads > 0 && (!r->q || !r->q_out)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(r->q_out) || !aligned16(r->q) || !aligned16(r->k) || !aligned16(r->v) || !aligned16(r->k_cache) ||
+        !aligned16(r->v_cache) || !aligned16(r->cos_sin) || (reinterpret_cast<uintptr_t>(r->positions) & 7u) ||
+        (reinterpret_cast<uintptr_t>(r->slot_mapping) & 7u))
+        return PA_ERR_INVALID_ARG;
+    if (r->num_tokens > 1) {  // rows apart by whole 16-byte chunks, and not into one another
+        const int64_t per16 = 16 / elem_bytes(r->dtype);
+        const int64_t q_row = static_cast<int64_t>(r->num_q_heads) * r->head_dim;
+        const int64_t k_row = static_cast<int64_t>(r->num_kv_heads) * r->head_dim;
+        if (r->k_stride % per16 || r->v_stride % per16 || r->k_stride < k_row || r->v_stride < k_row) return PA_ERR_INVALID_ARG;
+        if (r->num_q_heads > 0 &&
+            (r->q_stride % per16 || r->q_out_stride % per16 || r->q_stride < q_row || r->q_out_stride < q_row))
+            return PA_ERR_INVALID_ARG;
+    }
+    RotateArgs a{};
+    a.q_out = r->q_out, a.q = r->q, a.k = r->k, a.v = r->v;
+    a.q_out_stride = r->q_out_stride, a.q_stride = r->q_stride, a.k_stride = r->k_stride, a.v_stride = r->v_stride;
+    a.positions = r->positions, a.cos_sin = r->cos_sin;
+    a.k_cache = r->k_cache, a.v_cache = r->v_cache, a.slot_mapping = r->slot_mapping;
+    a.num_positions = r->num_positions, a.rotary_dim = r->rotary_dim, a.num_tokens = r->num_tokens;
+    a.num_q_heads = r->num_q_heads, a.num_kv_heads = r->num_kv_heads, a.head_dim = r->head_dim;
+    a.num_blocks = r->num_blocks, a.bs_log2 = block_size_log2(r->block_size);
+    a.interleaved = r->interleaved != 0, a.fp4 = fp4, a.dtype = r->dtype;
+    a.k_unscale = fp4 ? 1.f / r->k_scale : 1.f, a.v_unscale = fp4 ? 1.f / r->v_scale : 1.f;
+    if (rotate_ctas(a) > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    a.err = dev->err;
+    const cudaError_t e = launch_rotate_and_cache(a, dev->info.num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t max_seq_len, pa_dtype dtype) {
+    if (check_attention_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, 1, max_seq_len / 16 + 1, max_seq_len,
+                              dtype, PA_BLOCK_SIZE) != PA_OK)
+        return 0;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return 0;
+    return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
+        .workspace_bytes;
+}
+
+PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale, float k_scale,
+                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    DecodeArgs a;
+    pa_status st = prepare_decode(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
+                                  max_seq_len, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale * k_scale,
+                                  dtype, workspace, workspace_bytes, &a);
+    if (st == PA_OK && (!factor_ok(k_scale) || !factor_ok(v_scale))) st = PA_ERR_INVALID_ARG;
+    if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
+    if (st != PA_OK || num_seqs == 0) return st;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    a.err = dev->err;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const ScoredSimtPlan plan =
+        plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+        return PA_ERR_INVALID_ARG;
+    return launch_fp4_decode_simt(a, v_scale, plan, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                                            pa_dtype dtype) {
+    if (check_attention_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, 1, max_seq_len / 16 + 1, max_seq_len,
+                              dtype, PA_BLOCK_SIZE) != PA_OK || max_chunk_len <= 0 ||
+        static_cast<int64_t>(num_seqs) * max_chunk_len > 0x7fffffffLL)
+        return 0;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return 0;
+    return plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                            dev->info.num_sms).workspace_bytes;
+}
+
+PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
+                                int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, float scale, float k_scale, float v_scale,
+                                pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    PrefillArgs a;
+    pa_status st = prepare_prefill(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens,
+                                   query_start_loc, num_seqs, max_chunk_len, max_seq_len, num_q_heads, num_kv_heads,
+                                   head_dim, num_blocks, block_size, scale * k_scale, dtype, &a);
+    if (st == PA_OK && (!factor_ok(k_scale) || !factor_ok(v_scale))) st = PA_ERR_INVALID_ARG;
+    if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
+    if (st != PA_OK || !prefill_has_work(a)) return st;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    a.err = dev->err;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const ScoredSimtPlan plan = plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                 max_seq_len, dev->info.num_sms);
+    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+        return PA_ERR_INVALID_ARG;
+    return launch_fp4_prefill_simt(a, v_scale, plan, workspace, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_gather_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int64_t* slots, int32_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t num_blocks, int32_t block_size, float k_scale, float v_scale, pa_dtype dtype,
+                               void* stream) {
+    if (num_slots < 0 || num_kv_heads <= 0 || num_blocks <= 0 || head_dim <= 0) return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(block_size)) return block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || !factor_ok(k_scale) || !factor_ok(v_scale)) return PA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(num_blocks) * num_kv_heads * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (num_slots == 0) return PA_OK;
+    if (!k_out || !v_out || !k_cache || !v_cache || !slots) return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return PA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_slots) * num_kv_heads * (head_dim / 16) > 0x7fffffffLL * 128) return PA_ERR_UNSUPPORTED;
+    DeviceCache* dev = nullptr;
+    if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    const GatherFp4Args a{k_out, v_out, k_cache, v_cache, slots, num_slots, num_kv_heads, head_dim, num_blocks,
+                          block_size_log2(block_size), k_scale, v_scale, dtype, dev->err};
+    return launch_gather_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 PA_API pa_status pa_move_blocks(void* const* pools, int32_t num_pools, int32_t num_kv_heads, int32_t head_dim,
                                 int32_t num_blocks, int32_t block_size, pa_dtype dtype, const int32_t* block_pairs,
                                 int32_t n_pairs, const int32_t* tokens, int32_t* block_table,
                                 int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, void* stream) {
     if (num_pools < 0 || n_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
     if (!block_size_ok(block_size)) return block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype)) return PA_ERR_INVALID_ARG;
-    const int64_t row_bytes = static_cast<int64_t>(head_dim) * elem_bytes(dtype);
-    if (row_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
-    const int64_t chunks = row_bytes / 16 * num_kv_heads * block_size;
+    if (!dtype_ok(dtype) && dtype != PA_FP4) return PA_ERR_INVALID_ARG;
+    const bool fp4 = dtype == PA_FP4;  // rows of 9/16 head_dim bytes, spread over their page: whole blocks only
+    if (fp4 && (tokens || (head_dim != 64 && head_dim != 128))) return PA_ERR_UNSUPPORTED;
+    const int64_t row_bytes = fp4 ? static_cast<int64_t>(head_dim) * 9 / 16 : static_cast<int64_t>(head_dim) * elem_bytes(dtype);
+    if (!fp4 && row_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
+    const int64_t chunks = row_bytes * block_size / 16 * num_kv_heads;
     if (chunks > 0x3fffffffLL) return PA_ERR_UNSUPPORTED;  // the copies count chunks in 32 bits, with room to step past the end
     if (block_table && (num_seqs < 0 || max_blocks_per_seq <= 0 || !seq_lens || !aligned4(block_table) || !aligned4(seq_lens)))
         return PA_ERR_INVALID_ARG;

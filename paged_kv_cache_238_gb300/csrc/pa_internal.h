@@ -255,6 +255,48 @@ cudaError_t launch_prefill_scored_tc(const PrefillArgs& a, const ScoreArgs& scor
                                      void* workspace, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
+// rotation of new tokens on their way into the pool; the 4-bit pool
+// ------------------------------------------------------------------------------------------
+// pa_rotate as the kernel takes it. Strides in elements between tokens.
+struct RotateArgs {
+    void* q_out;
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;
+    const int64_t* positions;
+    const float* cos_sin;  // [num_positions][rotary_dim]: cosines, then sines
+    void* k_cache;
+    void* v_cache;
+    const int64_t* slot_mapping;
+    int32_t num_positions, rotary_dim, num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks, bs_log2;
+    bool interleaved, fp4;
+    float k_unscale, v_unscale;  // 1 / the 4-bit pools' factors
+    pa_dtype dtype;
+    uint32_t* err;
+};
+int64_t rotate_ctas(const RotateArgs& a);  // CTAs of a call, at most
+cudaError_t launch_rotate_and_cache(const RotateArgs& a, int num_sms, cudaStream_t stream);
+
+struct GatherFp4Args {
+    void* k_out;
+    void* v_out;
+    const void* k_cache;
+    const void* v_cache;
+    const int64_t* slots;
+    int32_t num_slots, num_kv_heads, head_dim, num_blocks, bs_log2;
+    float k_scale, v_scale;
+    pa_dtype dtype;
+    uint32_t* err;
+};
+cudaError_t launch_gather_fp4(const GatherFp4Args& a, cudaStream_t stream);
+
+// Attention over 4-bit pools on the CUDA cores: the scored kernel without a score; k_scale is in a.scale.
+cudaError_t launch_fp4_decode_simt(const DecodeArgs& a, float v_scale, const ScoredSimtPlan& plan, cudaStream_t stream);
+cudaError_t launch_fp4_prefill_simt(const PrefillArgs& a, float v_scale, const ScoredSimtPlan& plan, void* workspace,
+                                    cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
 // move_blocks (page copies in every layer's pools, block tables rewritten)
 // ------------------------------------------------------------------------------------------
 constexpr int kMoveMaxPools = 256;  // pools of one launch (their pointers are kernel parameters)

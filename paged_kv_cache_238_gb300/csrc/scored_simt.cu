@@ -12,7 +12,8 @@
 // output) meet in shared memory, and partitions of a decode row's pages in the workspace, where the
 // last CTA to arrive merges them by the same rule:
 //   M = max_p m_p,  w_p = l_p 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p.
-// The pages are those of the rows' visible spans only, so a window or a document start costs no
+// Pages of a 4-bit pool (fp4.cuh) land as they are, and their warp unpacks them into the room of an ordinary
+// page, exactly, before it uses them. The pages are those of the rows' visible spans only, so a window or a document start costs no
 // reads outside them. A page that a span cuts is read; its keys that no row sees are skipped in V.
 //
 // Bound: for a few rows the chain launch, lengths, block ids, pages, join (about 5 us: 24 sequences of up
@@ -23,6 +24,7 @@
 
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "pa_internal.h"
 #include "scored.cuh"
 
@@ -95,6 +97,7 @@ struct SimtArgs {
     int32_t G, head_chunks, tokens, groups;  // q heads per kv head; chunks of R heads; tokens per CTA; CTAs per chunk
     int32_t part_pages, num_parts;
     float scale;
+    float v_scale;  // 4-bit pools: the V pool's factor
     ScoreArgs score;
     int32_t* counter;
     float* ws_o;
@@ -103,7 +106,7 @@ struct SimtArgs {
 };
 
 // Shared memory in bytes: q, weights and pages while pages are walked, then the warps' outputs.
-template <typename T, int D, int R, int kWarps>
+template <typename T, int D, int R, int kWarps, bool F4>
 struct Smem {
     static constexpr int pad = 16 / sizeof(T);  // rows 16 bytes apart in bank: a lane reads its own row
     static constexpr int q_stride = D + 4;      // two rows in a broadcast lie in different banks
@@ -114,19 +117,20 @@ struct Smem {
     static constexpr int page = corr + 4 * kWarps * R;     // [kWarps] K page, V page
     static constexpr int k_stride = D + pad;
     static constexpr int k_bytes = 16 * k_stride * static_cast<int>(sizeof(T));
-    static constexpr int page_bytes = k_bytes + 16 * D * static_cast<int>(sizeof(T));
+    static constexpr int raw = k_bytes + 16 * D * static_cast<int>(sizeof(T));  // 4-bit pools: K and V page as they lie there
+    static constexpr int page_bytes = raw + (F4 ? 2 * fp4_page_bytes(D) : 0);
     static constexpr int walk = page + kWarps * page_bytes, join = 4 * kWarps * R * D;
     static constexpr int bytes = walk > join ? walk : join;
     static_assert(kMaxParts * R * 8 <= bytes, "the merge's weights");
 };
 
-template <typename T, int D, int R, int kWarps>
+template <typename T, int D, int R, int kWarps, bool F4>
 __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict__ out, const T* __restrict__ q,
                                                                const T* __restrict__ k_cache,
                                                                const T* __restrict__ v_cache,
                                                                const __grid_constant__ SimtArgs a) {
     constexpr int E = D / 32, RL = R / 2, kThreads = 32 * kWarps;
-    using L = Smem<T, D, R, kWarps>;
+    using L = Smem<T, D, R, kWarps, F4>;
     extern __shared__ float4 smem4[];
     char* sm = reinterpret_cast<char*>(smem4);
     __shared__ KeySpans spans[R];
@@ -196,6 +200,7 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
     const int32_t* table = a.block_table + static_cast<int64_t>(s) * a.max_blocks;
     T* k_page = reinterpret_cast<T*>(sm + L::page + warp * L::page_bytes);
     T* v_page = k_page + 16 * L::k_stride;
+    uint8_t* const raw_page = reinterpret_cast<uint8_t*>(k_page) + L::raw;  // F4: K, then V
     auto block_of = [&](int32_t i) { return i < end ? __ldg(table + (pl.page(i) >> a.sub_log2)) : 0; };
     auto in_pool = [&](int32_t block) { return block >= 0 && block < a.num_blocks; };
     // copy list page i of this warp, in this block, from a cache: 16 rows of D elements
@@ -203,12 +208,37 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
         if (i < end && in_pool(block)) {
             const int64_t row = ((static_cast<int64_t>(block) * a.num_kv_heads + hk) << a.sub_log2) +
                                 (pl.page(i) & ((1 << a.sub_log2) - 1));
-            const T* src = cache + row * (kPageTokens * D);
-            constexpr int kN = 16 / sizeof(T), kChunks = D / kN;  // 16-byte chunks of a row
+            if constexpr (F4) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(cache) + row * fp4_page_bytes(D);
+                uint8_t* to = raw_page + (dst == v_page ? fp4_page_bytes(D) : 0);
 #pragma unroll
-            for (int c = lane; c < 16 * kChunks; c += 32) cp_async16(dst + c / kChunks * stride + c % kChunks * kN, src + c * kN);
+                for (int c = lane; c < fp4_page_bytes(D) / 16; c += 32) cp_async16(to + c * 16, src + c * 16);
+            } else {
+                const T* src = cache + row * (kPageTokens * D);
+                constexpr int kN = 16 / sizeof(T), kChunks = D / kN;  // 16-byte chunks of a row
+#pragma unroll
+                for (int c = lane; c < 16 * kChunks; c += 32) cp_async16(dst + c / kChunks * stride + c % kChunks * kN, src + c * kN);
+            }
         }
         cp_async_commit();
+    };
+    // F4: the page that has landed, as values of T times factor: a lane takes 8 dims of a key at a time
+    auto unpack = [&](T* dst, int32_t stride, float factor) {
+        const uint8_t* raw = raw_page + (dst == v_page ? fp4_page_bytes(D) : 0);
+#pragma unroll
+        for (int c = lane; c < 2 * D; c += 32) {
+            const int key_row = c / (D / 8), d = c % (D / 8) * 8;
+            const float s = halves_to_floats(e4m3x2_halves(raw[fp4_scales_at(D) + key_row * (D / 16) + d / 16])).x * factor;
+            uint32_t h[4];
+            fp4_halves(reinterpret_cast<const uint32_t*>(raw)[c], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = halves_to_floats(h[e]);
+                T* to = dst + key_row * stride + d + 2 * e;
+                to[0] = narrow<T>(x.x * s), to[1] = narrow<T>(x.y * s);
+            }
+        }
+        __syncwarp();
     };
     int32_t block = block_of(first), block_next = block_of(first + kWarps);
     fetch(k_cache, k_page, L::k_stride, first, block);
@@ -248,6 +278,9 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
         else if (lane == 0) raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
         cp_async_wait<1>();
         __syncwarp();
+        if constexpr (F4) {
+            if (seen) unpack(k_page, L::k_stride, 1.f);
+        }
         // ---- scores of (key, rows hh RL + i) ----
         float z[RL];
         if (seen) {
@@ -362,6 +395,7 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
         cp_async_wait<1>();
         __syncwarp();
         if (seen) {
+            if constexpr (F4) unpack(v_page, D, a.v_scale);
             if (seen != 0xffffu) {  // keys that no row sees: their weights are 0, their V may be anything
                 for (uint32_t w = ~seen & 0xffffu; w != 0u; w &= w - 1)
 #pragma unroll
@@ -504,12 +538,12 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
     }
 }
 
-template <typename T, int D, int R, int kWarps>
+template <typename T, int D, int R, int kWarps, bool F4>
 cudaError_t launch_rows(void* out, const void* q, const void* k, const void* v, const SimtArgs& a, dim3 grid,
                         cudaStream_t stream) {
-    constexpr int bytes = Smem<T, D, R, kWarps>::bytes;
+    constexpr int bytes = Smem<T, D, R, kWarps, F4>::bytes;
     if (bytes > 40960) {  // with the static part, beyond what every kernel may use
-        const cudaError_t e = allow_smem<scored_simt_kernel<T, D, R, kWarps>>(bytes);
+        const cudaError_t e = allow_smem<scored_simt_kernel<T, D, R, kWarps, F4>>(bytes);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr[1];
@@ -522,11 +556,11 @@ cudaError_t launch_rows(void* out, const void* q, const void* k, const void* v, 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_simt_kernel<T, D, R, kWarps>, static_cast<T*>(out), static_cast<const T*>(q),
+    return cudaLaunchKernelEx(&cfg, scored_simt_kernel<T, D, R, kWarps, F4>, static_cast<T*>(out), static_cast<const T*>(q),
                               static_cast<const T*>(k), static_cast<const T*>(v), a);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool F4>
 cudaError_t launch_impl(void* out, const void* q, const void* k, const void* v, SimtArgs& a, const ScoredSimtPlan& p,
                         void* workspace, cudaStream_t stream) {
     a.head_chunks = p.head_chunks;
@@ -540,15 +574,15 @@ cudaError_t launch_impl(void* out, const void* q, const void* k, const void* v, 
         a.ws_ml = a.ws_o + static_cast<size_t>(p.grid_x) * a.num_kv_heads * p.head_chunks * p.rows * p.num_parts * D;
     }
     const dim3 grid(p.grid_x, a.num_kv_heads * a.head_chunks, a.num_parts);
-    if (p.rows == kFewRows) return launch_rows<T, D, kFewRows, 8>(out, q, k, v, a, grid, stream);
-    return p.warps == 8 ? launch_rows<T, D, kManyRows, 8>(out, q, k, v, a, grid, stream)
-                        : launch_rows<T, D, kManyRows, 4>(out, q, k, v, a, grid, stream);
+    if (p.rows == kFewRows) return launch_rows<T, D, kFewRows, 8, F4>(out, q, k, v, a, grid, stream);
+    return p.warps == 8 ? launch_rows<T, D, kManyRows, 8, F4>(out, q, k, v, a, grid, stream)
+                        : launch_rows<T, D, kManyRows, 4, F4>(out, q, k, v, a, grid, stream);
 }
 
-template <typename A>
+template <bool F4, typename A>
 cudaError_t launch_any(const A& d, SimtArgs& a, const ScoredSimtPlan& p, void* workspace, cudaStream_t stream) {
     auto run = [&](auto type, auto dim) {
-        return launch_impl<decltype(type), decltype(dim)::value>(d.out, d.q, d.k_cache, d.v_cache, a, p, workspace, stream);
+        return launch_impl<decltype(type), decltype(dim)::value, F4>(d.out, d.q, d.k_cache, d.v_cache, a, p, workspace, stream);
     };
     using D128 = std::integral_constant<int, 128>;
     using D64 = std::integral_constant<int, 64>;
@@ -614,7 +648,7 @@ ScoredSimtPlan plan_scored_simt(int32_t S, int32_t max_chunk, int32_t Hq, int32_
 cudaError_t launch_scored_decode_simt(const DecodeArgs& d, const ScoreArgs& score, const ScoredSimtPlan& plan,
                                       cudaStream_t stream) {
     SimtArgs a = common_args(d, score);
-    return launch_any(d, a, plan, d.workspace, stream);
+    return launch_any<false>(d, a, plan, d.workspace, stream);
 }
 
 cudaError_t launch_scored_prefill_simt(const PrefillArgs& p, const ScoreArgs& score, const ScoredSimtPlan& plan,
@@ -622,7 +656,22 @@ cudaError_t launch_scored_prefill_simt(const PrefillArgs& p, const ScoreArgs& sc
     SimtArgs a = common_args(p, score);
     a.query_start_loc = p.query_start_loc;
     a.max_chunk = p.max_chunk_len;
-    return launch_any(p, a, plan, workspace, stream);
+    return launch_any<false>(p, a, plan, workspace, stream);
+}
+
+cudaError_t launch_fp4_decode_simt(const DecodeArgs& d, float v_scale, const ScoredSimtPlan& plan, cudaStream_t stream) {
+    SimtArgs a = common_args(d, ScoreArgs{});
+    a.v_scale = v_scale;
+    return launch_any<true>(d, a, plan, d.workspace, stream);
+}
+
+cudaError_t launch_fp4_prefill_simt(const PrefillArgs& p, float v_scale, const ScoredSimtPlan& plan, void* workspace,
+                                    cudaStream_t stream) {
+    SimtArgs a = common_args(p, ScoreArgs{});
+    a.v_scale = v_scale;
+    a.query_start_loc = p.query_start_loc;
+    a.max_chunk = p.max_chunk_len;
+    return launch_any<true>(p, a, plan, workspace, stream);
 }
 
 }  // namespace pa
