@@ -706,6 +706,9 @@ PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads
         return 0;
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return 0;
+    DecodeScoredPlan plan;
+    if (dtype == PA_BF16 && plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &plan))
+        return plan.workspace_bytes;
     return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
         .workspace_bytes;
 }
@@ -726,6 +729,12 @@ PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, co
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DecodeScoredPlan fast;
+    if (dtype == PA_BF16 &&
+        plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &fast)) {
+        if (!workspace || workspace_bytes < fast.workspace_bytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+        return launch_decode_fp4(a, v_scale, fast, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     const ScoredSimtPlan plan =
         plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))

@@ -291,6 +291,11 @@ struct GatherFp4Args {
 };
 cudaError_t launch_gather_fp4(const GatherFp4Args& a, cudaStream_t stream);
 
+// Decode over 4-bit pools, bf16 queries (decode_fp4.cu); k_scale is in a.scale.
+bool plan_decode_fp4(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                     const DeviceInfo& dev, DecodeScoredPlan* plan);
+cudaError_t launch_decode_fp4(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream);
+
 // Attention over 4-bit pools on the CUDA cores: the scored kernel without a score; k_scale is in a.scale.
 cudaError_t launch_fp4_decode_simt(const DecodeArgs& a, float v_scale, const ScoredSimtPlan& plan, cudaStream_t stream);
 cudaError_t launch_fp4_prefill_simt(const PrefillArgs& a, float v_scale, const ScoredSimtPlan& plan, void* workspace,
