@@ -24,6 +24,8 @@
 // Bound: see the figures at plan_decode_fp4.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fp4.cuh"
 #include "pa_internal.h"
 #include "scored.cuh"
@@ -38,25 +40,26 @@ constexpr int kMinSlice = 4;    // units of a CTA's slice, at least
 constexpr float kJoinWeight = 1.f / 1.5f;  // a segment of n units is cut into about sqrt(1.5 n) pieces at most
 constexpr int kSegmentUnits = 1;           // a segment's start and end weigh as much as this many pages
 constexpr float kLag = 8.f;                // log2 units; weights stay below 2^8, within fp16
+constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
 
-// Pages of one step of a warp.
-__host__ __device__ constexpr int step_pages(int D) { return 256 / D; }
+constexpr int kStepPages = 4;              // pages of one step of a warp
 __host__ __device__ inline uint32_t up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
-    uint32_t stage, ring, piece0, piece_ml, weight, meta, bars, flags, prefix, lens, total;
+    uint32_t ring_bytes, ring, piece0, piece_ml, weight, meta, bars, flags, prefix, lens, total;
 };
-// NW warps, nst stages, hs q heads per segment, S sequences.
-__host__ __device__ inline Layout layout(int NW, int nst, int hs, int D, int S) {
+// NW warps, hs q heads per segment, S sequences.
+__host__ __device__ inline Layout layout(int NW, int hs, int D, int S) {
     Layout l;
     uint32_t o = 0;
-    l.stage = up(2u * fp4_page_bytes(D) * step_pages(D) + static_cast<uint32_t>(hs) * D * 2u, 128u);  // pages, query rows
-    l.ring = o;      o += static_cast<uint32_t>(NW) * nst * l.stage;
+    const uint32_t pages = 2u * fp4_page_bytes(D) * kStepPages, piece = static_cast<uint32_t>(hs) * D * 4u;
+    l.ring_bytes = pages > piece ? pages : piece;  // a step's K pages, its V pages; in the end the warp's last piece
+    l.ring = o;      o += static_cast<uint32_t>(NW) * l.ring_bytes;
     l.piece0 = o;    o += static_cast<uint32_t>(NW) * hs * D * 4u;       // each warp's first piece
     l.piece_ml = o;  o += static_cast<uint32_t>(NW) * 2u * hs * 8u;      // (max, sum) of both pieces
     l.weight = o;    o += static_cast<uint32_t>(NW) * 2u * hs * 12u;     // the pieces' weights, and (max, sum) of their run
     l.meta = up(o, 16u);  o = l.meta + static_cast<uint32_t>(NW) * 2u * 16u;  // segment of each piece
-    l.bars = up(o, 16u);  o = l.bars + static_cast<uint32_t>(NW) * nst * 8u;
+    l.bars = up(o, 16u);  o = l.bars + static_cast<uint32_t>(NW) * 2u * 8u;
     l.flags = o;     o += 32u;
     l.prefix = up(o, 16u);  o = l.prefix + up((S + 1) * 4u, 16u);
     l.lens = o;      o += static_cast<uint32_t>(S) * 4u;
@@ -71,7 +74,7 @@ struct Params {
     const uint8_t* v_cache;
     const int32_t* block_table;
     const int32_t* seq_lens;
-    int32_t max_blocks, S, num_kv_heads, G, head_chunks, num_blocks, sub_log2, cap_tokens, nst;
+    int32_t max_blocks, S, num_kv_heads, G, head_chunks, num_blocks, sub_log2, cap_tokens;
     float c1;          // scale log2 e
     float v_scale;
     int32_t* counter;  // [kScoredSegments] CTA pieces finished per segment; zero between calls
@@ -88,12 +91,30 @@ __device__ __forceinline__ void bulk_copy_g2s(void* smem_dst, const void* src, u
         "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void bulk_copy_g2s(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
 }
 
 // D = A(16x16, row) * B(16x8, col) + D, fp16 inputs, fp32 accumulators.
@@ -107,6 +128,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
 
@@ -126,8 +157,11 @@ __device__ __forceinline__ int32_t find_seq(const int32_t* prefix, int32_t S, in
 // Position in the work list: sequence s, its segment h of nh, unit j: page j of np, or, from np on, one
 // of the kSegmentUnits units without a page that stand for what a segment costs besides its pages.
 struct Cursor {
-    int32_t s, h, j, np;
-    __device__ __forceinline__ void load(const int32_t* lens) { np = (lens[s] + kPageTokens - 1) / kPageTokens; }
+    int32_t s, h, j, np, len;
+    __device__ __forceinline__ void load(const int32_t* lens) {
+        len = lens[s];
+        np = (len + kPageTokens - 1) / kPageTokens;
+    }
     __device__ __forceinline__ void at(const int32_t* prefix, const int32_t* lens, int32_t S, int32_t u) {
         s = find_seq(prefix, S, u);
         load(lens);
@@ -156,13 +190,13 @@ template <int D, int NW, int NH>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_fp4_kernel(const __grid_constant__ Params a) {
     constexpr uint32_t kPage = fp4_page_bytes(D), kScales = fp4_scales_at(D);
-    constexpr int KS = D / 16, NMT = D / 16, SP = step_pages(D), DL = D / 8;  // DL: dims of a lane's V rows
+    constexpr int KS = D / 16, NMT = D / 16, SP = kStepPages, DL = D / 8;  // DL: dims of a lane's V rows
     constexpr int NTH = NW * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    const int32_t S = a.S, G = a.G, nst = a.nst, NHC = a.head_chunks, Hq = G * a.num_kv_heads;
+    const int32_t S = a.S, G = a.G, NHC = a.head_chunks, Hq = G * a.num_kv_heads;
     const int32_t hs = min(G, kMaxHeads), nh = a.num_kv_heads * NHC;  // heads and segments per sequence
-    const Layout L = layout(NW, nst, hs, D, S);
+    const Layout L = layout(NW, hs, D, S);
     float* piece0 = reinterpret_cast<float*>(smem + L.piece0);
     float2* piece_ml = reinterpret_cast<float2*>(smem + L.piece_ml);
     Piece* meta = reinterpret_cast<Piece*>(smem + L.meta);  // [2 NW]
@@ -180,7 +214,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     if (lane == 0) {
         meta[warp * 2].seg = meta[warp * 2 + 1].seg = -1;
-        for (int i = 0; i < nst; ++i) mbar_init(&bars_all[warp * nst + i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars_all[warp * 2 + i], 1);
         fence_mbarrier_init();
     }
     // A programmatic launch: everything above ran beside the tail of the kernel before this one;
@@ -240,19 +274,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int32_t u0 = static_cast<int32_t>(first), u1 = min(U, u0 + chunk);
     const int32_t per_warp = (u1 - u0 + NW - 1) / NW;
     const int32_t a_w = u0 + warp * per_warp, n = max(0, min(u1 - a_w, per_warp));
-    uint8_t* ring = smem + L.ring + static_cast<uint32_t>(warp) * nst * L.stage;
+    uint8_t* ring = smem + L.ring + static_cast<uint32_t>(warp) * L.ring_bytes;
     const uint32_t ring_u32 = smem_u32(ring);
-    uint64_t* bars = bars_all + warp * nst;
+    uint64_t* bars = bars_all + warp * 2;  // a step's K has landed, its V
     const int32_t gid = lane >> 2, tig = lane & 3;
 
     if (n > 0) {
-        int32_t t_i = 0, k_i = 0;  // pages and steps issued
-        // Page in the pool of unit a_w + 32 k + lane.
+        // Page in the pool of unit a_w + 32 k + lane; -1: a unit without one.
         auto lane_page = [&](int32_t k) -> int32_t {
-            if (32 * k + lane >= n) return 0;
+            if (32 * k + lane >= n) return -1;
             Cursor c;
             c.at(prefix, lens, S, a_w + 32 * k + lane);
-            if (c.j >= c.np) return 0;
+            if (c.j >= c.np) return -1;
             int32_t phys = __ldg(a.block_table + static_cast<int64_t>(c.s) * a.max_blocks + (c.j >> a.sub_log2));
             if (phys < 0 || phys >= a.num_blocks) {
                 raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
@@ -260,60 +293,44 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
             return ((phys * a.num_kv_heads + c.h / NHC) << a.sub_log2) + (c.j & ((1 << a.sub_log2) - 1));
         };
-        int32_t kc = 0, id_cur = lane_page(0), id_nxt = 0;
         // pages are read once per call: let them leave L2 first
         const uint64_t kv_policy = l2_policy_evict_first();
-        Cursor wi;
-        wi.at(prefix, lens, S, a_w);
-        // Step k_i (pages t_i .. of one segment, up to SP) into stage k_i % nst. Lane 2 i + kv copies the
-        // K (kv = 0) or V of page i, lane 31 the query rows of a segment that begins here.
-        bool q_due = true;  // the segment's query rows have not been copied yet
-        auto next_block_ids = [&]() {
-            if ((t_i >> 5) > kc) {  // the next 32 block ids, fetched while these are used
-                ++kc;
-                id_cur = id_nxt;
-                id_nxt = 32 * (kc + 1) < n ? lane_page(kc + 1) : 0;
-            }
-        };
-        auto skip = [&]() {  // to the next page of the part
-            while (t_i < n && wi.j >= wi.np) {
-                const int32_t none = min(wi.np + kSegmentUnits - wi.j, n - t_i);
-                wi.advance(none, prefix, lens, S, nh);
-                t_i += none;
-                q_due = true;
-                next_block_ids();
-            }
-        };
-        auto issue = [&]() {
-            const int32_t cnt = min(min(SP, wi.np - wi.j), n - t_i), st = k_i % nst;
-            uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
-            const bool seg_first = q_due;
-            const int32_t hk = wi.h / NHC, g0 = (wi.h - hk * NHC) * kMaxHeads;
-            const uint32_t qbytes = static_cast<uint32_t>(min(G - g0, kMaxHeads)) * D * 2u;
-            const int32_t pg = t_i + (lane >> 1);
-            const int32_t r0 = __shfl_sync(0xffffffffu, id_cur, pg & 31), r1 = __shfl_sync(0xffffffffu, id_nxt, pg & 31);
-            const bool go = !*abort_flag;
-            if (lane == 0 && go)
-                mbar_arrive_expect_tx(&bars[st], static_cast<uint32_t>(cnt) * 2u * kPage + (seg_first ? qbytes : 0u));
+        // Step i holds units SP i .. of the part; lane x < SP copies the K or V page of unit x into its place. There is
+        // room for one step: the next one's K is sent for when this one's scores are done, its V at the step's end.
+        // Block ids come 32 units at a time, the next 32 on their way while these are used.
+        int32_t k_steps = 0, v_steps = 0, id_cur = lane_page(0), id_nxt = n > 32 ? lane_page(1) : -1, step_id = -1;
+        auto send = [&](const uint8_t* pool, uint8_t* to, uint64_t* bar) {
+            const bool mine = lane < SP && step_id >= 0 && !*abort_flag;
+            const uint32_t copies = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copies) * kPage);
             __syncwarp();
-            if (lane < 2 * cnt && go) {
-                const uint8_t* pool = (lane & 1) ? a.v_cache : a.k_cache;
-                bulk_copy_g2s(stage + static_cast<uint32_t>(lane) * kPage,
-                              pool + static_cast<int64_t>((pg >> 5) == kc ? r0 : r1) * kPage, kPage, &bars[st], kv_policy);
-            }
-            if (lane == 31 && seg_first && go)
-                bulk_copy_g2s(stage + 2u * kPage * SP, a.q + (static_cast<int64_t>(wi.s) * Hq + hk * G + g0) * D, qbytes,
-                              &bars[st]);
-            wi.advance(cnt, prefix, lens, S, nh);
-            t_i += cnt;
-            ++k_i;
-            q_due = false;
-            next_block_ids();
-            skip();
+            if (mine) bulk_copy_g2s(to + lane * kPage, pool + static_cast<int64_t>(step_id) * kPage, kPage, bar, kv_policy);
         };
-        if (n > 32) id_nxt = lane_page(1);
-        skip();
-        for (int32_t i = 0; i < nst && t_i < n; ++i) issue();
+        auto send_k = [&]() {
+            step_id = __shfl_sync(0xffffffffu, id_cur, (k_steps * SP + lane) & 31);
+            send(a.k_cache, ring, &bars[0]);
+            ++k_steps;
+            if (((k_steps * SP) & 31) == 0) {
+                id_cur = id_nxt;
+                const int32_t k = k_steps * SP / 32 + 1;
+                id_nxt = 32 * k < n ? lane_page(k) : -1;
+            }
+        };
+        auto send_v = [&]() {
+            send(a.v_cache, ring + SP * kPage, &bars[1]);
+            ++v_steps;
+        };
+        send_k();
+        send_v();
+        auto landed = [&](uint64_t* bar, int32_t step) {
+            if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(step) & 1u, abort_flag))) return true;
+            if (lane == 0) {
+                if (!*abort_flag) raise_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+            return false;
+        };
 
         Cursor wc;
         wc.at(prefix, lens, S, a_w);
@@ -325,146 +342,99 @@ __global__ void __launch_bounds__(NW * 32, 1)
         float acc[NH][NMT][4], mh[NH][2], lh[NH][2], c1[NH][2];
         int32_t ng = 0, head0 = 0;
         bool cut_left = false;
-        int32_t k = 0;  // steps consumed
         bool first_page = true;  // of a segment in this part
         const int32_t key_a = key_of(gid);  // and key_a + 8
-        for (int32_t t = 0; t < n;) {
-            if (wc.j >= wc.np) {  // units without a page
-                const int32_t none = min(wc.np + kSegmentUnits - wc.j, n - t);
-                wc.advance(none, prefix, lens, S, nh);
-                t += none;
-                first_page = true;
-                continue;
-            }
-            const int32_t st = k % nst, cnt = min(min(SP, wc.np - wc.j), n - t);
-            const bool landed = mbar_wait_bounded(&bars[st], static_cast<uint32_t>(k / nst) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, landed)) {
-                if (lane == 0) {
-                    if (!*abort_flag) raise_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
-                    *abort_flag = 1;
+        const float hidden = a.c1 < 0.f ? INFINITY : -INFINITY;  // a raw score whose weight is 0
+        // this lane's places: K's codes and scales, V's
+        const uint32_t at_k = ring_u32 + key_a * (D / 2) + tig * (D / 8);
+        const uint32_t at_ks = ring_u32 + kScales + key_a * (D / 16) + tig * (D / 64);
+        const uint32_t at_v = ring_u32 + SP * kPage + tig * (D / 2) + gid * (D / 16);
+        const uint32_t at_vs = ring_u32 + SP * kPage + kScales + tig * (D / 16) + gid * DL / 16;
+        // Pages slot .. of the step (`pages` of them, `left` keys from the first on). next: the step's last pages, and
+        // another step follows, whose K is sent for behind the scores and whose V at the end. False: a wait gave up.
+        auto attend = [&](auto pages, int32_t slot, int32_t left, bool wait_v, bool next) -> bool {
+            constexpr int NP = decltype(pages)::value;
+            const bool masked = left < NP * kPageTokens;
+            // ---- S^T = K Q^T ----
+            float sc[NP][NH][4];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                constexpr int WK = D / 32;  // words of a lane's dims of a key
+                const uint32_t page = (slot + i) * kPage;
+                uint32_t w0[WK], w1[WK], s0, s1;
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(at_k + page), y = lds128(at_k + page + 8 * (D / 2));
+                    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+                    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+                    s0 = e4m3x2_halves(lds16(at_ks + page));
+                    s1 = e4m3x2_halves(lds16(at_ks + page + 8 * (D / 16)));
+                } else {
+                    const uint2 x = lds64(at_k + page), y = lds64(at_k + page + 8 * (D / 2));
+                    w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
+                    s0 = e4m3x2_halves(static_cast<uint16_t>(lds8(at_ks + page)));
+                    s1 = e4m3x2_halves(static_cast<uint16_t>(lds8(at_ks + page + 8 * (D / 16))));
                 }
-                __syncwarp();
-                break;
-            }
-            ++k;
-            const uint8_t* stage = ring + static_cast<uint32_t>(st) * L.stage;
-            if (first_page) {  // a new segment: its query rows came with this step
-                first_page = false;
-                const int32_t hk = wc.h / NHC, g0 = (wc.h - hk * NHC) * kMaxHeads;
-                ng = min(G - g0, kMaxHeads);
-                head0 = hk * G + g0;
-                const uint8_t* qs = stage + 2u * kPage * SP;
-#pragma unroll
-                for (int f = 0; f < NH; ++f) {
-                    const bool valid = f * 8 + gid < ng;
-                    // the row to fp16: times 2^-e with 2^e <= its largest magnitude < 2^(e + 1)
-                    uint32_t raw[KS][2];
-                    float top = 0.f;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ks += 2) {
-                        const uint4 w = valid ? *reinterpret_cast<const uint4*>(qs + ((f * 8 + gid) * D + tig * (D / 4) + 4 * ks) * 2)
-                                              : make_uint4(0u, 0u, 0u, 0u);
-                        raw[ks][0] = w.x, raw[ks][1] = w.y, raw[ks + 1][0] = w.z, raw[ks + 1][1] = w.w;
-                    }
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[ks][x] << 16)), fabsf(__uint_as_float(raw[ks][x] & 0xffff0000u))));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
-                    const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;  // (not finite: as it is)
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    const float up2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            qb[f][ks][x] = pack_halves(__uint_as_float(raw[ks][x] << 16) * down,
-                                                       __uint_as_float(raw[ks][x] & 0xffff0000u) * down);
-#pragma unroll
-                    for (int mt = 0; mt < NMT; ++mt) acc[f][mt][0] = acc[f][mt][1] = acc[f][mt][2] = acc[f][mt][3] = 0.f;
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        mh[f][hh] = -INFINITY;
-                        lh[f][hh] = 0.f;
-                        c1[f][hh] = a.c1 * __shfl_sync(0xffffffffu, up2, (2 * tig + hh) * 4);
-                    }
-                }
-                cut_left = wc.j > 0;
-            }
-            // scores of the step's pages
-            const int32_t left = lens[wc.s] - wc.j * kPageTokens;  // keys from the step's first page on
-            float sc[SP][NH][4], mx[NH][2];
-#pragma unroll
-            for (int f = 0; f < NH; ++f) mx[f][0] = mx[f][1] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < SP; ++i) {
-                const uint8_t* page = stage + 2u * i * kPage;
 #pragma unroll
                 for (int f = 0; f < NH; ++f) sc[i][f][0] = sc[i][f][1] = sc[i][f][2] = sc[i][f][3] = 0.f;
-                if (i < cnt) {  // S^T = K Q^T
-                    constexpr int WK = D / 32;  // words of a lane's dims of a key
-                    uint32_t w0[WK], w1[WK], s0, s1;
-                    if constexpr (D == 128) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(page + key_a * 64 + tig * 16);
-                        const uint4 y = *reinterpret_cast<const uint4*>(page + (key_a + 8) * 64 + tig * 16);
-                        w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-                        w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-                        s0 = e4m3x2_halves(*reinterpret_cast<const uint16_t*>(page + kScales + key_a * 8 + tig * 2));
-                        s1 = e4m3x2_halves(*reinterpret_cast<const uint16_t*>(page + kScales + (key_a + 8) * 8 + tig * 2));
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(page + key_a * 32 + tig * 8);
-                        const uint2 y = *reinterpret_cast<const uint2*>(page + (key_a + 8) * 32 + tig * 8);
-                        w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
-                        s0 = e4m3x2_halves(page[kScales + key_a * 4 + tig]);
-                        s1 = e4m3x2_halves(page[kScales + (key_a + 8) * 4 + tig]);
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {  // two k16 steps
+                    const uint32_t pick = w < 2 ? 0x1010u : 0x3232u;
+                    const uint32_t m0 = __byte_perm(s0, 0u, pick), m1 = __byte_perm(s1, 0u, pick);
+                    uint32_t h0[4], h1[4];
+                    fp4_halves(w0[w], h0);
+                    fp4_halves(w1[w], h1);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t fa[4] = {hmul2(h0[2 * x], m0), hmul2(h1[2 * x], m1), hmul2(h0[2 * x + 1], m0),
+                                                hmul2(h1[2 * x + 1], m1)};
+#pragma unroll
+                        for (int f = 0; f < NH; ++f) mma_f16(sc[i][f], fa, qb[f][2 * w + x][0], qb[f][2 * w + x][1]);
                     }
-#pragma unroll
-                    for (int w = 0; w < WK; ++w) {  // two k16 steps
-                        const uint32_t pick = w < 2 ? 0x1010u : 0x3232u;
-                        const uint32_t m0 = __byte_perm(s0, 0u, pick), m1 = __byte_perm(s1, 0u, pick);
-                        uint32_t h0[4], h1[4];
-                        fp4_halves(w0[w], h0);
-                        fp4_halves(w1[w], h1);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t fa[4] = {hmul2(h0[2 * x], m0), hmul2(h1[2 * x], m1), hmul2(h0[2 * x + 1], m0),
-                                                    hmul2(h1[2 * x + 1], m1)};
-#pragma unroll
-                            for (int f = 0; f < NH; ++f) mma_f16(sc[i][f], fa, qb[f][2 * w + x][0], qb[f][2 * w + x][1]);
-                        }
-                    }
-                }
-                const bool see0 = i * kPageTokens + key_a < left && i < cnt, see1 = i * kPageTokens + key_a + 8 < left && i < cnt;
-#pragma unroll
-                for (int f = 0; f < NH; ++f) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[i][f][e] = (e < 2 ? see0 : see1) ? sc[i][f][e] * c1[f][e & 1] : -INFINITY;
-                    mx[f][0] = fmaxf(mx[f][0], fmaxf(sc[i][f][0], sc[i][f][2]));
-                    mx[f][1] = fmaxf(mx[f][1], fmaxf(sc[i][f][1], sc[i][f][3]));
                 }
             }
-            // the references move where a score exceeds one by more than kLag
-            bool grow = false;
+            if (next) {  // K has been read
+                __syncwarp();
+                send_k();
+            }
+            if (masked) {
 #pragma unroll
-            for (int f = 0; f < NH; ++f) grow |= mx[f][0] > mh[f][0] + kLag || mx[f][1] > mh[f][1] + kLag;
-            if (__any_sync(0xffffffffu, grow)) {
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
+                    for (int e = 0; e < 4; ++e)
+                        if (i * kPageTokens + key_a + 4 * (e & 2) >= left)
 #pragma unroll
-                    for (int f = 0; f < NH; ++f) {
-                        mx[f][0] = fmaxf(mx[f][0], __shfl_xor_sync(0xffffffffu, mx[f][0], off));
-                        mx[f][1] = fmaxf(mx[f][1], __shfl_xor_sync(0xffffffffu, mx[f][1], off));
-                    }
+                            for (int f = 0; f < NH; ++f) sc[i][f][e] = hidden;
+            }
+            // ---- weights 2^(score - reference); the references move where a score exceeds one by more than kLag ----
+            float x[NP][NH][4], top = -INFINITY;
+            auto shifted = [&]() {
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int f = 0; f < NH; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            unpack2(fma2(pack2(sc[i][f][e], sc[i][f][e + 1]), pack2(c1[f][0], c1[f][1]), pack2(-mh[f][0], -mh[f][1])),
+                                    x[i][f][e], x[i][f][e + 1]);
+            };
+            shifted();
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int f = 0; f < NH; ++f) top = max3(max3(top, x[i][f][0], x[i][f][1]), x[i][f][2], x[i][f][3]);
+            if (__any_sync(0xffffffffu, top > kLag)) {
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
                     float cc[2];
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const float mn = fmaxf(mh[f][hh], mx[f][hh]);
-                        cc[hh] = exp2_approx(mh[f][hh] - (mn == -INFINITY ? 0.f : mn));
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) mx = max3(mx, sc[i][f][hh] * c1[f][hh], sc[i][f][2 + hh] * c1[f][hh]);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        const float mn = fmaxf(mh[f][hh], mx);
+                        cc[hh] = exp2_approx(mh[f][hh] - mn);
                         mh[f][hh] = mn;
                         lh[f][hh] *= cc[hh];
                     }
@@ -476,46 +446,46 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         acc[f][mt][3] *= cc[1];
                     }
                 }
+                shifted();
             }
-            uint32_t pb[SP][NH][2];
+            uint32_t pb[NP][NH][2];
 #pragma unroll
-            for (int f = 0; f < NH; ++f) {
-                float ref[2];
+            for (int i = 0; i < NP; ++i)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) ref[hh] = mh[f][hh] == -INFINITY ? 0.f : mh[f][hh];
-#pragma unroll
-                for (int i = 0; i < SP; ++i) {
+                for (int f = 0; f < NH; ++f) {
                     float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = exp2_approx(sc[i][f][e] - ref[e & 1]);
-                    lh[f][0] += p[0] + p[2];
-                    lh[f][1] += p[1] + p[3];
+                    for (int e = 0; e < 4; ++e) p[e] = exp2_approx(x[i][f][e]);
+                    uint64_t l2 = pack2(lh[f][0], lh[f][1]);
+                    l2 = add2(add2(l2, pack2(p[0], p[1])), pack2(p[2], p[3]));
+                    unpack2(l2, lh[f][0], lh[f][1]);
                     pb[i][f][0] = movmatrix_trans(pack_halves(p[0], p[1]));
                     pb[i][f][1] = movmatrix_trans(pack_halves(p[2], p[3]));
                 }
-            }
-            // O^T += V^T P^T
+            // ---- O^T += V^T P^T ----
+            if (wait_v && !landed(&bars[1], v_steps - 1)) return false;
 #pragma unroll
-            for (int i = 0; i < SP; ++i) {
-                if (i >= cnt) break;
-                const uint8_t* page = stage + (2u * i + 1u) * kPage;
+            for (int i = 0; i < NP; ++i) {
                 constexpr int WV = D / 64;  // words of a lane's dims of a key
+                const uint32_t page = (slot + i) * kPage;
                 uint32_t w[4][WV], sb[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int32_t key = tig + 4 * x;
+                for (int x = 0; x < 4; ++x) {  // key tig + 4 x
                     if constexpr (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(page + key * 64 + gid * 8);
+                        const uint2 v = lds64(at_v + page + 4 * x * (D / 2));
                         w[x][0] = v.x, w[x][1] = v.y;
                     } else {
-                        w[x][0] = *reinterpret_cast<const uint32_t*>(page + key * 32 + gid * 4);
+                        w[x][0] = lds32(at_v + page + 4 * x * (D / 2));
                     }
-                    sb[x] = page[kScales + key * (D / 16) + gid * DL / 16];
-                    // a key past the end may hold anything, a scale of NaN too; codes are numbers
-                    if (i * kPageTokens + key >= left) sb[x] = 0u;
+                    sb[x] = lds8(at_vs + page + 4 * x * (D / 16));
                 }
-                const uint32_t m0 = e4m3x2_halves(static_cast<uint16_t>(sb[0] | sb[1] << 8));
-                const uint32_t m1 = e4m3x2_halves(static_cast<uint16_t>(sb[2] | sb[3] << 8));
+                if (masked) {  // a key that does not count may hold anything, a scale of NaN too; codes are numbers
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (i * kPageTokens + tig + 4 * x >= left) sb[x] = 0u;
+                }
+                const uint32_t m0 = e4m3x2_halves(static_cast<uint16_t>(__byte_perm(sb[0], sb[1], 0x0040u)));
+                const uint32_t m1 = e4m3x2_halves(static_cast<uint16_t>(__byte_perm(sb[2], sb[3], 0x0040u)));
 #pragma unroll
                 for (int x = 0; x < WV; ++x) {
                     uint32_t e0[4], e1[4], o0[4], o1[4];  // even dims and odd dims of keys (0, 1) and (2, 3)
@@ -531,8 +501,91 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     }
                 }
             }
+            if (next) {  // V has been read
+                __syncwarp();
+                send_v();
+            }
+            return true;
+        };
+        for (int32_t t = 0, cnt; t < n; t += cnt) {
+            // up to the end of the step, of the segment, of the part; or units without a page
+            const int32_t slot = t & (SP - 1);
+            const bool page_here = wc.j < wc.np;
+            cnt = min(min(SP - slot, n - t), (page_here ? wc.np : wc.np + kSegmentUnits) - wc.j);
+            const bool step_first = slot == 0, step_last = slot + cnt == SP;
+            uint32_t raw[NH][KS][2];
+            const bool fresh = page_here && first_page;
+            if (fresh) {  // a new segment: its query rows, on their way while the step's pages are waited for
+                const int32_t hk = wc.h / NHC, g0 = (wc.h - hk * NHC) * kMaxHeads;
+                ng = min(G - g0, kMaxHeads);
+                head0 = hk * G + g0;
+#pragma unroll
+                for (int f = 0; f < NH; ++f) {
+                    const __nv_bfloat16* row = a.q + (static_cast<int64_t>(wc.s) * Hq + head0 + f * 8 + gid) * D + tig * (D / 4);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ks += 2) {
+                        const uint4 w = f * 8 + gid < ng ? __ldg(reinterpret_cast<const uint4*>(row + 4 * ks)) : make_uint4(0u, 0u, 0u, 0u);
+                        raw[f][ks][0] = w.x, raw[f][ks][1] = w.y, raw[f][ks + 1][0] = w.z, raw[f][ks + 1][1] = w.w;
+                    }
+                }
+            }
+            if (step_first && !landed(&bars[0], k_steps - 1)) break;
+            first_page = !page_here;
+            if (!page_here) {
+                if (step_last && t + cnt < n) send_k();
+                if (step_first && !landed(&bars[1], v_steps - 1)) break;
+                if (step_last && t + cnt < n) send_v();
+                wc.advance(cnt, prefix, lens, S, nh);
+                continue;
+            }
+            if (fresh) {
+#pragma unroll
+                for (int f = 0; f < NH; ++f) {
+                    // the row to fp16: times 2^-e with 2^e <= its largest magnitude < 2^(e + 1)
+                    float top = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            top = max3(top, fabsf(__uint_as_float(raw[f][ks][x] << 16)), fabsf(__uint_as_float(raw[f][ks][x] & 0xffff0000u)));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
+                    const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;  // (not finite: as it is)
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    const float up2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            qb[f][ks][x] = pack_halves(__uint_as_float(raw[f][ks][x] << 16) * down,
+                                                       __uint_as_float(raw[f][ks][x] & 0xffff0000u) * down);
+#pragma unroll
+                    for (int mt = 0; mt < NMT; ++mt) acc[f][mt][0] = acc[f][mt][1] = acc[f][mt][2] = acc[f][mt][3] = 0.f;
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        mh[f][hh] = kLowest;
+                        lh[f][hh] = 0.f;
+                        c1[f][hh] = a.c1 * __shfl_sync(0xffffffffu, up2, (2 * tig + hh) * 4);
+                        if (fabsf(c1[f][hh]) < 1e-37f) c1[f][hh] = copysignf(1e-37f, a.c1);  // times `hidden`: -inf, not NaN
+                    }
+                }
+                cut_left = wc.j > 0;
+            }
+            // the step's pages at once, or those that this segment has of it one by one
+            int32_t left = wc.len - wc.j * kPageTokens;  // keys from here on
+            const bool more = step_last && t + cnt < n;
+            bool ok = true;
+            if (cnt == SP) {
+                ok = attend(std::integral_constant<int, SP>(), 0, left, true, more);
+            } else {
+#pragma unroll 1
+                for (int32_t x = 0; x < cnt && ok; ++x, left -= kPageTokens)
+                    ok = attend(std::integral_constant<int, 1>(), slot + x, left, step_first && x == 0, more && x == cnt - 1);
+            }
+            if (!ok) break;
 
-            if (t + cnt == n || wc.j + cnt == wc.np) {  // the warp's last page of this segment
+            if (t + cnt == n || wc.j + cnt == wc.np) {  // the part's last page of this segment
                 float Lh[NH][2];
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
@@ -576,60 +629,69 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     }
                 if (!inside && lane == 0) meta[warp * 2 + slot] = Piece{wc.s * nh + wc.h, wc.s, wc.h, wc.np};
             }
-            __syncwarp();
-            if (t_i < n) issue();
             wc.advance(cnt, prefix, lens, S, nh);
-            t += cnt;
         }
-        // after an abort: copies already issued land before the CTA can exit
-        if (k < k_i && lane == 0)
-            for (; k < k_i; ++k) mbar_wait_timeout(&bars[k % nst], static_cast<uint32_t>(k / nst) & 1u);
+        // copies still in flight after an abort land before the CTA can exit
+        if (*abort_flag && lane == 0) {
+            mbar_wait_timeout(&bars[0], static_cast<uint32_t>(k_steps - 1) & 1u);
+            mbar_wait_timeout(&bars[1], static_cast<uint32_t>(v_steps - 1) & 1u);
+        }
     }
     __syncthreads();
     if (*abort_flag) return;
 
     // ---- pieces cut between this CTA's warps: runs of equal segments in list order -------------
     // First every (piece, head) weighs itself against its run: e_i / sum e_k l_k with e_i = 2^(m_i - M)
-    // (pieces hold unnormalised outputs); then all threads add the pieces up.
+    // (pieces hold unnormalised outputs); then all threads add the pieces up. A lane stands for a piece; a place
+    // without one counts to the run before it, so that runs are contiguous.
     constexpr int V4 = D / 4;
     float* weight = reinterpret_cast<float*>(smem + L.weight);            // [2 NW][hs]
-    float2* run_ml = reinterpret_cast<float2*>(weight + 2 * NW * hs);     // [2 NW][hs] the run's (M, sum), at each piece
-    for (int32_t g = warp; g < hs; g += NW) {  // a warp per head, a lane per piece
+    float2* run_ml = reinterpret_cast<float2*>(weight + 2 * NW * hs);     // [2 NW][hs] the run's (M, sum), at its first piece
+    uint32_t held, starts;  // places with a piece; those whose predecessor belongs to another segment
+    int32_t my_first;       // the first place of this lane's run
+    {
         const int32_t seg = lane < 2 * NW ? meta[lane].seg : -1;
-        const float2 ml = seg >= 0 ? piece_ml[lane * hs + g] : make_float2(-INFINITY, 0.f);
-        float M = -INFINITY, den = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < 2 * NW; ++k) {
-            const int32_t sk = __shfl_sync(0xffffffffu, seg, k);
-            const float mk = __shfl_sync(0xffffffffu, ml.x, k);
-            if (sk == seg) M = fmaxf(M, mk);
+        held = __ballot_sync(0xffffffffu, seg >= 0);
+        const uint32_t before = held & ((1u << lane) - 1u);
+        const int32_t prev = __shfl_sync(0xffffffffu, seg, before ? 31 - __clz(before) : lane);
+        starts = __ballot_sync(0xffffffffu, seg >= 0 && (before == 0u || prev != seg));
+        const uint32_t upto = starts & (0xffffffffu >> (31 - lane));
+        my_first = upto ? 31 - __clz(upto) : -1;
+    }
+    for (int32_t g = warp; g < hs; g += NW) {  // a warp per head
+        const bool piece = (held >> lane & 1u) != 0u;
+        const float2 ml = piece ? piece_ml[lane * hs + g] : make_float2(-INFINITY, 0.f);
+        float M = ml.x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {  // over the run's places from here on
+            const float o = __shfl_down_sync(0xffffffffu, M, off);
+            const int32_t f = __shfl_down_sync(0xffffffffu, my_first, off);
+            if (lane + off < 32 && f == my_first) M = fmaxf(M, o);
         }
-        const float e = exp2_approx(ml.x - (M == -INFINITY ? 0.f : M)), el = e * ml.y;
-#pragma unroll 4
-        for (int k = 0; k < 2 * NW; ++k) {
-            const int32_t sk = __shfl_sync(0xffffffffu, seg, k);
-            const float lk = __shfl_sync(0xffffffffu, el, k);
-            if (sk == seg) den += lk;
+        M = __shfl_sync(0xffffffffu, M, my_first < 0 ? lane : my_first);
+        const float e = exp2_approx(ml.x - (M == -INFINITY ? 0.f : M));
+        float den = e * ml.y;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float o = __shfl_down_sync(0xffffffffu, den, off);
+            const int32_t f = __shfl_down_sync(0xffffffffu, my_first, off);
+            if (lane + off < 32 && f == my_first) den += o;
         }
-        if (seg >= 0) {
+        den = __shfl_sync(0xffffffffu, den, my_first < 0 ? lane : my_first);
+        if (piece) {
             weight[lane * hs + g] = den == 0.f ? 0.f : e / den;
             run_ml[lane * hs + g] = make_float2(M, den);
         }
     }
     __syncthreads();
-    // Runs begin at the pieces whose predecessor belongs to another segment; the warps share the runs,
-    // and several warps share a run where there are few.
-    uint32_t starts;
-    {
-        const int32_t seg = lane < 2 * NW ? meta[lane].seg : -1;
-        const uint32_t held = __ballot_sync(0xffffffffu, seg >= 0);
-        const uint32_t before = held & ((1u << lane) - 1u);
-        const int32_t prev = __shfl_sync(0xffffffffu, seg, before ? 31 - __clz(before) : lane);
-        starts = __ballot_sync(0xffffffffu, seg >= 0 && (before == 0u || prev != seg));
-    }
+    // the warps share the runs, and several warps share a run where there are few
     const int32_t runs = __popc(starts);
     for (int32_t run = runs > 0 ? warp % runs : 0; run < runs; run += NW) {
-        const int32_t i0 = __fns(starts, 0, run + 1), i1 = run + 1 < runs ? __fns(starts, 0, run + 2) : 2 * NW;
+        uint32_t rest = starts;
+        for (int32_t k = 0; k < run; ++k) rest &= rest - 1u;
+        const int32_t i0 = __ffs(rest) - 1;
+        rest &= rest - 1u;
+        const uint32_t pieces = held & ~((1u << i0) - 1u) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xffffffffu);
         const int32_t shares = runs < NW ? (NW - 1 - run) / runs + 1 : 1, mine = runs < NW ? warp / runs : 0;
         const Piece pc = meta[i0];
         const int32_t seg_a = prefix[pc.s] + pc.h * (pc.np + kSegmentUnits);
@@ -639,10 +701,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         for (int32_t i = mine * 32 + lane; i < heads * V4; i += shares * 32) {
             const int32_t g = i / V4, d = (i - g * V4) * 4;
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int32_t k = i0; k < i1; ++k) {
-                if (meta[k].seg < 0) continue;
-                const float* p = (k & 1) ? reinterpret_cast<const float*>(smem + L.ring + static_cast<uint32_t>(k >> 1) * nst * L.stage)
+            for (uint32_t left = pieces; left != 0u; left &= left - 1u) {
+                const int32_t k = __ffs(left) - 1;
+                const float* p = (k & 1) ? reinterpret_cast<const float*>(smem + L.ring + static_cast<uint32_t>(k >> 1) * L.ring_bytes)
                                          : piece0 + static_cast<uint32_t>(k >> 1) * hs * D;
                 const float4 v = *reinterpret_cast<const float4*>(p + g * D + d);
                 const float w = weight[k * hs + g];
@@ -750,7 +811,6 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
     a.num_blocks = d.num_blocks;
     a.sub_log2 = block_size_log2(d.block_size) - 4;
     a.cap_tokens = min(table_tokens(a.max_blocks, a.sub_log2), d.max_seq_len);
-    a.nst = plan.stages;
     a.c1 = d.scale * kLog2e;
     a.v_scale = v_scale;
     char* ws = static_cast<char*>(d.workspace);
@@ -775,7 +835,7 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
         a.q = static_cast<const __nv_bfloat16*>(d.q) + static_cast<int64_t>(s0) * d.num_q_heads * D;
         a.block_table = d.block_table + static_cast<int64_t>(s0) * d.max_blocks_per_seq;
         a.seq_lens = d.seq_lens + s0;
-        const Layout l = layout(NW, plan.stages, hs, D, S);
+        const Layout l = layout(NW, hs, D, S);
         cudaError_t e = allow_smem<decode_fp4_kernel<D, NW, NH>>(static_cast<int>(l.total));
         if (e != cudaSuccess) return e;
         cfg.dynamicSmemBytes = l.total;
@@ -806,13 +866,10 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
     plan->batch = static_cast<int32_t>(batch < S ? batch : S);
     plan->num_ctas = dev.num_sms;
     plan->warps = G > 8 ? 8 : 12;
-    for (int nst = 4; nst >= 2; --nst) {
-        if (layout(plan->warps, nst, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) continue;
-        plan->stages = nst;
-        plan->workspace_bytes = kScoredCounterBytes + static_cast<size_t>(plan->num_ctas) * 2 * hs * (D * 4 + 8);
-        return true;
-    }
-    return false;
+    if (layout(plan->warps, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) return false;
+    plan->stages = 1;
+    plan->workspace_bytes = kScoredCounterBytes + static_cast<size_t>(plan->num_ctas) * 2 * hs * (D * 4 + 8);
+    return true;
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {

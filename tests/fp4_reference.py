@@ -159,10 +159,10 @@ class Case:
                 k, v = K[h // (self.H_q // self.H_kv)], V[h // (self.H_q // self.H_kv)]
                 qs = q[r0:r0 + C, h]
                 z = np.where(vis, qs @ k.T * self.scale, -np.inf)
-                mag = np.where(vis, np.abs(qs) @ np.abs(k).T * self.scale, 0).max(1)
+                mag = np.where(vis, np.abs(qs) @ np.abs(k).T * abs(self.scale), 0).max(1)
                 dz = 2 * (self.D + 16) * U * mag + 8 * U * np.abs(np.where(vis, z, 0)).max(1)
                 if self.dtype == "bf16":
-                    dz = dz + self.scale * np.abs(qs).max(1) * 2.0 ** -24 * np.abs(k).sum(1).max()
+                    dz = dz + abs(self.scale) * np.abs(qs).max(1) * 2.0 ** -24 * np.abs(k).sum(1).max()
                 w = np.exp(z - z.max(1, keepdims=True))
                 w /= w.sum(1, keepdims=True)
                 o, A, n = w @ v, w @ np.abs(v), vis.sum(1)

@@ -381,3 +381,16 @@ def test_move_of_whole_blocks():
     with pytest.raises(B.PaError):
         B.pa_move_blocks(pools, torch.tensor(pairs, dtype=torch.int32, device="cuda"),
                          tokens=torch.ones(3, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factor", [0.0, -1.0, 1e-38])
+@pytest.mark.parametrize("chunks", [None, [40, 3]])
+def test_other_scales(dtype, factor, chunks):
+    """Scales of zero (uniform weights), below zero, and so small that they vanish."""
+    c = R.Case(13, [77, 9], 8, 2, 64, 16, dtype, chunks=chunks)
+    c.scale *= factor
+    d = Device(c)
+    d.run()
+    ref, tol = c.reference()
+    assert (np.abs(d.got() - ref) <= np.abs(tol)).all()
