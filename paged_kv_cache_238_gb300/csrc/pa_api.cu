@@ -751,6 +751,11 @@ PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_
         return 0;
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return 0;
+    PrefillArgs a{};
+    a.dtype = dtype, a.num_seqs = num_seqs, a.num_q_heads = num_q_heads, a.num_kv_heads = num_kv_heads;
+    if (prefill_fp4_tc_ok(a, dev->info))
+        return plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                dev->info.num_sms).workspace_bytes;
     return plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
                             dev->info.num_sms).workspace_bytes;
 }
@@ -772,10 +777,19 @@ PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, c
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto room = [&](size_t bytes) {
+        return bytes == 0 || (workspace && workspace_bytes >= bytes && aligned16(workspace));
+    };
+    if (prefill_fp4_tc_ok(a, dev->info)) {
+        const PrefillScoredPlan plan = plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
+                                                        max_seq_len, dev->info.num_sms);
+        if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
+        const cudaError_t e = launch_prefill_fp4_tc(a, v_scale, plan, workspace, dev->info.num_sms, s);
+        return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     const ScoredSimtPlan plan = plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
                                                  max_seq_len, dev->info.num_sms);
-    if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
-        return PA_ERR_INVALID_ARG;
+    if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
     return launch_fp4_prefill_simt(a, v_scale, plan, workspace, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
