@@ -3,16 +3,19 @@
 //
 // One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head): row r of a tile is token r / G, q head
 // r % G of the G heads that share the kv head, so that every key is unpacked once for both. Keys come in tiles of
-// 128. Five warpgroups:
-//   0     warp 0 owns the tensor memory and issues every MMA (kind::f16, fp16 operands, fp32 accumulation):
-//         S = Q K^T, O += P V with P from tensor memory, in the order PV_a(j), QK_a(j+1), PV_b(j), QK_b(j+1), so that
-//         the tensor cores serve one query tile while the other one's softmax runs
-//   1, 2  softmax of query tile a, of b: a thread per row (one lane of tensor memory), online in the log2 domain, in two
-//         passes over S (maximum, exponentials); O is rescaled only where the maximum grows by more than 2^8
-//   3, 4  unpack K tiles, V tiles: a thread per key reads the key's codes and scales two tiles ahead (block id), one
-//         tile ahead (bytes), converts them (e2m1x2 -> f16x2, times the scale, exact) and stores the row in the
-//         128-byte-swizzled layout that the MMAs read; a key past the sequence's end becomes zeros, whatever its cell holds
-// Registers move from the unpacking warps to the softmax ones (setmaxnreg; the shares add up to the launch's).
+// 128. Twenty-four warps:
+//   0           owns the tensor memory and issues every MMA (kind::f16, fp16 operands, fp32 accumulation):
+//               S = Q K^T, O += P V with P from tensor memory, in the order PV_a(j), QK_a(j+1), PV_b(j), QK_b(j+1), so
+//               that the tensor cores serve one query tile while the other one's softmax runs
+//   4-19        softmax, two threads per query row, each on 64 of the tile's 128 keys, online in the log2 domain, in one
+//               pass over S against the reference of the tiles before. Where a score exceeds that by more than 2^8
+//               (rarely), both threads of the row learn it at a barrier of their two warps, agree on a new reference,
+//               do the tile again and rescale O
+//   1-3, 20-23  unpack: a unit is 32 keys of K or of V, eight units a key tile, dealt to these warps in turn; a lane per
+//               key reads the key's codes and scales two units ahead, converts them (e2m1x2 -> f16x2, times the
+//               scale, exact) and stores the row in the 128-byte-swizzled layout that the MMAs read; a key past the
+//               sequence's end becomes zeros, whatever its cell holds
+// Registers move from the other warps to the softmax ones (setmaxnreg; the shares add up to the launch's).
 //
 // Query rows are brought to fp16 by a power of two per row, which the row's score factor takes back: bf16's 8 bits fit,
 // and what is 2^-24 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
@@ -35,7 +38,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
-constexpr int kThreads = 640;
+constexpr int kThreads = 768, kUnpackWarps = 7;
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 fp16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr float kLowest = -3e38f;         // a maximum before the first score: finite, so that no difference is NaN
@@ -107,6 +110,10 @@ template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 __device__ __forceinline__ int32_t read_flag(uint32_t flag) {
     int32_t v;
     asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(flag) : "memory");
@@ -133,6 +140,24 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
     }
 }
 
+// 16 columns of the warp's tensor-memory lanes; the wait takes the registers too, so that no use of them moves above it.
+__device__ __forceinline__ void ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void wait_x16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // A key's codes and scales.
 template <int D>
 struct RawRow {
@@ -148,21 +173,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L_::bars);
-    uint64_t* k_full = bars;                // [kKStages] K tile stored (4 warps)
+    uint64_t* k_full = bars;                // [kKStages] K tile stored (4 units)
     uint64_t* k_empty = k_full + kKStages;  // [kKStages] the QKs that read the stage are done
     uint64_t* v_full = k_empty + kKStages;  // [kVStages]
     uint64_t* v_empty = v_full + kVStages;  // [kVStages] the PVs that read the stage are done
     uint64_t* s_full = v_empty + kVStages;  // [2] S of query tile a / b written
-    uint64_t* p_full = s_full + 2;          // [2] its P written (4 softmax warps)
+    uint64_t* p_full = s_full + 2;          // [2] its P written (8 softmax warps)
     uint64_t* o_done = p_full + 2;          // [2] its last PV finished
-    uint64_t* q_full = o_done + 2;          // both query tiles stored (8 softmax warps)
+    uint64_t* q_full = o_done + 2;          // both query tiles stored (16 softmax warps)
     uint64_t* idle = q_full + 1;            // every MMA issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L_::misc);
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
 
     __shared__ int4 chosen[2];  // the entry's sequence, pair, first row of q, rows; length
-    __shared__ alignas(16) uint32_t rank_key[kRankMax];  // the entries' work
+    __shared__ union {  // one after the other
+        alignas(16) uint32_t rank_key[kRankMax];  // the entries' work
+        float row[2][kRows];                      // per query tile: what the two threads of a row tell one another
+    } shared;
+    // per query tile and quadrant: the last key tile (+ 1) whose scores exceed a reference; a wait has given up
+    __shared__ int32_t grow_at[2][4], stopped[2][4];
     // A CTA's entry: one pair of query tiles of a sequence (sub = the pairs of a chunk) or, sub = 1, a
     // whole sequence, whose pairs and heads follow one another. Entries with the most keys come first:
     // work that a long CTA leaves to the end of the grid keeps one SM busy and the others idle.
@@ -185,13 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
             // 24 bits of keys (all of them up to 2^24 tokens), and the number: no two alike
             mine = static_cast<uint32_t>(max(keys, 0)) >> max(8 - __clz(a.cap_tokens), 0) << 8 | (kRankMax - 1 - tid);
         }
-        if (tid < kRankMax) rank_key[tid] = mine;
+        if (tid < kRankMax) shared.rank_key[tid] = mine;
         __syncthreads();
         if (tid < n_entries) {
             int32_t rank = 0;
 #pragma unroll 4
             for (int32_t u = 0; u < n_entries; u += 4) {
-                const uint4 k = *reinterpret_cast<const uint4*>(rank_key + u);
+                const uint4 k = *reinterpret_cast<const uint4*>(shared.rank_key + u);
                 rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
             }
             if (rank == place) {
@@ -231,15 +261,74 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     }
     const int32_t n_a = min(max(all_a - base, 0), n_kv), n_b = min(max(all_b - base, 0), n_kv);
 
+    // ---- loads on their way while barriers and tensor memory are set up ----------------------------
+    const bool softmax_warp = group >= 1 && group <= 4;
+    // softmax: query tile, half of the key tile, TMEM lane quadrant, row
+    const int32_t x = (group - 1) & 1, half = (group - 1) >> 1, quad = warp & 3, r = tid & 127;
+    const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // i / G = i inv_G / 2^16 for i, G <= 128
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kLoads = 16 / kPer;  // lanes of a query row, rows of a load, loads
+    uint4 q_raw[kLoads];
+    if (softmax_warp) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes, tt = static_cast<int32_t>(rr * inv_G >> 16);
+            const int32_t t = (x ? t0b : t0a) + tt;
+            q_raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (tt < TT && t < C)
+                q_raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D) +
+                                 (lane & (kLanes - 1)));
+        }
+    }
+    // Unit u: K (bit 2 clear) or V of key tile u / 8, keys 32 (u % 4) ..; this warp has every kUnpackWarps-th.
+    const int32_t u_first = group == 0 ? warp - 1 : warp - 17, n_units = 8 * n_kv;
+    const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.max_blocks;
+    auto key_at = [&](int32_t u) { return (base + (u >> 3)) * kKeys + (u & 3) * 32 + lane; };
+    // block id of this lane's key of unit u; -1: no such key
+    auto block_of = [&](int32_t u) -> int32_t {
+        const int32_t key = key_at(u);
+        if (u >= n_units || key >= L) return -1;
+        return __ldg(table + (key >> (4 + a.sub_log2)));  // (checked when it is used, so that nothing waits for it here)
+    };
+    auto load = [&](int32_t u, int32_t block, RawRow<D>& raw) {
+        const bool held = u < n_units && key_at(u) < L;
+        if (held && (block < 0 || block >= a.num_blocks)) {
+            raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
+            block = 0;
+        }
+        if (!held) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) raw.scales[i] = 0u;
+            return;
+        }
+        const int32_t key = key_at(u), page = key >> 4;
+        const uint8_t* p = (u & 4 ? a.v_cache : a.k_cache) +
+                           fp4_page_at(block, a.num_kv_heads, h, a.sub_log2, page & ((1 << a.sub_log2) - 1), D);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(p + (key & 15) * (D / 2)) + i);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            raw.scales[i] = __ldg(reinterpret_cast<const uint32_t*>(p + fp4_scales_at(D) + (key & 15) * (D / 16)) + i);
+    };
+    const bool unpack_warp = !softmax_warp && warp != 0;
+    int32_t block_a = -1, block_b = -1, block_c = -1;  // of this warp's unit, of the next, of the one after
+    if (unpack_warp) {
+        block_a = block_of(u_first);
+        block_b = block_of(u_first + kUnpackWarps);
+        block_c = block_of(u_first + 2 * kUnpackWarps);
+    }
+
     if (tid == 0) {
         *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
         for (int i = 0; i < L_::num_bars; ++i) {  // each once: an object in use must not be initialised again
             uint64_t* bar = bars + i;
-            const bool four = bar < k_empty || (bar >= v_full && bar < v_empty) || (bar >= p_full && bar < o_done);
-            mbar_init(bar, four ? 4 : bar == q_full ? 8 : 1);
+            const bool four = bar < k_empty || (bar >= v_full && bar < v_empty);
+            mbar_init(bar, bar >= p_full && bar < o_done ? 8 : four ? 4 : bar == q_full ? 16 : 1);
         }
         fence_mbarrier_init();
     }
+    if (tid < 8) grow_at[tid >> 2][tid & 3] = stopped[tid >> 2][tid & 3] = 0;
     if (warp == 0) {
         umma::tmem_alloc(tmem_holder, 512);
         umma::tmem_relinquish();
@@ -247,58 +336,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    // tensor memory columns: S of tile x at 128 x (its P, fp16 pairs, overwrites the first 64 once read),
-    // O of tile x at 256 + 128 x
+    // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, fp16 pairs, overwrites the first
+    // 32 of the half's 64 columns once read), O of tile x at 256 + 128 x
     const uint32_t tmem = *tmem_holder;
 
-    if (group >= 3) {
-        // ================================ unpack: K (group 3), V ================================
-        fewer_registers<64>();
-        const bool is_v = group == 4;
-        const int32_t nst = is_v ? kVStages : kKStages, r = tid & 127;  // this thread's key of each tile
-        uint64_t* full = is_v ? v_full : k_full;
-        uint64_t* empty = is_v ? v_empty : k_empty;
-        uint8_t* ring = smem + (is_v ? L_::v : L_::k);
-        const uint8_t* pool = is_v ? a.v_cache : a.k_cache;
-        const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.max_blocks;
-        // block id of this thread's key in tile j; -1: no such key
-        auto block_of = [&](int32_t j) -> int32_t {
-            const int32_t key = (base + j) * kKeys + r;
-            if (j >= n_kv || key >= L) return -1;
-            int32_t phys = __ldg(table + (key >> (4 + a.sub_log2)));
-            if (phys < 0 || phys >= a.num_blocks) {
-                raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
-                phys = 0;
-            }
-            return phys;
-        };
-        auto load = [&](int32_t j, int32_t block, RawRow<D>& raw) {
-            if (block < 0) {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) raw.scales[i] = 0u;
-                return;
-            }
-            const int32_t page = ((base + j) * kKeys + r) >> 4;
-            const uint8_t* p = pool + fp4_page_at(block, a.num_kv_heads, h, a.sub_log2, page & ((1 << a.sub_log2) - 1), D);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(p + (r & 15) * (D / 2)) + i);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                raw.scales[i] = __ldg(reinterpret_cast<const uint32_t*>(p + fp4_scales_at(D) + (r & 15) * (D / 16)) + i);
-        };
-        RawRow<D> raw;
-        int32_t next = block_of(1);
-        load(0, block_of(0), raw);
-        int32_t st = 0;
-        uint32_t use = 0;
-        for (int32_t j = 0; j < n_kv; ++j) {
+    if (!softmax_warp) fewer_registers<64>();
+    if (unpack_warp) {
+        // ======================================== unpack ========================================
+        RawRow<D> raw_a, raw_b;
+        load(u_first, block_a, raw_a);
+        load(u_first + kUnpackWarps, block_b, raw_b);
+        auto unit = [&](int32_t u, RawRow<D>& raw) -> bool {  // unpacks u, and sends for the unit two turns on
+            const int32_t j = u >> 3, r0 = (u & 3) * 32 + lane;
+            const bool is_v = u & 4;
+            const int32_t nst = is_v ? kVStages : kKStages, st = j % nst, use = j / nst;
             if (use > 0) {
-                const bool ok = wait_or_abort<40>(&empty[st], (use - 1) & 1u, abort_flag, a.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                const bool ok = wait_or_abort<40>(is_v ? &v_empty[st] : &k_empty[st], static_cast<uint32_t>(use - 1) & 1u, abort_flag, a.err);
+                if (!__all_sync(0xffffffffu, ok)) return false;
             }
-            uint8_t* tile = ring + st * kTile;
+            uint8_t* tile = smem + (is_v ? L_::v : L_::k) + st * kTile;
 #pragma unroll
             for (int g = 0; g < D / 16; ++g) {
                 const uint32_t s2 = e4m3x2_halves(static_cast<uint16_t>(raw.scales[g / 4] >> (16 * (g / 2 % 2))));
@@ -306,28 +362,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
                 const uint4 w = raw.codes[g / 2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t x[4];
-                    fp4_halves(g % 2 ? (c ? w.w : w.z) : (c ? w.y : w.x), x);
+                    uint32_t y[4];
+                    fp4_halves(g % 2 ? (c ? w.w : w.z) : (c ? w.y : w.x), y);
                     const int chunk = 2 * g + c;
-                    *reinterpret_cast<uint4*>(tile + (chunk >> 3) * kHalf + sw128_offset(r, chunk & 7)) =
-                        make_uint4(hmul2(x[0], m), hmul2(x[1], m), hmul2(x[2], m), hmul2(x[3], m));
+                    *reinterpret_cast<uint4*>(tile + (chunk >> 3) * kHalf + sw128_offset(r0, chunk & 7)) =
+                        make_uint4(hmul2(y[0], m), hmul2(y[1], m), hmul2(y[2], m), hmul2(y[3], m));
                 }
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
-            if (++st == nst) {
-                st = 0;
-                ++use;
-            }
-            const int32_t block = next;
-            next = block_of(j + 2);
-            load(j + 1, block, raw);
+            if (lane == 0) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
+            const int32_t block = block_c;
+            block_c = block_of(u + 3 * kUnpackWarps);
+            load(u + 2 * kUnpackWarps, block, raw);
+            return true;
+        };
+#pragma unroll 1
+        for (int32_t u = u_first; u < n_units; u += 2 * kUnpackWarps) {
+            if (!unit(u, raw_a)) break;
+            if (u + kUnpackWarps >= n_units) break;
+            if (!unit(u + kUnpackWarps, raw_b)) break;
         }
-    } else if (group == 0) {
+    } else if (warp == 0) {
         // ======================================= MMA issuer =====================================
-        fewer_registers<32>();
-        if (warp == 0 && umma::elect_one()) {
+        if (umma::elect_one()) {
             // One thread issues every MMA (a commit tracks those of its own thread) and does all the waiting.
             constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, 0);  // Q, K both K-major
             constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, 1);    // P (TMEM), V MN-major
@@ -349,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
                 const uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (kTile >> 4);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
-                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + k * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
+                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
                                           idesc_pv, acc || k > 0);
             };
             auto wait_k = [&]() {
@@ -397,196 +455,208 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         }
     } else {
         // ==================================== queries, softmax ==================================
-        more_registers<152>();
-        const int32_t x = group - 1, quad = warp & 3, r = tid & 127;  // query tile, TMEM lane quadrant, row
-        const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // x / G = x inv_G / 2^16 for x, G <= 128
+        more_registers<88>();
         const int32_t tl = static_cast<int32_t>(r * inv_G >> 16), g = r - tl * G;
         const int32_t t_row = (x ? t0b : t0a) + tl, n_x = x ? n_b : n_a;
         const bool row_valid = tl < TT && t_row < C;
-        const int64_t row_off = (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D;
-        float c1 = a.c1;
-        {  // the row to fp16: times 2^-e with 2^e <= its largest magnitude < 2^(e + 1)
-            auto chunk = [&](int c) {  // read twice, rather than held
-                return row_valid ? __ldg(reinterpret_cast<const uint4*>(a.q + row_off) + c) : make_uint4(0u, 0u, 0u, 0u);
-            };
-            float top = 0.f;
-#pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = chunk(c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const int32_t pair_bar = 1 + x * 4 + quad;  // the barrier of the two warps that share 32 rows
+        {  // this warp's 16 rows to fp16, D / 8 lanes a row: times 2^-e with 2^e <= the row's largest magnitude < 2^(e + 1)
+            const int32_t c = lane & (kLanes - 1);
+            uint8_t* sq = smem + x * kTile;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const uint32_t w[4] = {q_raw[k].x, q_raw[k].y, q_raw[k].z, q_raw[k].w};
+                float top = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     top = max3(top, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
-            }
-            const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);     // 127 + e
-            const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;         // (not finite: as it is)
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            c1 *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            c1 = fmaxf(c1, 1e-37f);  // a hidden score of -inf times it stays -inf
-            const float f = a.negate ? -down : down;
-            uint8_t* sq = smem + x * kTile;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = chunk(c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
+                const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;      // (not finite: as it is)
+                const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), f = a.negate ? -down : down;
                 uint32_t o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     o[i] = pack_halves(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-                *reinterpret_cast<uint4*>(sq + (c >> 3) * kHalf + sw128_offset(r, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(sq + (c >> 3) * kHalf + sw128_offset(rr, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (c == 0) shared.row[x][rr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
+        named_barrier(pair_bar, 64);
+        const float c1 = fmaxf(a.c1 * shared.row[x][r], 1e-37f);  // (a hidden score of -inf times it stays -inf)
+        named_barrier(pair_bar, 64);
         const int32_t pos = row_valid ? P0 + t_row : L - 1;  // (rows without a query: zeros that go nowhere)
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tmem_s = tmem + x * 128 + lane_off, tmem_o = tmem + 256 + x * 128 + lane_off;
-        float m_ref = kLowest, l_sum = 0.f;
+        const uint32_t tmem_s = tmem + x * 128 + half * 64 + lane_off;
+        const uint32_t tmem_o = tmem + 256 + x * 128 + half * (D / 2) + lane_off;  // the columns that it rescales and writes
+        float m_ref = kLowest, l_sum = 0.f;  // the reference is the same in both threads of a row
+        uint32_t pk[32];
         bool ok = true;
+        int32_t keys = 0;  // of this half, those that the row sees are below this
+        // P = 2^(s c1 - m) in fp16 pairs, 16 keys at a time, the next 16 on their way; the weights wait in registers
+        // until the tile's maximum is known. Returns their sum; over: the largest exponent.
+        auto weights = [&](auto masked, float& over) -> float {
+            const uint64_t scale2 = pack2(c1, c1), shift2 = pack2(-m_ref, -m_ref);
+            uint64_t psum[2] = {0ull, 0ull};
+            float top[2] = {-INFINITY, -INFINITY};
+            uint32_t raw[2][16];
+            ld_x16(tmem_s, raw[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                wait_x16(raw[c & 1]);
+                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
+                if constexpr (decltype(masked)::value) {  // hidden keys: -inf, so that their weight is exactly 0
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c * 16 + i >= keys) raw[c & 1][i] = __float_as_uint(-INFINITY);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float x0, x1;
+                    unpack2(fma2(pack2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1])), scale2, shift2), x0, x1);
+                    top[e & 1] = max3(top[e & 1], x0, x1);
+                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                    psum[e & 1] = add2(psum[e & 1], pack2(p0, p1));
+                    pk[c * 8 + e] = pack_halves(p0, p1);
+                }
+            }
+            over = fmaxf(top[0], top[1]);
+            float s0, s1;
+            unpack2(add2(psum[0], psum[1]), s0, s1);
+            return s0 + s1;
+        };
+        // f(the first half's value, the second's) of this row, for both of its threads
+        auto both = [&](auto f, float mine) -> float {
+            volatile float* row = &shared.row[x][r];
+            if (half == 1) *row = mine;
+            named_barrier(pair_bar, 64);
+            if (half == 0) *row = mine = f(mine, *row);
+            named_barrier(pair_bar, 64);
+            return half == 0 ? mine : *row;
+        };
+        // The row's largest score of this tile, over both halves: the reference moves there if it is more than 2^8
+        // above. Returns what sums and outputs so far are worth under the new one.
+        auto move_reference = [&]() -> float {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t raw[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ld_x16(tmem_s + c * 16, raw);
+                wait_x16(raw);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c * 16 + i < keys) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(raw[i]));
+            }
+            const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c1;
+            const float m = both([](float p, float q) { return fmaxf(p, q); }, mine);
+            const float m_new = m > m_ref + kRescaleThreshold ? m : m_ref, alpha = exp2_approx(m_ref - m_new);
+            m_ref = m_new;
+            return alpha;
+        };
         for (int32_t j = 0; j < n_x; ++j) {
             ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a.err);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) *const_cast<volatile int32_t*>(&stopped[x][quad]) = 1;
             umma::fence_after_sync();
-            const int32_t kbase = (base + j) * kKeys;
-            const bool diag = kbase + kKeys - 1 > pos;  // only these tiles need the causal mask
-            // pass 1: row maximum of the raw scores (c1 > 0), eight independent chains
-            float mxk[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mxk[k] = -INFINITY;
-#pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-                uint32_t raw[2][32];
-                umma::ld_32x32b_x32(tmem_s + c2 * 64, raw[0]);
-                umma::ld_32x32b_x32(tmem_s + c2 * 64 + 32, raw[1]);
-                umma::wait_ld();
-                if (!diag) {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2)
-                        mxk[(i >> 1) & 7] = max3(mxk[(i >> 1) & 7], __uint_as_float(raw[i >> 5][i & 31]),
-                                                 __uint_as_float(raw[i >> 5][(i + 1) & 31]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        const float x0 = kbase + c2 * 64 + i > pos ? -INFINITY : __uint_as_float(raw[i >> 5][i & 31]);
-                        const float x1 =
-                            kbase + c2 * 64 + i + 1 > pos ? -INFINITY : __uint_as_float(raw[i >> 5][(i + 1) & 31]);
-                        mxk[(i >> 1) & 7] = max3(mxk[(i >> 1) & 7], x0, x1);
-                    }
-                }
+            keys = pos - ((base + j) * kKeys + half * 64) + 1;
+            const bool masked = __any_sync(0xffffffffu, keys < 64);  // the last tiles
+            float alpha = 1.f, over = 0.f, sum;
+            if (__any_sync(0xffffffffu, m_ref == kLowest)) alpha = move_reference();  // a row's first keys (alike in both warps)
+            sum = masked ? weights(std::true_type(), over) : weights(std::false_type(), over);
+            if (__any_sync(0xffffffffu, over > kRescaleThreshold) && lane == 0)
+                *const_cast<volatile int32_t*>(&grow_at[x][quad]) = j + 1;
+            named_barrier(pair_bar, 64);
+            // both warps leave at the same tile, so that each meets the other at every barrier
+            ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
+            if (!ok) break;
+            if (*const_cast<volatile int32_t*>(&grow_at[x][quad]) == j + 1) {
+                alpha *= move_reference();
+                sum = masked ? weights(std::true_type(), over) : weights(std::false_type(), over);
             }
-            const float mx = fmaxf(max3(max3(mxk[0], mxk[1], mxk[2]), mxk[3], mxk[4]), max3(mxk[5], mxk[6], mxk[7])) * c1;
-            // reference: moved only when the tile's maximum exceeds it by more than 2^8
-            const bool grow = mx > m_ref + kRescaleThreshold;
-            const float m_new = grow ? mx : m_ref;
-            const float alpha = exp2_approx(m_ref - m_new);
-            const uint64_t scale2 = pack2(c1, c1), shift2 = pack2(-m_new, -m_new);
-            // pass 2: P = 2^(s c1 - m) in fp16 pairs over the first 64 columns of S, 32 keys at a time (each group of S
-            // is read before the P columns that overwrite part of it are written)
-            uint64_t psum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-                uint32_t raw[32];
-                umma::ld_32x32b_x32(tmem_s + c4 * 32, raw);
-                umma::wait_ld();
-                if (diag) {  // hidden keys: -inf, so that their weight is exactly 0
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (kbase + c4 * 32 + i > pos) raw[i] = __float_as_uint(-INFINITY);
-                }
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float x0, x1;
-                    unpack2(fma2(pack2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), scale2, shift2), x0, x1);
-                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
-                    psum[e & 3] = add2(psum[e & 3], pack2(p0, p1));
-                    pk[e] = pack_halves(p0, p1);
-                }
-                umma::st_32x32b_x16(tmem_s + c4 * 16, pk);
-            }
-            umma::wait_st();
-            float s0, s1;
-            unpack2(add2(add2(psum[0], psum[1]), add2(psum[2], psum[3])), s0, s1);
-            l_sum = l_sum * alpha + (s0 + s1);
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            umma::st_32x32b_x32(tmem_s, pk);
+            l_sum = l_sum * alpha + sum;
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                 // O holds the tiles before under the old reference; the PV of tile j - 1 finished
                 // before S of tile j was committed, so O can be rescaled now
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t raw[32];
-                    umma::ld_32x32b_x32(tmem_o + c * 32, raw);
-                    umma::wait_ld();
+                    uint32_t o[16];
+                    ld_x16(tmem_o + c * 16, o);
+                    wait_x16(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * alpha);
-                    umma::st_32x32b_x32(tmem_o + c * 32, raw);
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    umma::st_32x32b_x16(tmem_o + c * 16, o);
                 }
-                umma::wait_st();
             }
-            m_ref = m_new;
+            umma::wait_st();
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[x]);
         }
         if (ok && n_x > 0) ok = wait_or_abort<20>(&o_done[x], 0, abort_flag, a.err);
-        // A tile that no key tile of this CTA concerns (a run that only the other tile sees) has no MMAs: its queries are
-        // in shared memory by now, where nothing reads them.
         ok = __all_sync(0xffffffffu, ok);
         umma::fence_after_sync();
+        l_sum = both([](float p, float q) { return p + q; }, l_sum);
+        // columns half (D / 2) + 16 c .. of the row's output; a tile that no key tile of this CTA concerns (a run that only
+        // the other tile sees) has no MMAs
+        auto output = [&](int c, uint32_t(&o)[16]) {
+            if (n_x > 0) {
+                ld_x16(tmem_o + c * 16, o);
+                wait_x16(o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0u;
+            }
+        };
         if (SPLIT && n_parts > 1) {
             if (ok) {
                 const int64_t run = static_cast<int64_t>(cta) * a.split.parts + blockIdx.x;
-                a.split.ml[run * (2 * kRows) + x * kRows + r] = make_float2(m_ref, l_sum);
-                float4* po = a.split.o + run * (D / 4) * (2 * kRows) + x * kRows + r;
+                if (half == 0) a.split.ml[run * (2 * kRows) + x * kRows + r] = make_float2(m_ref, l_sum);
+                float4* po = a.split.o + (run * (D / 4) + half * (D / 8)) * (2 * kRows) + x * kRows + r;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    if (n_x > 0) {
-                        umma::ld_32x32b_x32(tmem_o + c * 32, o);
-                        umma::wait_ld();
-                    }
+                    uint32_t o[16];
+                    output(c, o);
 #pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        po[(c * 8 + v) * (2 * kRows)] =
-                            n_x == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                     : make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                                   __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                    for (int v = 0; v < 4; ++v)
+                        po[(c * 4 + v) * (2 * kRows)] =
+                            make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                        __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                 }
             }
-        } else {
+        } else if (ok && n_x > 0) {
             const float inv = l_sum == 0.f ? 0.f : a.v_scale / l_sum;
-            // the warp's 32 rows through its own rows of the query tile, which no MMA reads any more, so that the
-            // stores go out whole lines at a time (a row's 16-byte pieces in different banks, lane by lane)
-            constexpr int kPieces = D / 8;
-            uint8_t* stage = smem + x * kTile + quad * (32 * 2 * D);
-            if (ok && n_x > 0) {
+            // this warp's rows x D / 2 columns through its own part of the query tile, which no MMA reads any more, so
+            // that the stores go out whole lines at a time (a row's 16-byte pieces in different banks, lane by lane)
+            constexpr int kPieces = D / 16;
+            uint8_t* stage = smem + x * kTile + (half * 4 + quad) * (32 * D);
+            const int32_t turn = D == 128 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    umma::ld_32x32b_x32(tmem_o + c * 32, o);
-                    umma::wait_ld();
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[16];
+                output(c, o);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        float f[8];
+                for (int v = 0; v < 2; ++v) {
+                    float f[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[v * 8 + k]) * inv;
-                        *reinterpret_cast<uint4*>(stage + lane * (2 * D) + ((c * 4 + v) ^ (lane & 7)) * 16) =
-                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                       pack_bf16x2(f[6], f[7]));
-                    }
+                    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(o[v * 8 + k]) * inv;
+                    *reinterpret_cast<uint4*>(stage + lane * D + ((c * 2 + v) ^ turn) * 16) =
+                        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
                 }
-                __syncwarp();
-                const int64_t to = row_valid ? row_off : -1;
+            }
+            __syncwarp();
+            const int64_t to = row_valid ? (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2) : -1;
 #pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                    const int32_t i = k * 32 + lane, rr = i / kPieces, c = i % kPieces;
-                    const int64_t off = __shfl_sync(0xffffffffu, to, rr);
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + (c ^ (rr & 7)) * 16);
-                    if (off >= 0) *reinterpret_cast<uint4*>(a.out + off + c * 8) = v;
-                }
+            for (int k = 0; k < kPieces; ++k) {
+                const int32_t i = k * 32 + lane, rr = i / kPieces, c = i % kPieces;
+                const int64_t off = __shfl_sync(0xffffffffu, to, rr);
+                const int32_t t = D == 128 ? rr & 7 : (rr >> 1) & 3;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * D + (c ^ t) * 16);
+                if (off >= 0) *reinterpret_cast<uint4*>(a.out + off + c * 8) = v;
             }
         }
     }
