@@ -12,7 +12,7 @@
 //               (rarely), both threads of the row learn it at a barrier of their two warps, agree on a new reference,
 //               do the tile again and rescale O
 //   1-3, 20-23  unpack: a unit is 32 keys of K or of V, eight units a key tile, dealt to these warps in turn; a lane per
-//               key reads the key's codes and scales two units ahead, converts them (e2m1x2 -> f16x2, times the
+//               key reads the key's codes and scales a unit ahead, converts them (e2m1x2 -> f16x2, times the
 //               scale, exact) and stores the row in the 128-byte-swizzled layout that the MMAs read; a key past the
 //               sequence's end becomes zeros, whatever its cell holds
 // Registers move from the other warps to the softmax ones (setmaxnreg; the shares add up to the launch's).
@@ -49,7 +49,7 @@ constexpr int kMinPartTiles = 2;          // key tiles of a run, at least, when 
 
 template <int D>
 struct Smem {
-    static constexpr int k_stages = D == 128 ? 3 : 4, v_stages = D == 128 ? 2 : 4;
+    static constexpr int k_stages = D == 128 ? 2 : 4, v_stages = D == 128 ? 3 : 4;
     static constexpr uint32_t tile = (D / 64) * kHalf;  // 128 x D fp16
     static constexpr uint32_t q = 0;                    // query tiles a, b; in the end the outputs on their way
     static constexpr uint32_t k = q + 2 * tile;
@@ -158,6 +158,20 @@ __device__ __forceinline__ void wait_x16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// 8 columns, likewise.
+__device__ __forceinline__ void ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void wait_x8(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
 // A key's codes and scales.
 template <int D>
 struct RawRow {
@@ -186,13 +200,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
 
+    // ---- barriers and tensor memory, while the entry is found -----------------------------------------
+    // per query tile and quadrant: the last key tile (+ 1) whose scores exceed a reference; a wait has given up
+    __shared__ int32_t grow_at[2][4], stopped[2][4];
+    if (tid == 64) *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
+    if (tid >= 96 && tid < 104) grow_at[tid >> 2 & 1][tid & 3] = stopped[tid >> 2 & 1][tid & 3] = 0;
+    if (warp == 1 && lane < L_::num_bars) {  // each once: an object in use must not be initialised again
+        uint64_t* bar = bars + lane;
+        const bool four = bar < k_empty || (bar >= v_full && bar < v_empty);
+        mbar_init(bar, bar >= p_full && bar < o_done ? 8 : four ? 4 : bar == q_full ? 16 : 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 0) {
+        umma::tmem_alloc(tmem_holder, 512);
+        umma::tmem_relinquish();
+    }
+    umma::fence_before_sync();
+    auto leave = [&]() {  // a CTA without work: all threads have passed a barrier since the allocation
+        if (warp == 0) {
+            umma::fence_after_sync();
+            umma::tmem_dealloc(*tmem_holder, 512);
+        }
+    };
+
     __shared__ int4 chosen[2];  // the entry's sequence, pair, first row of q, rows; length
     __shared__ union {  // one after the other
         alignas(16) uint32_t rank_key[kRankMax];  // the entries' work
         float row[2][kRows];                      // per query tile: what the two threads of a row tell one another
     } shared;
-    // per query tile and quadrant: the last key tile (+ 1) whose scores exceed a reference; a wait has given up
-    __shared__ int32_t grow_at[2][4], stopped[2][4];
     // A CTA's entry: one pair of query tiles of a sequence (sub = the pairs of a chunk) or, sub = 1, a
     // whole sequence, whose pairs and heads follow one another. Entries with the most keys come first:
     // work that a long CTA leaves to the end of the grid keeps one SM busy and the others idle.
@@ -234,16 +269,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         seq = c0.x, pair = c0.y, q0 = c0.z, C = c0.w, L = chosen[1].x;
     } else {
         entry(place);
+        __syncthreads();
     }
+    umma::fence_after_sync();
     if (sub == 1) pair = SPLIT ? 0 : gridDim.x - 1 - blockIdx.x;
     const int32_t cta = place * a.num_kv_heads + h;
     if (SPLIT && tid == 0 && blockIdx.x == 0) a.split.rows[cta] = make_int4(0, 0, 0, 0);
     if (C < 0 || C > a.max_chunk || C > L || L > a.cap_tokens) {
         if (tid == 0 && pair == 0) raise_error(a.err, PA_DEVERR_LEN_RANGE);
+        leave();
         return;
     }
     const int32_t t0a = 2 * pair * TT, t0b = t0a + TT;
-    if (t0a >= C) return;  // uniform over the CTA
+    if (t0a >= C) {  // uniform over the CTA
+        leave();
+        return;
+    }
     const int32_t P0 = L - C;
 
     // ---- key tiles of the CTA, and of each query tile: up to its last row's own key ---------------
@@ -253,7 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     if constexpr (SPLIT) {  // this CTA takes one of up to split.parts equal runs of the list
         const int32_t most = max(min(a.split.parts, n_kv / kMinPartTiles), 1), share = (n_kv + most - 1) / most;
         n_parts = (n_kv + share - 1) / share;
-        if (static_cast<int32_t>(blockIdx.x) >= n_parts) return;  // uniform over the CTA
+        if (static_cast<int32_t>(blockIdx.x) >= n_parts) {  // uniform over the CTA
+            leave();
+            return;
+        }
         base = blockIdx.x * share;
         n_kv = min(share, n_kv - base);
         if (tid == 0 && blockIdx.x == 0 && n_parts > 1)
@@ -261,24 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     }
     const int32_t n_a = min(max(all_a - base, 0), n_kv), n_b = min(max(all_b - base, 0), n_kv);
 
-    // ---- loads on their way while barriers and tensor memory are set up ----------------------------
+    // ---- roles ------------------------------------------------------------------------------------
     const bool softmax_warp = group >= 1 && group <= 4;
     // softmax: query tile, half of the key tile, TMEM lane quadrant, row
     const int32_t x = (group - 1) & 1, half = (group - 1) >> 1, quad = warp & 3, r = tid & 127;
     const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // i / G = i inv_G / 2^16 for i, G <= 128
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kLoads = 16 / kPer;  // lanes of a query row, rows of a load, loads
-    uint4 q_raw[kLoads];
-    if (softmax_warp) {
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-            const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes, tt = static_cast<int32_t>(rr * inv_G >> 16);
-            const int32_t t = (x ? t0b : t0a) + tt;
-            q_raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (tt < TT && t < C)
-                q_raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D) +
-                                 (lane & (kLanes - 1)));
-        }
-    }
     // Unit u: K (bit 2 clear) or V of key tile u / 8, keys 32 (u % 4) ..; this warp has every kUnpackWarps-th.
     const int32_t u_first = group == 0 ? warp - 1 : warp - 17, n_units = 8 * n_kv;
     const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.max_blocks;
@@ -312,41 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
             raw.scales[i] = __ldg(reinterpret_cast<const uint32_t*>(p + fp4_scales_at(D) + (key & 15) * (D / 16)) + i);
     };
     const bool unpack_warp = !softmax_warp && warp != 0;
-    int32_t block_a = -1, block_b = -1, block_c = -1;  // of this warp's unit, of the next, of the one after
-    if (unpack_warp) {
-        block_a = block_of(u_first);
-        block_b = block_of(u_first + kUnpackWarps);
-        block_c = block_of(u_first + 2 * kUnpackWarps);
-    }
-
-    if (tid == 0) {
-        *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
-        for (int i = 0; i < L_::num_bars; ++i) {  // each once: an object in use must not be initialised again
-            uint64_t* bar = bars + i;
-            const bool four = bar < k_empty || (bar >= v_full && bar < v_empty);
-            mbar_init(bar, bar >= p_full && bar < o_done ? 8 : four ? 4 : bar == q_full ? 16 : 1);
-        }
-        fence_mbarrier_init();
-    }
-    if (tid < 8) grow_at[tid >> 2][tid & 3] = stopped[tid >> 2][tid & 3] = 0;
-    if (warp == 0) {
-        umma::tmem_alloc(tmem_holder, 512);
-        umma::tmem_relinquish();
-    }
-    umma::fence_before_sync();
-    __syncthreads();
-    umma::fence_after_sync();
     // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, fp16 pairs, overwrites the first
     // 32 of the half's 64 columns once read), O of tile x at 256 + 128 x
     const uint32_t tmem = *tmem_holder;
 
-    if (!softmax_warp) fewer_registers<64>();
+    if (!softmax_warp) fewer_registers<48>();
     if (unpack_warp) {
         // ======================================== unpack ========================================
-        RawRow<D> raw_a, raw_b;
-        load(u_first, block_a, raw_a);
-        load(u_first + kUnpackWarps, block_b, raw_b);
-        auto unit = [&](int32_t u, RawRow<D>& raw) -> bool {  // unpacks u, and sends for the unit two turns on
+        RawRow<D> raw;
+        load(u_first, block_of(u_first), raw);
+        int32_t block_n = block_of(u_first + kUnpackWarps);  // of the next unit
+        auto unit = [&](int32_t u) -> bool {  // unpacks u, and sends for this warp's next unit
             const int32_t j = u >> 3, r0 = (u & 3) * 32 + lane;
             const bool is_v = u & 4;
             const int32_t nst = is_v ? kVStages : kKStages, st = j % nst, use = j / nst;
@@ -372,17 +380,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
-            const int32_t block = block_c;
-            block_c = block_of(u + 3 * kUnpackWarps);
-            load(u + 2 * kUnpackWarps, block, raw);
+            const int32_t block = block_n;
+            block_n = block_of(u + 2 * kUnpackWarps);
+            load(u + kUnpackWarps, block, raw);
             return true;
         };
 #pragma unroll 1
-        for (int32_t u = u_first; u < n_units; u += 2 * kUnpackWarps) {
-            if (!unit(u, raw_a)) break;
-            if (u + kUnpackWarps >= n_units) break;
-            if (!unit(u + kUnpackWarps, raw_b)) break;
-        }
+        for (int32_t u = u_first; u < n_units; u += kUnpackWarps)
+            if (!unit(u)) break;
     } else if (warp == 0) {
         // ======================================= MMA issuer =====================================
         if (umma::elect_one()) {
@@ -394,8 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
             const uint64_t dv0 = umma::smem_desc_sw128(smem_u32(smem + L_::v), kHalf, 1024);
             int32_t ks = 0, vs = 0;  // stages of the K tile of the last QK, of V tile j
             uint32_t k_use = 0, v_use = 0;
+            // (descriptors are stepped where they are used: kept for the whole loop, they do not fit the registers)
+            auto here = [](uint64_t& d) { asm volatile("" : "+l"(d)); };
             auto qk = [&](int x) {
-                const uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4), dk = dk0 + static_cast<uint64_t>(ks) * (kTile >> 4);
+                uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4), dk = dk0 + static_cast<uint64_t>(ks) * (kTile >> 4);
+                here(dq);
+                here(dk);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint64_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
@@ -404,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
                 umma::commit(&s_full[x]);
             };
             auto pv = [&](int x, bool acc) {
-                const uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (kTile >> 4);
+                uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (kTile >> 4);
+                here(dv);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
                     umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         }
     } else {
         // ==================================== queries, softmax ==================================
-        more_registers<88>();
+        more_registers<96>();
         const int32_t tl = static_cast<int32_t>(r * inv_G >> 16), g = r - tl * G;
         const int32_t t_row = (x ? t0b : t0a) + tl, n_x = x ? n_b : n_a;
         const bool row_valid = tl < TT && t_row < C;
@@ -463,6 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         {  // this warp's 16 rows to fp16, D / 8 lanes a row: times 2^-e with 2^e <= the row's largest magnitude < 2^(e + 1)
             const int32_t c = lane & (kLanes - 1);
             uint8_t* sq = smem + x * kTile;
+            uint4 q_raw[kLoads];
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes, tt = static_cast<int32_t>(rr * inv_G >> 16);
+                const int32_t t = (x ? t0b : t0a) + tt;
+                q_raw[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (tt < TT && t < C)
+                    q_raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D) +
+                                     (lane & (kLanes - 1)));
+            }
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const uint32_t w[4] = {q_raw[k].x, q_raw[k].y, q_raw[k].z, q_raw[k].w};
@@ -504,25 +524,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
             const uint64_t scale2 = pack2(c1, c1), shift2 = pack2(-m_ref, -m_ref);
             uint64_t psum[2] = {0ull, 0ull};
             float top[2] = {-INFINITY, -INFINITY};
-            uint32_t raw[2][16];
-            ld_x16(tmem_s, raw[0]);
+            uint32_t raw[2][8];
+            ld_x8(tmem_s, raw[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                wait_x16(raw[c & 1]);
-                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
+            for (int c = 0; c < 8; ++c) {
+                wait_x8(raw[c & 1]);
+                if (c < 7) ld_x8(tmem_s + (c + 1) * 8, raw[(c + 1) & 1]);
                 if constexpr (decltype(masked)::value) {  // hidden keys: -inf, so that their weight is exactly 0
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c * 16 + i >= keys) raw[c & 1][i] = __float_as_uint(-INFINITY);
+                    for (int i = 0; i < 8; ++i)
+                        if (c * 8 + i >= keys) raw[c & 1][i] = __float_as_uint(-INFINITY);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     float x0, x1;
                     unpack2(fma2(pack2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1])), scale2, shift2), x0, x1);
                     top[e & 1] = max3(top[e & 1], x0, x1);
                     const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
                     psum[e & 1] = add2(psum[e & 1], pack2(p0, p1));
-                    pk[c * 8 + e] = pack_halves(p0, p1);
+                    pk[c * 4 + e] = pack_halves(p0, p1);
                 }
             }
             over = fmaxf(top[0], top[1]);
