@@ -8,6 +8,7 @@ the library cannot be built or loaded, the first call raises: there is no fallba
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 from typing import Optional
 
@@ -164,7 +165,7 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
                                                          sz, vp]),
                     ("pa_move_blocks", ctypes.c_int, [vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, i32, vp, vp, i32,
                                                       vp, i32, vp]),
-                    ("pa_rotate_and_cache", ctypes.c_int, [ctypes.POINTER(RotateDesc), vp]),
+                    ("pa_rotate_and_cache", ctypes.c_int, [vp, vp]),
                     ("pa_decode_fp4_workspace_size", sz, [i32, i32, i32, i32, i32, ctypes.c_int]),
                     ("pa_decode_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
                                                      f32, f32, f32, ctypes.c_int, vp, sz, vp]),
@@ -740,6 +741,8 @@ def pa_move_blocks(pools, block_pairs, tokens=None, block_table=None, seq_lens=N
 # rotation into the cache, 4-bit pools
 # ------------------------------------------------------------------------------------------
 
+#: RotateDesc's fields for struct.pack: a call fills it in one step (0.7 us; field by field 3)
+_pack_rotate = struct.Struct("@4P4q2P3i3P8i2f").pack
 #: row bytes of a 4-bit pool -> head_dim
 _FP4_ROWS = {36: 64, 72: 128}
 
@@ -761,18 +764,16 @@ def fp4_pool_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim
     return num_blocks, num_kv_heads, block_size, head_dim * 9 // 16
 
 
-def _token_rows(what: str, t, dtype, tokens: int, D: int, device: int) -> int:
-    """A CUDA tensor [tokens, heads, D] whose rows of heads are contiguous; returns the elements between tokens."""
+def _need_rows(what: str, t, dtype, tokens: int, heads: int, D: int, device: int) -> None:
+    """A CUDA tensor [tokens, heads, D] whose rows of heads are contiguous."""
     if t.get_device() != device or device < 0:
         raise ValueError(f"{what}: on device {t.get_device()}, the others on device {device} (libpa takes CUDA tensors)")
     if t.dtype is not dtype:
         raise TypeError(f"{what}: {t.dtype} where {dtype} is needed")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != D:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} where {(tokens, -1, D)} is needed (-1: any size)")
-    step, head, one = t.stride()
-    if one != 1 or (head != D and t.shape[1] > 1):
+    if tuple(t.shape) != (tokens, heads, D):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} where {(tokens, heads, D)} is needed")
+    if t.stride(2) != 1 or (t.stride(1) != D and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return step
 
 
 def pa_rotate_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved: bool = False,
@@ -786,41 +787,45 @@ def pa_rotate_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, sl
     dt, dev, i64 = k.dtype, k.get_device(), torch.int64
     code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(k)
     fp4 = k_cache.dtype is torch.uint8
-    if k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2:
-        raise ValueError("k is [T, H_kv, D], the pools have four dimensions, cos_sin two")
-    T, H_kv, D = k.shape
+    if k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2 or (q is not None and q.dim() != 3):
+        raise ValueError("q and k are [T, heads, D], the pools have four dimensions, cos_sin two")
+    T, H_kv, D = k_shape = k.shape
     NB, _, BS, _ = pool = k_cache.shape
+    longest, R = cos_sin.shape
     want, row = (torch.uint8, D * 9 // 16) if fp4 else (dt, D)
-    if not (pool[1] == H_kv and pool[3] == row and k_cache.dtype is want and k_cache.get_device() == dev and
+    # written out, not as calls of _fits: a call takes as long as the comparisons
+    if not (dev >= 0 and pool[1] == H_kv and pool[3] == row and k_cache.dtype is want and k_cache.get_device() == dev and
             k_cache.is_contiguous() and v_cache.dtype is want and v_cache.shape == pool and v_cache.get_device() == dev and
             v_cache.is_contiguous() and cos_sin.dtype is torch.float32 and cos_sin.get_device() == dev and
             cos_sin.is_contiguous() and positions.dtype is i64 and positions.shape == (T,) and
             positions.get_device() == dev and positions.is_contiguous() and slot_mapping.dtype is i64 and
-            slot_mapping.shape == (T,) and slot_mapping.get_device() == dev and slot_mapping.is_contiguous() and dev >= 0):
+            slot_mapping.shape == (T,) and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()):
         _need("k_cache", k_cache, want, (-1, H_kv, -1, row), dev)
         _need("v_cache", v_cache, want, tuple(pool), dev)
         _need("cos_sin", cos_sin, torch.float32, (-1, -1), dev)
         _need("positions", positions, i64, (T,), dev)
         _need("slot_mapping", slot_mapping, i64, (T,), dev)
+    ks, vs = k.stride(), v.stride()
+    if not (v.dtype is dt and v.shape == k_shape and v.get_device() == dev and ks[1] == vs[1] == D and ks[2] == vs[2] == 1):
+        _need_rows("k", k, dt, T, H_kv, D, dev)
+        _need_rows("v", v, dt, T, H_kv, D, dev)
+    H_q = q_ptr = o_ptr = q_step = o_step = 0
+    if q is not None:
+        q_shape = q.shape
+        H_q = q_shape[1]
+        qs, outs = q.stride(), q_out.stride()
+        if not (q.dtype is dt and q_out.dtype is dt and q_shape[0] == T and q_shape[2] == D and q_out.shape == q_shape and
+                q.get_device() == dev and q_out.get_device() == dev and qs[1] == outs[1] == D and qs[2] == outs[2] == 1):
+            _need_rows("q", q, dt, T, H_q, D, dev)
+            _need_rows("q_out", q_out, dt, T, H_q, D, dev)
+        q_ptr, o_ptr, q_step, o_step = q.data_ptr(), q_out.data_ptr(), qs[0], outs[0]
     if dev != torch._C._cuda_getDevice():
         _need_current(dev)
-    d = RotateDesc()
-    if q is not None:
-        H_q = q.shape[1] if q.dim() == 3 else -1
-        d.q_stride, d.q_out_stride = _token_rows("q", q, dt, T, D, dev), _token_rows("q_out", q_out, dt, T, D, dev)
-        if q_out.shape[1] != H_q:
-            raise ValueError(f"q_out: shape {tuple(q_out.shape)} where {tuple(q.shape)} is needed")
-        d.q, d.q_out, d.num_q_heads = q.data_ptr(), q_out.data_ptr(), H_q
-    d.k_stride, d.v_stride = _token_rows("k", k, dt, T, D, dev), _token_rows("v", v, dt, T, D, dev)
-    if v.shape[1] != H_kv:
-        raise ValueError(f"v: shape {tuple(v.shape)} where {tuple(k.shape)} is needed")
-    d.k, d.v, d.positions, d.cos_sin = k.data_ptr(), v.data_ptr(), positions.data_ptr(), cos_sin.data_ptr()
-    d.num_positions, d.rotary_dim = cos_sin.shape
-    d.interleaved = 1 if interleaved else 0
-    d.k_cache, d.v_cache, d.slot_mapping = k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr()
-    d.num_tokens, d.num_kv_heads, d.head_dim, d.num_blocks, d.block_size = T, H_kv, D, NB, BS
-    d.dtype, d.cache_dtype, d.k_scale, d.v_scale = code, PA_FP4 if fp4 else code, k_scale, v_scale
-    st = (_lib or load()).pa_rotate_and_cache(d, _raw_stream(stream, dev))
+    st = (_lib or load()).pa_rotate_and_cache(
+        _pack_rotate(o_ptr, q_ptr, k.data_ptr(), v.data_ptr(), o_step, q_step, ks[0], vs[0], positions.data_ptr(),
+                     cos_sin.data_ptr(), longest, R, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                     slot_mapping.data_ptr(), T, H_q, H_kv, D, NB, BS, code, PA_FP4 if fp4 else code, k_scale, v_scale),
+        _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_rotate_and_cache", st)
 

@@ -81,10 +81,11 @@ __device__ __forceinline__ uint32_t e4m3_byte(float x) {
 }
 
 // 16 values that share a scale -> 8 bytes of codes, and the scale: s = e4m3(max |y| / 6), code = e2m1(y / s).
-// Both divisions are correctly rounded, and that is enough to decide every border exactly: a border is t s (t
-// halfway between two codes) or 6 t (halfway between two scales), which fp32 holds exactly, and a different
-// fp32 number divided by s (or 6) rounds to another number than t, because it is at least half a step of t
-// away from it. A scale of 0 makes all codes 0. A NaN takes no part in the maximum; its code is some number's.
+// Every border is decided exactly. A border is t s (t halfway between two codes) or 6 t (halfway between two
+// scales), which fp32 holds exactly; a different fp32 number divided by s (or 6) is more than 0.53 steps of t away from
+// t, as s has 4 bits. So the quotient must be exact where it is representable and within 0.53 steps elsewhere: y / s is
+// the product with 1 / s, corrected once by its exact residual. A scale of 0 makes all codes 0. A NaN takes no part in
+// the maximum; its code is some number's.
 __device__ __forceinline__ uint2 fp4_pack16(const float (&y)[16], uint32_t* scale_byte) {
     float top = 0.f;
 #pragma unroll
@@ -92,11 +93,19 @@ __device__ __forceinline__ uint2 fp4_pack16(const float (&y)[16], uint32_t* scal
     const uint32_t byte = e4m3_byte(__fdiv_rn(top, 6.f));
     *scale_byte = byte;
     if (byte == 0u) return make_uint2(0u, 0u);
-    const uint32_t sh = e4m3x2_halves(static_cast<uint16_t>(byte));
-    const float s = halves_to_floats(sh).x;
+    const float s = halves_to_floats(e4m3x2_halves(static_cast<uint16_t>(byte))).x;
+    const float inv = __frcp_rn(s);
     float z[16];
+    if (top < 1e30f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = __fdiv_rn(y[i], s);
+        for (int i = 0; i < 16; ++i) {
+            const float q = __fmul_rn(y[i], inv);
+            z[i] = __fmaf_rn(__fmaf_rn(-q, s, y[i]), inv, q);
+        }
+    } else {  // the residual would overflow; s is 448
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = __fdiv_rn(y[i], s);
+    }
     return make_uint2(fp4_codes4(z[0], z[1], z[2], z[3]) | fp4_codes4(z[4], z[5], z[6], z[7]) << 16,
                       fp4_codes4(z[8], z[9], z[10], z[11]) | fp4_codes4(z[12], z[13], z[14], z[15]) << 16);
 }

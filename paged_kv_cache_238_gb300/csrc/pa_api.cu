@@ -691,7 +691,8 @@ PA_API pa_status pa_rotate_and_cache(const pa_rotate* r, void* stream) {
     a.num_blocks = r->num_blocks, a.bs_log2 = block_size_log2(r->block_size);
     a.interleaved = r->interleaved != 0, a.fp4 = fp4, a.dtype = r->dtype;
     a.k_unscale = fp4 ? 1.f / r->k_scale : 1.f, a.v_unscale = fp4 ? 1.f / r->v_scale : 1.f;
-    if (rotate_ctas(a) > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    const int32_t most = r->num_q_heads > r->num_kv_heads ? r->num_q_heads : r->num_kv_heads;
+    if (static_cast<int64_t>(most) * (r->head_dim / 16) > 0x7fffffffLL / r->num_tokens) return PA_ERR_UNSUPPORTED;  // items count 31 bits
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     a.err = dev->err;
@@ -807,7 +808,7 @@ PA_API pa_status pa_gather_fp4(void* k_out, void* v_out, const void* k_cache, co
     if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(slots) & 7u))
         return PA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(num_slots) * num_kv_heads * (head_dim / 16) > 0x7fffffffLL * 128) return PA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(num_slots) * num_kv_heads > 0x7fffffffLL / (head_dim / 8)) return PA_ERR_UNSUPPORTED;  // items count 31 bits
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
     const GatherFp4Args a{k_out, v_out, k_cache, v_cache, slots, num_slots, num_kv_heads, head_dim, num_blocks,

@@ -275,7 +275,6 @@ struct RotateArgs {
     pa_dtype dtype;
     uint32_t* err;
 };
-int64_t rotate_ctas(const RotateArgs& a);  // CTAs of a call, at most
 cudaError_t launch_rotate_and_cache(const RotateArgs& a, int num_sms, cudaStream_t stream);
 
 struct GatherFp4Args {

@@ -19,7 +19,7 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Eight consecutive elements as they lie in memory, and as floats.
 template <typename T>
@@ -27,7 +27,7 @@ struct Chunk;
 template <>
 struct Chunk<uint16_t> {
     uint4 v;
-    __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const uint16_t* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -45,8 +45,8 @@ template <>
 struct Chunk<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void store(float* p) const {
         reinterpret_cast<float4*>(p)[0] = a;
@@ -81,11 +81,30 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+
+// The four pairs of a chunk.
+template <typename T>
+__device__ __forceinline__ void turn_pairs(Chunk<T>& v, const float* c, const float* s) {
+    float x[8];
+    v.get(x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x0 = x[2 * i], x1 = x[2 * i + 1];
+        x[2 * i] = fmaf(x0, c[i], -(x1 * s[i]));
+        x[2 * i + 1] = fmaf(x1, c[i], x0 * s[i]);
+    }
+    v.put(x);
+}
+
+// Grid: y = kind (q, k, v), so that a warp's threads take one path; x = units of that kind (`per` heads of a token).
 struct Shape {
-    int32_t parts;             // threads of a row: head_dim / 16
-    int32_t q_units, k_units;  // units (groups of `per` rows) of a token: q's, then k's, then v's (as many as k's)
-    int32_t per;
-    int64_t units;             // of all tokens
+    int32_t parts_log2;        // threads of a row: head_dim / 16
+    int32_t q_units, k_units;  // units of a token
+    int32_t q_per, k_per;
 };
 
 template <typename T, bool F4, bool INTERLEAVED>
@@ -94,17 +113,15 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     // the kernel before may produce the inputs, or read the pool
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t unit = item / g.parts;
-    if (unit >= g.units) return;
-    const int32_t p = static_cast<int32_t>(item - unit * g.parts);
-    const int32_t of_token = g.q_units + 2 * g.k_units;
-    const int32_t t = static_cast<int32_t>(unit / of_token);
-    int32_t u = static_cast<int32_t>(unit - static_cast<int64_t>(t) * of_token);
-    const int kind = u < g.q_units ? 0 : u < g.q_units + g.k_units ? 1 : 2;  // q, k, v
-    u -= kind == 0 ? 0 : kind == 1 ? g.q_units : g.q_units + g.k_units;
-    const int32_t heads = kind == 0 ? a.num_q_heads : a.num_kv_heads;
-    const int32_t h0 = u * g.per, h1 = min(heads, h0 + g.per), D = a.head_dim, R = a.rotary_dim;
+    const int kind = 2 - blockIdx.y;  // v, k, q: the longest come first
+    const int32_t parts = 1 << g.parts_log2, p = static_cast<int32_t>(threadIdx.x) & (parts - 1);
+    const uint32_t unit = (blockIdx.x * kThreads + threadIdx.x) >> g.parts_log2;  // (tokens x heads x parts fit 31 bits)
+    const uint32_t of_token = max(kind == 0 ? g.q_units : g.k_units, 1);
+    const int32_t t = static_cast<int32_t>(unit / of_token), u = static_cast<int32_t>(unit - t * of_token);
+    if (t >= a.num_tokens) return;  // (the grid is as wide as its widest kind)
+    if (kind == 0 && a.num_q_heads == 0) return;
+    const int32_t heads = kind == 0 ? a.num_q_heads : a.num_kv_heads, per = kind == 0 ? g.q_per : g.k_per;
+    const int32_t h0 = u * per, h1 = min(heads, h0 + per), D = a.head_dim, R = a.rotary_dim;
 
     const int64_t pos = __ldg(a.positions + t);
     if (pos < 0 || pos >= a.num_positions) {  // the token is left out
@@ -191,13 +208,24 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
         return;
     }
 
-    // ---- the pool's own type, and q: two chunks of each row -------------------------------------------
-    const bool turned = kind != 2 && p < R / 16;
-    const int32_t c0 = turned && !INTERLEAVED ? p : 2 * p, c1 = turned && !INTERLEAVED ? p + R / 16 : 2 * p + 1;
-    float c[8], s[8];
-    if (turned) {
+    // ---- the pool's own type, and q: two chunks of each row, the lanes' side by side -----------------------
+    // halves: chunk p with chunk R / 16 + p; else p with p + parts; what lies behind a part that turns, in order
+    const bool halves = !INTERLEAVED && kind != 2 && p < R / 16, behind = !INTERLEAVED && kind != 2 && !halves;
+    const int32_t c0 = behind ? 2 * p : p, c1 = behind ? 2 * p + 1 : p + (halves ? R / 16 : parts);
+    const bool turned0 = halves || (INTERLEAVED && kind != 2 && 8 * c0 < R), turned1 = halves || (INTERLEAVED && kind != 2 && 8 * c1 < R);
+    float c[8], s[8];  // halves: of the pairs; interleaved: four of each chunk
+    if (halves) {
         load8(turn + 8 * p, c);
         load8(turn + R / 2 + 8 * p, s);
+    } else {
+        if (turned0) {
+            load4(turn + 4 * c0, c);
+            load4(turn + R / 2 + 4 * c0, s);
+        }
+        if (turned1) {
+            load4(turn + 4 * c1, c + 4);
+            load4(turn + R / 2 + 4 * c1, s + 4);
+        }
     }
     T* dst;
     int64_t step;  // between heads
@@ -214,29 +242,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
         Chunk<T> lo, hi;
         lo.load(row + 8 * c0);
         hi.load(row + 8 * c1);
-        if (turned) {
+        if (halves) {
             float x[8], y[8];
             lo.get(x);
             hi.get(y);
-            if (INTERLEAVED) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float x0 = x[i], x1 = x[i + 1], y0 = y[i], y1 = y[i + 1];
-                    x[i] = fmaf(x0, c[i / 2], -(x1 * s[i / 2]));
-                    x[i + 1] = fmaf(x1, c[i / 2], x0 * s[i / 2]);
-                    y[i] = fmaf(y0, c[4 + i / 2], -(y1 * s[4 + i / 2]));
-                    y[i + 1] = fmaf(y1, c[4 + i / 2], y0 * s[4 + i / 2]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x0 = x[i], y0 = y[i];
-                    x[i] = fmaf(x0, c[i], -(y0 * s[i]));
-                    y[i] = fmaf(y0, c[i], x0 * s[i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float x0 = x[i], y0 = y[i];
+                x[i] = fmaf(x0, c[i], -(y0 * s[i]));
+                y[i] = fmaf(y0, c[i], x0 * s[i]);
             }
             lo.put(x);
             hi.put(y);
+        } else if (INTERLEAVED) {
+            if (turned0) turn_pairs(lo, c, s);
+            if (turned1) turn_pairs(hi, c + 4, s + 4);
         }
         lo.store(dst + h * step + 8 * c0);
         hi.store(dst + h * step + 8 * c1);
@@ -249,7 +269,8 @@ cudaError_t launch_rotate(const RotateArgs& a, const Shape& g, cudaStream_t stre
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((g.units * g.parts + kThreads - 1) / kThreads));
+    const int64_t units = static_cast<int64_t>(a.num_tokens) * (g.q_units > g.k_units ? g.q_units : g.k_units);
+    cfg.gridDim = dim3(static_cast<unsigned>(((units << g.parts_log2) + kThreads - 1) / kThreads), 3);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -257,81 +278,80 @@ cudaError_t launch_rotate(const RotateArgs& a, const Shape& g, cudaStream_t stre
     return cudaLaunchKernelEx(&cfg, rotate_kernel<T, F4, INTERLEAVED>, a, g);
 }
 
-// ---- rows of a 4-bit pool by slot, as values: a thread reads a group of K and of V ----------------------
+// ---- rows of a 4-bit pool by slot, as values: a thread reads 8 dims of K and of V ---------------------------
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gather_fp4_kernel(const __grid_constant__ GatherFp4Args a, int32_t parts,
-                                                              int64_t items) {
+__global__ void __launch_bounds__(kThreads) gather_fp4_kernel(const __grid_constant__ GatherFp4Args a, uint32_t chunks_log2,
+                                                              uint32_t items) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
     if (i >= items) return;
-    const int64_t row = i / parts;  // (slot, kv head)
-    const int32_t p = static_cast<int32_t>(i - row * parts);
-    const int64_t n = row / a.num_kv_heads;
-    const int32_t h = static_cast<int32_t>(row - n * a.num_kv_heads), D = a.head_dim;
+    const uint32_t row = i >> chunks_log2, n = row / static_cast<uint32_t>(a.num_kv_heads);  // (slot, kv head)
+    const int32_t c = static_cast<int32_t>(i & ((1u << chunks_log2) - 1)), h = static_cast<int32_t>(row - n * a.num_kv_heads);
+    const int32_t D = a.head_dim;
     const int64_t slot = __ldg(a.slots + n);
     const bool in = slot >= 0 && slot < static_cast<int64_t>(a.num_blocks) << a.bs_log2;
-    if (!in && slot >= 0 && p == 0 && h == 0) raise_error(a.err, PA_DEVERR_SLOT_RANGE);
+    if (!in && slot >= 0 && c == 0 && h == 0) raise_error(a.err, PA_DEVERR_SLOT_RANGE);
+    uint32_t codes[2] = {0u, 0u}, scale[2] = {0u, 0u};
+    if (in) {
+        const int32_t at = static_cast<int32_t>(slot & ((1 << a.bs_log2) - 1));
+        const int64_t page = fp4_page_at(static_cast<int32_t>(slot >> a.bs_log2), a.num_kv_heads, h, a.bs_log2 - 4, at >> 4, D);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t* p = static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache) + page;
+            codes[kv] = __ldg(reinterpret_cast<const uint32_t*>(p + (at & 15) * (D / 2)) + c);
+            scale[kv] = __ldg(p + fp4_scales_at(D) + (at & 15) * (D / 16) + c / 2);
+        }
+    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        uint2 codes = make_uint2(0u, 0u);
-        float s = 0.f;
-        if (in) {
-            const int32_t at = static_cast<int32_t>(slot & ((1 << a.bs_log2) - 1));
-            const uint8_t* page = static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache) +
-                                  fp4_page_at(static_cast<int32_t>(slot >> a.bs_log2), a.num_kv_heads, h, a.bs_log2 - 4, at >> 4, D);
-            codes = __ldg(reinterpret_cast<const uint2*>(page + (at & 15) * (D / 2) + 8 * p));
-            s = halves_to_floats(e4m3x2_halves(__ldg(page + fp4_scales_at(D) + (at & 15) * (D / 16) + p))).x;
-        }
-        s *= kv ? a.v_scale : a.k_scale;
-        T* dst = static_cast<T*>(kv ? a.v_out : a.k_out) + row * D + 16 * p;
+        const float s = halves_to_floats(e4m3x2_halves(static_cast<uint16_t>(scale[kv]))).x * (kv ? a.v_scale : a.k_scale);
+        uint32_t hv[4];
+        fp4_halves(codes[kv], hv);
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t hv[4];
-            fp4_halves(j ? codes.y : codes.x, hv);
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = halves_to_floats(hv[e]);
-                x[2 * e] = f.x * s;
-                x[2 * e + 1] = f.y * s;
-            }
-            Chunk<T> o;
-            o.put(x);
-            o.store(dst + 8 * j);
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = halves_to_floats(hv[e]);
+            x[2 * e] = f.x * s;
+            x[2 * e + 1] = f.y * s;
         }
+        Chunk<T> o;
+        o.put(x);
+        o.store(static_cast<T*>(kv ? a.v_out : a.k_out) + static_cast<int64_t>(row) * D + 8 * c);
     }
 }
 
 template <typename T>
 cudaError_t launch_gather(const GatherFp4Args& a, cudaStream_t stream) {
-    const int32_t parts = a.head_dim / 16;
-    const int64_t items = static_cast<int64_t>(a.num_slots) * a.num_kv_heads * parts;
+    const uint32_t chunks_log2 = a.head_dim == 128 ? 4 : 3;
+    const uint32_t items = static_cast<uint32_t>(a.num_slots) * a.num_kv_heads << chunks_log2;  // (fit 31 bits)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((items + kThreads - 1) / kThreads));
+    cfg.gridDim = dim3((items + kThreads - 1) / kThreads);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gather_fp4_kernel<T>, a, parts, items);
+    return cudaLaunchKernelEx(&cfg, gather_fp4_kernel<T>, a, chunks_log2, items);
 }
 
 }  // namespace
 
-int64_t rotate_ctas(const RotateArgs& a) {
-    return (static_cast<int64_t>(a.num_tokens) * (a.num_q_heads + 2 * a.num_kv_heads) * (a.head_dim / 16) + kThreads - 1) / kThreads;
-}
-
 cudaError_t launch_rotate_and_cache(const RotateArgs& a, int num_sms, cudaStream_t stream) {
+    // Heads of a unit: several, which share the angles and keep more loads in flight, where 16 CTAs an SM are left.
+    // 8448 tokens, 32 q / 8 kv heads of 128: q by 8 37.4 us in all, by 4 38.8, by 2 46.4; k, v into 4 bits by 8 47.9 us (with
+    // the read of the pool), by 4 51.2, by 1 58.3. 64 tokens into 4 bits by 1 4.2 us, by 4 6.7.
+    auto per = [&](int32_t heads, bool packs) {
+        const int64_t ctas = static_cast<int64_t>(a.num_tokens) * heads * (a.head_dim / 16) / kThreads;
+        return ctas <= 16LL * num_sms ? 1 : packs || ctas > 96LL * num_sms ? 8 : 4;
+    };
     Shape g;
-    g.parts = a.head_dim / 16;
-    g.per = rotate_ctas(a) > 16LL * num_sms ? 4 : 1;
-    g.q_units = (a.num_q_heads + g.per - 1) / g.per;
-    g.k_units = (a.num_kv_heads + g.per - 1) / g.per;
-    g.units = static_cast<int64_t>(a.num_tokens) * (g.q_units + 2 * g.k_units);
+    g.parts_log2 = a.head_dim == 128 ? 3 : 2;
+    g.q_per = per(a.num_q_heads, false), g.k_per = per(a.num_kv_heads, a.fp4);
+    g.q_units = (a.num_q_heads + g.q_per - 1) / g.q_per;
+    g.k_units = (a.num_kv_heads + g.k_per - 1) / g.k_per;
     auto go = [&](auto type, auto f4) {
         using T = decltype(type);
         return a.interleaved ? launch_rotate<T, decltype(f4)::value, true>(a, g, stream)

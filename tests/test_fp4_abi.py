@@ -53,6 +53,7 @@ def rotate(**kw):
     (dict(v_scale=2.0 ** 25), B.PA_ERR_INVALID_ARG),
     (dict(v_scale=2.0 ** -25), B.PA_ERR_INVALID_ARG),
     (dict(num_blocks=1 << 27), B.PA_ERR_UNSUPPORTED),
+    (dict(num_tokens=1 << 26), B.PA_ERR_UNSUPPORTED),     # more items than 31 bits count
     (dict(k=None), B.PA_ERR_INVALID_ARG),
     (dict(q=None), B.PA_ERR_INVALID_ARG),
     (dict(q_out=FAKE + 8), B.PA_ERR_INVALID_ARG),
@@ -68,7 +69,7 @@ def rotate(**kw):
     (dict(num_tokens=0, k=None, q=None), B.PA_OK),
 ])
 def test_rotate_refuses(kw, expect):
-    assert B.load().pa_rotate_and_cache(rotate(**kw), None) == expect
+    assert B.load().pa_rotate_and_cache(ctypes.byref(rotate(**kw)), None) == expect
 
 
 def test_rotate_refuses_no_descriptor():
@@ -176,6 +177,12 @@ def test_rotate_desc_layout_matches_the_header(tmp_path):
     subprocess.run([gcc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(B.RotateDesc)] + [getattr(B.RotateDesc, n).offset for n in names]
+    # the packed form that the binding passes
+    values = list(range(1, len(names) + 1))
+    packed = B._pack_rotate(*values)
+    assert len(packed) <= ctypes.sizeof(B.RotateDesc)
+    d = B.RotateDesc.from_buffer_copy(packed.ljust(ctypes.sizeof(B.RotateDesc), b"\0"))
+    assert [getattr(d, n) for n in names] == values
 
 
 def test_binding_refuses_host_tensors():
