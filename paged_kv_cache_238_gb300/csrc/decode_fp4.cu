@@ -38,7 +38,7 @@ constexpr int kMaxSeqs = 1024;  // sequences of one launch: their units live in 
 constexpr int kMaxHeads = 16;   // q heads of one segment
 constexpr int kMinSlice = 4;    // units of a CTA's slice, at least
 constexpr float kJoinWeight = 1.f / 1.5f;  // a segment of n units is cut into about sqrt(1.5 n) pieces at most
-constexpr int kSegmentUnits = 1;           // a segment's start and end weigh as much as this many pages
+constexpr int kSegmentUnits = 4;           // a segment's start and end weigh as much as this many pages
 constexpr float kLag = 8.f;                // log2 units; weights stay below 2^8, within fp16
 constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
 
@@ -848,7 +848,7 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
 template <int D>
 cudaError_t pick(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {
     if (a.num_q_heads / a.num_kv_heads > 8) return launch_impl<D, 8, 2>(a, v_scale, plan, stream);
-    return launch_impl<D, 12, 1>(a, v_scale, plan, stream);
+    return D == 64 ? launch_impl<D, 16, 1>(a, v_scale, plan, stream) : launch_impl<D, 12, 1>(a, v_scale, plan, stream);
 }
 
 }  // namespace
@@ -865,7 +865,7 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
     if (batch < 1 || S < 1) return false;
     plan->batch = static_cast<int32_t>(batch < S ? batch : S);
     plan->num_ctas = dev.num_sms;
-    plan->warps = G > 8 ? 8 : 12;
+    plan->warps = G > 8 ? 8 : D == 64 ? 16 : 12;
     if (layout(plan->warps, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) return false;
     plan->stages = 1;
     plan->workspace_bytes = kScoredCounterBytes + static_cast<size_t>(plan->num_ctas) * 2 * hs * (D * 4 + 8);

@@ -236,7 +236,7 @@ struct ScoredSimtPlan {
 };
 int32_t scored_simt_head_chunks(int32_t group);
 ScoredSimtPlan plan_scored_simt(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,
-                                int32_t head_dim, int32_t max_seq_len, int num_sms);
+                                int32_t head_dim, int32_t max_seq_len, int num_sms, int32_t min_pages = 32);
 cudaError_t launch_scored_decode_simt(const DecodeArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
                                       cudaStream_t stream);
 cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,

@@ -35,6 +35,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewRows = 4, kManyRows = 16;  // R: rows of a CTA
 constexpr int kMaxParts = 128;  // partitions: the merge holds their weights in shared memory
 constexpr float kLag = 8.f;  // log2 units
+constexpr int kRawPairs = 3;  // 4-bit pools: page pairs of a warp on their way or at hand
 constexpr int32_t kFar = 0x7fffffff;
 
 // Four consecutive elements as two packed pairs.
@@ -89,6 +90,16 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
     return *reinterpret_cast<uint16_t*>(&b);
 }
 
+// Eight consecutive elements, 16-byte aligned.
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
 struct SimtArgs {
     const int32_t* block_table;
     const int32_t* seq_lens;
@@ -117,8 +128,8 @@ struct Smem {
     static constexpr int page = corr + 4 * kWarps * R;     // [kWarps] K page, V page
     static constexpr int k_stride = D + pad;
     static constexpr int k_bytes = 16 * k_stride * static_cast<int>(sizeof(T));
-    static constexpr int raw = k_bytes + 16 * D * static_cast<int>(sizeof(T));  // 4-bit pools: K and V page as they lie there
-    static constexpr int page_bytes = raw + (F4 ? 2 * fp4_page_bytes(D) : 0);
+    static constexpr int raw = k_bytes + 16 * D * static_cast<int>(sizeof(T));  // 4-bit pools: pairs of a K and a V page
+    static constexpr int page_bytes = raw + (F4 ? kRawPairs * 2 * fp4_page_bytes(D) : 0);
     static constexpr int walk = page + kWarps * page_bytes, join = 4 * kWarps * R * D;
     static constexpr int bytes = walk > join ? walk : join;
     static_assert(kMaxParts * R * 8 <= bytes, "the merge's weights");
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
     const int32_t* table = a.block_table + static_cast<int64_t>(s) * a.max_blocks;
     T* k_page = reinterpret_cast<T*>(sm + L::page + warp * L::page_bytes);
     T* v_page = k_page + 16 * L::k_stride;
-    uint8_t* const raw_page = reinterpret_cast<uint8_t*>(k_page) + L::raw;  // F4: K, then V
+    uint8_t* const raw_pages = reinterpret_cast<uint8_t*>(k_page) + L::raw;  // F4: [kRawPairs] K, then V
     auto block_of = [&](int32_t i) { return i < end ? __ldg(table + (pl.page(i) >> a.sub_log2)) : 0; };
     auto in_pool = [&](int32_t block) { return block >= 0 && block < a.num_blocks; };
     // copy list page i of this warp, in this block, from a cache: 16 rows of D elements
@@ -208,41 +219,56 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
         if (i < end && in_pool(block)) {
             const int64_t row = ((static_cast<int64_t>(block) * a.num_kv_heads + hk) << a.sub_log2) +
                                 (pl.page(i) & ((1 << a.sub_log2) - 1));
-            if constexpr (F4) {
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(cache) + row * fp4_page_bytes(D);
-                uint8_t* to = raw_page + (dst == v_page ? fp4_page_bytes(D) : 0);
+            const T* src = cache + row * (kPageTokens * D);
+            constexpr int kN = 16 / sizeof(T), kChunks = D / kN;  // 16-byte chunks of a row
 #pragma unroll
-                for (int c = lane; c < fp4_page_bytes(D) / 16; c += 32) cp_async16(to + c * 16, src + c * 16);
-            } else {
-                const T* src = cache + row * (kPageTokens * D);
-                constexpr int kN = 16 / sizeof(T), kChunks = D / kN;  // 16-byte chunks of a row
+            for (int c = lane; c < 16 * kChunks; c += 32) cp_async16(dst + c / kChunks * stride + c % kChunks * kN, src + c * kN);
+        }
+        cp_async_commit();
+    };
+    // F4: copy list page i of this warp, K and V, as they lie there
+    auto fetch_pair = [&](int32_t slot, int32_t i, int32_t block) {
+        if (i < end && in_pool(block)) {
+            const int64_t at = (((static_cast<int64_t>(block) * a.num_kv_heads + hk) << a.sub_log2) +
+                                (pl.page(i) & ((1 << a.sub_log2) - 1))) * fp4_page_bytes(D);
+            uint8_t* to = raw_pages + slot * 2 * fp4_page_bytes(D);
 #pragma unroll
-                for (int c = lane; c < 16 * kChunks; c += 32) cp_async16(dst + c / kChunks * stride + c % kChunks * kN, src + c * kN);
+            for (int c = lane; c < fp4_page_bytes(D) / 16; c += 32) {
+                cp_async16(to + c * 16, reinterpret_cast<const uint8_t*>(k_cache) + at + c * 16);
+                cp_async16(to + fp4_page_bytes(D) + c * 16, reinterpret_cast<const uint8_t*>(v_cache) + at + c * 16);
             }
         }
         cp_async_commit();
     };
-    // F4: the page that has landed, as values of T times factor: a lane takes 8 dims of a key at a time
-    auto unpack = [&](T* dst, int32_t stride, float factor) {
-        const uint8_t* raw = raw_page + (dst == v_page ? fp4_page_bytes(D) : 0);
+    // F4: a page that has landed, as values of T times factor: a lane takes 8 dims of a key at a time
+    auto unpack = [&](T* dst, int32_t stride, const uint8_t* raw, float factor) {
 #pragma unroll
         for (int c = lane; c < 2 * D; c += 32) {
             const int key_row = c / (D / 8), d = c % (D / 8) * 8;
             const float s = halves_to_floats(e4m3x2_halves(raw[fp4_scales_at(D) + key_row * (D / 16) + d / 16])).x * factor;
             uint32_t h[4];
             fp4_halves(reinterpret_cast<const uint32_t*>(raw)[c], h);
+            float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 x = halves_to_floats(h[e]);
-                T* to = dst + key_row * stride + d + 2 * e;
-                to[0] = narrow<T>(x.x * s), to[1] = narrow<T>(x.y * s);
+                const float2 v = halves_to_floats(h[e]);
+                x[2 * e] = v.x * s, x[2 * e + 1] = v.y * s;
             }
+            store8(dst + key_row * stride + d, x);
         }
         __syncwarp();
     };
     int32_t block = block_of(first), block_next = block_of(first + kWarps);
-    fetch(k_cache, k_page, L::k_stride, first, block);
-    fetch(v_cache, v_page, D, first, block);
+    int32_t block_third = F4 ? block_of(first + 2 * kWarps) : 0, slot = 0;
+    if constexpr (F4) {
+        static_assert(kRawPairs == 3, "the ids that the loop carries");
+        fetch_pair(0, first, block);
+        fetch_pair(1, first + kWarps, block_next);
+        fetch_pair(2, first + 2 * kWarps, block_third);
+    } else {
+        fetch(k_cache, k_page, L::k_stride, first, block);
+        fetch(v_cache, v_page, D, first, block);
+    }
     // ---- q, scaled, rows without a query zero ---------------------------------------------------
     for (int32_t i = tid; i < R * D / 4; i += kThreads) {
         const int32_t r = i / (D / 4), c = i - r * (D / 4);
@@ -276,10 +302,11 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
         uint32_t seen = 0u;  // keys of the page that some row sees
         if (in_pool(block)) seen = 0xffffu;
         else if (lane == 0) raise_error(a.err, PA_DEVERR_BLOCK_RANGE);
-        cp_async_wait<1>();
+        cp_async_wait<F4 ? kRawPairs - 1 : 1>();
         __syncwarp();
+        const uint8_t* raw_k = raw_pages + slot * 2 * fp4_page_bytes(D);
         if constexpr (F4) {
-            if (seen) unpack(k_page, L::k_stride, 1.f);
+            if (seen) unpack(k_page, L::k_stride, raw_k, 1.f);
         }
         // ---- scores of (key, rows hh RL + i) ----
         float z[RL];
@@ -331,8 +358,8 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
             }
         }
         __syncwarp();  // the K page has been read
-        const int32_t block_after = block_of(i0 + 2 * kWarps);
-        fetch(k_cache, k_page, L::k_stride, i0 + kWarps, block_next);
+        const int32_t block_after = block_of(i0 + (F4 ? kRawPairs : 2) * kWarps);
+        if constexpr (!F4) fetch(k_cache, k_page, L::k_stride, i0 + kWarps, block_next);
         const bool whole = (j0 >= inner.a0 && j0 + kPageTokens <= inner.a1) || (j0 >= inner.b0 && j0 + kPageTokens <= inner.b1);
         if (seen) {
             if (a.score.cap > 0.f) {
@@ -392,10 +419,10 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
                 *reinterpret_cast<float2*>(ps + key * L::p_stride + hh * RL + i) = make_float2(z[i], z[i + 1]);
             }
         }
-        cp_async_wait<1>();
+        if constexpr (!F4) cp_async_wait<1>();
         __syncwarp();
         if (seen) {
-            if constexpr (F4) unpack(v_page, D, a.v_scale);
+            if constexpr (F4) unpack(v_page, D, raw_k + fp4_page_bytes(D), a.v_scale);
             if (seen != 0xffffu) {  // keys that no row sees: their weights are 0, their V may be anything
                 for (uint32_t w = ~seen & 0xffffu; w != 0u; w &= w - 1)
 #pragma unroll
@@ -426,9 +453,16 @@ __global__ void __launch_bounds__(32 * kWarps) scored_simt_kernel(T* __restrict_
             }
         }
         __syncwarp();  // the V page and the weights have been read
-        fetch(v_cache, v_page, D, i0 + kWarps, block_next);
         block = block_next;
-        block_next = block_after;
+        if constexpr (F4) {
+            fetch_pair(slot, i0 + kRawPairs * kWarps, block_after);
+            slot = slot + 1 == kRawPairs ? 0 : slot + 1;
+            block_next = block_third;
+            block_third = block_after;
+        } else {
+            fetch(v_cache, v_page, D, i0 + kWarps, block);
+            block_next = block_after;
+        }
     }
 
     // ---- the warps' parts meet -------------------------------
@@ -619,8 +653,8 @@ int32_t scored_simt_head_chunks(int32_t group) {
 // of at least kMinPages pages each. Measured, 24 sequences of up to 777 keys, 4 kv heads of 64 in fp32: 9.1 us with 32 or 64 pages,
 // 10.7 with 8 or 16.
 ScoredSimtPlan plan_scored_simt(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len,
-                                int num_sms) {
-    constexpr int64_t kMinPages = 32;
+                                int num_sms, int32_t min_pages) {
+    const int64_t kMinPages = min_pages;
     ScoredSimtPlan p{};
     const int32_t G = Hq / Hkv;
     // (24 sequences, 12 q / 4 kv heads of 64 in fp32: 5.8 us with 4 rows, 8.0 with 16; chunks of 17 to 96 rows, 8 q / 2
