@@ -222,8 +222,11 @@ def _stream(stream) -> Optional[int]:
 
 def _need_cuda(*ts) -> None:
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("libpa takes contiguous CUDA tensors")
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("libpa takes contiguous CUDA tensors")
+            if t.dim() == 4 and t.element_size() == 1:
+                raise TypeError("a 4-bit pool: this call takes pools in bf16 or fp32")
 
 
 def _use_bs(k_cache, force: bool) -> bool:

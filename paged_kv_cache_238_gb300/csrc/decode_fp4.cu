@@ -21,7 +21,11 @@
 // The softmax is online in the log2 domain against a reference that moves only when a score exceeds it by 2^kLag:
 // most steps then need no reduction across lanes at all (a vote) and rescale nothing.
 //
-// Bound: see the figures at plan_decode_fp4.
+// Bound: the unpacking's issue slots and latencies, then HBM: 300 warp instructions a page of K and V at D = 128 (64
+// conversions, 64 products with scales, 16 MMAs among them), 2.6 issued a cycle and SM. 8 sequences of 20000 to 32768 keys,
+// 64 q / 8 kv heads of 128: 57 us, 4.2 TB/s, 62 % of the measured copy rate (32 sequences of 32768: 228 us, 78 %); 64 of 500
+// to 16384, 32 q / 8 kv heads: 75 us (67 %), of which 4.4 pass until the first pages have come and 8 to 11 go to the slowest
+// SM and the joins. 4 sequences of up to 700 keys: 9.1 us in a graph, a chain of latencies.
 #include <math.h>
 
 #include <type_traits>
@@ -38,11 +42,15 @@ constexpr int kMaxSeqs = 1024;  // sequences of one launch: their units live in 
 constexpr int kMaxHeads = 16;   // q heads of one segment
 constexpr int kMinSlice = 4;    // units of a CTA's slice, at least
 constexpr float kJoinWeight = 1.f / 1.5f;  // a segment of n units is cut into about sqrt(1.5 n) pieces at most
-constexpr int kSegmentUnits = 4;           // a segment's start and end weigh as much as this many pages
+// A segment's start and end weigh as much as this many pages: 96 sequences of 16 to 2048 keys, 16 heads of 64, 24.8 us (1:
+// 29.2, 2: 28.1, 7: 24.9); 64 of 500 to 16384, 32 q / 8 kv heads of 128, 75.2 us (1: 77.1).
+constexpr int kSegmentUnits = 4;
 constexpr float kLag = 8.f;                // log2 units; weights stay below 2^8, within fp16
 constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
 
-constexpr int kStepPages = 4;              // pages of one step of a warp
+// Pages of one step of a warp, and room for one step: 64 sequences of 500 to 16384 keys 76 us, with steps of two pages and
+// room for two or four of them 85.
+constexpr int kStepPages = 4;
 __host__ __device__ inline uint32_t up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
 struct Layout {
@@ -859,12 +867,15 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
     const int64_t nh = static_cast<int64_t>(Hkv) * ((G + kMaxHeads - 1) / kMaxHeads);
     // sequences of one launch: their segments have counters, and units are counted in 32 bits
     int64_t batch = kScoredSegments / nh;
-    const int64_t by_units = 0x70000000LL / (nh * (max_seq_len / kPageTokens + 2));  // (room for a slice past the end)
+    const int64_t by_units = 0x70000000LL / (nh * (max_seq_len / kPageTokens + 1 + kSegmentUnits));  // (room for a slice past the end)
     if (by_units < batch) batch = by_units;
     if (batch > kMaxSeqs) batch = kMaxSeqs;
     if (batch < 1 || S < 1) return false;
     plan->batch = static_cast<int32_t>(batch < S ? batch : S);
     plan->num_ctas = dev.num_sms;
+    // Warps in fours, for the four schedulers, as many as registers allow without spilling. Up to 8 heads, D = 128: 75 us with
+    // 12 (64 sequences of 500 to 16384 keys), 8: 101, 10: 86, 14: 84, 16 (spilled): 77; D = 64: 23.7 with 16 (96 of 16 to
+    // 2048), 12: 24.8. Twice the accumulators (more than 8 heads) leave room for 8.
     plan->warps = G > 8 ? 8 : D == 64 ? 16 : 12;
     if (layout(plan->warps, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) return false;
     plan->stages = 1;

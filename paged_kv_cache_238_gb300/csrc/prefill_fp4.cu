@@ -1,9 +1,10 @@
 // Chunked causal prefill over a 4-bit pool on the 5th-generation tensor cores (bf16 queries, head_dim 64 or 128, up
 // to 128 q heads per kv head).
 //
-// One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head): row r of a tile is token r / G, q head
+// One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head), or one, with two CTAs on an SM that cover
+// each other's start and end, where that serves better (plan_prefill_fp4): row r of a tile is token r / G, q head
 // r % G of the G heads that share the kv head, so that every key is unpacked once for both. Keys come in tiles of
-// 128. Twenty-four warps:
+// 128. Of two tiles, twenty-four warps (of one: 0-11, two warps of each quadrant for the softmax):
 //   0           owns the tensor memory and issues every MMA (kind::f16, fp16 operands, fp32 accumulation):
 //               S = Q K^T, O += P V with P from tensor memory, in the order PV_a(j), QK_a(j+1), PV_b(j), QK_b(j+1), so
 //               that the tensor cores serve one query tile while the other one's softmax runs
@@ -19,6 +20,12 @@
 //
 // Query rows are brought to fp16 by a power of two per row, which the row's score factor takes back: bf16's 8 bits fit,
 // and what is 2^-24 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
+//
+// Bound: the chain S -> softmax -> P -> P V, Q K^T -> next S of each query tile, about 3000 cycles a key tile of which 1024 are
+// its own MMAs (both tiles' MMAs take 2048), and each CTA's start (5 us) and end (1.5). 16 sequences of 512 new rows on 512 to
+// 4608 keys, 32 q / 8 kv heads of 128: 292 us, 1.06 PFLOP/s over visible pairs, 56 % of the measured bf16 rate. Forms that were
+// slower there: a thread per row (8 softmax warps) in two passes 351 us, in one 352 to 378; the mask in every tile instead of in
+// a copy of the loop 338; registers 56 / 88 instead of 48 / 96 (the softmax spills) 318; three stages of K and two of V 302.
 //
 // Few rows on many keys: the key list is cut into runs (Split), one CTA each, and a second kernel merges their
 // outputs by M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l. Every wait is bounded; a timeout sets
@@ -38,7 +45,13 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
-constexpr int kThreads = 768, kUnpackWarps = 7;
+// Of a CTA of NQ query tiles: warps of softmax, of unpacking (three beside the MMA warp, and a warpgroup where two tiles
+// share the keys), threads; tensor memory columns of O, of all.
+template <int NQ>
+struct Roles {
+    static constexpr int soft = 8 * NQ, unpack = NQ == 2 ? 7 : 3, threads = 32 * (soft + unpack + 1);
+    static constexpr uint32_t o = NQ * 128, columns = NQ * 256;
+};
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 fp16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr float kLowest = -3e38f;         // a maximum before the first score: finite, so that no difference is NaN
@@ -46,13 +59,17 @@ constexpr int kRankMax = 256;             // entries that each CTA ranks by thei
 constexpr int kFewWaves = 4;              // grids of up to this many CTAs an SM are ordered pair by pair
 constexpr size_t kSplitRowBytes = kRankMax * 16 * 16;  // Split::rows, in a workspace
 constexpr int kMinPartTiles = 2;          // key tiles of a run, at least, when a list is split
+// Contexts up to which a CTA has one query tile. Measured with one and two tiles: 16 chunks of 300, 16 heads of 64, 28.5 and
+// 35.2 us, on 700 keys before them 73.9 and 68.0; 12 chunks of 100 on 20, 32 q / 8 kv heads of 128, 17.0 and 19.7, 8 of 500
+// 58.2 and 52.6. A chunk that fits one tile has one in any case (64 of 20 rows on 30 keys 19.5 and 31.9, on 2020 136 and 139).
+__host__ __device__ constexpr int short_keys(int D) { return D == 64 ? 768 : 192; }
 
-template <int D>
+template <int D, int NQ>
 struct Smem {
-    static constexpr int k_stages = D == 128 ? 2 : 4, v_stages = D == 128 ? 3 : 4;
+    static constexpr int k_stages = NQ == 1 ? 128 / D : D == 128 ? 2 : 4, v_stages = NQ == 1 ? 128 / D : D == 128 ? 3 : 4;
     static constexpr uint32_t tile = (D / 64) * kHalf;  // 128 x D fp16
-    static constexpr uint32_t q = 0;                    // query tiles a, b; in the end the outputs on their way
-    static constexpr uint32_t k = q + 2 * tile;
+    static constexpr uint32_t q = 0;                    // query tiles; in the end the outputs on their way
+    static constexpr uint32_t k = q + NQ * tile;
     static constexpr uint32_t v = k + k_stages * tile;
     static constexpr uint32_t bars = v + v_stages * tile;
     static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 8;
@@ -105,6 +122,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -179,9 +201,11 @@ struct RawRow {
     uint32_t scales[D / 64];  // 4 scales a word
 };
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_constant__ Args a) {
-    using L_ = Smem<D>;
+template <int D, int NQ, bool SPLIT>
+__global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel(const __grid_constant__ Args a) {
+    using L_ = Smem<D, NQ>;
+    constexpr int kUnpackWarps = Roles<NQ>::unpack;
+    constexpr uint32_t kO = Roles<NQ>::o;
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
     extern __shared__ uint8_t smem_raw[];
@@ -194,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     uint64_t* s_full = v_empty + kVStages;  // [2] S of query tile a / b written
     uint64_t* p_full = s_full + 2;          // [2] its P written (8 softmax warps)
     uint64_t* o_done = p_full + 2;          // [2] its last PV finished
-    uint64_t* q_full = o_done + 2;          // both query tiles stored (16 softmax warps)
+    uint64_t* q_full = o_done + 2;          // both query tiles stored (8 softmax warps a tile)
     uint64_t* idle = q_full + 1;            // every MMA issued has finished
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L_::misc);
     const uint32_t abort_flag = smem_u32(smem + L_::misc + 4);
@@ -208,18 +232,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     if (warp == 1 && lane < L_::num_bars) {  // each once: an object in use must not be initialised again
         uint64_t* bar = bars + lane;
         const bool four = bar < k_empty || (bar >= v_full && bar < v_empty);
-        mbar_init(bar, bar >= p_full && bar < o_done ? 8 : four ? 4 : bar == q_full ? 16 : 1);
+        mbar_init(bar, bar >= p_full && bar < o_done ? 8 : four ? 4 : bar == q_full ? 8 * NQ : 1);
         fence_mbarrier_init();
     }
     if (warp == 0) {
-        umma::tmem_alloc(tmem_holder, 512);
+        umma::tmem_alloc(tmem_holder, Roles<NQ>::columns);
         umma::tmem_relinquish();
     }
     umma::fence_before_sync();
     auto leave = [&]() {  // a CTA without work: all threads have passed a barrier since the allocation
         if (warp == 0) {
             umma::fence_after_sync();
-            umma::tmem_dealloc(*tmem_holder, 512);
+            umma::tmem_dealloc(*tmem_holder, Roles<NQ>::columns);
         }
     };
 
@@ -245,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         uint32_t mine = 0;
         if (tid < n_entries) {
             entry(tid);
-            const int32_t first = 2 * pair * TT, rows = sub > 1 ? min(2 * TT, C - first) : C;
+            const int32_t first = NQ * pair * TT, rows = sub > 1 ? min(NQ * TT, C - first) : C;
             const int32_t keys = rows <= 0 ? 0 : L - C + first + rows;  // up to the last row's own
             // 24 bits of keys (all of them up to 2^24 tokens), and the number: no two alike
             mine = static_cast<uint32_t>(max(keys, 0)) >> max(8 - __clz(a.cap_tokens), 0) << 8 | (kRankMax - 1 - tid);
@@ -280,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         leave();
         return;
     }
-    const int32_t t0a = 2 * pair * TT, t0b = t0a + TT;
+    const int32_t t0a = NQ * pair * TT, t0b = t0a + TT;
     if (t0a >= C) {  // uniform over the CTA
         leave();
         return;
@@ -289,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
 
     // ---- key tiles of the CTA, and of each query tile: up to its last row's own key ---------------
     const int32_t all_a = (P0 + min(t0a + TT, C) - 1) / kKeys + 1;
-    const int32_t all_b = t0b < C ? (P0 + min(t0b + TT, C) - 1) / kKeys + 1 : 0;
+    const int32_t all_b = NQ == 2 && t0b < C ? (P0 + min(t0b + TT, C) - 1) / kKeys + 1 : 0;
     int32_t n_kv = max(all_a, all_b), base = 0, n_parts = 1;
     if constexpr (SPLIT) {  // this CTA takes one of up to split.parts equal runs of the list
         const int32_t most = max(min(a.split.parts, n_kv / kMinPartTiles), 1), share = (n_kv + most - 1) / most;
@@ -306,13 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     const int32_t n_a = min(max(all_a - base, 0), n_kv), n_b = min(max(all_b - base, 0), n_kv);
 
     // ---- roles ------------------------------------------------------------------------------------
-    const bool softmax_warp = group >= 1 && group <= 4;
+    const bool softmax_warp = group >= 1 && group <= 2 * NQ;
     // softmax: query tile, half of the key tile, TMEM lane quadrant, row
-    const int32_t x = (group - 1) & 1, half = (group - 1) >> 1, quad = warp & 3, r = tid & 127;
+    const int32_t x = NQ == 2 ? (group - 1) & 1 : 0, half = (NQ == 2 ? (group - 1) >> 1 : group - 1) & 1, quad = warp & 3, r = tid & 127;
     const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // i / G = i inv_G / 2^16 for i, G <= 128
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kLoads = 16 / kPer;  // lanes of a query row, rows of a load, loads
     // Unit u: K (bit 2 clear) or V of key tile u / 8, keys 32 (u % 4) ..; this warp has every kUnpackWarps-th.
-    const int32_t u_first = group == 0 ? warp - 1 : warp - 17, n_units = 8 * n_kv;
+    const int32_t u_first = group == 0 ? warp - 1 : warp - (4 + Roles<NQ>::soft) + 3, n_units = 8 * n_kv;
     const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.max_blocks;
     auto key_at = [&](int32_t u) { return (base + (u >> 3)) * kKeys + (u & 3) * 32 + lane; };
     // block id of this lane's key of unit u; -1: no such key
@@ -345,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     };
     const bool unpack_warp = !softmax_warp && warp != 0;
     // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, fp16 pairs, overwrites the first
-    // 32 of the half's 64 columns once read), O of tile x at 256 + 128 x
+    // 32 of the half's 64 columns once read), O of tile x at kO + 128 x
     const uint32_t tmem = *tmem_holder;
 
     if (!softmax_warp) fewer_registers<48>();
@@ -417,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
                 here(dv);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
-                    umma::mma_bf16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
+                    umma::mma_bf16_tmem_a(tmem + kO + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
                                           idesc_pv, acc || k > 0);
             };
             auto wait_k = [&]() {
@@ -486,14 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const uint32_t w[4] = {q_raw[k].x, q_raw[k].y, q_raw[k].z, q_raw[k].w};
-                float top = 0.f;
+                uint32_t top = 0u;  // magnitudes as bf16 bits, two at a time
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = max3(top, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
+                for (int i = 0; i < 4; ++i) top = max_u16x2(top, w[i] & 0x7fff7fffu);
 #pragma unroll
-                for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
-                const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;      // (not finite: as it is)
+                for (int off = 1; off < kLanes; off <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const int32_t field = static_cast<int32_t>(max(top & 0xffffu, top >> 16) >> 7);  // 127 + e
+                const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;              // (not finite: as it is)
                 const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), f = a.negate ? -down : down;
                 uint32_t o[4];
@@ -513,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
         const int32_t pos = row_valid ? P0 + t_row : L - 1;  // (rows without a query: zeros that go nowhere)
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + x * 128 + half * 64 + lane_off;
-        const uint32_t tmem_o = tmem + 256 + x * 128 + half * (D / 2) + lane_off;  // the columns that it rescales and writes
+        const uint32_t tmem_o = tmem + kO + x * 128 + half * (D / 2) + lane_off;  // the columns that it rescales and writes
         float m_ref = kLowest, l_sum = 0.f;  // the reference is the same in both threads of a row
         uint32_t pk[32];
         bool ok = true;
@@ -686,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_fp4_kernel(const __grid_c
     __syncthreads();
     if (warp == 0) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, 512);
+        umma::tmem_dealloc(tmem, Roles<NQ>::columns);
     }
 }
 
@@ -724,14 +747,15 @@ __global__ void __launch_bounds__(2 * kRows) prefill_fp4_merge_kernel(__nv_bfloa
 }
 
 // Grids of few waves are ordered pair by pair, others sequence by sequence.
-bool few_waves(int64_t entries, int32_t num_kv_heads, int num_sms) {
-    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * num_sms;
+// tiles: query tiles of a CTA; of one tile, two CTAs share an SM.
+bool few_waves(int64_t entries, int32_t num_kv_heads, int tiles, int num_sms) {
+    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * (3 - tiles) * num_sms;
 }
 
-template <int D, bool SPLIT>
+template <int D, int NQ, bool SPLIT>
 cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScoredPlan& plan, void* workspace, int num_sms,
                         cudaStream_t stream) {
-    cudaError_t e = allow_smem<prefill_fp4_kernel<D, SPLIT>>(static_cast<int>(Smem<D>::total));
+    cudaError_t e = allow_smem<prefill_fp4_kernel<D, NQ, SPLIT>>(static_cast<int>(Smem<D, NQ>::total));
     if (e != cudaSuccess) return e;
     Args a{};
     a.out = static_cast<__nv_bfloat16*>(p.out);
@@ -752,9 +776,9 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
     a.negate = p.scale < 0.f;
     a.v_scale = v_scale;
     a.err = p.err;
-    const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len + 2 * TT - 1) / (2 * TT);
+    const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len + NQ * TT - 1) / (NQ * TT);
     const int64_t entries = static_cast<int64_t>(pairs) * p.num_seqs;
-    const bool by_pair = few_waves(entries, p.num_kv_heads, num_sms);
+    const bool by_pair = few_waves(entries, p.num_kv_heads, NQ, num_sms);
     a.sub = by_pair ? pairs : 1;
     a.inv_sub = 65536u / a.sub + 1;
     const dim3 grid(SPLIT ? plan.parts : by_pair ? 1 : pairs, p.num_kv_heads, p.num_seqs * a.sub);
@@ -765,7 +789,7 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
         a.split.o = reinterpret_cast<float4*>(ws + kScoredCounterBytes + kSplitRowBytes);
         a.split.ml = reinterpret_cast<float2*>(a.split.o + entries * p.num_kv_heads * plan.parts * (D / 4) * (2 * kRows));
     }
-    prefill_fp4_kernel<D, SPLIT><<<grid, kThreads, Smem<D>::total, stream>>>(a);
+    prefill_fp4_kernel<D, NQ, SPLIT><<<grid, Roles<NQ>::threads, Smem<D, NQ>::total, stream>>>(a);
     e = cudaGetLastError();
     if (!SPLIT || e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];  // the merge's CTAs may be set up while the last runs end
@@ -787,29 +811,32 @@ PrefillScoredPlan plan_prefill_fp4(int32_t S, int32_t max_chunk, int32_t Hq, int
     PrefillScoredPlan plan{1, 2, 0};
     if (Hq / Hkv > kRows) return plan;
     const int32_t TT = kRows / (Hq / Hkv);
+    if (max_chunk <= TT || max_len <= short_keys(D)) plan.tiles = 1;
     const int64_t most = static_cast<int64_t>(max_len / kKeys + 1) / kMinPartTiles;  // runs of the longest list
     if (most < 2) return plan;
     // room for a wave of CTAs, whatever the chunks: a workspace serves every call up to its max_len
     plan.workspace_bytes = kScoredCounterBytes + kSplitRowBytes + static_cast<size_t>(num_sms) * (2 * kRows) * (D * 4 + 8);
     if (S < 1 || max_chunk < 1) return plan;
     const int64_t entries = (static_cast<int64_t>(max_chunk) + 2 * TT - 1) / (2 * TT) * S;
-    if (few_waves(entries, Hkv, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
+    if (few_waves(entries, Hkv, 2, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
         plan.parts = static_cast<int32_t>(max(min(num_sms / (entries * Hkv), most), static_cast<int64_t>(1)));
     return plan;
 }
 
 bool prefill_fp4_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
     return a.dtype == PA_BF16 && a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
-           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128>::total) <= dev.max_smem_optin;
+           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128, 2>::total) <= dev.max_smem_optin;
 }
 
 cudaError_t launch_prefill_fp4_tc(const PrefillArgs& a, float v_scale, const PrefillScoredPlan& plan, void* workspace,
                                   int num_sms, cudaStream_t stream) {
-    if (a.head_dim == 128)
-        return plan.parts > 1 ? launch_impl<128, true>(a, v_scale, plan, workspace, num_sms, stream)
-                              : launch_impl<128, false>(a, v_scale, plan, workspace, num_sms, stream);
-    return plan.parts > 1 ? launch_impl<64, true>(a, v_scale, plan, workspace, num_sms, stream)
-                          : launch_impl<64, false>(a, v_scale, plan, workspace, num_sms, stream);
+    auto go = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (plan.parts > 1) return launch_impl<D, 2, true>(a, v_scale, plan, workspace, num_sms, stream);
+        return plan.tiles == 1 ? launch_impl<D, 1, false>(a, v_scale, plan, workspace, num_sms, stream)
+                               : launch_impl<D, 2, false>(a, v_scale, plan, workspace, num_sms, stream);
+    };
+    return a.head_dim == 128 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 64>());
 }
 
 }  // namespace pa

@@ -124,6 +124,39 @@ def test_prefill_tiles(H_q, H_kv, D):
     check(R.Case(6, [300, 700, 257, 520], H_q, H_kv, D, 16, "bf16", chunks=[300, 256, 1, 391], v_scale=2.0 ** -6))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunks", [None, [150, 40, 3]])
+def test_rows_that_are_no_numbers(dtype, chunks):
+    """NaN and infinities in one row of q reach that row's outputs alone."""
+    c = R.Case(14, [300, 40, 17], 8, 2, 128, 16, dtype, chunks=chunks)
+    ref, tol = c.reference()
+    bad = {(0, 1): np.nan, (len(c.q) - 1, 6): np.inf}
+    for (r, h), x in bad.items():
+        c.q[r, h, 5] = R.W.f32_to_bf16_bits(np.float32([x]))[0] if dtype == "bf16" else x
+    d = Device(c)
+    d.run()
+    got = d.got()
+    keep = np.ones(got.shape[:2], dtype=bool)
+    for rh in bad:
+        keep[rh] = False
+    assert np.isnan(got[0, 1]).all()
+    assert (np.abs(got - ref) <= tol)[keep].all()
+
+
+def test_pools_do_not_reach_calls_of_another_type():
+    c = R.Case(15, [20], 4, 2, 64, 16)
+    d = Device(c)
+    with pytest.raises(TypeError):
+        B.pa_decode(d.out, d.q, d.k, d.v, d.table, d.lens, 20, 0.1, d.ws)
+    with pytest.raises(TypeError):
+        B.pa_reshape_and_cache(d.q[:, :2].contiguous(), d.q[:, :2].contiguous(), d.k, d.v, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(TypeError):
+        B.pa_decode_scored(d.out, d.q, d.k, d.v, d.table, d.lens, 20, 0.1, None, d.ws)
+    wide = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(TypeError):
+        B.pa_decode_fp4(d.out, d.q, wide, wide, d.table, d.lens, 20, 0.1, d.ws)
+
+
 def test_prefill_magnitudes_of_q():
     for sharp in (0.0, 1e-30, 30.0):
         c = R.Case(7, [200, 40], 4, 2, 128, 16, "bf16", chunks=[150, 40], sharp=sharp)
