@@ -553,20 +553,37 @@ typedef struct {
 PA_API pa_status pa_rotate_and_cache(const pa_rotate* rotate, void* stream);
 
 /*
- * pa_decode_fp4: pa_decode_bs over 4-bit pools: K_i[j] and V_i[j] are the values described above.
- * q and out are dtype (bf16 or fp32); any number of q heads per kv head. Products with bf16 queries run
- * on the tensor cores in fp16, which holds the pool's values exactly: each q head's row is scaled by a
- * power of two to fp16 (elements 2^-24 below the row's largest magnitude are lost), weights are rounded
- * to fp16; sums and softmax statistics are fp32. fp32 queries compute in fp32 throughout.
+ * A call of pa_decode_fp4 or pa_prefill_fp4. Fields as the arguments of pa_decode_bs and
+ * pa_prefill_chunk_bs; k_cache and v_cache are 4-bit pools with their factors, dtype (bf16 or fp32) is
+ * that of q and out. query_start_loc and max_chunk_len are read by pa_prefill_fp4 only.
+ */
+typedef struct {
+    void* out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* query_start_loc;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t max_blocks_per_seq, num_seqs, max_chunk_len, max_seq_len;
+    int32_t num_q_heads, num_kv_heads, head_dim, num_blocks, block_size;
+    pa_dtype dtype;
+    float scale, k_scale, v_scale;
+} pa_fp4_attention;
+
+/*
+ * pa_decode_fp4: pa_decode_bs over 4-bit pools: K_i[j] and V_i[j] are the values described above. Any
+ * number of q heads per kv head. Products with bf16 queries run on the tensor cores in fp16, which holds
+ * the pool's values exactly: each q head's row is scaled by a power of two to fp16 (elements 2^-24 below
+ * the row's largest magnitude are lost), weights are rounded to fp16; sums and softmax statistics are
+ * fp32. fp32 queries compute in fp32 throughout.
  * workspace: >= pa_decode_fp4_workspace_size(...) bytes, under the rules of pa_decode_scored's.
  */
 PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                            int32_t head_dim, int32_t max_seq_len, pa_dtype dtype);
-PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
-                               const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                               int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
-                               int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale, float k_scale,
-                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+PA_API pa_status pa_decode_fp4(const pa_fp4_attention* call, void* stream);
 
 /*
  * pa_prefill_fp4: pa_prefill_chunk_bs over 4-bit pools, with pa_decode_fp4's values and arithmetic. A
@@ -577,12 +594,7 @@ PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, co
 PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads,
                                             int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
                                             pa_dtype dtype);
-PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
-                                const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                                const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
-                                int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                int32_t num_blocks, int32_t block_size, float scale, float k_scale, float v_scale,
-                                pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+PA_API pa_status pa_prefill_fp4(const pa_fp4_attention* call, void* stream);
 
 /*
  * pa_gather_fp4: rows of 4-bit pools as values, e.g. to move a sequence into another pool:
@@ -590,10 +602,18 @@ PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, c
  * values exactly) are what slot slots[i] (int64) holds. A negative slot gives a row of zeros; one
  * outside the pool too, and sets PA_DEVERR_SLOT_RANGE. Slots may repeat.
  */
-PA_API pa_status pa_gather_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
-                               const int64_t* slots, int32_t num_slots, int32_t num_kv_heads, int32_t head_dim,
-                               int32_t num_blocks, int32_t block_size, float k_scale, float v_scale, pa_dtype dtype,
-                               void* stream);
+typedef struct {
+    void* k_out;
+    void* v_out;
+    const void* k_cache;
+    const void* v_cache;
+    const int64_t* slots;
+    int32_t num_slots, num_kv_heads, head_dim, num_blocks, block_size;
+    pa_dtype dtype;
+    float k_scale, v_scale;
+} pa_fp4_rows;
+
+PA_API pa_status pa_gather_fp4(const pa_fp4_rows* rows, void* stream);
 
 /*
  * pa_get_device_errors: read the device error word of the current device (PA_DEVERR_*

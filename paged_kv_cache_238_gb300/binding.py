@@ -89,6 +89,23 @@ class RotateDesc(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class Fp4AttentionDesc(ctypes.Structure):
+    """Mirror of pa_fp4_attention in include/pa.h (same fields, same order, C layout)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("out", "q", "k_cache", "v_cache", "block_table", "seq_lens",
+                                               "query_start_loc", "workspace")] + \
+               [("workspace_bytes", ctypes.c_size_t)] + \
+               [(n, ctypes.c_int32) for n in ("max_blocks_per_seq", "num_seqs", "max_chunk_len", "max_seq_len",
+                                              "num_q_heads", "num_kv_heads", "head_dim", "num_blocks", "block_size")] + \
+               [("dtype", ctypes.c_int)] + [(n, ctypes.c_float) for n in ("scale", "k_scale", "v_scale")]
+
+
+class Fp4RowsDesc(ctypes.Structure):
+    """Mirror of pa_fp4_rows in include/pa.h (same fields, same order, C layout)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_out", "v_out", "k_cache", "v_cache", "slots")] + \
+               [(n, ctypes.c_int32) for n in ("num_slots", "num_kv_heads", "head_dim", "num_blocks", "block_size")] + \
+               [("dtype", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 class PaError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -167,13 +184,10 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
                                                       vp, i32, vp]),
                     ("pa_rotate_and_cache", ctypes.c_int, [vp, vp]),
                     ("pa_decode_fp4_workspace_size", sz, [i32, i32, i32, i32, i32, ctypes.c_int]),
-                    ("pa_decode_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
-                                                     f32, f32, f32, ctypes.c_int, vp, sz, vp]),
+                    ("pa_decode_fp4", ctypes.c_int, [vp, vp]),
                     ("pa_prefill_fp4_workspace_size", sz, [i32, i32, i32, i32, i32, i32, ctypes.c_int]),
-                    ("pa_prefill_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32,
-                                                      i32, f32, f32, f32, ctypes.c_int, vp, sz, vp]),
-                    ("pa_gather_fp4", ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, f32, ctypes.c_int,
-                                                     vp]),
+                    ("pa_prefill_fp4", ctypes.c_int, [vp, vp]),
+                    ("pa_gather_fp4", ctypes.c_int, [vp, vp]),
                     ("pa_bm_release_behind", ctypes.c_int, [vp, i64, i32, i32, pi32]),
                     ("pa_bm_resize", ctypes.c_int, [vp, i32, pi32, pi32, i32, pi32]),
                     ("pa_bm_create_bs", ctypes.c_int, [i32, i32, i32, ctypes.c_char_p, ctypes.POINTER(vp)]),
@@ -744,8 +758,11 @@ def pa_move_blocks(pools, block_pairs, tokens=None, block_table=None, seq_lens=N
 # rotation into the cache, 4-bit pools
 # ------------------------------------------------------------------------------------------
 
-#: RotateDesc's fields for struct.pack: a call fills it in one step (0.7 us; field by field 3)
-_pack_rotate = struct.Struct("@4P4q2P3i3P8i2f").pack
+#: fields of the descriptors for struct.pack: a call fills one in one step and passes two arguments (0.5 us; the 21
+#: arguments of an attention call one by one 2.7)
+_pack_rotate = struct.Struct("@4P4q2P3i3P8i2f0P").pack
+_pack_attention = struct.Struct("@8PN10i3f0P").pack
+_pack_rows = struct.Struct("@5P6i2f0P").pack
 #: row bytes of a 4-bit pool -> head_dim
 _FP4_ROWS = {36: 64, 72: 128}
 
@@ -886,9 +903,9 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_table, seq_lens, max_seq_len: 
     if T != S:
         raise ValueError(f"decode takes one query row per sequence: {T} rows, {S} sequences")
     st = (_lib or load()).pa_decode_fp4(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
-        seq_lens.data_ptr(), S, int(max_seq_len), H_q, H_kv, D, NB, BS, scale, k_scale, v_scale, code, _ptr(workspace),
-        ws_bytes, _raw_stream(stream, dev))
+        _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                        seq_lens.data_ptr(), 0, 0 if workspace is None else workspace.data_ptr(), ws_bytes, mb, S, 0,
+                        int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale, v_scale), _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_decode_fp4", st)
 
@@ -912,9 +929,10 @@ def pa_prefill_fp4(out, q, k_cache, v_cache, block_table, seq_lens, query_start_
     if not _fits(query_start_loc, torch.int32, (S + 1,), dev):
         _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), dev)
     st = (_lib or load()).pa_prefill_fp4(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
-        seq_lens.data_ptr(), query_start_loc.data_ptr(), S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS,
-        scale, k_scale, v_scale, code, _ptr(workspace), ws_bytes, _raw_stream(stream, dev))
+        _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                        seq_lens.data_ptr(), query_start_loc.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
+                        ws_bytes, mb, S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale,
+                        v_scale), _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_prefill_fp4", st)
 
@@ -943,8 +961,8 @@ def pa_gather_fp4(k_out, v_out, k_cache, v_cache, slots, k_scale: float = 1.0, v
     if dev != torch._C._cuda_getDevice():
         _need_current(dev)
     st = (_lib or load()).pa_gather_fp4(
-        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), n, H_kv, D, NB, BS,
-        k_scale, v_scale, code, _raw_stream(stream, dev))
+        _pack_rows(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), n, H_kv, D,
+                   NB, BS, code, k_scale, v_scale), _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_gather_fp4", st)
 

@@ -717,15 +717,18 @@ PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads
         .workspace_bytes;
 }
 
-PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
-                               const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                               int32_t num_seqs, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
-                               int32_t head_dim, int32_t num_blocks, int32_t block_size, float scale, float k_scale,
-                               float v_scale, pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+PA_API pa_status pa_decode_fp4(const pa_fp4_attention* c, void* stream) {
+    if (!c) return PA_ERR_INVALID_ARG;
+    const int32_t num_seqs = c->num_seqs, max_seq_len = c->max_seq_len, num_q_heads = c->num_q_heads;
+    const int32_t num_kv_heads = c->num_kv_heads, head_dim = c->head_dim;
+    const float k_scale = c->k_scale, v_scale = c->v_scale;
+    const pa_dtype dtype = c->dtype;
+    void* const workspace = c->workspace;
+    const size_t workspace_bytes = c->workspace_bytes;
     DecodeArgs a;
-    pa_status st = prepare_decode(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens, num_seqs,
-                                  max_seq_len, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, scale * k_scale,
-                                  dtype, workspace, workspace_bytes, &a);
+    pa_status st = prepare_decode(c->out, c->q, c->k_cache, c->v_cache, c->block_table, c->max_blocks_per_seq, c->seq_lens,
+                                  num_seqs, max_seq_len, num_q_heads, num_kv_heads, head_dim, c->num_blocks, c->block_size,
+                                  c->scale * k_scale, dtype, workspace, workspace_bytes, &a);
     if (st == PA_OK && (!factor_ok(k_scale) || !factor_ok(v_scale))) st = PA_ERR_INVALID_ARG;
     if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
     if (st != PA_OK || num_seqs == 0) return st;
@@ -764,16 +767,17 @@ PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_
                             dev->info.num_sms, kFp4MinPages).workspace_bytes;
 }
 
-PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
-                                const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                                const int32_t* query_start_loc, int32_t num_seqs, int32_t max_chunk_len,
-                                int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                int32_t num_blocks, int32_t block_size, float scale, float k_scale, float v_scale,
-                                pa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+PA_API pa_status pa_prefill_fp4(const pa_fp4_attention* c, void* stream) {
+    if (!c) return PA_ERR_INVALID_ARG;
+    const int32_t num_seqs = c->num_seqs, max_chunk_len = c->max_chunk_len, max_seq_len = c->max_seq_len;
+    const int32_t num_q_heads = c->num_q_heads, num_kv_heads = c->num_kv_heads, head_dim = c->head_dim;
+    const float k_scale = c->k_scale, v_scale = c->v_scale;
+    void* const workspace = c->workspace;
+    const size_t workspace_bytes = c->workspace_bytes;
     PrefillArgs a;
-    pa_status st = prepare_prefill(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, seq_lens,
-                                   query_start_loc, num_seqs, max_chunk_len, max_seq_len, num_q_heads, num_kv_heads,
-                                   head_dim, num_blocks, block_size, scale * k_scale, dtype, &a);
+    pa_status st = prepare_prefill(c->out, c->q, c->k_cache, c->v_cache, c->block_table, c->max_blocks_per_seq, c->seq_lens,
+                                   c->query_start_loc, num_seqs, max_chunk_len, max_seq_len, num_q_heads, num_kv_heads,
+                                   head_dim, c->num_blocks, c->block_size, c->scale * k_scale, c->dtype, &a);
     if (st == PA_OK && (!factor_ok(k_scale) || !factor_ok(v_scale))) st = PA_ERR_INVALID_ARG;
     if (st == PA_OK) st = check_scored_grid(num_q_heads, num_kv_heads);
     if (st != PA_OK || !prefill_has_work(a)) return st;
@@ -797,25 +801,24 @@ PA_API pa_status pa_prefill_fp4(void* out, const void* q, const void* k_cache, c
     return launch_fp4_prefill_simt(a, v_scale, plan, workspace, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-PA_API pa_status pa_gather_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
-                               const int64_t* slots, int32_t num_slots, int32_t num_kv_heads, int32_t head_dim,
-                               int32_t num_blocks, int32_t block_size, float k_scale, float v_scale, pa_dtype dtype,
-                               void* stream) {
-    if (num_slots < 0 || num_kv_heads <= 0 || num_blocks <= 0 || head_dim <= 0) return PA_ERR_INVALID_ARG;
-    if (!block_size_ok(block_size)) return block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || !factor_ok(k_scale) || !factor_ok(v_scale)) return PA_ERR_INVALID_ARG;
-    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(num_blocks) * num_kv_heads * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-    if (num_slots == 0) return PA_OK;
-    if (!k_out || !v_out || !k_cache || !v_cache || !slots) return PA_ERR_INVALID_ARG;
-    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
-        (reinterpret_cast<uintptr_t>(slots) & 7u))
+PA_API pa_status pa_gather_fp4(const pa_fp4_rows* r, void* stream) {
+    if (!r) return PA_ERR_INVALID_ARG;
+    if (r->num_slots < 0 || r->num_kv_heads <= 0 || r->num_blocks <= 0 || r->head_dim <= 0) return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(r->block_size)) return r->block_size > 0 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    if (!dtype_ok(r->dtype) || !factor_ok(r->k_scale) || !factor_ok(r->v_scale)) return PA_ERR_INVALID_ARG;
+    if (r->head_dim != 64 && r->head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(r->num_blocks) * r->num_kv_heads * r->block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    if (r->num_slots == 0) return PA_OK;
+    if (!r->k_out || !r->v_out || !r->k_cache || !r->v_cache || !r->slots) return PA_ERR_INVALID_ARG;
+    if (!aligned16(r->k_out) || !aligned16(r->v_out) || !aligned16(r->k_cache) || !aligned16(r->v_cache) ||
+        (reinterpret_cast<uintptr_t>(r->slots) & 7u))
         return PA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(num_slots) * num_kv_heads > 0x7fffffffLL / (head_dim / 8)) return PA_ERR_UNSUPPORTED;  // items count 31 bits
+    if (static_cast<int64_t>(r->num_slots) * r->num_kv_heads > 0x7fffffffLL / (r->head_dim / 8))
+        return PA_ERR_UNSUPPORTED;  // items count 31 bits
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return PA_ERR_CUDA;
-    const GatherFp4Args a{k_out, v_out, k_cache, v_cache, slots, num_slots, num_kv_heads, head_dim, num_blocks,
-                          block_size_log2(block_size), k_scale, v_scale, dtype, dev->err};
+    const GatherFp4Args a{r->k_out, r->v_out, r->k_cache, r->v_cache, r->slots, r->num_slots, r->num_kv_heads, r->head_dim,
+                          r->num_blocks, block_size_log2(r->block_size), r->k_scale, r->v_scale, r->dtype, dev->err};
     return launch_gather_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -72,8 +72,9 @@ def test_rotate_refuses(kw, expect):
     assert B.load().pa_rotate_and_cache(ctypes.byref(rotate(**kw)), None) == expect
 
 
-def test_rotate_refuses_no_descriptor():
-    assert B.load().pa_rotate_and_cache(None, None) == B.PA_ERR_INVALID_ARG
+def test_no_descriptor_is_refused():
+    for call in ("pa_rotate_and_cache", "pa_decode_fp4", "pa_prefill_fp4", "pa_gather_fp4"):
+        assert getattr(B.load(), call)(None, None) == B.PA_ERR_INVALID_ARG
 
 
 SHAPES = [
@@ -101,12 +102,21 @@ def base(**kw):
     return a
 
 
+def attention(**kw):
+    a = base(**kw)
+    d = B.Fp4AttentionDesc()
+    for field, key in (("out", "out"), ("q", "q"), ("k_cache", "kc"), ("v_cache", "vc"), ("block_table", "bt"), ("seq_lens", "lens"),
+                       ("query_start_loc", "qsl"), ("max_blocks_per_seq", "mb"), ("num_seqs", "S"), ("max_chunk_len", "chunk"),
+                       ("max_seq_len", "max_len"), ("num_q_heads", "Hq"), ("num_kv_heads", "Hkv"), ("head_dim", "D"),
+                       ("num_blocks", "NB"), ("block_size", "bs"), ("dtype", "dt"), ("k_scale", "ks"), ("v_scale", "vs")):
+        setattr(d, field, a[key])
+    d.scale, d.workspace, d.workspace_bytes = 0.1, FAKE, 1 << 30
+    return ctypes.byref(d)
+
+
 @pytest.mark.parametrize("kw,expect", SHAPES)
 def test_decode_fp4_refuses(kw, expect):
-    a = base(**kw)
-    assert B.load().pa_decode_fp4(a["out"], a["q"], a["kc"], a["vc"], a["bt"], a["mb"], a["lens"], a["S"], a["max_len"],
-                                  a["Hq"], a["Hkv"], a["D"], a["NB"], a["bs"], 0.1, a["ks"], a["vs"], a["dt"], FAKE,
-                                  1 << 30, None) == expect
+    assert B.load().pa_decode_fp4(attention(**kw), None) == expect
 
 
 @pytest.mark.parametrize("kw,expect", SHAPES + [
@@ -116,10 +126,7 @@ def test_decode_fp4_refuses(kw, expect):
     (dict(S=1 << 27, chunk=64), B.PA_ERR_UNSUPPORTED),
 ])
 def test_prefill_fp4_refuses(kw, expect):
-    a = base(**kw)
-    assert B.load().pa_prefill_fp4(a["out"], a["q"], a["kc"], a["vc"], a["bt"], a["mb"], a["lens"], a["qsl"], a["S"],
-                                   a["chunk"], a["max_len"], a["Hq"], a["Hkv"], a["D"], a["NB"], a["bs"], 0.1, a["ks"],
-                                   a["vs"], a["dt"], FAKE, 1 << 30, None) == expect
+    assert B.load().pa_prefill_fp4(attention(**kw), None) == expect
 
 
 @pytest.mark.parametrize("kw,expect", [
@@ -138,8 +145,12 @@ def test_prefill_fp4_refuses(kw, expect):
 def test_gather_fp4_refuses(kw, expect):
     a = dict(k=FAKE, v=FAKE, kc=FAKE, vc=FAKE, slots=FAKE, n=3, H=2, D=128, NB=16, bs=16, ks=1.0, vs=1.0, dt=B.PA_BF16)
     a.update(kw)
-    assert B.load().pa_gather_fp4(a["k"], a["v"], a["kc"], a["vc"], a["slots"], a["n"], a["H"], a["D"], a["NB"], a["bs"],
-                                  a["ks"], a["vs"], a["dt"], None) == expect
+    d = B.Fp4RowsDesc()
+    for field, key in (("k_out", "k"), ("v_out", "v"), ("k_cache", "kc"), ("v_cache", "vc"), ("slots", "slots"), ("num_slots", "n"),
+                       ("num_kv_heads", "H"), ("head_dim", "D"), ("num_blocks", "NB"), ("block_size", "bs"), ("dtype", "dt"),
+                       ("k_scale", "ks"), ("v_scale", "vs")):
+        setattr(d, field, a[key])
+    assert B.load().pa_gather_fp4(ctypes.byref(d), None) == expect
 
 
 @pytest.mark.parametrize("kw,expect", [
@@ -164,24 +175,27 @@ def test_pool_size_for_memory():
     assert B.pa_bm_num_blocks_for_memory(1 << 30, 1.0, 1, 4, 72, B.PA_FP4) == -1
 
 
-def test_rotate_desc_layout_matches_the_header(tmp_path):
+@pytest.mark.parametrize("name,desc,pack", [("pa_rotate", B.RotateDesc, B._pack_rotate),
+                                            ("pa_fp4_attention", B.Fp4AttentionDesc, B._pack_attention),
+                                            ("pa_fp4_rows", B.Fp4RowsDesc, B._pack_rows)])
+def test_descriptors_match_the_header(tmp_path, name, desc, pack):
     gcc = shutil.which("gcc")
     if gcc is None:
         pytest.skip("needs gcc")
-    names = [f[0] for f in B.RotateDesc._fields_]
+    names = [f[0] for f in desc._fields_]
     src = tmp_path / "layout.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "pa.h"\nint main(void) {\n'
-                   '  printf("%zu\\n", sizeof(pa_rotate));\n' +
-                   "".join(f'  printf("%zu\\n", offsetof(pa_rotate, {n}));\n' for n in names) + "  return 0;\n}\n")
+                   f'  printf("%zu\\n", sizeof({name}));\n' +
+                   "".join(f'  printf("%zu\\n", offsetof({name}, {n}));\n' for n in names) + "  return 0;\n}\n")
     exe = tmp_path / "layout"
     subprocess.run([gcc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
-    assert got == [ctypes.sizeof(B.RotateDesc)] + [getattr(B.RotateDesc, n).offset for n in names]
-    # the packed form that the binding passes
+    assert got == [ctypes.sizeof(desc)] + [getattr(desc, n).offset for n in names]
+    # the packed form that the binding passes: every field in its place, the same size
     values = list(range(1, len(names) + 1))
-    packed = B._pack_rotate(*values)
-    assert len(packed) <= ctypes.sizeof(B.RotateDesc)
-    d = B.RotateDesc.from_buffer_copy(packed.ljust(ctypes.sizeof(B.RotateDesc), b"\0"))
+    packed = pack(*values)
+    assert len(packed) == ctypes.sizeof(desc)
+    d = desc.from_buffer_copy(packed)
     assert [getattr(d, n) for n in names] == values
 
 
