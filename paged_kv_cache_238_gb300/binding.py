@@ -807,8 +807,9 @@ def pa_rotate_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, sl
     dt, dev, i64 = k.dtype, k.get_device(), torch.int64
     code = PA_BF16 if dt is torch.bfloat16 else _dtype_code(k)
     fp4 = k_cache.dtype is torch.uint8
-    if k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2 or (q is not None and q.dim() != 3):
-        raise ValueError("q and k are [T, heads, D], the pools have four dimensions, cos_sin two")
+    if (k.dim() != 3 or k_cache.dim() != 4 or cos_sin.dim() != 2 or (q is None) != (q_out is None) or
+            (q is not None and q.dim() != 3)):
+        raise ValueError("q and k are [T, heads, D], the pools have four dimensions, cos_sin two; q and q_out go together")
     T, H_kv, D = k_shape = k.shape
     NB, _, BS, _ = pool = k_cache.shape
     longest, R = cos_sin.shape

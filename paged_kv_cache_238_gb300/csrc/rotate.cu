@@ -74,12 +74,13 @@ __device__ __forceinline__ float rounded<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float rounded<uint16_t>(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-// a c + b s to about 45 bits, rounded once.
+// a c + b s to about 45 bits, rounded once; what is not finite is the plain sum (its error terms are NaN).
 __device__ __forceinline__ float turn_exact(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p), r = __fmul_rn(b, s), re = __fmaf_rn(b, s, -r);
     const float sum = __fadd_rn(p, r), z = __fsub_rn(sum, p);
     const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, z)), __fsub_rn(r, z));  // p + r = sum + e
-    return __fadd_rn(sum, __fadd_rn(e, __fadd_rn(pe, re)));
+    const float full = __fadd_rn(sum, __fadd_rn(e, __fadd_rn(pe, re)));
+    return full == full ? full : sum;
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {

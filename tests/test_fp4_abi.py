@@ -208,6 +208,9 @@ def test_binding_refuses_host_tensors():
     i64, cs = torch.zeros(2, dtype=torch.int64), torch.zeros(9, 128)
     with pytest.raises(ValueError):
         B.pa_rotate_and_cache(t, t, k, k, i64, cs, pool, pool, i64)
+    for q_out, q in ((None, t), (t, None)):
+        with pytest.raises(ValueError, match="go together"):
+            B.pa_rotate_and_cache(q_out, q, k, k, i64, cs, pool, pool, i64)
     with pytest.raises(ValueError):
         B.pa_decode_fp4(t, t, pool, pool, table, lens, 64, 0.1)
     with pytest.raises(ValueError):

@@ -201,6 +201,38 @@ def test_numbers_without_a_code():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_turns_that_are_infinite(dtype, interleaved):
+    """An infinity turned is two infinities (its angle's sine and cosine are not zero), and so is a turn past the type's
+    range: stored as the largest code under the largest scale. Other groups are as ever."""
+    n = New(3, 1, 1, 64, 64, 16, dtype, True)
+    n.pos[:] = 1
+    i = 9  # a pair whose angle is neither small nor near a multiple of 90 degrees
+    angle = np.float32(0.7)
+    n.cs[1, i], n.cs[1, 32 + i] = np.cos(angle), np.sin(angle)
+    lo, hi = (2 * i, 2 * i + 1) if interleaved else (i, 32 + i)
+    x = n.x[:, 1:2].copy()
+    x[0, 0, lo] = np.inf
+    x[1, 0, hi] = -np.inf
+    x[2, 0, [lo, hi]] = 3e38
+    n.bits[:, 1:2] = typed(x, dtype)
+    n.k = to_dev(n.bits[:, 1:2].copy())
+    n.run(interleaved)
+    out = [torch.empty(3, 1, 64, dtype=torch.float32, device="cuda") for _ in range(2)]
+    B.pa_gather_fp4(*out, *n.pools, to_dev(n.slots))
+    got = out[0].cpu().numpy()[:, 0]
+    assert np.isfinite(got).all()
+    assert (got[0, [lo, hi]] == 2688.0).all()
+    assert (got[1, [lo, hi]] == [2688.0, -2688.0]).all()
+    assert got[2, hi] == 2688.0  # 3e38 (cos + sin)
+    k, _ = R.rotate(n.x[:, 1:2], n.cs[n.pos].astype(np.float64), interleaved)
+    codes, scales = R.quantise(R.rounded(k, dtype))
+    want = R.GRID[codes & 7] * np.where(codes & 8, -1, 1) * np.repeat(R.e4m3_values(scales), 16, axis=-1)
+    same = ~np.isin(np.arange(64) // 16, [lo // 16, hi // 16])
+    assert (got[:, same] == want[:, 0][:, same]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H,D,BS", [(1, 64, 16), (3, 128, 32), (8, 128, 128)])
 def test_gather(dtype, H, D, BS):
     rng = np.random.default_rng(3)
