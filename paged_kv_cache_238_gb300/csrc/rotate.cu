@@ -13,10 +13,10 @@
 // bits it owns the 16 dims of a group instead, and reads what they rotate with (again, from L1). A grid row per kind keeps
 // a warp's threads on one path: with the kinds of a token side by side the pool's own type took 39 us and 4 bits 71.
 //
-// Bound: HBM in the pool's own type (8448 tokens, 32 q / 8 kv heads of 128, bf16: 36.2 us, 5.9 TB/s, 86 % of the measured copy
-// rate); in 4 bits the latency of a group's loads at 24 warps an SM and its arithmetic, about 20 instructions an
-// element of k and 7 of v (37 us of 48 with the read of the pool; with a division per element 58).
-// 64 tokens: 2.1 us, in 4 bits and read back 4.3.
+// Bound: HBM in the pool's own type (8448 tokens, 32 q / 8 kv heads of 128, bf16: 34.4 us, 6.2 TB/s, 91 % of the measured copy
+// rate; loads row by row 36.2); in 4 bits the latency of a group's loads at 24 warps an SM and its arithmetic, about 20 instructions an
+// element of k and 7 of v (37.5 us of 48.5 with the read of the pool; with a division per element 58).
+// 64 tokens: 2.2 us, in 4 bits and read back 4.5.
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -34,6 +34,7 @@ template <>
 struct Chunk<uint16_t> {
     uint4 v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load_plain(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -53,6 +54,10 @@ struct Chunk<float> {
     __device__ __forceinline__ void load(const float* p) {
         a = __ldg(reinterpret_cast<const float4*>(p));
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void load_plain(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void store(float* p) const {
         reinterpret_cast<float4*>(p)[0] = a;
@@ -245,30 +250,40 @@ __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_consta
         dst = static_cast<T*>(kind == 1 ? a.k_cache : a.v_cache) + (((block * a.num_kv_heads) << a.bs_log2) + at) * D;
         step = static_cast<int64_t>(D) << a.bs_log2;
     }
-#pragma unroll 4
-    for (int32_t h = h0; h < h1; ++h) {
-        const T* row = src + static_cast<int64_t>(h) * D;
-        Chunk<T> lo, hi;
-        lo.load(row + 8 * c0);
-        hi.load(row + 8 * c1);
-        if (halves) {
-            float x[8], y[8];
-            lo.get(x);
-            hi.get(y);
+    // several rows' loads before their stores (fp32: two, whose 32 registers four in bf16 take as well): q_out may be q, so
+    // these loads are ordinary ones, which the compiler does not move above the stores of rows before
+    constexpr int kAhead = 8 / sizeof(T);
+    for (int32_t h = h0; h < h1; h += kAhead) {
+        Chunk<T> lo[kAhead], hi[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x0 = x[i], y0 = y[i];
-                x[i] = fmaf(x0, c[i], -(y0 * s[i]));
-                y[i] = fmaf(y0, c[i], x0 * s[i]);
-            }
-            lo.put(x);
-            hi.put(y);
-        } else if (INTERLEAVED) {
-            if (turned0) turn_pairs(lo, c, s);
-            if (turned1) turn_pairs(hi, c + 4, s + 4);
+        for (int x = 0; x < kAhead; ++x) {
+            if (h + x >= h1) continue;
+            const T* row = src + static_cast<int64_t>(h + x) * D;
+            lo[x].load_plain(row + 8 * c0);
+            hi[x].load_plain(row + 8 * c1);
         }
-        lo.store(dst + h * step + 8 * c0);
-        hi.store(dst + h * step + 8 * c1);
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            if (h + x >= h1) continue;
+            if (halves) {
+                float y0[8], y1[8];
+                lo[x].get(y0);
+                hi[x].get(y1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x0 = y0[i], x1 = y1[i];
+                    y0[i] = fmaf(x0, c[i], -(x1 * s[i]));
+                    y1[i] = fmaf(x1, c[i], x0 * s[i]);
+                }
+                lo[x].put(y0);
+                hi[x].put(y1);
+            } else if (INTERLEAVED) {
+                if (turned0) turn_pairs(lo[x], c, s);
+                if (turned1) turn_pairs(hi[x], c + 4, s + 4);
+            }
+            lo[x].store(dst + (h + x) * step + 8 * c0);
+            hi[x].store(dst + (h + x) * step + 8 * c1);
+        }
     }
 }
 
