@@ -1,6 +1,7 @@
-// Decode over a 4-bit pool for bf16 queries: one query row per sequence, on mma.sync in fp16 with pages staged by
-// bulk copies. The pool's values (code * scale, 6 significant bits, fp4.cuh) are exact in fp16; a q head's row is
-// brought to fp16 by a power of two; weights are rounded to fp16, everything else is fp32.
+// Decode over a 4-bit pool: one query row per sequence, on mma.sync in fp16 with pages staged by bulk copies. The pool's
+// values (code * scale, 6 significant bits, fp4.cuh) are exact in fp16; a q head's row is brought to fp16 by a power of
+// two; weights are rounded to fp16, everything else is fp32. fp32 queries and their weights are sums of two halves, which
+// takes twice the MMAs but unpacks no more.
 //
 // Work list, slices and joins are those of the scored decode kernel (decode_scored.cu): a unit is one page of 16
 // tokens of one segment (sequence, kv head, chunk of up to 16 of the kv head's q heads); every CTA builds the list's
@@ -26,6 +27,8 @@
 // 64 q / 8 kv heads of 128: 57 us, 4.2 TB/s, 62 % of the measured copy rate (32 sequences of 32768: 228 us, 78 %); 64 of 500
 // to 16384, 32 q / 8 kv heads: 75 us (67 %), of which 4.4 pass until the first pages have come and 8 to 11 go to the slowest
 // SM and the joins. 4 sequences of up to 700 keys: 9.1 us in a graph, a chain of latencies.
+// fp32 queries (before on the CUDA cores): 8 of 8000 to 9000 keys, 16 q / 4 kv heads of 128, 21.9 us (54.8); 64 of 10 to
+// 2000, 16 heads of 64, 21.7 (58.1); 24 of up to 777, 12 q / 4 kv heads of 64, 10.2 (12.1).
 #include <math.h>
 
 #include <type_traits>
@@ -47,6 +50,16 @@ constexpr float kJoinWeight = 1.f / 1.5f;  // a segment of n units is cut into a
 constexpr int kSegmentUnits = 4;
 constexpr float kLag = 8.f;                // log2 units; weights stay below 2^8, within fp16
 constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
+
+// How q of type T and the weights come to fp16. bf16: q's row as it is once its largest magnitude lies in [1, 2), the
+// weights rounded. fp32: both as sums of two halves, 22 bits; the row's largest magnitude in [2^14, 2^15) and a weight of 2^7
+// at the reference keep what is small next to them within fp16's range (2^-39 of the row's largest, 2^-32 of a weight of 1).
+template <typename T>
+struct Fp16Form {
+    static constexpr bool kTwo = std::is_same<T, float>::value;
+    static constexpr int kPieces = kTwo ? 2 : 1, kTop = kTwo ? 14 : 0;  // a row's largest magnitude: 2^kTop ..
+    static constexpr float kAbove = kTwo ? 7.f : 0.f;                   // log2 of the weight of a score at the reference
+};
 
 // Pages of one step of a warp, and room for one step: 64 sequences of 500 to 16384 keys 76 us, with steps of two pages and
 // room for two or four of them 85.
@@ -76,8 +89,8 @@ __host__ __device__ inline Layout layout(int NW, int hs, int D, int S) {
 }
 
 struct Params {
-    __nv_bfloat16* out;
-    const __nv_bfloat16* q;
+    void* out;
+    const void* q;
     const uint8_t* k_cache;
     const uint8_t* v_cache;
     const int32_t* block_table;
@@ -137,6 +150,12 @@ __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+}
+__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
+    *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -194,12 +213,15 @@ struct Piece {
 };
 
 // NH: groups of 8 q heads of a segment (up to 8 NH heads).
-template <int D, int NW, int NH>
+template <typename T, int D, int NW, int NH>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_fp4_kernel(const __grid_constant__ Params a) {
     constexpr uint32_t kPage = fp4_page_bytes(D), kScales = fp4_scales_at(D);
     constexpr int KS = D / 16, NMT = D / 16, SP = kStepPages, DL = D / 8;  // DL: dims of a lane's V rows
     constexpr int NTH = NW * 32;
+    using F = Fp16Form<T>;
+    constexpr int PC = F::kPieces, QW = 2 * PC;  // halves of a number; words of 4 elements of q
+    T* const out = static_cast<T*>(a.out);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int32_t S = a.S, G = a.G, NHC = a.head_chunks, Hq = G * a.num_kv_heads;
@@ -274,8 +296,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     // rows that see nothing are zero (spread over the CTAs)
     for (int32_t s = blockIdx.x; s < S; s += gridDim.x) {
         if (prefix[s + 1] != prefix[s]) continue;
-        uint32_t* z = reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(s) * Hq * D);
-        for (int32_t i = tid; i < Hq * D / 2; i += NTH) z[i] = 0u;
+        uint32_t* z = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(s) * Hq * D);
+        for (int32_t i = tid; i < Hq * D / 4 * QW; i += NTH) z[i] = 0u;
     }
     const int64_t first = static_cast<int64_t>(blockIdx.x) * chunk;
     if (first >= U) return;  // uniform over the CTA
@@ -343,10 +365,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
         Cursor wc;
         wc.at(prefix, lens, S, a_w);
         // Fragment ownership (gid = lane / 4, tig = lane % 4):
-        //   qb[f][ks]   Q^T as B: head 8 f + gid, dims tig D / 4 + 4 ks .. + 3
+        //   qb[f][c][ks] Q^T as B, piece c: head 8 f + gid, dims tig D / 4 + 4 ks .. + 3
         //   sc[i][f][e] S^T of page i: key key_of(gid + 8 (e / 2)), head 8 f + 2 tig + e % 2
         //   acc[f][mt]  O^T: head_dim gid D / 8 + 2 mt + e / 2, head 8 f + 2 tig + e % 2
-        uint32_t qb[NH][KS][2];
+        uint32_t qb[NH][PC][KS][2];
         float acc[NH][NMT][4], mh[NH][2], lh[NH][2], c1[NH][2];
         int32_t ng = 0, head0 = 0;
         bool cut_left = false;
@@ -396,7 +418,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         const uint32_t fa[4] = {hmul2(h0[2 * x], m0), hmul2(h1[2 * x], m1), hmul2(h0[2 * x + 1], m0),
                                                 hmul2(h1[2 * x + 1], m1)};
 #pragma unroll
-                        for (int f = 0; f < NH; ++f) mma_f16(sc[i][f], fa, qb[f][2 * w + x][0], qb[f][2 * w + x][1]);
+                        for (int f = 0; f < NH; ++f)
+#pragma unroll
+                            for (int c = 0; c < PC; ++c) mma_f16(sc[i][f], fa, qb[f][c][2 * w + x][0], qb[f][c][2 * w + x][1]);
                     }
                 }
             }
@@ -430,7 +454,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int f = 0; f < NH; ++f) top = max3(max3(top, x[i][f][0], x[i][f][1]), x[i][f][2], x[i][f][3]);
-            if (__any_sync(0xffffffffu, top > kLag)) {
+            if (__any_sync(0xffffffffu, top > F::kAbove + kLag)) {
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
                     float cc[2];
@@ -441,7 +465,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         for (int i = 0; i < NP; ++i) mx = max3(mx, sc[i][f][hh] * c1[f][hh], sc[i][f][2 + hh] * c1[f][hh]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        const float mn = fmaxf(mh[f][hh], mx);
+                        const float mn = fmaxf(mh[f][hh], mx - F::kAbove);
                         cc[hh] = exp2_approx(mh[f][hh] - mn);
                         mh[f][hh] = mn;
                         lh[f][hh] *= cc[hh];
@@ -456,7 +480,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 }
                 shifted();
             }
-            uint32_t pb[NP][NH][2];
+            uint32_t pb[NP][NH][PC][2];
 #pragma unroll
             for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -467,8 +491,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     uint64_t l2 = pack2(lh[f][0], lh[f][1]);
                     l2 = add2(add2(l2, pack2(p[0], p[1])), pack2(p[2], p[3]));
                     unpack2(l2, lh[f][0], lh[f][1]);
-                    pb[i][f][0] = movmatrix_trans(pack_halves(p[0], p[1]));
-                    pb[i][f][1] = movmatrix_trans(pack_halves(p[2], p[3]));
+#pragma unroll
+                    for (int c = 0; c < PC; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t h = pack_halves(p[2 * e], p[2 * e + 1]);
+                            pb[i][f][c][e] = movmatrix_trans(h);
+                            if (c + 1 < PC) {  // what it leaves
+                                const float2 held = halves_to_floats(h);
+                                p[2 * e] -= held.x;
+                                p[2 * e + 1] -= held.y;
+                            }
+                        }
                 }
             // ---- O^T += V^T P^T ----
             if (wait_v && !landed(&bars[1], v_steps - 1)) return false;
@@ -505,7 +539,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int b = 0; b < 4; ++b) {
                         const uint32_t fa[4] = {hmul2(e0[b], m0), hmul2(o0[b], m0), hmul2(e1[b], m1), hmul2(o1[b], m1)};
 #pragma unroll
-                        for (int f = 0; f < NH; ++f) mma_f16(acc[f][4 * x + b], fa, pb[i][f][0], pb[i][f][1]);
+                        for (int f = 0; f < NH; ++f)
+#pragma unroll
+                            for (int c = 0; c < PC; ++c) mma_f16(acc[f][4 * x + b], fa, pb[i][f][c][0], pb[i][f][c][1]);
                     }
                 }
             }
@@ -521,7 +557,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             const bool page_here = wc.j < wc.np;
             cnt = min(min(SP - slot, n - t), (page_here ? wc.np : wc.np + kSegmentUnits) - wc.j);
             const bool step_first = slot == 0, step_last = slot + cnt == SP;
-            uint32_t raw[NH][KS][2];
+            uint32_t raw[NH][KS][QW];  // 4 elements of q each
             const bool fresh = page_here && first_page;
             if (fresh) {  // a new segment: its query rows, on their way while the step's pages are waited for
                 const int32_t hk = wc.h / NHC, g0 = (wc.h - hk * NHC) * kMaxHeads;
@@ -529,11 +565,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 head0 = hk * G + g0;
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
-                    const __nv_bfloat16* row = a.q + (static_cast<int64_t>(wc.s) * Hq + head0 + f * 8 + gid) * D + tig * (D / 4);
+                    const T* row = static_cast<const T*>(a.q) + (static_cast<int64_t>(wc.s) * Hq + head0 + f * 8 + gid) * D + tig * (D / 4);
 #pragma unroll
-                    for (int ks = 0; ks < KS; ks += 2) {
+                    for (int ks = 0; ks < KS; ks += 4 / QW) {
                         const uint4 w = f * 8 + gid < ng ? __ldg(reinterpret_cast<const uint4*>(row + 4 * ks)) : make_uint4(0u, 0u, 0u, 0u);
-                        raw[f][ks][0] = w.x, raw[f][ks][1] = w.y, raw[f][ks + 1][0] = w.z, raw[f][ks + 1][1] = w.w;
+                        raw[f][ks][0] = w.x, raw[f][ks][1] = w.y;
+                        if constexpr (F::kTwo) raw[f][ks][2] = w.z, raw[f][ks][3] = w.w;
+                        else raw[f][ks + 1][0] = w.z, raw[f][ks + 1][1] = w.w;
                     }
                 }
             }
@@ -549,25 +587,39 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (fresh) {
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
-                    // the row to fp16: times 2^-e with 2^e <= its largest magnitude < 2^(e + 1)
+                    // the row to fp16: times 2^(kTop - e) with 2^e <= its largest magnitude < 2^(e + 1)
+                    auto element = [&](int ks, int x) -> float {
+                        if constexpr (F::kTwo) return __uint_as_float(raw[f][ks][x]);
+                        else return __uint_as_float(x & 1 ? raw[f][ks][x / 2] & 0xffff0000u : raw[f][ks][x / 2] << 16);
+                    };
                     float top = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            top = max3(top, fabsf(__uint_as_float(raw[f][ks][x] << 16)), fabsf(__uint_as_float(raw[f][ks][x] & 0xffff0000u)));
+                        for (int x = 0; x < 4; x += 2) top = max3(top, fabsf(element(ks, x)), fabsf(element(ks, x + 1)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
-                    const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;  // (not finite: as it is)
+                    // (not finite: as it is; rows below 2^-112: times 2^126)
+                    const int32_t e = field == 255 ? 0 : min(max(field, 1 + F::kTop), 253 + F::kTop) - 127 - F::kTop;
                     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                     const float up2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            qb[f][ks][x] = pack_halves(__uint_as_float(raw[f][ks][x] << 16) * down,
-                                                       __uint_as_float(raw[f][ks][x] & 0xffff0000u) * down);
+                        for (int x = 0; x < 2; ++x) {
+                            float y0 = element(ks, 2 * x) * down, y1 = element(ks, 2 * x + 1) * down;
+#pragma unroll
+                            for (int c = 0; c < PC; ++c) {
+                                const uint32_t h = pack_halves(y0, y1);
+                                qb[f][c][ks][x] = h;
+                                if (c + 1 < PC) {  // what it leaves, exactly
+                                    const float2 held = halves_to_floats(h);
+                                    y0 -= held.x;
+                                    y1 -= held.y;
+                                }
+                            }
+                        }
 #pragma unroll
                     for (int mt = 0; mt < NMT; ++mt) acc[f][mt][0] = acc[f][mt][1] = acc[f][mt][2] = acc[f][mt][3] = 0.f;
 #pragma unroll
@@ -611,7 +663,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 const int slot = cut_left ? 0 : 1;  // a piece cut on the left is the part's first, else its last
                 __syncwarp();                           // slot 1 reuses the ring, idle after the last page
                 float* pa_acc = slot == 0 ? piece0 + static_cast<uint32_t>(warp) * hs * D : reinterpret_cast<float*>(ring);
-                __nv_bfloat16* o = a.out + (static_cast<int64_t>(wc.s) * Hq + head0) * D;
+                T* o = out + (static_cast<int64_t>(wc.s) * Hq + head0) * D;
 #pragma unroll
                 for (int f = 0; f < NH; ++f)
 #pragma unroll
@@ -620,13 +672,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         if (head >= ng) continue;
                         if (inside) {
                             const float inv = Lh[f][hh] == 0.f ? 0.f : a.v_scale / Lh[f][hh];
-                            uint32_t w[DL / 2];
 #pragma unroll
-                            for (int mt = 0; mt < NMT; ++mt) w[mt] = pack_bf16x2(acc[f][mt][hh] * inv, acc[f][mt][2 + hh] * inv);
-#pragma unroll
-                            for (int c = 0; c < DL / 8; ++c)
-                                *reinterpret_cast<uint4*>(o + head * D + gid * DL + 8 * c) =
-                                    make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                            for (int c = 0; c < DL / 4; ++c)
+                                store4(o + head * D + gid * DL + 4 * c, acc[f][2 * c][hh] * inv, acc[f][2 * c][2 + hh] * inv,
+                                       acc[f][2 * c + 1][hh] * inv, acc[f][2 * c + 1][2 + hh] * inv);
                         } else {
 #pragma unroll
                             for (int mt = 0; mt < NMT; ++mt)
@@ -721,8 +770,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 r.w = fmaf(w, v.w, r.w);
             }
             if (complete) {
-                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
-                    make_uint2(pack_bf16x2(r.x * a.v_scale, r.y * a.v_scale), pack_bf16x2(r.z * a.v_scale, r.w * a.v_scale));
+                store4(out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d, r.x * a.v_scale, r.y * a.v_scale,
+                       r.z * a.v_scale, r.w * a.v_scale);
             } else {
                 const int64_t pg = (static_cast<int64_t>(blockIdx.x) * 2 + cslot) * hs + g;
                 *reinterpret_cast<float4*>(a.piece_o + pg * D + d) = r;
@@ -765,8 +814,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         };
         auto put = [&](int32_t g, int32_t d, float den, const float4 r) {
             const float inv = den == 0.f ? 0.f : a.v_scale / den;
-            *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d) =
-                make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+            store4(out + (static_cast<int64_t>(pc.s) * Hq + hk * G + g0 + g) * D + d, r.x * inv, r.y * inv, r.z * inv, r.w * inv);
         };
         for (int32_t i = tid; i < cols * shares; i += NTH) {  // one round unless a head chunk has more columns
             const int32_t sh = i / cols, col = i - sh * cols, g = col / V4, d = (col - g * V4) * 4;
@@ -806,7 +854,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 }
 
-template <int D, int NW, int NH>
+template <typename T, int D, int NW, int NH>
 cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {
     const int32_t G = d.num_q_heads / d.num_kv_heads, hs = G < kMaxHeads ? G : kMaxHeads;
     Params a{};
@@ -839,30 +887,31 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
     for (int32_t s0 = 0; s0 < d.num_seqs; s0 += plan.batch) {
         const int32_t S = d.num_seqs - s0 < plan.batch ? d.num_seqs - s0 : plan.batch;
         a.S = S;
-        a.out = static_cast<__nv_bfloat16*>(d.out) + static_cast<int64_t>(s0) * d.num_q_heads * D;
-        a.q = static_cast<const __nv_bfloat16*>(d.q) + static_cast<int64_t>(s0) * d.num_q_heads * D;
+        a.out = static_cast<T*>(d.out) + static_cast<int64_t>(s0) * d.num_q_heads * D;
+        a.q = static_cast<const T*>(d.q) + static_cast<int64_t>(s0) * d.num_q_heads * D;
         a.block_table = d.block_table + static_cast<int64_t>(s0) * d.max_blocks_per_seq;
         a.seq_lens = d.seq_lens + s0;
         const Layout l = layout(NW, hs, D, S);
-        cudaError_t e = allow_smem<decode_fp4_kernel<D, NW, NH>>(static_cast<int>(l.total));
+        cudaError_t e = allow_smem<decode_fp4_kernel<T, D, NW, NH>>(static_cast<int>(l.total));
         if (e != cudaSuccess) return e;
         cfg.dynamicSmemBytes = l.total;
-        e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, NW, NH>, a);
+        e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<T, D, NW, NH>, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-template <int D>
+template <typename T, int D>
 cudaError_t pick(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {
-    if (a.num_q_heads / a.num_kv_heads > 8) return launch_impl<D, 8, 2>(a, v_scale, plan, stream);
-    return D == 64 ? launch_impl<D, 16, 1>(a, v_scale, plan, stream) : launch_impl<D, 12, 1>(a, v_scale, plan, stream);
+    constexpr int kWarps = D == 64 ? 16 : Fp16Form<T>::kTwo ? 8 : 12;
+    if (a.num_q_heads / a.num_kv_heads > 8) return launch_impl<T, D, 8, 2>(a, v_scale, plan, stream);
+    return launch_impl<T, D, kWarps, 1>(a, v_scale, plan, stream);
 }
 
 }  // namespace
 
-bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len, const DeviceInfo& dev,
-                     DecodeScoredPlan* plan) {
+bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len, pa_dtype dtype,
+                     const DeviceInfo& dev, DecodeScoredPlan* plan) {
     const int32_t G = Hq / Hkv, hs = G < kMaxHeads ? G : kMaxHeads;
     const int64_t nh = static_cast<int64_t>(Hkv) * ((G + kMaxHeads - 1) / kMaxHeads);
     // sequences of one launch: their segments have counters, and units are counted in 32 bits
@@ -875,8 +924,8 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
     plan->num_ctas = dev.num_sms;
     // Warps in fours, for the four schedulers, as many as registers allow without spilling. Up to 8 heads, D = 128: 75 us with
     // 12 (64 sequences of 500 to 16384 keys), 8: 101, 10: 86, 14: 84, 16 (spilled): 77; D = 64: 23.7 with 16 (96 of 16 to
-    // 2048), 12: 24.8. Twice the accumulators (more than 8 heads) leave room for 8.
-    plan->warps = G > 8 ? 8 : D == 64 ? 16 : 12;
+    // 2048), 12: 24.8. Twice the accumulators (more than 8 heads), or twice the queries (fp32, D = 128), leave room for 8.
+    plan->warps = G > 8 ? 8 : D == 64 ? 16 : dtype == PA_F32 ? 8 : 12;
     if (layout(plan->warps, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) return false;
     plan->stages = 1;
     plan->workspace_bytes = kScoredCounterBytes + static_cast<size_t>(plan->num_ctas) * 2 * hs * (D * 4 + 8);
@@ -884,7 +933,10 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {
-    return a.head_dim == 128 ? pick<128>(a, v_scale, plan, stream) : pick<64>(a, v_scale, plan, stream);
+    if (a.dtype == PA_F32)
+        return a.head_dim == 128 ? pick<float, 128>(a, v_scale, plan, stream) : pick<float, 64>(a, v_scale, plan, stream);
+    return a.head_dim == 128 ? pick<__nv_bfloat16, 128>(a, v_scale, plan, stream)
+                             : pick<__nv_bfloat16, 64>(a, v_scale, plan, stream);
 }
 
 }  // namespace pa

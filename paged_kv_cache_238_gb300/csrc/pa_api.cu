@@ -711,7 +711,7 @@ PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads
     DeviceCache* dev = nullptr;
     if (device_cache(&dev) != cudaSuccess) return 0;
     DecodeScoredPlan plan;
-    if (dtype == PA_BF16 && plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &plan))
+    if (plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dtype, dev->info, &plan))
         return plan.workspace_bytes;
     return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms, kFp4MinPages)
         .workspace_bytes;
@@ -737,8 +737,7 @@ PA_API pa_status pa_decode_fp4(const pa_fp4_attention* c, void* stream) {
     a.err = dev->err;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     DecodeScoredPlan fast;
-    if (dtype == PA_BF16 &&
-        plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info, &fast)) {
+    if (plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dtype, dev->info, &fast)) {
         if (!workspace || workspace_bytes < fast.workspace_bytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
         return launch_decode_fp4(a, v_scale, fast, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }

@@ -290,9 +290,10 @@ struct GatherFp4Args {
 };
 cudaError_t launch_gather_fp4(const GatherFp4Args& a, cudaStream_t stream);
 
-// Decode over 4-bit pools, bf16 queries (decode_fp4.cu); k_scale is in a.scale.
+// Decode over 4-bit pools (decode_fp4.cu); k_scale is in a.scale. plan_decode_fp4: false where it does not apply (more
+// segments in a sequence, or more keys, than it counts).
 bool plan_decode_fp4(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
-                     const DeviceInfo& dev, DecodeScoredPlan* plan);
+                     pa_dtype dtype, const DeviceInfo& dev, DecodeScoredPlan* plan);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream);
 
 // Tensor-core prefill over 4-bit pools (prefill_fp4.cu): bf16 queries, up to 128 q heads per kv head.

@@ -17,6 +17,10 @@ Attention, with A = sum_j softmax(z)_j |v_j|, n visible keys:
   * sums over n keys in fp32, cut or rounded: 4 (n + 16) u A;
   * bf16 queries: weights rounded to fp16 (2^-11), those below 2^-14 of the largest to 2^-25: 2^-11 A + n 2^-25 max |v|;
     where they are rounded to bf16 instead (CUDA cores do not round): covered by 2^-11 as well, since none is;
+  * fp32 queries on the tensor cores: q and the weights as sums of two halves. A row's largest magnitude lies in
+    [2^14, 2^15), so q_d is off by max(2^-22 |q_d|, 2^-25), the latter 2^-39 qmax: 4 u sum |q_d k_d| of the 2 (D + 16) u
+    above, and scale qmax 2^-39 sum_d |k_d| more. The largest weight is 2^7 at least, so a weight w of a sum l is off by
+    max(2^-22 w, 2^-25), 2^-25 being 2^-32 l at most: with the 2^-22 of the exponential, 2^-21, and n 2^-32 max |v|;
   * the output rounded once: 2^-8 (bf16) or u.
 """
 from __future__ import annotations
@@ -163,11 +167,13 @@ class Case:
                 dz = 2 * (self.D + 16) * U * mag + 8 * U * np.abs(np.where(vis, z, 0)).max(1)
                 if self.dtype == "bf16":
                     dz = dz + abs(self.scale) * np.abs(qs).max(1) * 2.0 ** -24 * np.abs(k).sum(1).max()
+                else:
+                    dz = dz + abs(self.scale) * np.abs(qs).max(1) * 2.0 ** -39 * np.abs(k).sum(1).max()
                 w = np.exp(z - z.max(1, keepdims=True))
                 w /= w.sum(1, keepdims=True)
                 o, A, n = w @ v, w @ np.abs(v), vis.sum(1)
                 rel = 2 * (dz + 2.0 ** -21) * (1 + dz) + 4 * (n + 16) * U + (2.0 ** -11 if self.dtype == "bf16" else 0.0)
-                err = rel[:, None] * A + (n[:, None] * 2.0 ** -25 * np.abs(v).max() if self.dtype == "bf16" else 0.0)
+                err = rel[:, None] * A + n[:, None] * (2.0 ** -25 if self.dtype == "bf16" else 2.0 ** -32) * np.abs(v).max()
                 out[r0:r0 + C, h] = o
                 tol[r0:r0 + C, h] = err + half * (np.abs(o) + err)
         return out, tol
