@@ -760,7 +760,7 @@ PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_
     PrefillArgs a{};
     a.dtype = dtype, a.num_seqs = num_seqs, a.num_q_heads = num_q_heads, a.num_kv_heads = num_kv_heads;
     if (prefill_fp4_tc_ok(a, dev->info))
-        return plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+        return plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len, dtype,
                                 dev->info.num_sms).workspace_bytes;
     return plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
                             dev->info.num_sms, kFp4MinPages).workspace_bytes;
@@ -789,7 +789,7 @@ PA_API pa_status pa_prefill_fp4(const pa_fp4_attention* c, void* stream) {
     };
     if (prefill_fp4_tc_ok(a, dev->info)) {
         const PrefillScoredPlan plan = plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
-                                                        max_seq_len, dev->info.num_sms);
+                                                        max_seq_len, c->dtype, dev->info.num_sms);
         if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
         const cudaError_t e = launch_prefill_fp4_tc(a, v_scale, plan, workspace, dev->info.num_sms, s);
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

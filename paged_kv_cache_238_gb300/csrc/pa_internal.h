@@ -296,10 +296,10 @@ bool plan_decode_fp4(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads
                      pa_dtype dtype, const DeviceInfo& dev, DecodeScoredPlan* plan);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream);
 
-// Tensor-core prefill over 4-bit pools (prefill_fp4.cu): bf16 queries, up to 128 q heads per kv head.
+// Tensor-core prefill over 4-bit pools (prefill_fp4.cu): up to 128 q heads per kv head.
 bool prefill_fp4_tc_ok(const PrefillArgs& a, const DeviceInfo& dev);
 PrefillScoredPlan plan_prefill_fp4(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,
-                                   int32_t head_dim, int32_t max_seq_len, int num_sms);
+                                   int32_t head_dim, int32_t max_seq_len, pa_dtype dtype, int num_sms);
 cudaError_t launch_prefill_fp4_tc(const PrefillArgs& a, float v_scale, const PrefillScoredPlan& plan, void* workspace,
                                   int num_sms, cudaStream_t stream);
 

@@ -45,11 +45,14 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
-// Of a CTA of NQ query tiles: warps of softmax, of unpacking (three beside the MMA warp, and a warpgroup where two tiles
-// share the keys), threads; tensor memory columns of O, of all.
-template <int NQ>
+// Of a CTA of NQ query tiles: halves that make a number of q or a weight (fp32: two), CTAs on an SM, warps of softmax, of
+// unpacking (three beside the MMA warp, and a warpgroup more in a CTA that has the SM to itself), threads; whether
+// registers move; tensor memory columns of O, of all.
+template <typename T, int D, int NQ>
 struct Roles {
-    static constexpr int soft = 8 * NQ, unpack = NQ == 2 ? 7 : 3, threads = 32 * (soft + unpack + 1);
+    static constexpr int pieces = std::is_same<T, float>::value ? 2 : 1, per_sm = NQ == 2 || pieces * D == 256 ? 1 : 2;
+    static constexpr int soft = 8 * NQ, unpack = per_sm == 1 ? 7 : 3, threads = 32 * (soft + unpack + 1);
+    static constexpr bool moved = per_sm == 2 || NQ == 2;
     static constexpr uint32_t o = NQ * 128, columns = NQ * 256;
 };
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 fp16 columns)
@@ -64,12 +67,13 @@ constexpr int kMinPartTiles = 2;          // key tiles of a run, at least, when 
 // 58.2 and 52.6. A chunk that fits one tile has one in any case (64 of 20 rows on 30 keys 19.5 and 31.9, on 2020 136 and 139).
 __host__ __device__ constexpr int short_keys(int D) { return D == 64 ? 768 : 192; }
 
-template <int D, int NQ>
+template <typename T, int D, int NQ>
 struct Smem {
-    static constexpr int k_stages = NQ == 1 ? 128 / D : D == 128 ? 2 : 4, v_stages = NQ == 1 ? 128 / D : D == 128 ? 3 : 4;
+    static constexpr int per_sm = Roles<T, D, NQ>::per_sm, pieces = Roles<T, D, NQ>::pieces;
+    static constexpr int k_stages = per_sm == 2 ? 128 / D : D == 128 ? 2 : 4, v_stages = per_sm == 2 ? 128 / D : D == 128 ? 3 : 4;
     static constexpr uint32_t tile = (D / 64) * kHalf;  // 128 x D fp16
     static constexpr uint32_t q = 0;                    // query tiles; in the end the outputs on their way
-    static constexpr uint32_t k = q + NQ * tile;
+    static constexpr uint32_t k = q + NQ * pieces * tile;
     static constexpr uint32_t v = k + k_stages * tile;
     static constexpr uint32_t bars = v + v_stages * tile;
     static constexpr int num_bars = 2 * k_stages + 2 * v_stages + 8;
@@ -87,8 +91,8 @@ struct Split {
 };
 
 struct Args {
-    __nv_bfloat16* out;
-    const __nv_bfloat16* q;
+    void* out;
+    const void* q;
     const uint8_t* k_cache;
     const uint8_t* v_cache;
     const int32_t* block_table;
@@ -201,11 +205,13 @@ struct RawRow {
     uint32_t scales[D / 64];  // 4 scales a word
 };
 
-template <int D, int NQ, bool SPLIT>
-__global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel(const __grid_constant__ Args a) {
-    using L_ = Smem<D, NQ>;
-    constexpr int kUnpackWarps = Roles<NQ>::unpack;
-    constexpr uint32_t kO = Roles<NQ>::o;
+template <typename T, int D, int NQ, bool SPLIT>
+__global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per_sm)
+    prefill_fp4_kernel(const __grid_constant__ Args a) {
+    using L_ = Smem<T, D, NQ>;
+    using Roles = Roles<T, D, NQ>;
+    constexpr int kUnpackWarps = Roles::unpack, kPieces = Roles::pieces;
+    constexpr uint32_t kO = Roles::o;
     constexpr uint32_t kTile = L_::tile;
     constexpr int kKStages = L_::k_stages, kVStages = L_::v_stages;
     extern __shared__ uint8_t smem_raw[];
@@ -236,14 +242,14 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
         fence_mbarrier_init();
     }
     if (warp == 0) {
-        umma::tmem_alloc(tmem_holder, Roles<NQ>::columns);
+        umma::tmem_alloc(tmem_holder, Roles::columns);
         umma::tmem_relinquish();
     }
     umma::fence_before_sync();
     auto leave = [&]() {  // a CTA without work: all threads have passed a barrier since the allocation
         if (warp == 0) {
             umma::fence_after_sync();
-            umma::tmem_dealloc(*tmem_holder, Roles<NQ>::columns);
+            umma::tmem_dealloc(*tmem_holder, Roles::columns);
         }
     };
 
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
         base = blockIdx.x * share;
         n_kv = min(share, n_kv - base);
         if (tid == 0 && blockIdx.x == 0 && n_parts > 1)
-            a.split.rows[cta] = make_int4(q0 + t0a, min(TT, C - t0a) * G, max(min(TT, C - t0b), 0) * G, n_parts);
+            a.split.rows[cta] = make_int4(q0 + t0a, min(TT, C - t0a) * G, NQ == 2 ? max(min(TT, C - t0b), 0) * G : 0, n_parts);
     }
     const int32_t n_a = min(max(all_a - base, 0), n_kv), n_b = min(max(all_b - base, 0), n_kv);
 
@@ -334,9 +340,9 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
     // softmax: query tile, half of the key tile, TMEM lane quadrant, row
     const int32_t x = NQ == 2 ? (group - 1) & 1 : 0, half = (NQ == 2 ? (group - 1) >> 1 : group - 1) & 1, quad = warp & 3, r = tid & 127;
     const uint32_t inv_G = 65536u / static_cast<uint32_t>(G) + 1;  // i / G = i inv_G / 2^16 for i, G <= 128
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kLoads = 16 / kPer;  // lanes of a query row, rows of a load, loads
+    constexpr int kLanes = D / 8 * kPieces, kPer = 32 / kLanes, kLoads = 16 / kPer;  // lanes of a query row, rows of a load, loads
     // Unit u: K (bit 2 clear) or V of key tile u / 8, keys 32 (u % 4) ..; this warp has every kUnpackWarps-th.
-    const int32_t u_first = group == 0 ? warp - 1 : warp - (4 + Roles<NQ>::soft) + 3, n_units = 8 * n_kv;
+    const int32_t u_first = group == 0 ? warp - 1 : warp - (4 + Roles::soft) + 3, n_units = 8 * n_kv;
     const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.max_blocks;
     auto key_at = [&](int32_t u) { return (base + (u >> 3)) * kKeys + (u & 3) * 32 + lane; };
     // block id of this lane's key of unit u; -1: no such key
@@ -369,10 +375,13 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
     };
     const bool unpack_warp = !softmax_warp && warp != 0;
     // tensor memory columns: S of tile x at 128 x (the P of each half of its keys, fp16 pairs, overwrites the first
-    // 32 of the half's 64 columns once read), O of tile x at kO + 128 x
+    // 32 of the half's 64 columns once read; in two pieces, 16 keys' pairs of both overwrite their 16 columns), O of tile x
+    // at kO + 128 x
     const uint32_t tmem = *tmem_holder;
 
-    if (!softmax_warp) fewer_registers<48>();
+    if constexpr (Roles::moved) {
+        if (!softmax_warp) fewer_registers<48>();
+    }
     if (unpack_warp) {
         // ======================================== unpack ========================================
         RawRow<D> raw;
@@ -426,14 +435,16 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
             // (descriptors are stepped where they are used: kept for the whole loop, they do not fit the registers)
             auto here = [](uint64_t& d) { asm volatile("" : "+l"(d)); };
             auto qk = [&](int x) {
-                uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kTile >> 4), dk = dk0 + static_cast<uint64_t>(ks) * (kTile >> 4);
+                uint64_t dq = dq0 + static_cast<uint64_t>(x) * (kPieces * kTile >> 4), dk = dk0 + static_cast<uint64_t>(ks) * (kTile >> 4);
                 here(dq);
                 here(dk);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                    umma::mma_bf16(tmem + x * 128, dq + off, dk + off, idesc_qk, s > 0);
-                }
+                for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint64_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+                        umma::mma_bf16(tmem + x * 128, dq + (c * kTile >> 4) + off, dk + off, idesc_qk, s > 0 || c > 0);
+                    }
                 umma::commit(&s_full[x]);
             };
             auto pv = [&](int x, bool acc) {
@@ -441,8 +452,10 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
                 here(dv);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
-                    umma::mma_bf16_tmem_a(tmem + kO + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8, dv + static_cast<uint64_t>(k * (2048 >> 4)),
-                                          idesc_pv, acc || k > 0);
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c)
+                        umma::mma_bf16_tmem_a(tmem + kO + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * (8 * kPieces) + 8 * c,
+                                              dv + static_cast<uint64_t>(k * (2048 >> 4)), idesc_pv, acc || k > 0 || c > 0);
             };
             auto wait_k = [&]() {
                 const bool ok = wait_or_abort<0>(&k_full[ks], k_use & 1u, abort_flag, a.err);
@@ -489,14 +502,14 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
         }
     } else {
         // ==================================== queries, softmax ==================================
-        more_registers<96>();
+        if constexpr (Roles::moved) more_registers<96>();
         const int32_t tl = static_cast<int32_t>(r * inv_G >> 16), g = r - tl * G;
         const int32_t t_row = (x ? t0b : t0a) + tl, n_x = x ? n_b : n_a;
         const bool row_valid = tl < TT && t_row < C;
         const int32_t pair_bar = 1 + x * 4 + quad;  // the barrier of the two warps that share 32 rows
-        {  // this warp's 16 rows to fp16, D / 8 lanes a row: times 2^-e with 2^e <= the row's largest magnitude < 2^(e + 1)
+        {  // this warp's 16 rows to fp16, 16 bytes a lane: times 2^-e with 2^e <= the row's largest magnitude < 2^(e + 1)
             const int32_t c = lane & (kLanes - 1);
-            uint8_t* sq = smem + x * kTile;
+            uint8_t* sq = smem + x * (kPieces * kTile);
             uint4 q_raw[kLoads];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
@@ -504,26 +517,48 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
                 const int32_t t = (x ? t0b : t0a) + tt;
                 q_raw[k] = make_uint4(0u, 0u, 0u, 0u);
                 if (tt < TT && t < C)
-                    q_raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D) +
+                    q_raw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (static_cast<int64_t>(q0 + t) * Hq + h * G + (rr - tt * G)) * D) +
                                      (lane & (kLanes - 1)));
             }
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const uint32_t w[4] = {q_raw[k].x, q_raw[k].y, q_raw[k].z, q_raw[k].w};
-                uint32_t top = 0u;  // magnitudes as bf16 bits, two at a time
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = max_u16x2(top, w[i] & 0x7fff7fffu);
-#pragma unroll
-                for (int off = 1; off < kLanes; off <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const int32_t field = static_cast<int32_t>(max(top & 0xffffu, top >> 16) >> 7);  // 127 + e
-                const int32_t e = field == 255 ? 0 : min(max(field, 1), 253) - 127;              // (not finite: as it is)
                 const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes;
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), f = a.negate ? -down : down;
-                uint32_t o[4];
+                int32_t e;
+                if constexpr (kPieces == 1) {
+                    uint32_t top = 0u;  // magnitudes as bf16 bits, two at a time
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = pack_halves(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-                *reinterpret_cast<uint4*>(sq + (c >> 3) * kHalf + sw128_offset(rr, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int i = 0; i < 4; ++i) top = max_u16x2(top, w[i] & 0x7fff7fffu);
+#pragma unroll
+                    for (int off = 1; off < kLanes; off <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const int32_t field = static_cast<int32_t>(max(top & 0xffffu, top >> 16) >> 7);  // 127 + e
+                    e = field == 255 ? 0 : min(max(field, 1), 253) - 127;                            // (not finite: as it is)
+                } else {  // the largest magnitude in [2^14, 2^15), so that the second halves lie within fp16's range
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = max(top, w[i] & 0x7fffffffu);
+#pragma unroll
+                    for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const int32_t field = static_cast<int32_t>(top >> 23);
+                    e = field == 255 ? 0 : max(field, 15) - 141;
+                }
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), f = a.negate ? -down : down;
+                if constexpr (kPieces == 1) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = pack_halves(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+                    *reinterpret_cast<uint4*>(sq + (c >> 3) * kHalf + sw128_offset(rr, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {  // 4 dims: half of a 16-byte piece in each tile
+                    uint8_t* at = sq + (c >> 4) * kHalf + sw128_offset(rr, c >> 1 & 7) + (c & 1) * 8;
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = __uint_as_float(w[i]) * f;
+                    const uint32_t o0 = pack_halves(y[0], y[1]), o1 = pack_halves(y[2], y[3]);
+                    const float2 h0 = halves_to_floats(o0), h1 = halves_to_floats(o1);
+                    *reinterpret_cast<uint2*>(at) = make_uint2(o0, o1);
+                    *reinterpret_cast<uint2*>(at + kTile) = make_uint2(pack_halves(y[0] - h0.x, y[1] - h0.y), pack_halves(y[2] - h1.x, y[3] - h1.y));
+                }
                 if (c == 0) shared.row[x][rr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             }
             fence_proxy_async_shared();
@@ -537,13 +572,15 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + x * 128 + half * 64 + lane_off;
         const uint32_t tmem_o = tmem + kO + x * 128 + half * (D / 2) + lane_off;  // the columns that it rescales and writes
+        // log2 of the weight of a score at the reference; in two pieces 2^7, so that small weights' second halves lie within
+        // fp16's range too (2^-25 is 2^-32 of that)
+        constexpr float kAbove = kPieces == 2 ? 7.f : 0.f;
         float m_ref = kLowest, l_sum = 0.f;  // the reference is the same in both threads of a row
-        uint32_t pk[32];
         bool ok = true;
         int32_t keys = 0;  // of this half, those that the row sees are below this
         // P = 2^(s c1 - m) in fp16 pairs, 16 keys at a time, the next 16 on their way; the weights wait in registers
         // until the tile's maximum is known. Returns their sum; over: the largest exponent.
-        auto weights = [&](auto masked, float& over) -> float {
+        auto weights = [&](auto masked, float& over, uint32_t (&pk)[32]) -> float {
             const uint64_t scale2 = pack2(c1, c1), shift2 = pack2(-m_ref, -m_ref);
             uint64_t psum[2] = {0ull, 0ull};
             float top[2] = {-INFINITY, -INFINITY};
@@ -597,30 +634,66 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
             }
             const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c1;
             const float m = both([](float p, float q) { return fmaxf(p, q); }, mine);
-            const float m_new = m > m_ref + kRescaleThreshold ? m : m_ref, alpha = exp2_approx(m_ref - m_new);
+            const float m_new = m > m_ref + (kAbove + kRescaleThreshold) ? m - kAbove : m_ref, alpha = exp2_approx(m_ref - m_new);
             m_ref = m_new;
             return alpha;
+        };
+        // The weights of a tile as sums of two halves, in the place of their scores, 16 keys at a time. Returns their sum.
+        auto weights_in_place = [&]() -> float {
+            uint64_t psum = 0ull;
+            uint32_t raw[2][16];
+            ld_x16(tmem_s, raw[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                wait_x16(raw[c & 1]);
+                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float x0 = fmaf(__uint_as_float(raw[c & 1][2 * e]), c1, -m_ref), x1 = fmaf(__uint_as_float(raw[c & 1][2 * e + 1]), c1, -m_ref);
+                    if (c * 16 + 2 * e >= keys) x0 = -INFINITY;  // hidden: weight 0
+                    if (c * 16 + 2 * e + 1 >= keys) x1 = -INFINITY;
+                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                    psum = add2(psum, pack2(p0, p1));
+                    o[e] = pack_halves(p0, p1);
+                    const float2 held = halves_to_floats(o[e]);
+                    o[8 + e] = pack_halves(p0 - held.x, p1 - held.y);
+                }
+                umma::st_32x32b_x16(tmem_s + c * 16, o);
+            }
+            float s0, s1;
+            unpack2(psum, s0, s1);
+            return s0 + s1;
         };
         for (int32_t j = 0; j < n_x; ++j) {
             ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a.err);
             if (!__all_sync(0xffffffffu, ok) && lane == 0) *const_cast<volatile int32_t*>(&stopped[x][quad]) = 1;
             umma::fence_after_sync();
             keys = pos - ((base + j) * kKeys + half * 64) + 1;
-            const bool masked = __any_sync(0xffffffffu, keys < 64);  // the last tiles
-            float alpha = 1.f, over = 0.f, sum;
-            if (__any_sync(0xffffffffu, m_ref == kLowest)) alpha = move_reference();  // a row's first keys (alike in both warps)
-            sum = masked ? weights(std::true_type(), over) : weights(std::false_type(), over);
-            if (__any_sync(0xffffffffu, over > kRescaleThreshold) && lane == 0)
-                *const_cast<volatile int32_t*>(&grow_at[x][quad]) = j + 1;
-            named_barrier(pair_bar, 64);
-            // both warps leave at the same tile, so that each meets the other at every barrier
-            ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
-            if (!ok) break;
-            if (*const_cast<volatile int32_t*>(&grow_at[x][quad]) == j + 1) {
-                alpha *= move_reference();
-                sum = masked ? weights(std::true_type(), over) : weights(std::false_type(), over);
+            float alpha = 1.f, sum;
+            if constexpr (kPieces == 1) {
+                const bool masked = __any_sync(0xffffffffu, keys < 64);  // the last tiles
+                float over = 0.f;
+                uint32_t pk[32];
+                if (__any_sync(0xffffffffu, m_ref == kLowest)) alpha = move_reference();  // a row's first keys (alike in both warps)
+                sum = masked ? weights(std::true_type(), over, pk) : weights(std::false_type(), over, pk);
+                if (__any_sync(0xffffffffu, over > kRescaleThreshold) && lane == 0)
+                    *const_cast<volatile int32_t*>(&grow_at[x][quad]) = j + 1;
+                named_barrier(pair_bar, 64);
+                // both warps leave at the same tile, so that each meets the other at every barrier
+                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
+                if (!ok) break;
+                if (*const_cast<volatile int32_t*>(&grow_at[x][quad]) == j + 1) {
+                    alpha *= move_reference();
+                    sum = masked ? weights(std::true_type(), over, pk) : weights(std::false_type(), over, pk);
+                }
+                umma::st_32x32b_x32(tmem_s, pk);
+            } else {  // the maximum first (a barrier of both warps), then the weights
+                alpha = move_reference();
+                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
+                if (!ok) break;
+                sum = weights_in_place();
             }
-            umma::st_32x32b_x32(tmem_s, pk);
             l_sum = l_sum * alpha + sum;
             if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                 // O holds the tiles before under the old reference; the PV of tile j - 1 finished
@@ -671,11 +744,25 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
                                         __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
                 }
             }
+        } else if (kPieces == 2 && ok && n_x > 0) {
+            const float inv = l_sum == 0.f ? 0.f : a.v_scale / l_sum;
+            float* to = static_cast<float*>(a.out) + (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[16];
+                output(c, o);
+                if (!row_valid) continue;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    reinterpret_cast<float4*>(to)[c * 4 + v] =
+                        make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                    __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+            }
         } else if (ok && n_x > 0) {
             const float inv = l_sum == 0.f ? 0.f : a.v_scale / l_sum;
             // this warp's rows x D / 2 columns through its own part of the query tile, which no MMA reads any more, so
             // that the stores go out whole lines at a time (a row's 16-byte pieces in different banks, lane by lane)
-            constexpr int kPieces = D / 16;
+            constexpr int kChunks = D / 16;
             uint8_t* stage = smem + x * kTile + (half * 4 + quad) * (32 * D);
             const int32_t turn = D == 128 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
@@ -694,12 +781,12 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
             __syncwarp();
             const int64_t to = row_valid ? (static_cast<int64_t>(q0 + t_row) * Hq + h * G + g) * D + half * (D / 2) : -1;
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int32_t i = k * 32 + lane, rr = i / kPieces, c = i % kPieces;
+            for (int k = 0; k < kChunks; ++k) {
+                const int32_t i = k * 32 + lane, rr = i / kChunks, c = i % kChunks;
                 const int64_t off = __shfl_sync(0xffffffffu, to, rr);
                 const int32_t t = D == 128 ? rr & 7 : (rr >> 1) & 3;
                 const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * D + (c ^ t) * 16);
-                if (off >= 0) *reinterpret_cast<uint4*>(a.out + off + c * 8) = v;
+                if (off >= 0) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + off + c * 8) = v;
             }
         }
     }
@@ -709,14 +796,14 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ) prefill_fp4_kernel
     __syncthreads();
     if (warp == 0) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, Roles<NQ>::columns);
+        umma::tmem_dealloc(tmem, Roles::columns);
     }
 }
 
 // Merges the runs of split key lists. Grid: four columns of head_dim x CTA of the unsplit grid; a thread has one row of
 // the CTA's two tiles.
-template <int D>
-__global__ void __launch_bounds__(2 * kRows) prefill_fp4_merge_kernel(__nv_bfloat16* __restrict__ out,
+template <typename T, int D>
+__global__ void __launch_bounds__(2 * kRows) prefill_fp4_merge_kernel(T* __restrict__ out,
                                                                       const __grid_constant__ Split split,
                                                                       int32_t num_kv_heads, int32_t G, float v_scale) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -741,25 +828,27 @@ __global__ void __launch_bounds__(2 * kRows) prefill_fp4_merge_kernel(__nv_bfloa
     }
     const float inv = den == 0.f ? 0.f : v_scale / den;
     const int32_t h = cta % num_kv_heads, TT = kRows / G, tt = rr / G, t = (R < kRows ? 0 : TT) + tt;
-    __nv_bfloat16* to = out + (static_cast<int64_t>(rows.x + t) * G * num_kv_heads + h * G + (rr - tt * G)) * D + c4 * 4;
-    *reinterpret_cast<uint2*>(to) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    T* to = out + (static_cast<int64_t>(rows.x + t) * G * num_kv_heads + h * G + (rr - tt * G)) * D + c4 * 4;
+    if constexpr (std::is_same<T, float>::value)
+        *reinterpret_cast<float4*>(to) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 // Grids of few waves are ordered pair by pair, others sequence by sequence.
-// tiles: query tiles of a CTA; of one tile, two CTAs share an SM.
-bool few_waves(int64_t entries, int32_t num_kv_heads, int tiles, int num_sms) {
-    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * (3 - tiles) * num_sms;
+bool few_waves(int64_t entries, int32_t num_kv_heads, int ctas_per_sm, int num_sms) {
+    return entries <= kRankMax && entries * num_kv_heads <= static_cast<int64_t>(kFewWaves) * ctas_per_sm * num_sms;
 }
 
-template <int D, int NQ, bool SPLIT>
+template <typename T, int D, int NQ, bool SPLIT>
 cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScoredPlan& plan, void* workspace, int num_sms,
                         cudaStream_t stream) {
-    cudaError_t e = allow_smem<prefill_fp4_kernel<D, NQ, SPLIT>>(static_cast<int>(Smem<D, NQ>::total));
+    cudaError_t e = allow_smem<prefill_fp4_kernel<T, D, NQ, SPLIT>>(static_cast<int>(Smem<T, D, NQ>::total));
     if (e != cudaSuccess) return e;
     Args a{};
-    a.out = static_cast<__nv_bfloat16*>(p.out);
-    a.q = static_cast<const __nv_bfloat16*>(p.q);
+    a.out = p.out;
+    a.q = p.q;
     a.k_cache = static_cast<const uint8_t*>(p.k_cache);
     a.v_cache = static_cast<const uint8_t*>(p.v_cache);
     a.block_table = p.block_table;
@@ -778,7 +867,7 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
     a.err = p.err;
     const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len + NQ * TT - 1) / (NQ * TT);
     const int64_t entries = static_cast<int64_t>(pairs) * p.num_seqs;
-    const bool by_pair = few_waves(entries, p.num_kv_heads, NQ, num_sms);
+    const bool by_pair = few_waves(entries, p.num_kv_heads, Roles<T, D, NQ>::per_sm, num_sms);
     a.sub = by_pair ? pairs : 1;
     a.inv_sub = 65536u / a.sub + 1;
     const dim3 grid(SPLIT ? plan.parts : by_pair ? 1 : pairs, p.num_kv_heads, p.num_seqs * a.sub);
@@ -789,7 +878,7 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
         a.split.o = reinterpret_cast<float4*>(ws + kScoredCounterBytes + kSplitRowBytes);
         a.split.ml = reinterpret_cast<float2*>(a.split.o + entries * p.num_kv_heads * plan.parts * (D / 4) * (2 * kRows));
     }
-    prefill_fp4_kernel<D, NQ, SPLIT><<<grid, Roles<NQ>::threads, Smem<D, NQ>::total, stream>>>(a);
+    prefill_fp4_kernel<T, D, NQ, SPLIT><<<grid, Roles<T, D, NQ>::threads, Smem<T, D, NQ>::total, stream>>>(a);
     e = cudaGetLastError();
     if (!SPLIT || e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];  // the merge's CTAs may be set up while the last runs end
@@ -801,40 +890,45 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefill_fp4_merge_kernel<D>, a.out, a.split, p.num_kv_heads, a.G, v_scale);
+    return cudaLaunchKernelEx(&cfg, prefill_fp4_merge_kernel<T, D>, static_cast<T*>(a.out), a.split, p.num_kv_heads, a.G, v_scale);
 }
 
 }  // namespace
 
 PrefillScoredPlan plan_prefill_fp4(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_len,
-                                   int num_sms) {
+                                   pa_dtype dtype, int num_sms) {
     PrefillScoredPlan plan{1, 2, 0};
     if (Hq / Hkv > kRows) return plan;
     const int32_t TT = kRows / (Hq / Hkv);
-    if (max_chunk <= TT || max_len <= short_keys(D)) plan.tiles = 1;
+    if (dtype == PA_F32 || max_chunk <= TT || max_len <= short_keys(D)) plan.tiles = 1;
     const int64_t most = static_cast<int64_t>(max_len / kKeys + 1) / kMinPartTiles;  // runs of the longest list
     if (most < 2) return plan;
     // room for a wave of CTAs, whatever the chunks: a workspace serves every call up to its max_len
     plan.workspace_bytes = kScoredCounterBytes + kSplitRowBytes + static_cast<size_t>(num_sms) * (2 * kRows) * (D * 4 + 8);
     if (S < 1 || max_chunk < 1) return plan;
-    const int64_t entries = (static_cast<int64_t>(max_chunk) + 2 * TT - 1) / (2 * TT) * S;
-    if (few_waves(entries, Hkv, 2, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
+    const int32_t of_split = (dtype == PA_F32 ? 1 : 2) * TT;  // rows of a CTA whose keys are split
+    const int64_t entries = (static_cast<int64_t>(max_chunk) + of_split - 1) / of_split * S;
+    if (few_waves(entries, Hkv, 1, num_sms))  // one wave of CTAs, each with kMinPartTiles key tiles at least
         plan.parts = static_cast<int32_t>(max(min(num_sms / (entries * Hkv), most), static_cast<int64_t>(1)));
     return plan;
 }
 
 bool prefill_fp4_tc_ok(const PrefillArgs& a, const DeviceInfo& dev) {
-    return a.dtype == PA_BF16 && a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
-           a.num_kv_heads <= 65535 && static_cast<int>(Smem<128, 2>::total) <= dev.max_smem_optin;
+    return a.num_q_heads / a.num_kv_heads <= kRows && a.num_seqs <= 65535 &&
+           a.num_kv_heads <= 65535 && static_cast<int>(Smem<__nv_bfloat16, 128, 2>::total) <= dev.max_smem_optin;
 }
 
 cudaError_t launch_prefill_fp4_tc(const PrefillArgs& a, float v_scale, const PrefillScoredPlan& plan, void* workspace,
                                   int num_sms, cudaStream_t stream) {
     auto go = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        if (plan.parts > 1) return launch_impl<D, 2, true>(a, v_scale, plan, workspace, num_sms, stream);
-        return plan.tiles == 1 ? launch_impl<D, 1, false>(a, v_scale, plan, workspace, num_sms, stream)
-                               : launch_impl<D, 2, false>(a, v_scale, plan, workspace, num_sms, stream);
+        if (a.dtype == PA_F32)
+            return plan.parts > 1 ? launch_impl<float, D, 1, true>(a, v_scale, plan, workspace, num_sms, stream)
+                                  : launch_impl<float, D, 1, false>(a, v_scale, plan, workspace, num_sms, stream);
+        using T = __nv_bfloat16;
+        if (plan.parts > 1) return launch_impl<T, D, 2, true>(a, v_scale, plan, workspace, num_sms, stream);
+        return plan.tiles == 1 ? launch_impl<T, D, 1, false>(a, v_scale, plan, workspace, num_sms, stream)
+                               : launch_impl<T, D, 2, false>(a, v_scale, plan, workspace, num_sms, stream);
     };
     return a.head_dim == 128 ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 64>());
 }
