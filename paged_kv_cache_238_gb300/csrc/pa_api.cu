@@ -700,9 +700,6 @@ PA_API pa_status pa_rotate_and_cache(const pa_rotate* r, void* stream) {
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Pages of a partition, at least, on the CUDA cores over 4-bit pools.
-constexpr int32_t kFp4MinPages = 8;
-
 PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                            int32_t head_dim, int32_t max_seq_len, pa_dtype dtype) {
     if (check_attention_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, 1, max_seq_len / 16 + 1, max_seq_len,
@@ -713,7 +710,7 @@ PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads
     DecodeScoredPlan plan;
     if (plan_decode_fp4(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, dtype, dev->info, &plan))
         return plan.workspace_bytes;
-    return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms, kFp4MinPages)
+    return plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms)
         .workspace_bytes;
 }
 
@@ -742,7 +739,7 @@ PA_API pa_status pa_decode_fp4(const pa_fp4_attention* c, void* stream) {
         return launch_decode_fp4(a, v_scale, fast, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const ScoredSimtPlan plan =
-        plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms, kFp4MinPages);
+        plan_scored_simt(num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_seq_len, dev->info.num_sms);
     if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
     return launch_fp4_decode_simt(a, v_scale, plan, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -763,7 +760,7 @@ PA_API size_t pa_prefill_fp4_workspace_size(int32_t num_seqs, int32_t max_chunk_
         return plan_prefill_fp4(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len, dtype,
                                 dev->info.num_sms).workspace_bytes;
     return plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim, max_seq_len,
-                            dev->info.num_sms, kFp4MinPages).workspace_bytes;
+                            dev->info.num_sms).workspace_bytes;
 }
 
 PA_API pa_status pa_prefill_fp4(const pa_fp4_attention* c, void* stream) {
@@ -795,7 +792,7 @@ PA_API pa_status pa_prefill_fp4(const pa_fp4_attention* c, void* stream) {
         return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     const ScoredSimtPlan plan = plan_scored_simt(num_seqs, max_chunk_len, num_q_heads, num_kv_heads, head_dim,
-                                                 max_seq_len, dev->info.num_sms, kFp4MinPages);
+                                                 max_seq_len, dev->info.num_sms);
     if (!room(plan.workspace_bytes)) return PA_ERR_INVALID_ARG;
     return launch_fp4_prefill_simt(a, v_scale, plan, workspace, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -236,7 +236,7 @@ struct ScoredSimtPlan {
 };
 int32_t scored_simt_head_chunks(int32_t group);
 ScoredSimtPlan plan_scored_simt(int32_t num_seqs, int32_t max_chunk_len, int32_t num_q_heads, int32_t num_kv_heads,
-                                int32_t head_dim, int32_t max_seq_len, int num_sms, int32_t min_pages = 32);
+                                int32_t head_dim, int32_t max_seq_len, int num_sms);
 cudaError_t launch_scored_decode_simt(const DecodeArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
                                       cudaStream_t stream);
 cudaError_t launch_scored_prefill_simt(const PrefillArgs& a, const ScoreArgs& score, const ScoredSimtPlan& plan,
@@ -303,7 +303,8 @@ PrefillScoredPlan plan_prefill_fp4(int32_t num_seqs, int32_t max_chunk_len, int3
 cudaError_t launch_prefill_fp4_tc(const PrefillArgs& a, float v_scale, const PrefillScoredPlan& plan, void* workspace,
                                   int num_sms, cudaStream_t stream);
 
-// Attention over 4-bit pools on the CUDA cores: the scored kernel without a score; k_scale is in a.scale.
+// Attention over 4-bit pools on the CUDA cores, where neither of these applies: the scored kernel without a score;
+// k_scale is in a.scale.
 cudaError_t launch_fp4_decode_simt(const DecodeArgs& a, float v_scale, const ScoredSimtPlan& plan, cudaStream_t stream);
 cudaError_t launch_fp4_prefill_simt(const PrefillArgs& a, float v_scale, const ScoredSimtPlan& plan, void* workspace,
                                     cudaStream_t stream);

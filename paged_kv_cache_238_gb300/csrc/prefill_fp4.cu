@@ -1,5 +1,5 @@
-// Chunked causal prefill over a 4-bit pool on the 5th-generation tensor cores (bf16 queries, head_dim 64 or 128, up
-// to 128 q heads per kv head).
+// Chunked causal prefill over a 4-bit pool on the 5th-generation tensor cores (head_dim 64 or 128, up to 128 q heads per
+// kv head).
 //
 // One CTA computes two 128-row query tiles (a, b) of one (sequence, kv head), or one, with two CTAs on an SM that cover
 // each other's start and end, where that serves better (plan_prefill_fp4): row r of a tile is token r / G, q head
@@ -20,6 +20,12 @@
 //
 // Query rows are brought to fp16 by a power of two per row, which the row's score factor takes back: bf16's 8 bits fit,
 // and what is 2^-24 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
+//
+// fp32 queries: q and the weights are sums of two halves, 22 bits, so that S takes two Q K^T and O two P V; a CTA has one
+// query tile (the second half lies where a second tile would), and its softmax reads S twice, for the maximum and for the
+// weights, whose two halves take the place of the scores that they come from. 9 chunks of 90 to 300 on up to 1543 keys, 64 q
+// / 16 kv heads of 64: 107 us (869 on the CUDA cores); 4 of 17 to 96 on up to 900, 12 q / 4 kv heads of 64: 18 (53); 16 of 256
+// on up to 4352, 32 q / 8 kv heads of 128: 401. Bound: S, softmax and P V of a tile follow one another.
 //
 // Bound: the chain S -> softmax -> P -> P V, Q K^T -> next S of each query tile, about 3000 cycles a key tile of which 1024 are
 // its own MMAs (both tiles' MMAs take 2048), and each CTA's start (5 us) and end (1.5). 16 sequences of 512 new rows on 512 to

@@ -653,8 +653,8 @@ int32_t scored_simt_head_chunks(int32_t group) {
 // of at least kMinPages pages each. Measured, 24 sequences of up to 777 keys, 4 kv heads of 64 in fp32: 9.1 us with 32 or 64 pages,
 // 10.7 with 8 or 16.
 ScoredSimtPlan plan_scored_simt(int32_t S, int32_t max_chunk, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len,
-                                int num_sms, int32_t min_pages) {
-    const int64_t kMinPages = min_pages;
+                                int num_sms) {
+    constexpr int64_t kMinPages = 32;
     ScoredSimtPlan p{};
     const int32_t G = Hq / Hkv;
     // (24 sequences, 12 q / 4 kv heads of 64 in fp32: 5.8 us with 4 rows, 8.0 with 16; chunks of 17 to 96 rows, 8 q / 2

@@ -427,3 +427,39 @@ def test_other_scales(dtype, factor, chunks):
     d.run()
     ref, tol = c.reference()
     assert (np.abs(d.got() - ref) <= np.abs(tol)).all()
+
+
+@pytest.mark.parametrize("chunks", [None, [150, 40, 3]])
+@pytest.mark.parametrize("sharp,factor", [(1e-30, 1.0), (1e-6, 1.0), (30.0, 1.0), (3e36, 1e-36), (3e-38, 1e30)])
+def test_fp32_queries_of_any_size(chunks, sharp, factor):
+    """fp32 queries whose halves need the whole range of their row's power of two; elements of one row 2^-32 to 1 apart."""
+    c = R.Case(17, [300, 40, 17], 8, 2, 128, 16, "f32", chunks=chunks, sharp=sharp)
+    c.scale *= factor
+    c.q[1, 3] = 0
+    c.q[0, 0] = np.float32(2.0) ** -np.arange(0, 64, 0.5, dtype=np.float32) * np.float32(sharp)
+    check(c)
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (16, 16, 64), (6, 2, 64), (10, 2, 128), (96, 1, 64)])
+def test_prefill_tiles_of_fp32_queries(H_q, H_kv, D):
+    check(R.Case(18, [300, 700, 257, 520], H_q, H_kv, D, 16, "f32", chunks=[300, 256, 1, 391], v_scale=2.0 ** -6))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_heads_than_a_tile_has_rows(dtype):
+    check(R.Case(15, [40, 17, 0, 300], 130, 1, 64, 16, dtype))
+    check(R.Case(15, [40, 17, 0, 300], 130, 1, 64, 16, dtype, chunks=[9, 17, 0, 5]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunks", [None, [20, 0, 150]])
+def test_the_largest_bound(dtype, chunks):
+    """A table of 2^24 - 1 blocks a sequence, of which a few are used: more units than a launch counts."""
+    c = R.Case(16, [40, 0, 300], 16, 16, 64, 128, dtype, chunks=chunks)
+    d = Device(c, max_len=(2 ** 24 - 1) * 128)
+    wide = torch.zeros(3, 2 ** 24 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :d.table.shape[1]] = d.table
+    d.table = wide
+    d.run()
+    ref, tol = c.reference()
+    assert (np.abs(d.got() - ref) <= tol).all()
