@@ -1,7 +1,8 @@
 // Decode over a 4-bit pool: one query row per sequence, on mma.sync in fp16 with pages staged by bulk copies. The pool's
 // values (code * scale, 6 significant bits, fp4.cuh) are exact in fp16; a q head's row is brought to fp16 by a power of
 // two; weights are rounded to fp16, everything else is fp32. fp32 queries and their weights are sums of two halves, which
-// takes twice the MMAs but unpacks no more.
+// takes twice the MMAs but unpacks no more. The MMAs cut their sums off, always towards zero: over 8000 keys 3e-6 of an
+// output. So the second halves are summed by themselves in S, and a page's part of O before it is added (4e-7).
 //
 // Work list, slices and joins are those of the scored decode kernel (decode_scored.cu): a unit is one page of 16
 // tokens of one segment (sequence, kv head, chunk of up to 16 of the kv head's q heads); every CTA builds the list's
@@ -27,8 +28,8 @@
 // 64 q / 8 kv heads of 128: 57 us, 4.2 TB/s, 62 % of the measured copy rate (32 sequences of 32768: 228 us, 78 %); 64 of 500
 // to 16384, 32 q / 8 kv heads: 75 us (67 %), of which 4.4 pass until the first pages have come and 8 to 11 go to the slowest
 // SM and the joins. 4 sequences of up to 700 keys: 9.1 us in a graph, a chain of latencies.
-// fp32 queries (before on the CUDA cores): 8 of 8000 to 9000 keys, 16 q / 4 kv heads of 128, 21.9 us (54.8); 64 of 10 to
-// 2000, 16 heads of 64, 21.7 (58.1); 24 of up to 777, 12 q / 4 kv heads of 64, 10.2 (12.1).
+// fp32 queries (before on the CUDA cores): 8 of 8000 to 9000 keys, 16 q / 4 kv heads of 128, 21.6 us (54.8); 64 of 10 to
+// 2000, 16 heads of 64, 22.3 (58.1); 24 of up to 777, 12 q / 4 kv heads of 64, 10.2 (12.1).
 #include <math.h>
 
 #include <type_traits>
@@ -145,6 +146,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A B
+__device__ __forceinline__ void mma_f16_fresh(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -404,8 +413,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     s0 = e4m3x2_halves(static_cast<uint16_t>(lds8(at_ks + page)));
                     s1 = e4m3x2_halves(static_cast<uint16_t>(lds8(at_ks + page + 8 * (D / 16))));
                 }
+                float low[NH][4];  // two pieces: the products of the second ones, which are small, by themselves
 #pragma unroll
-                for (int f = 0; f < NH; ++f) sc[i][f][0] = sc[i][f][1] = sc[i][f][2] = sc[i][f][3] = 0.f;
+                for (int f = 0; f < NH; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i][f][e] = low[f][e] = 0.f;
 #pragma unroll
                 for (int w = 0; w < WK; ++w) {  // two k16 steps
                     const uint32_t pick = w < 2 ? 0x1010u : 0x3232u;
@@ -418,10 +430,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         const uint32_t fa[4] = {hmul2(h0[2 * x], m0), hmul2(h1[2 * x], m1), hmul2(h0[2 * x + 1], m0),
                                                 hmul2(h1[2 * x + 1], m1)};
 #pragma unroll
-                        for (int f = 0; f < NH; ++f)
-#pragma unroll
-                            for (int c = 0; c < PC; ++c) mma_f16(sc[i][f], fa, qb[f][c][2 * w + x][0], qb[f][c][2 * w + x][1]);
+                        for (int f = 0; f < NH; ++f) {
+                            if constexpr (F::kTwo) mma_f16(low[f], fa, qb[f][1][2 * w + x][0], qb[f][1][2 * w + x][1]);
+                            mma_f16(sc[i][f], fa, qb[f][0][2 * w + x][0], qb[f][0][2 * w + x][1]);
+                        }
                     }
+                }
+                if constexpr (F::kTwo) {
+#pragma unroll
+                    for (int f = 0; f < NH; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[i][f][e] += low[f][e];
                 }
             }
             if (next) {  // K has been read
@@ -539,9 +558,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
                     for (int b = 0; b < 4; ++b) {
                         const uint32_t fa[4] = {hmul2(e0[b], m0), hmul2(o0[b], m0), hmul2(e1[b], m1), hmul2(o1[b], m1)};
 #pragma unroll
-                        for (int f = 0; f < NH; ++f)
+                        for (int f = 0; f < NH; ++f) {
+                            float(&o)[4] = acc[f][4 * x + b];
+                            if constexpr (F::kTwo) {  // the page's part by itself, added with rounding
+                                float part[4];
+                                mma_f16_fresh(part, fa, pb[i][f][1][0], pb[i][f][1][1]);
+                                mma_f16(part, fa, pb[i][f][0][0], pb[i][f][0][1]);
 #pragma unroll
-                            for (int c = 0; c < PC; ++c) mma_f16(acc[f][4 * x + b], fa, pb[i][f][c][0], pb[i][f][c][1]);
+                                for (int e = 0; e < 4; e += 2) unpack2(add2(pack2(o[e], o[e + 1]), pack2(part[e], part[e + 1])), o[e], o[e + 1]);
+                            } else {
+                                mma_f16(o, fa, pb[i][f][0][0], pb[i][f][0][1]);
+                            }
+                        }
                     }
                 }
             }

@@ -24,8 +24,9 @@
 // fp32 queries: q and the weights are sums of two halves, 22 bits, so that S takes two Q K^T and O two P V; a CTA has one
 // query tile (the second half lies where a second tile would), and its softmax reads S twice, for the maximum and for the
 // weights, whose two halves take the place of the scores that they come from. 9 chunks of 90 to 300 on up to 1543 keys, 64 q
-// / 16 kv heads of 64: 107 us (869 on the CUDA cores); 4 of 17 to 96 on up to 900, 12 q / 4 kv heads of 64: 18 (53); 16 of 256
-// on up to 4352, 32 q / 8 kv heads of 128: 401. Bound: S, softmax and P V of a tile follow one another.
+// / 16 kv heads of 64: 117 us (869 on the CUDA cores; 107 with O summed by the MMAs alone, which cut sums off); 4 of 17 to 96
+// on up to 900, 12 q / 4 kv heads of 64: 19 (53); 16 of 256 on up to 4352, 32 q / 8 kv heads of 128: 419 (466 with 128
+// registers for every warp). Bound: S, softmax and P V of a tile follow one another.
 //
 // Bound: the chain S -> softmax -> P -> P V, Q K^T -> next S of each query tile, about 3000 cycles a key tile of which 1024 are
 // its own MMAs (both tiles' MMAs take 2048), and each CTA's start (5 us) and end (1.5). 16 sequences of 512 new rows on 512 to
@@ -52,13 +53,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;  // query rows per tile (M)
 constexpr int kKeys = 128;  // keys per key tile (N of S = Q K^T, K of O += P V)
 // Of a CTA of NQ query tiles: halves that make a number of q or a weight (fp32: two), CTAs on an SM, warps of softmax, of
-// unpacking (three beside the MMA warp, and a warpgroup more in a CTA that has the SM to itself), threads; whether
-// registers move; tensor memory columns of O, of all.
+// unpacking (three beside the MMA warp, and a warpgroup more in a CTA that has the SM to itself), threads; tensor
+// memory columns of O, of all.
 template <typename T, int D, int NQ>
 struct Roles {
     static constexpr int pieces = std::is_same<T, float>::value ? 2 : 1, per_sm = NQ == 2 || pieces * D == 256 ? 1 : 2;
     static constexpr int soft = 8 * NQ, unpack = per_sm == 1 ? 7 : 3, threads = 32 * (soft + unpack + 1);
-    static constexpr bool moved = per_sm == 2 || NQ == 2;
+    // registers a thread: at launch, then of the softmax and of the other warps
+    static constexpr int at_launch = pieces * D == 256 ? 128 : 80, soft_regs = at_launch == 128 ? 200 : 96, other_regs = at_launch == 128 ? 56 : 48;
+    static_assert(32 * (soft * soft_regs + (unpack + 1) * other_regs) == threads * at_launch, "setmaxnreg's shares");
     static constexpr uint32_t o = NQ * 128, columns = NQ * 256;
 };
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 fp16 columns)
@@ -385,9 +388,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
     // at kO + 128 x
     const uint32_t tmem = *tmem_holder;
 
-    if constexpr (Roles::moved) {
-        if (!softmax_warp) fewer_registers<48>();
-    }
+    if (!softmax_warp) fewer_registers<Roles::other_regs>();
     if (unpack_warp) {
         // ======================================== unpack ========================================
         RawRow<D> raw;
@@ -445,11 +446,11 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 here(dq);
                 here(dk);
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c)
+                for (int c = kPieces - 1; c >= 0; --c)  // the second halves first: the sums are cut off, so the small ones come early
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint64_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                        umma::mma_bf16(tmem + x * 128, dq + (c * kTile >> 4) + off, dk + off, idesc_qk, s > 0 || c > 0);
+                        umma::mma_bf16(tmem + x * 128, dq + (c * kTile >> 4) + off, dk + off, idesc_qk, s > 0 || c < kPieces - 1);
                     }
                 umma::commit(&s_full[x]);
             };
@@ -457,11 +458,12 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 uint64_t dv = dv0 + static_cast<uint64_t>(vs) * (kTile >> 4);
                 here(dv);
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
+                for (int c = kPieces - 1; c >= 0; --c)
 #pragma unroll
-                    for (int c = 0; c < kPieces; ++c)
+                    for (int k = 0; k < kKeys / 16; ++k)  // 16 keys per instruction: 8 P columns
                         umma::mma_bf16_tmem_a(tmem + kO + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * (8 * kPieces) + 8 * c,
-                                              dv + static_cast<uint64_t>(k * (2048 >> 4)), idesc_pv, acc || k > 0 || c > 0);
+                                              dv + static_cast<uint64_t>(k * (2048 >> 4)), idesc_pv,
+                                              (acc && kPieces == 1) || k > 0 || c < kPieces - 1);
             };
             auto wait_k = [&]() {
                 const bool ok = wait_or_abort<0>(&k_full[ks], k_use & 1u, abort_flag, a.err);
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         }
     } else {
         // ==================================== queries, softmax ==================================
-        if constexpr (Roles::moved) more_registers<96>();
+        more_registers<Roles::soft_regs>();
         const int32_t tl = static_cast<int32_t>(r * inv_G >> 16), g = r - tl * G;
         const int32_t t_row = (x ? t0b : t0a) + tl, n_x = x ? n_b : n_a;
         const bool row_valid = tl < TT && t_row < C;
@@ -647,16 +649,14 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         // The weights of a tile as sums of two halves, in the place of their scores, 16 keys at a time. Returns their sum.
         auto weights_in_place = [&]() -> float {
             uint64_t psum = 0ull;
-            uint32_t raw[2][16];
-            ld_x16(tmem_s, raw[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                wait_x16(raw[c & 1]);
-                if (c < 3) ld_x16(tmem_s + (c + 1) * 16, raw[(c + 1) & 1]);
-                uint32_t o[16];
+                uint32_t raw[16], o[16];
+                ld_x16(tmem_s + c * 16, raw);
+                wait_x16(raw);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float x0 = fmaf(__uint_as_float(raw[c & 1][2 * e]), c1, -m_ref), x1 = fmaf(__uint_as_float(raw[c & 1][2 * e + 1]), c1, -m_ref);
+                    float x0 = fmaf(__uint_as_float(raw[2 * e]), c1, -m_ref), x1 = fmaf(__uint_as_float(raw[2 * e + 1]), c1, -m_ref);
                     if (c * 16 + 2 * e >= keys) x0 = -INFINITY;  // hidden: weight 0
                     if (c * 16 + 2 * e + 1 >= keys) x1 = -INFINITY;
                     const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
@@ -670,6 +670,23 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             float s0, s1;
             unpack2(psum, s0, s1);
             return s0 + s1;
+        };
+        // Two pieces: O so far, in registers. The MMAs cut their sums off, always towards zero, which over 8000 keys is 2e-5 of an
+        // output; a tile's part by itself, added here with rounding, leaves 3e-7.
+        float o_sum[kPieces == 2 ? D / 2 : 1];
+#pragma unroll
+        for (float& o : o_sum) o = 0.f;
+        auto collect = [&]() {
+            if constexpr (kPieces == 2) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[16];
+                    ld_x16(tmem_o + c * 16, o);
+                    wait_x16(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o_sum[c * 16 + i] += __uint_as_float(o[i]);
+                }
+            }
         };
         for (int32_t j = 0; j < n_x; ++j) {
             ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a.err);
@@ -695,13 +712,17 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 }
                 umma::st_32x32b_x32(tmem_s, pk);
             } else {  // the maximum first (a barrier of both warps), then the weights
+                if (j > 0) collect();  // the PV of tile j - 1 finished before S of tile j was committed
                 alpha = move_reference();
                 ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
                 if (!ok) break;
                 sum = weights_in_place();
             }
             l_sum = l_sum * alpha + sum;
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if constexpr (kPieces == 2) {
+#pragma unroll
+                for (float& o : o_sum) o *= alpha;
+            } else if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                 // O holds the tiles before under the old reference; the PV of tile j - 1 finished
                 // before S of tile j was committed, so O can be rescaled now
 #pragma unroll
@@ -722,11 +743,15 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         if (ok && n_x > 0) ok = wait_or_abort<20>(&o_done[x], 0, abort_flag, a.err);
         ok = __all_sync(0xffffffffu, ok);
         umma::fence_after_sync();
+        if (n_x > 0) collect();
         l_sum = both([](float p, float q) { return p + q; }, l_sum);
         // columns half (D / 2) + 16 c .. of the row's output; a tile that no key tile of this CTA concerns (a run that only
         // the other tile sees) has no MMAs
         auto output = [&](int c, uint32_t(&o)[16]) {
-            if (n_x > 0) {
+            if constexpr (kPieces == 2) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(o_sum[c * 16 + i]);
+            } else if (n_x > 0) {
                 ld_x16(tmem_o + c * 16, o);
                 wait_x16(o);
             } else {
