@@ -49,18 +49,20 @@ constexpr float kJoinWeight = 1.f / 1.5f;  // a segment of n units is cut into a
 // A segment's start and end weigh as much as this many pages: 96 sequences of 16 to 2048 keys, 16 heads of 64, 24.8 us (1:
 // 29.2, 2: 28.1, 7: 24.9); 64 of 500 to 16384, 32 q / 8 kv heads of 128, 75.2 us (1: 77.1).
 constexpr int kSegmentUnits = 4;
-constexpr float kLag = 8.f;                // log2 units; weights stay below 2^8, within fp16
+constexpr float kLag = 8.f;                // log2 units
 constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
 
 // How q of type T and the weights come to fp16. bf16: q's row as it is once its largest magnitude lies in [1, 2), the
-// weights rounded. fp32: both as sums of two halves, 22 bits; the row's largest magnitude in [2^14, 2^15) and a weight of 2^7
-// at the reference keep what is small next to them within fp16's range (2^-39 of the row's largest, 2^-32 of a weight of 1).
+// weights rounded. fp32: both as sums of two halves, 22 bits; the row's largest magnitude in [2^14, 2^15) keeps what is small
+// next to it within fp16's range (2^-39 of the largest). A weight of 2^7 at the reference does that for the weights: those
+// down to 2^-21 of the largest keep their 11 bits, and what is lost is 2^-32 of it; many keys far below one add up to a part
+// of the output that 2^-25, with a weight of 1 there, would round away.
 template <typename T>
 struct Fp16Form {
     static constexpr bool kTwo = std::is_same<T, float>::value;
     static constexpr int kPieces = kTwo ? 2 : 1, kTop = kTwo ? 14 : 0;  // a row's largest magnitude: 2^kTop ..
-    static constexpr float kAbove = kTwo ? 7.f : 0.f;                   // log2 of the weight of a score at the reference
 };
+constexpr float kAbove = 7.f;  // log2 of the weight of a score at the reference; 2^(kAbove + kLag) is within fp16
 
 // Pages of one step of a warp, and room for one step: 64 sequences of 500 to 16384 keys 76 us, with steps of two pages and
 // room for two or four of them 85.
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int f = 0; f < NH; ++f) top = max3(max3(top, x[i][f][0], x[i][f][1]), x[i][f][2], x[i][f][3]);
-            if (__any_sync(0xffffffffu, top > F::kAbove + kLag)) {
+            if (__any_sync(0xffffffffu, top > kAbove + kLag)) {
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
                     float cc[2];
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         for (int i = 0; i < NP; ++i) mx = max3(mx, sc[i][f][hh] * c1[f][hh], sc[i][f][2 + hh] * c1[f][hh]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        const float mn = fmaxf(mh[f][hh], mx - F::kAbove);
+                        const float mn = fmaxf(mh[f][hh], mx - kAbove);
                         cc[hh] = exp2_approx(mh[f][hh] - mn);
                         mh[f][hh] = mn;
                         lh[f][hh] *= cc[hh];

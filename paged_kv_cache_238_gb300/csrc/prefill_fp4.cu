@@ -66,6 +66,10 @@ struct Roles {
 };
 constexpr uint32_t kHalf = 16384;         // 128 rows x 128 bytes (64 fp16 columns)
 constexpr float kRescaleThreshold = 8.f;  // log2 units
+// log2 of the weight of a score at the reference, so that weights far below it (and fp32's second halves) lie within fp16's
+// range: 2^-25, which is lost, is 2^-32 of that, and many keys far below one add up to a part of the output. The largest
+// weight, 2^(kAbove + kRescaleThreshold), is within fp16 too.
+constexpr float kAbove = 7.f;
 constexpr float kLowest = -3e38f;         // a maximum before the first score: finite, so that no difference is NaN
 constexpr int kRankMax = 256;             // entries that each CTA ranks by their work
 constexpr int kFewWaves = 4;              // grids of up to this many CTAs an SM are ordered pair by pair
@@ -580,9 +584,6 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t tmem_s = tmem + x * 128 + half * 64 + lane_off;
         const uint32_t tmem_o = tmem + kO + x * 128 + half * (D / 2) + lane_off;  // the columns that it rescales and writes
-        // log2 of the weight of a score at the reference; in two pieces 2^7, so that small weights' second halves lie within
-        // fp16's range too (2^-25 is 2^-32 of that)
-        constexpr float kAbove = kPieces == 2 ? 7.f : 0.f;
         float m_ref = kLowest, l_sum = 0.f;  // the reference is the same in both threads of a row
         bool ok = true;
         int32_t keys = 0;  // of this half, those that the row sees are below this
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 uint32_t pk[32];
                 if (__any_sync(0xffffffffu, m_ref == kLowest)) alpha = move_reference();  // a row's first keys (alike in both warps)
                 sum = masked ? weights(std::true_type(), over, pk) : weights(std::false_type(), over, pk);
-                if (__any_sync(0xffffffffu, over > kRescaleThreshold) && lane == 0)
+                if (__any_sync(0xffffffffu, over > kAbove + kRescaleThreshold) && lane == 0)
                     *const_cast<volatile int32_t*>(&grow_at[x][quad]) = j + 1;
                 named_barrier(pair_bar, 64);
                 // both warps leave at the same tile, so that each meets the other at every barrier
