@@ -577,9 +577,8 @@ typedef struct {
  * pa_decode_fp4: pa_decode_bs over 4-bit pools: K_i[j] and V_i[j] are the values described above. Any
  * number of q heads per kv head. Products run on the tensor cores in fp16, which holds the pool's values
  * exactly; sums and softmax statistics are fp32. bf16 queries: each q head's row is scaled by a power of
- * two to fp16 (elements 2^-24 below the row's largest magnitude are lost), weights are rounded to fp16
- * (11 bits; what is 2^-32 below the largest is lost). fp32 queries: both are sums of two fp16 numbers,
- * 22 bits (what is 2^-39 below a row's largest magnitude, or 2^-32 below the weights' sum, is lost).
+ * two to fp16, weights are rounded to fp16 (11 bits). fp32 queries: both are sums of two fp16 numbers, 22 bits.
+ * What is 2^-39 below a row's largest magnitude, or 2^-32 below the weights' sum, is lost.
  * workspace: >= pa_decode_fp4_workspace_size(...) bytes, under the rules of pa_decode_scored's.
  */
 PA_API size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,

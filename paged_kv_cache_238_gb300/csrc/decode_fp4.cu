@@ -52,16 +52,17 @@ constexpr int kSegmentUnits = 4;
 constexpr float kLag = 8.f;                // log2 units
 constexpr float kLowest = -3e38f;          // a reference before the first score: finite, so that no difference is NaN
 
-// How q of type T and the weights come to fp16. bf16: q's row as it is once its largest magnitude lies in [1, 2), the
-// weights rounded. fp32: both as sums of two halves, 22 bits; the row's largest magnitude in [2^14, 2^15) keeps what is small
-// next to it within fp16's range (2^-39 of the largest). A weight of 2^7 at the reference does that for the weights: those
+// How q of type T and the weights come to fp16. bf16: q's row as it is once its largest magnitude lies in [2^14, 2^15), the
+// weights rounded. fp32: both as sums of two halves, 22 bits. The row's top of 2^14 keeps what is small next to it within
+// fp16's range (2^-39 of the largest is lost). A weight of 2^7 at the reference does that for the weights: those
 // down to 2^-21 of the largest keep their 11 bits, and what is lost is 2^-32 of it; many keys far below one add up to a part
 // of the output that 2^-25, with a weight of 1 there, would round away.
 template <typename T>
 struct Fp16Form {
     static constexpr bool kTwo = std::is_same<T, float>::value;
-    static constexpr int kPieces = kTwo ? 2 : 1, kTop = kTwo ? 14 : 0;  // a row's largest magnitude: 2^kTop ..
+    static constexpr int kPieces = kTwo ? 2 : 1;
 };
+constexpr int kTop = 14;       // a row's largest magnitude: 2^kTop ..
 constexpr float kAbove = 7.f;  // log2 of the weight of a score at the reference; 2^(kAbove + kLag) is within fp16
 
 // Pages of one step of a warp, and room for one step: 64 sequences of 500 to 16384 keys 76 us, with steps of two pages and
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             if (fresh) {
 #pragma unroll
                 for (int f = 0; f < NH; ++f) {
-                    // the row to fp16: times 2^(kTop - e) with 2^e <= its largest magnitude < 2^(e + 1)
+                    // the row to fp16: times 2^-e, so that its largest magnitude lies in [2^kTop, 2^(kTop + 1))
                     auto element = [&](int ks, int x) -> float {
                         if constexpr (F::kTwo) return __uint_as_float(raw[f][ks][x]);
                         else return __uint_as_float(x & 1 ? raw[f][ks][x / 2] & 0xffff0000u : raw[f][ks][x / 2] << 16);
@@ -629,9 +630,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         for (int x = 0; x < 4; x += 2) top = max3(top, fabsf(element(ks, x)), fabsf(element(ks, x + 1)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + e
+                    const int32_t field = static_cast<int32_t>(__float_as_uint(top) >> 23);  // 127 + kTop + e
                     // (not finite: as it is; rows below 2^-112: times 2^126)
-                    const int32_t e = field == 255 ? 0 : min(max(field, 1 + F::kTop), 253 + F::kTop) - 127 - F::kTop;
+                    const int32_t e = field == 255 ? 0 : max(field, 1 + kTop) - 127 - kTop;
                     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                     const float up2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll

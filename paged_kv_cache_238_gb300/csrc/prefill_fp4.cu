@@ -19,7 +19,7 @@
 // Registers move from the other warps to the softmax ones (setmaxnreg; the shares add up to the launch's).
 //
 // Query rows are brought to fp16 by a power of two per row, which the row's score factor takes back: bf16's 8 bits fit,
-// and what is 2^-24 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
+// and what is 2^-39 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
 //
 // fp32 queries: q and the weights are sums of two halves, 22 bits, so that S takes two Q K^T and O two P V; a CTA has one
 // query tile (the second half lies where a second tile would), and its softmax reads S twice, for the maximum and for the
@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         const int32_t t_row = (x ? t0b : t0a) + tl, n_x = x ? n_b : n_a;
         const bool row_valid = tl < TT && t_row < C;
         const int32_t pair_bar = 1 + x * 4 + quad;  // the barrier of the two warps that share 32 rows
-        {  // this warp's 16 rows to fp16, 16 bytes a lane: times 2^-e with 2^e <= the row's largest magnitude < 2^(e + 1)
+        {  // this warp's 16 rows to fp16, 16 bytes a lane: times 2^-e, so that the row's largest magnitude lies in [2^14, 2^15) and
+           // what is small next to it, or its second halves, within fp16's range
             const int32_t c = lane & (kLanes - 1);
             uint8_t* sq = smem + x * (kPieces * kTile);
             uint4 q_raw[kLoads];
@@ -536,24 +537,23 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             for (int k = 0; k < kLoads; ++k) {
                 const uint32_t w[4] = {q_raw[k].x, q_raw[k].y, q_raw[k].z, q_raw[k].w};
                 const int32_t rr = quad * 32 + half * 16 + k * kPer + lane / kLanes;
-                int32_t e;
+                int32_t field;  // 141 + e
                 if constexpr (kPieces == 1) {
                     uint32_t top = 0u;  // magnitudes as bf16 bits, two at a time
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = max_u16x2(top, w[i] & 0x7fff7fffu);
 #pragma unroll
                     for (int off = 1; off < kLanes; off <<= 1) top = max_u16x2(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    const int32_t field = static_cast<int32_t>(max(top & 0xffffu, top >> 16) >> 7);  // 127 + e
-                    e = field == 255 ? 0 : min(max(field, 1), 253) - 127;                            // (not finite: as it is)
-                } else {  // the largest magnitude in [2^14, 2^15), so that the second halves lie within fp16's range
+                    field = static_cast<int32_t>(max(top & 0xffffu, top >> 16) >> 7);
+                } else {
                     uint32_t top = 0u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = max(top, w[i] & 0x7fffffffu);
 #pragma unroll
                     for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                    const int32_t field = static_cast<int32_t>(top >> 23);
-                    e = field == 255 ? 0 : max(field, 15) - 141;
+                    field = static_cast<int32_t>(top >> 23);
                 }
+                const int32_t e = field == 255 ? 0 : max(field, 15) - 141;  // (not finite: as it is; rows below 2^-112: times 2^126)
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), f = a.negate ? -down : down;
                 if constexpr (kPieces == 1) {
                     uint32_t o[4];

@@ -1,8 +1,11 @@
-"""Attention over 4-bit pools where what is small next to a row's largest weight decides the output. The bounds are those of fp4_reference.py for fp32 queries, whose halves lie within fp16's range in the same
+"""Attention over 4-bit pools where what is small next to a row's largest weight, or to a query's largest element, decides
+the output. The bounds are those of fp4_reference.py for fp32 queries, whose halves lie within fp16's range in the same
 way; bf16 queries add the rounding of the weights to fp16:
 
   * the largest weight is 2^7 at least, and fp16's numbers below 2^-14 are 2^-24 apart: a weight w of a sum l is off by
-    max(2^-11 w, 2^-25), 2^-25 being 2^-32 l at most: 2^-11 A + n 2^-32 max |v|.
+    max(2^-11 w, 2^-25), 2^-25 being 2^-32 l at most: 2^-11 A + n 2^-32 max |v|;
+  * a query's largest magnitude lies in [2^14, 2^15): 8 bits fit above 2^-14, and an element below is off by 2^-25 at
+    most, 2^-39 of the largest magnitude.
 """
 import numpy as np
 import pytest
@@ -78,3 +81,19 @@ def sinks(dtype, S, chunk, H, L=2000):
                                        (170, 8, 1), (160, 130, 1)])  # one query tile and two, lists that are not split
 def test_many_weights_far_below_the_largest(dtype, S, chunk, H):
     check(sinks(dtype, S, chunk, H))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunks", [None, [150, 40, 3]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_elements_of_q_far_below_the_largest(dtype, chunks, D):
+    """The largest element of each row meets keys that are 0 in its dim; the others, 2^-24 of it, decide the scores."""
+    c = R.Case(42, [300, 40, 17], 8, 2, D, 16, dtype, chunks=chunks)
+    for b in {int(x) for x in c.table.ravel()} - {0}:  # code 0 in dim 0 of every key
+        c.pools[0][b].reshape(2, 9 * D)[:, :8 * D].reshape(2, 16, D // 2)[..., 0] &= 0xF0
+    c.values[0] = R.from_pool(c.pools[0])
+    q = R.W.as_f64(c.q) * 2.0 ** -24
+    q[..., 0] = 1.5
+    c.q = bits(q, dtype)
+    c.scale *= 2.0 ** 24
+    check(c)
