@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                         mh[f][hh] = kLowest;
                         lh[f][hh] = 0.f;
                         c1[f][hh] = a.c1 * __shfl_sync(0xffffffffu, up2, (2 * tig + hh) * 4);
-                        if (fabsf(c1[f][hh]) < 1e-37f) c1[f][hh] = copysignf(1e-37f, a.c1);  // times `hidden`: -inf, not NaN
+                        if (fabsf(c1[f][hh]) < 1e-37f) c1[f][hh] = copysignf(1e-37f, -hidden);  // times `hidden`: -inf, also for a scale of -0
                     }
                 }
                 cut_left = wc.j > 0;
