@@ -323,12 +323,12 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         leave();
         return;
     }
-    const int32_t t0a = NQ * pair * TT, t0b = t0a + TT;
+    const int32_t t0a = NQ * pair * TT;
     if (t0a >= C) {  // uniform over the CTA
         leave();
         return;
     }
-    const int32_t P0 = L - C;
+    const int32_t t0b = t0a + TT, P0 = L - C;
 
     // ---- key tiles of the CTA, and of each query tile: up to its last row's own key ---------------
     const int32_t all_a = (P0 + min(t0a + TT, C) - 1) / kKeys + 1;
@@ -897,7 +897,7 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
     a.negate = p.scale < 0.f;
     a.v_scale = v_scale;
     a.err = p.err;
-    const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len + NQ * TT - 1) / (NQ * TT);
+    const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len - 1) / (NQ * TT) + 1;  // (rounded up, whatever the bound)
     const int64_t entries = static_cast<int64_t>(pairs) * p.num_seqs;
     const bool by_pair = few_waves(entries, p.num_kv_heads, Roles<T, D, NQ>::per_sm, num_sms);
     a.sub = by_pair ? pairs : 1;

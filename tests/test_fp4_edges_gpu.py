@@ -8,7 +8,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 import fp4_reference as R  # noqa: E402
 from paged_kv_cache_238_gb300 import binding as B  # noqa: E402
-from test_fp4_gpu import check  # noqa: E402
+from test_fp4_gpu import Device, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,18 @@ def test_scales_that_vanish(dtype, scale, k_scale, chunks):
     c = R.Case(50, [77, 9], 8, 2, 64, 16, dtype, chunks=chunks, k_scale=k_scale)
     c.scale = scale
     check(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H_q", [1, 8])
+def test_the_largest_chunk_bound(dtype, H_q):
+    """A bound of the chunk's length of 2^31 - 1, and a table for as many keys: the chunks themselves are short."""
+    c = R.Case(51, [300], H_q, 1, 64, 128, dtype, chunks=[150])
+    bound = 2 ** 31 - 1
+    d = Device(c, max_len=bound, max_chunk=bound)
+    wide = torch.zeros(1, 2 ** 24, dtype=torch.int32, device="cuda")
+    wide[:, :d.table.shape[1]] = d.table
+    d.table = wide
+    d.run()
+    ref, tol = c.reference()
+    assert (np.abs(d.got() - ref) <= tol).all()
