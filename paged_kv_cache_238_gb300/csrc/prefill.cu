@@ -654,7 +654,7 @@ cudaError_t launch_tc(const PrefillArgs& a, cudaStream_t stream) {
                              static_cast<int>(TcSmem::total));
     if (e != cudaSuccess) return e;
     constexpr int TT = kTcRows / G;
-    const int32_t tiles = (a.max_chunk_len + TT - 1) / TT;
+    const int32_t tiles = (a.max_chunk_len - 1) / TT + 1;  // (rounded up, whatever the bound)
     const int32_t pairs = a.sp.rows > 0 ? tiles : (tiles + 1) / 2;  // Q tiles (pairs) per (sequence, kv head)
     dim3 grid(pairs, a.num_kv_heads, a.sp.rows > 0 ? 1 : a.num_seqs);
     const WaitDrill drill = wait_drill();

@@ -394,9 +394,9 @@ __global__ void __launch_bounds__(Warps<NQ>::threads, 3 - NQ) prefill_scored_ker
         if (tid == 0 && pair == 0) raise_error(err, PA_DEVERR_LEN_RANGE);
         return;
     }
-    const int32_t t0a = NQ * pair * TT, t0b = t0a + TT;
+    const int32_t t0a = NQ * pair * TT;
     if (t0a >= C) return;  // uniform over the CTA
-    const int32_t P0 = L - C;
+    const int32_t t0b = t0a + TT, P0 = L - C;
 
     // ---- rows of the softmax threads --------------------------------------------------------------
     const bool softmax_warp = warp < kSoftWarps;
@@ -1073,7 +1073,7 @@ cudaError_t launch_impl(const PrefillArgs& a, const TcScore& sc, const PrefillSc
     const int32_t G = a.num_q_heads / a.num_kv_heads, TT = kRows / G;
     const int32_t sub_log2 = block_size_log2(a.block_size) - 4;
     const int32_t cap_tokens = min(table_tokens(a.max_blocks_per_seq, sub_log2), a.max_seq_len);
-    const int32_t pairs = (a.max_chunk_len + NQ * TT - 1) / (NQ * TT);
+    const int32_t pairs = (a.max_chunk_len - 1) / (NQ * TT) + 1;  // (rounded up, whatever the bound)
     const int64_t entries = static_cast<int64_t>(pairs) * a.num_seqs;
     const bool by_pair = few_waves(entries, a.num_kv_heads, NQ, num_sms);
     const int32_t sub = by_pair ? pairs : 1;

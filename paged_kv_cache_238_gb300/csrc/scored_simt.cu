@@ -662,7 +662,7 @@ ScoredSimtPlan plan_scored_simt(int32_t S, int32_t max_chunk, int32_t Hq, int32_
     p.rows = static_cast<int64_t>(G) * (max_chunk > 0 ? max_chunk : 1) <= kFewRows ? kFewRows : kManyRows;
     p.head_chunks = (G + p.rows - 1) / p.rows;
     p.tokens = G < p.rows ? p.rows / G : 1;
-    p.groups = max_chunk > 0 ? (max_chunk + p.tokens - 1) / p.tokens : 1;
+    p.groups = max_chunk > 0 ? (max_chunk - 1) / p.tokens + 1 : 1;
     p.grid_x = S * p.groups;
     const int64_t ctas = static_cast<int64_t>(p.grid_x) * Hkv * p.head_chunks, pages = max_seq_len / kPageTokens + 2;
     int64_t parts = ctas > 0 ? (p.rows == kFewRows ? 2LL : 1LL) * num_sms / ctas : 1;
