@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
     const int32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
 
     // ---- barriers and tensor memory, while the entry is found -----------------------------------------
-    // per query tile and quadrant: the last key tile (+ 1) whose scores exceed a reference; a wait has given up
+    // per query tile and quadrant: the last key tile (+ 1) whose scores exceed a reference; the one whose wait has given up
     __shared__ int32_t grow_at[2][4], stopped[2][4];
     if (tid == 64) *reinterpret_cast<volatile int32_t*>(smem + L_::misc + 4) = 0;
     if (tid >= 96 && tid < 104) grow_at[tid >> 2 & 1][tid & 3] = stopped[tid >> 2 & 1][tid & 3] = 0;
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
         };
         for (int32_t j = 0; j < n_x; ++j) {
             ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a.err);
-            if (!__all_sync(0xffffffffu, ok) && lane == 0) *const_cast<volatile int32_t*>(&stopped[x][quad]) = 1;
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) *const_cast<volatile int32_t*>(&stopped[x][quad]) = j + 1;
             umma::fence_after_sync();
             keys = pos - ((base + j) * kKeys + half * 64) + 1;
             float alpha = 1.f, sum;
@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 if (__any_sync(0xffffffffu, over > kAbove + kRescaleThreshold) && lane == 0)
                     *const_cast<volatile int32_t*>(&grow_at[x][quad]) = j + 1;
                 named_barrier(pair_bar, 64);
-                // both warps leave at the same tile, so that each meets the other at every barrier
-                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
+                // both warps leave at the same tile, so that each meets the other at every barrier: a stop that the other warp
+                // has met since, a tile later, does not count yet
+                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) != j + 1;
                 if (!ok) break;
                 if (*const_cast<volatile int32_t*>(&grow_at[x][quad]) == j + 1) {
                     alpha *= move_reference();
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             } else {  // the maximum first (a barrier of both warps), then the weights
                 if (j > 0) collect();  // the PV of tile j - 1 finished before S of tile j was committed
                 alpha = move_reference();
-                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) == 0;
+                ok = *const_cast<volatile int32_t*>(&stopped[x][quad]) != j + 1;
                 if (!ok) break;
                 sum = weights_in_place();
             }
