@@ -631,13 +631,16 @@ PA_API pa_status pa_get_device_errors(uint32_t* errors, int32_t clear);
  *   PA_DRILL_OFF              normal operation (limit back to 1 s; limit_ns is ignored)
  *   PA_DRILL_DECODE_STAGE     bf16 grouped decode (pa_decode, pa_decode_append, pa_step):
  *                             the warp that holds the first page of the work list announces
- *                             16 bytes more on its first ring stage than its copies bring
+ *                             16 bytes more on its first ring stage than its copies bring;
+ *                             pa_decode_fp4: likewise, on its first step of K
  *   PA_DRILL_PREFILL_K_TILE   tensor-core prefill (pa_prefill_chunk, pa_step): the CTA of the
  *                             first Q-tile pair of kv head 0 of the longest sequence announces
- *                             16 bytes more on its first K tile
+ *                             16 bytes more on its first K tile; pa_prefill_fp4 on the tensor cores: the
+ *                             CTA of kv head 0 that is first in the order of work (up to 256 entries: the
+ *                             longest; else the first sequence's) likewise
  * While a drill is on, limit_ns (1000 .. 10^9) is the wait limit of those kernels. The setting
  * is process-wide and is read when a kernel is launched (a captured graph keeps the values of
- * its capture). After a drilled call the results of that call are invalid and the decode
+ * its capture). After a drilled call the results of that call are invalid and its
  * workspace must be zero-filled again before its next use. Returns PA_ERR_INVALID_ARG for an
  * unknown kind or a limit out of range, else PA_OK.
  */

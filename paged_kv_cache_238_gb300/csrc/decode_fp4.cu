@@ -106,6 +106,8 @@ struct Params {
     float* piece_o;    // [C][2][hs][D]
     float2* piece_ml;  // [C][2][hs]
     uint32_t* err;
+    uint64_t wait_limit_ns;
+    int32_t drill;  // the warp of the list's first unit: its first K step waits for 16 bytes that no copy brings
 };
 
 __device__ __forceinline__ void bulk_copy_g2s(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar,
@@ -341,16 +343,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
         // room for one step: the next one's K is sent for when this one's scores are done, its V at the step's end.
         // Block ids come 32 units at a time, the next 32 on their way while these are used.
         int32_t k_steps = 0, v_steps = 0, id_cur = lane_page(0), id_nxt = n > 32 ? lane_page(1) : -1, step_id = -1;
-        auto send = [&](const uint8_t* pool, uint8_t* to, uint64_t* bar) {
+        auto send = [&](const uint8_t* pool, uint8_t* to, uint64_t* bar, uint32_t more) {
             const bool mine = lane < SP && step_id >= 0 && !*abort_flag;
             const uint32_t copies = __ballot_sync(0xffffffffu, mine);
-            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copies) * kPage);
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copies) * kPage + more);
             __syncwarp();
             if (mine) bulk_copy_g2s(to + lane * kPage, pool + static_cast<int64_t>(step_id) * kPage, kPage, bar, kv_policy);
         };
         auto send_k = [&]() {
             step_id = __shfl_sync(0xffffffffu, id_cur, (k_steps * SP + lane) & 31);
-            send(a.k_cache, ring, &bars[0]);
+            send(a.k_cache, ring, &bars[0], a.drill && k_steps == 0 && a_w == 0 ? 16u : 0u);
             ++k_steps;
             if (((k_steps * SP) & 31) == 0) {
                 id_cur = id_nxt;
@@ -359,13 +361,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
         };
         auto send_v = [&]() {
-            send(a.v_cache, ring + SP * kPage, &bars[1]);
+            send(a.v_cache, ring + SP * kPage, &bars[1], 0u);
             ++v_steps;
         };
         send_k();
         send_v();
         auto landed = [&](uint64_t* bar, int32_t step) {
-            if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(step) & 1u, abort_flag))) return true;
+            if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, static_cast<uint32_t>(step) & 1u, abort_flag, a.wait_limit_ns)))
+                return true;
             if (lane == 0) {
                 if (!*abort_flag) raise_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
                 *abort_flag = 1;
@@ -721,8 +724,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
         // copies still in flight after an abort land before the CTA can exit
         if (*abort_flag && lane == 0) {
-            mbar_wait_timeout(&bars[0], static_cast<uint32_t>(k_steps - 1) & 1u);
-            mbar_wait_timeout(&bars[1], static_cast<uint32_t>(v_steps - 1) & 1u);
+            mbar_wait_timeout(&bars[0], static_cast<uint32_t>(k_steps - 1) & 1u, a.wait_limit_ns);
+            mbar_wait_timeout(&bars[1], static_cast<uint32_t>(v_steps - 1) & 1u, a.wait_limit_ns);
         }
     }
     __syncthreads();
@@ -905,6 +908,9 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
     a.piece_o = reinterpret_cast<float*>(ws + kScoredCounterBytes);
     a.piece_ml = reinterpret_cast<float2*>(a.piece_o + static_cast<size_t>(plan.num_ctas) * 2 * hs * D);
     a.err = d.err;
+    const WaitDrill drill = wait_drill();
+    a.wait_limit_ns = drill.limit_ns;
+    a.drill = drill.kind == kDrillDecodeStage ? 1 : 0;
     // Programmatic launch: the grid may be set up while the kernel before it drains.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

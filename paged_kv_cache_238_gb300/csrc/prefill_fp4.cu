@@ -119,6 +119,8 @@ struct Args {
     float v_scale;
     Split split;
     uint32_t* err;
+    uint64_t wait_limit_ns;
+    int32_t drill;  // the CTA with the longest list: the first K tile's barrier waits for 16 bytes that nothing brings
 };
 
 // Instruction descriptor for kind::f16 with fp16 A and B and an fp32 accumulator.
@@ -161,7 +163,7 @@ __device__ __forceinline__ int32_t read_flag(uint32_t flag) {
 // Bounded wait; kSleep > 0: polls are that many ns apart, so that the many warps that wait leave the
 // issue slots to those that compute (the MMA warp, alone on the critical path, polls at once).
 template <uint32_t kSleep>
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint32_t flag, uint32_t* err) {
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, uint32_t flag, const Args& a) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
@@ -171,8 +173,8 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, ui
             if (mbar_try_wait(bar, parity)) return true;
         }
         if (read_flag(flag)) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            raise_error(err, PA_DEVERR_WAIT_TIMEOUT);
+        if (global_timer_ns() - t0 > a.wait_limit_ns) {
+            raise_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
             asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(flag) : "memory");
             return false;
         }
@@ -395,6 +397,8 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
     if (!softmax_warp) fewer_registers<Roles::other_regs>();
     if (unpack_warp) {
         // ======================================== unpack ========================================
+        if (a.drill && tid == 32 && place == 0 && h == 0 && (SPLIT || sub > 1 ? blockIdx.x == 0 : pair == 0))
+            mbar_expect_tx(&k_full[0], 16u);  // (before this warp stores its unit of the tile)
         RawRow<D> raw;
         load(u_first, block_of(u_first), raw);
         int32_t block_n = block_of(u_first + kUnpackWarps);  // of the next unit
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             const bool is_v = u & 4;
             const int32_t nst = is_v ? kVStages : kKStages, st = j % nst, use = j / nst;
             if (use > 0) {
-                const bool ok = wait_or_abort<40>(is_v ? &v_empty[st] : &k_empty[st], static_cast<uint32_t>(use - 1) & 1u, abort_flag, a.err);
+                const bool ok = wait_or_abort<40>(is_v ? &v_empty[st] : &k_empty[st], static_cast<uint32_t>(use - 1) & 1u, abort_flag, a);
                 if (!__all_sync(0xffffffffu, ok)) return false;
             }
             uint8_t* tile = smem + (is_v ? L_::v : L_::k) + st * kTile;
@@ -470,11 +474,11 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                                               (acc && kPieces == 1) || k > 0 || c < kPieces - 1);
             };
             auto wait_k = [&]() {
-                const bool ok = wait_or_abort<0>(&k_full[ks], k_use & 1u, abort_flag, a.err);
+                const bool ok = wait_or_abort<0>(&k_full[ks], k_use & 1u, abort_flag, a);
                 umma::fence_after_sync();
                 return ok;
             };
-            bool ok = wait_or_abort<0>(q_full, 0, abort_flag, a.err) && wait_k();
+            bool ok = wait_or_abort<0>(q_full, 0, abort_flag, a) && wait_k();
             if (ok) {
                 if (n_a > 0) qk(0);
                 if (n_b > 0) qk(1);
@@ -486,9 +490,9 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                     ks = 0;
                     ++k_use;
                 }
-                ok = wait_or_abort<0>(&v_full[vs], v_use & 1u, abort_flag, a.err);
+                ok = wait_or_abort<0>(&v_full[vs], v_use & 1u, abort_flag, a);
                 if (ok && j < n_a) {  // P written, S read
-                    ok = wait_or_abort<0>(&p_full[0], j & 1, abort_flag, a.err);
+                    ok = wait_or_abort<0>(&p_full[0], j & 1, abort_flag, a);
                     umma::fence_after_sync();
                     if (ok) pv(0, j > 0);
                     if (ok && j + 1 == n_a) umma::commit(&o_done[0]);
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 if (ok && more) ok = wait_k();
                 if (ok && j + 1 < n_a) qk(0);
                 if (ok && j < n_b) {
-                    ok = wait_or_abort<0>(&p_full[1], j & 1, abort_flag, a.err);
+                    ok = wait_or_abort<0>(&p_full[1], j & 1, abort_flag, a);
                     umma::fence_after_sync();
                     if (ok) pv(1, j > 0);
                     if (ok && j + 1 == n_b) umma::commit(&o_done[1]);
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
                 }
             }
             umma::commit(idle);  // arrives once every MMA issued above has finished
-            mbar_wait_timeout(idle, 0);
+            mbar_wait_timeout(idle, 0, a.wait_limit_ns);
         }
     } else {
         // ==================================== queries, softmax ==================================
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             }
         };
         for (int32_t j = 0; j < n_x; ++j) {
-            ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a.err);
+            ok = wait_or_abort<20>(&s_full[x], j & 1, abort_flag, a);
             if (!__all_sync(0xffffffffu, ok) && lane == 0) *const_cast<volatile int32_t*>(&stopped[x][quad]) = j + 1;
             umma::fence_after_sync();
             keys = pos - ((base + j) * kKeys + half * 64) + 1;
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(Roles<T, D, NQ>::threads, Roles<T, D, NQ>::per
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        if (ok && n_x > 0) ok = wait_or_abort<20>(&o_done[x], 0, abort_flag, a.err);
+        if (ok && n_x > 0) ok = wait_or_abort<20>(&o_done[x], 0, abort_flag, a);
         ok = __all_sync(0xffffffffu, ok);
         umma::fence_after_sync();
         if (n_x > 0) collect();
@@ -898,6 +902,9 @@ cudaError_t launch_impl(const PrefillArgs& p, float v_scale, const PrefillScored
     a.negate = p.scale < 0.f;
     a.v_scale = v_scale;
     a.err = p.err;
+    const WaitDrill drill = wait_drill();
+    a.wait_limit_ns = drill.limit_ns;
+    a.drill = drill.kind == kDrillPrefillKTile ? 1 : 0;
     const int32_t TT = kRows / a.G, pairs = (p.max_chunk_len - 1) / (NQ * TT) + 1;  // (rounded up, whatever the bound)
     const int64_t entries = static_cast<int64_t>(pairs) * p.num_seqs;
     const bool by_pair = few_waves(entries, p.num_kv_heads, Roles<T, D, NQ>::per_sm, num_sms);
