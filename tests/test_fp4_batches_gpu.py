@@ -9,7 +9,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 import fp4_reference as R  # noqa: E402
 from paged_kv_cache_238_gb300 import binding as B  # noqa: E402
-from test_fp4_gpu import check  # noqa: E402
+from test_fp4_gpu import Device, check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,34 @@ def test_prefill_of_many_sequences(dtype, S, chunk, prior, H_q, H_kv, D):
     lens = chunks + ragged(76, S, 0, prior)
     chunks[5] = lens[5] = 0
     check(R.Case(77, lens, H_q, H_kv, D, 64, dtype, chunks=chunks))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunks", [True, False])
+def test_more_sequences_than_a_grid_has_rows(dtype, chunks):
+    """Sequences of one key or none: an output is the key's V, or zero (decode), or not there (prefill)."""
+    n, block = np.arange(66000), 1 + np.arange(66000) % 97
+    lens = (n % 3 != 0).astype(np.int32)
+    c = R.Case(78, [16] * 97, 2, 2, 64, 16, dtype)  # 97 blocks of keys, which the sequences share
+    held = c.values[1][:, :, 0]  # [block][head][64]: of each block's first key
+    q = np.random.default_rng(79).standard_normal((len(n), 2, 64))
+    rows = lens > 0
+    c.lens, c.table, c.decode, c.chunks = lens, c.table[:, :1][block - 1], not chunks, lens
+    c.qsl = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    if chunks:
+        q = q[rows]
+    c.q = R.W.f32_to_bf16_bits(q.astype(np.float32)) if dtype == "bf16" else q.astype(np.float32)
+    d = Device(c)
+    d.run()
+    want = held[c.table[:, 0]] * lens[:, None, None]
+    want = want[rows] if chunks else want
+    # one weight over itself, as the tolerance has it for one key without an error of its score; 6 significant bits are bf16's own
+    tol = (2.0 ** -20 + (4 * 17 + 1) * R.U) * np.abs(want) if dtype == "f32" else 0.0
+    assert (np.abs(d.got() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_heads_than_a_tile_has_rows_on_long_contexts(dtype, D):
+    """On the CUDA cores, with the keys in partitions."""
+    check(R.Case(80, [3000, 700], 130, 1, D, 32, dtype, chunks=[1, 1], k_scale=0.25, v_scale=4.0))
