@@ -938,11 +938,16 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
     return cudaSuccess;
 }
 
+// Warps of a CTA, in fours for the four schedulers. Up to 8 heads, D = 128: 75 us with 12 (64 sequences of 500 to 16384 keys),
+// 8: 101, 10: 86, 14: 84, 16 (spilled): 77; D = 64: 23.7 with 16 (96 of 16 to 2048), 12: 24.8. Twice the accumulators (more
+// than 8 heads), or twice the queries (fp32, D = 128), leave registers for 8.
+constexpr int warps_of(int NH, int D, bool two_pieces) { return NH == 2 ? 8 : D == 64 ? 16 : two_pieces ? 8 : 12; }
+
 template <typename T, int D>
 cudaError_t pick(const DecodeArgs& a, float v_scale, const DecodeScoredPlan& plan, cudaStream_t stream) {
-    constexpr int kWarps = D == 64 ? 16 : Fp16Form<T>::kTwo ? 8 : 12;
-    if (a.num_q_heads / a.num_kv_heads > 8) return launch_impl<T, D, 8, 2>(a, v_scale, plan, stream);
-    return launch_impl<T, D, kWarps, 1>(a, v_scale, plan, stream);
+    constexpr bool two = Fp16Form<T>::kTwo;
+    if (a.num_q_heads / a.num_kv_heads > 8) return launch_impl<T, D, warps_of(2, D, two), 2>(a, v_scale, plan, stream);
+    return launch_impl<T, D, warps_of(1, D, two), 1>(a, v_scale, plan, stream);
 }
 
 }  // namespace
@@ -959,10 +964,7 @@ bool plan_decode_fp4(int32_t S, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_
     if (batch < 1 || S < 1) return false;
     plan->batch = static_cast<int32_t>(batch < S ? batch : S);
     plan->num_ctas = dev.num_sms;
-    // Warps in fours, for the four schedulers, as many as registers allow without spilling. Up to 8 heads, D = 128: 75 us with
-    // 12 (64 sequences of 500 to 16384 keys), 8: 101, 10: 86, 14: 84, 16 (spilled): 77; D = 64: 23.7 with 16 (96 of 16 to
-    // 2048), 12: 24.8. Twice the accumulators (more than 8 heads), or twice the queries (fp32, D = 128), leave room for 8.
-    plan->warps = G > 8 ? 8 : D == 64 ? 16 : dtype == PA_F32 ? 8 : 12;
+    plan->warps = warps_of(G > 8 ? 2 : 1, D, dtype == PA_F32);
     if (layout(plan->warps, hs, D, plan->batch).total + 64 > static_cast<uint32_t>(dev.max_smem_optin)) return false;
     plan->stages = 1;
     plan->workspace_bytes = kScoredCounterBytes + static_cast<size_t>(plan->num_ctas) * 2 * hs * (D * 4 + 8);
