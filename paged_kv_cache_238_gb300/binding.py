@@ -842,11 +842,13 @@ def pa_rotate_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, sl
         q_ptr, o_ptr, q_step, o_step = q.data_ptr(), q_out.data_ptr(), qs[0], outs[0]
     if dev != torch._C._cuda_getDevice():
         _need_current(dev)
-    st = (_lib or load()).pa_rotate_and_cache(
-        _pack_rotate(o_ptr, q_ptr, k.data_ptr(), v.data_ptr(), o_step, q_step, ks[0], vs[0], positions.data_ptr(),
-                     cos_sin.data_ptr(), longest, R, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-                     slot_mapping.data_ptr(), T, H_q, H_kv, D, NB, BS, code, PA_FP4 if fp4 else code, k_scale, v_scale),
-        _raw_stream(stream, dev))
+    try:
+        desc = _pack_rotate(o_ptr, q_ptr, k.data_ptr(), v.data_ptr(), o_step, q_step, ks[0], vs[0], positions.data_ptr(),
+                            cos_sin.data_ptr(), longest, R, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                            slot_mapping.data_ptr(), T, H_q, H_kv, D, NB, BS, code, PA_FP4 if fp4 else code, k_scale, v_scale)
+    except struct.error as e:
+        raise ValueError(f"pa_rotate_and_cache: {e}") from None
+    st = (_lib or load()).pa_rotate_and_cache(desc, _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_rotate_and_cache", st)
 
@@ -903,10 +905,13 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_table, seq_lens, max_seq_len: 
                                                                     workspace)
     if T != S:
         raise ValueError(f"decode takes one query row per sequence: {T} rows, {S} sequences")
-    st = (_lib or load()).pa_decode_fp4(
-        _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                        seq_lens.data_ptr(), 0, 0 if workspace is None else workspace.data_ptr(), ws_bytes, mb, S, 0,
-                        int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale, v_scale), _raw_stream(stream, dev))
+    try:
+        desc = _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               seq_lens.data_ptr(), 0, 0 if workspace is None else workspace.data_ptr(), ws_bytes, mb, S, 0,
+                               int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale, v_scale)
+    except struct.error as e:
+        raise ValueError(f"pa_decode_fp4: {e}") from None
+    st = (_lib or load()).pa_decode_fp4(desc, _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_decode_fp4", st)
 
@@ -929,11 +934,14 @@ def pa_prefill_fp4(out, q, k_cache, v_cache, block_table, seq_lens, query_start_
                                                                     workspace)
     if not _fits(query_start_loc, torch.int32, (S + 1,), dev):
         _need("query_start_loc", query_start_loc, torch.int32, (S + 1,), dev)
-    st = (_lib or load()).pa_prefill_fp4(
-        _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                        seq_lens.data_ptr(), query_start_loc.data_ptr(), 0 if workspace is None else workspace.data_ptr(),
-                        ws_bytes, mb, S, int(max_chunk_len), int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale,
-                        v_scale), _raw_stream(stream, dev))
+    try:
+        desc = _pack_attention(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                               seq_lens.data_ptr(), query_start_loc.data_ptr(),
+                               0 if workspace is None else workspace.data_ptr(), ws_bytes, mb, S, int(max_chunk_len),
+                               int(max_seq_len), H_q, H_kv, D, NB, BS, code, scale, k_scale, v_scale)
+    except struct.error as e:
+        raise ValueError(f"pa_prefill_fp4: {e}") from None
+    st = (_lib or load()).pa_prefill_fp4(desc, _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_prefill_fp4", st)
 
@@ -961,9 +969,12 @@ def pa_gather_fp4(k_out, v_out, k_cache, v_cache, slots, k_scale: float = 1.0, v
         _need("slots", slots, torch.int64, (n,), dev)
     if dev != torch._C._cuda_getDevice():
         _need_current(dev)
-    st = (_lib or load()).pa_gather_fp4(
-        _pack_rows(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), n, H_kv, D,
-                   NB, BS, code, k_scale, v_scale), _raw_stream(stream, dev))
+    try:
+        desc = _pack_rows(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(), n, H_kv,
+                          D, NB, BS, code, k_scale, v_scale)
+    except struct.error as e:
+        raise ValueError(f"pa_gather_fp4: {e}") from None
+    st = (_lib or load()).pa_gather_fp4(desc, _raw_stream(stream, dev))
     if st != PA_OK:
         _check("pa_gather_fp4", st)
 

@@ -43,3 +43,23 @@ def test_the_largest_chunk_bound(dtype, H_q):
     d.run()
     ref, tol = c.reference()
     assert (np.abs(d.got() - ref) <= tol).all()
+
+
+def test_numbers_that_no_field_holds():
+    """Bounds past 32 bits and factors that are no numbers are refused as other bad arguments are."""
+    for chunks in (None, [20, 3]):
+        c = R.Case(52, [20, 5], 8, 2, 64, 16, chunks=chunks)
+        d = Device(c)
+        d.max_len = 2 ** 31
+        with pytest.raises(ValueError):
+            d.run()
+        d.max_len, c.v_scale = 20, "1"
+        with pytest.raises(ValueError):
+            d.run()
+        assert (d.got() == 7.0).all()
+    rows, pool = torch.zeros(1, 2, 64, device="cuda"), torch.zeros(B.fp4_pool_shape(2, 2, 16, 64), dtype=torch.uint8, device="cuda")
+    one = torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        B.pa_gather_fp4(rows, rows.clone(), pool, pool, one, k_scale=None)
+    with pytest.raises(ValueError):
+        B.pa_rotate_and_cache(None, None, rows, rows, one, torch.zeros(1, 64, device="cuda"), pool, pool.clone(), one, k_scale=None)
