@@ -517,8 +517,8 @@ PA_API pa_status pa_prefill_scored(void* out, const void* q, const void* k_cache
  * every kv head of k[t] rotated and of v[t] goes to slot slot_mapping[t] of the pools, as
  * pa_reshape_and_cache writes them (a negative slot: q_out only).
  * The rotation is computed in fp32 and rounded once to dtype. Into a 4-bit pool k is first rounded to
- * dtype (from a sum of about 45 bits), then stored: the bytes are those of rotating first and
- * storing what that gave.
+ * fp32 (from a sum of about 45 bits) and to dtype, then stored: the bytes are those of storing the
+ * exactly rotated k so rounded (one rotated in fp32 may lie on the other side of a border of dtype).
  *   q_out, q      [num_tokens] rows of [num_q_heads][head_dim], q_out_stride and q_stride elements
  *                 apart; q_out may be q itself (same stride). Both NULL with num_q_heads 0.
  *   k, v          [num_tokens] rows of [num_kv_heads][head_dim], k_stride and v_stride apart
@@ -575,7 +575,9 @@ typedef struct {
 
 /*
  * pa_decode_fp4: pa_decode_bs over 4-bit pools: K_i[j] and V_i[j] are the values described above. Any
- * number of q heads per kv head. Products run on the tensor cores in fp16, which holds the pool's values
+ * number of q heads per kv head. Products run on the tensor cores in fp16 (on the CUDA cores in fp32 where
+ * num_kv_heads * ceil(heads per kv head / 16) exceeds 16384, or that times max_seq_len / 16 nears 2^31;
+ * pa_prefill_fp4: above 128 q heads per kv head or 65535 sequences), which holds the pool's values
  * exactly; sums and softmax statistics are fp32. bf16 queries: each q head's row is scaled by a power of
  * two to fp16, weights are rounded to fp16 (11 bits). fp32 queries: both are sums of two fp16 numbers, 22 bits.
  * What is 2^-39 below a row's largest magnitude, or 2^-32 below the weights' sum, is lost.

@@ -28,7 +28,7 @@
 // 64 q / 8 kv heads of 128: 57 us, 4.2 TB/s, 62 % of the measured copy rate (32 sequences of 32768: 228 us, 78 %); 64 of 500
 // to 16384, 32 q / 8 kv heads: 75 us (67 %), of which 4.4 pass until the first pages have come and 8 to 11 go to the slowest
 // SM and the joins. 4 sequences of up to 700 keys: 9.1 us in a graph, a chain of latencies.
-// fp32 queries (before on the CUDA cores): 8 of 8000 to 9000 keys, 16 q / 4 kv heads of 128, 21.6 us (54.8); 64 of 10 to
+// fp32 queries (before on the CUDA cores): 8 of 8000 to 9000 keys, 16 q / 4 kv heads of 128, 21.7 us (54.8); 64 of 10 to
 // 2000, 16 heads of 64, 22.3 (58.1); 24 of up to 777, 12 q / 4 kv heads of 64, 10.2 (12.1).
 #include <math.h>
 
@@ -940,7 +940,8 @@ cudaError_t launch_impl(const DecodeArgs& d, float v_scale, const DecodeScoredPl
 
 // Warps of a CTA, in fours for the four schedulers. Up to 8 heads, D = 128: 75 us with 12 (64 sequences of 500 to 16384 keys),
 // 8: 101, 10: 86, 14: 84, 16 (spilled): 77; D = 64: 23.7 with 16 (96 of 16 to 2048), 12: 24.8. Twice the accumulators (more
-// than 8 heads), or twice the queries (fp32, D = 128), leave registers for 8.
+// than 8 heads), or twice the queries (fp32, D = 128), leave registers for 8. fp32 spills 4 to 20 bytes, and 412 with more than 8
+// heads of 128, both at once: 64 sequences of 2000 to 8000 keys, 64 q / 4 kv heads, 95 us (bf16 64; of 64 54 and 43).
 constexpr int warps_of(int NH, int D, bool two_pieces) { return NH == 2 ? 8 : D == 64 ? 16 : two_pieces ? 8 : 12; }
 
 template <typename T, int D>

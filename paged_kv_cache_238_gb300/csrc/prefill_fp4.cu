@@ -16,7 +16,8 @@
 //               key reads the key's codes and scales a unit ahead, converts them (e2m1x2 -> f16x2, times the
 //               scale, exact) and stores the row in the 128-byte-swizzled layout that the MMAs read; a key past the
 //               sequence's end becomes zeros, whatever its cell holds
-// Registers move from the other warps to the softmax ones (setmaxnreg; the shares add up to the launch's).
+// Registers move from the other warps to the softmax ones (setmaxnreg; the shares add up to the launch's). Every form but bf16 with
+// two tiles of head_dim 64 spills some: 36 to 64 bytes, fp32 at head_dim 64, whose running O has 32 of the 96 registers, 180 to 200.
 //
 // Query rows are brought to fp16 by a power of two per row, which the row's score factor takes back: bf16's 8 bits fit,
 // and what is 2^-39 below the row's largest magnitude is lost. Weights are rounded to fp16, outputs once to bf16.
@@ -30,9 +31,9 @@
 //
 // Bound: the chain S -> softmax -> P -> P V, Q K^T -> next S of each query tile, about 3000 cycles a key tile of which 1024 are
 // its own MMAs (both tiles' MMAs take 2048), and each CTA's start (5 us) and end (1.5). 16 sequences of 512 new rows on 512 to
-// 4608 keys, 32 q / 8 kv heads of 128: 292 us, 1.06 PFLOP/s over visible pairs, 56 % of the measured bf16 rate. Forms that were
+// 4608 keys, 32 q / 8 kv heads of 128: 289 us, 1.07 PFLOP/s over visible pairs, 56 % of the measured bf16 rate. Forms that were
 // slower there: a thread per row (8 softmax warps) in two passes 351 us, in one 352 to 378; the mask in every tile instead of in
-// a copy of the loop 338; registers 56 / 88 instead of 48 / 96 (the softmax spills) 318; three stages of K and two of V 302.
+// a copy of the loop 338; registers 56 / 88 instead of 48 / 96 (the softmax spills more) 318; three stages of K and two of V 302.
 //
 // Few rows on many keys: the key list is cut into runs (Split), one CTA each, and a second kernel merges their
 // outputs by M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l. Every wait is bounded; a timeout sets

@@ -6,7 +6,7 @@
 //   interleaved  (x_2i, x_(2i + 1))   -> the same
 // dims from R on stay. bf16 and fp32 results are rounded once. A k that goes into 4 bits is computed to
 // about 45 bits first (each product as a rounded product and its error, summed with theirs), so that its
-// rounding to the call's type, and with it the code, is the exact result's.
+// rounding to fp32 and on to the call's type, and with it the code, is the exact result's.
 //
 // A thread owns 16 dims of a token's rows, as two chunks of 8 that rotate into one another (halves: chunk p and
 // chunk R/16 + p), and walks up to 8 rows of one kind (q, k or v heads) with the table's 16 values in registers. In 4
@@ -16,7 +16,8 @@
 // Bound: HBM in the pool's own type (8448 tokens, 32 q / 8 kv heads of 128, bf16: 34.4 us, 6.2 TB/s, 91 % of the measured copy
 // rate; loads row by row 36.2); in 4 bits the latency of a group's loads at 24 warps an SM and its arithmetic, about 20 instructions an
 // element of k and 7 of v (37.5 us of 48.5 with the read of the pool; with a division per element 58).
-// 64 tokens: 2.2 us, in 4 bits and read back 4.5.
+// 64 tokens: 2.2 us, in 4 bits and read back 4.5. fp32, 8448 tokens: 66.1 us; into 4 bits 61.9 (5.8 TB/s). Rows read back: 11.0 us
+// (4.2 TB/s), as fp32 19.6 (4.2): loads of 4 bytes of codes and 1 of scales a thread, waited for at 42 warps an SM.
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -119,8 +120,8 @@ struct Shape {
     int32_t q_per, k_per;
 };
 
-// Six CTAs an SM (80 registers) against five (96): the prompt 36.2 and 37.4 us; in 4 bits, which spill 15 registers for it,
-// 47.7 and 48.1.
+// Six CTAs an SM (80 registers) against five (96): the prompt 36.2 and 37.4 us; in 4 bits, where halves spill for it (76 bytes, fp32
+// 148), 47.7 and 48.1.
 template <typename T, bool F4, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 6) rotate_kernel(const __grid_constant__ RotateArgs a,
                                                           const __grid_constant__ Shape g) {
